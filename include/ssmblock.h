@@ -1,0 +1,118 @@
+/*
+ * ssmblock.h -- C ABI of libssmscan, second part: the operators that a block of
+ * a recurrent language model needs around its scan (ssmscan.h holds the scans).
+ *
+ *   ssm_add_norm_*    residual add, residual scale and norm before a block
+ *   ssm_gated_norm_*  the norm after a block, over groups of channels, with
+ *                     the SiLU gate
+ *   ssm_linattn_*     linear attention with a decay for each head
+ *   ssm_q4_*          products of few rows with 4-bit weights
+ *
+ * Ownership, errors, asynchrony, graph capture and reproducibility are those
+ * of ssmscan.h: every pointer is a device pointer owned by the caller, every
+ * argument is checked on the host before anything is enqueued, a non-OK status
+ * means that nothing was enqueued and ssm_last_error() says why, calls enqueue
+ * only kernels on `stream` (and the stream-ordered workspace that a call's
+ * comment names), and results are bitwise reproducible (no atomics).
+ * These calls need no alignment beyond the element's unless their comment says
+ * so.  Outputs must not overlap an input or each other except where stated.
+ * A required pointer may be NULL only when its tensor has no elements.
+ */
+#ifndef SSMBLOCK_H
+#define SSMBLOCK_H
+
+#include "ssmscan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Bits of the norm calls' flags:
+ *   SSM_NORM_CENTER     subtract the mean first (layer norm); without it the
+ *                       rows are divided by their root mean square.
+ *   SSM_NORM_GATE_LAST  gated norm only: norm first, then the gate.
+ */
+#define SSM_NORM_CENTER 1
+#define SSM_NORM_GATE_LAST 2
+
+/* Largest width that one norm runs over (width, or width / ngroups). */
+#define SSM_NORM_MAX_WIDTH 8192
+
+/*
+ * The norm before a block, with the residual add that precedes it:
+ *
+ *   r[i,d]   = alpha * residual[i,d] + scale[d] * x[i,d]
+ *   out[i,d] = (r[i,d] - m_i) / sqrt(v_i + eps) * weight[d] + bias[d]
+ *
+ * with m_i the row's mean under SSM_NORM_CENTER and 0 without it, and v_i the
+ * mean of (r[i,.] - m_i)^2.  Statistics and r are fp32; out is formed from the
+ * fp32 r, not from the rounded residual_out.
+ *   x            : [rows, width] in x_dtype, rows x_stride elements apart
+ *                  (x_stride >= width)
+ *   residual     : [rows, width] in res_dtype, or NULL (r = scale x)
+ *   weight, bias, scale: [width] fp32, or NULL (1, 0, 1)
+ *   residual_out : [rows, width] in res_dtype, or NULL (r is not stored); may be
+ *                  the same buffer as residual (in place)
+ *   out          : [rows, width] in out_dtype
+ */
+ssm_status ssm_add_norm_fwd(const void* x, int64_t x_stride, const void* residual, const float* weight,
+                            const float* bias, const float* scale, float alpha, float eps, int flags, void* out,
+                            void* residual_out, int64_t rows, int64_t width, ssm_dtype x_dtype,
+                            ssm_dtype res_dtype, ssm_dtype out_dtype, void* stream);
+
+/*
+ * Its gradients, from the stored r (= residual_out), dout = dL/dout and,
+ * optionally, dresidual_out = dL/dresidual_out (what arrives at the residual
+ * stream behind the block; NULL: nothing).  With n the normed rows before
+ * weight and u = dout weight:
+ *
+ *   dr        = (u - [mean u] - n mean(u n)) / sqrt(v + eps) + dresidual_out
+ *               ([mean u] under SSM_NORM_CENTER)
+ *   dresidual = alpha dr;  dx = scale dr;  dweight[d] = sum_i dout n;
+ *   dbias[d] = sum_i dout;  dscale[d] = sum_i x dr
+ *
+ *   dout in out_dtype; r, dresidual_out, dresidual in res_dtype; x, dx in
+ *   x_dtype; dweight, dbias, dscale: [width] fp32.  Each output may be NULL (not
+ *   computed); x is needed for dscale only.  dresidual may be the same buffer as
+ *   dresidual_out.  The sums over rows run in a fixed order over a workspace
+ *   of at most SSM_NORM_MAX_BLOCKS * 3 * width * 4 bytes, taken on `stream`
+ *   where one of them is asked for.
+ */
+#define SSM_NORM_MAX_BLOCKS 1024
+ssm_status ssm_add_norm_bwd(const void* dout, const void* r, const float* weight, const void* dresidual_out,
+                            const void* x, int64_t x_stride, const float* scale, float alpha, float eps, int flags,
+                            void* dx, void* dresidual, float* dweight, float* dbias, float* dscale, int64_t rows,
+                            int64_t width, ssm_dtype x_dtype, ssm_dtype res_dtype, ssm_dtype out_dtype,
+                            void* stream);
+
+/*
+ * The norm after a block's mixer, over ngroups contiguous groups of
+ * width / ngroups channels, with the gate z (NULL: no gate):
+ *
+ *   without SSM_NORM_GATE_LAST:  out = norm(x * silu(z)) * weight + bias
+ *   with it:                     out = (norm(x) * weight + bias) * silu(z)
+ *
+ *   x, z : [rows, width] in in_dtype, rows x_stride and z_stride elements apart
+ *   weight, bias: [width] fp32, or NULL (1, 0);  out: [rows, width] in out_dtype
+ */
+ssm_status ssm_gated_norm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const float* weight,
+                              const float* bias, float eps, int flags, void* out, int64_t rows, int64_t width,
+                              int64_t ngroups, ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream);
+
+/*
+ * Its gradients, from the forward's inputs and dout [rows, width] in out_dtype:
+ * dx and dz (iff z is given) [rows, width] in in_dtype; dweight and dbias
+ * [width] fp32, each NULL if not wanted (bias enters dz under
+ * SSM_NORM_GATE_LAST).  Workspace as for ssm_add_norm_bwd.
+ */
+ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride, const void* z, int64_t z_stride,
+                              const float* weight, const float* bias, float eps, int flags, void* dx, void* dz,
+                              float* dweight, float* dbias, int64_t rows, int64_t width, int64_t ngroups,
+                              ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSMBLOCK_H */

@@ -544,3 +544,7 @@ def ssm_ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, so
                                         _ptr(dt_bias), _flags(softplus, False), _ptr(out), batch, nheads, headdim,
                                         ngroups, d_state, _dtype_code(x), _dtype_code(out), _stream(stream)))
     return out
+
+
+from .block import (SSM_NORM_CENTER, SSM_NORM_GATE_LAST, ssm_add_norm_bwd, ssm_add_norm_fwd,  # noqa: E402,F401
+                    ssm_gated_norm_bwd, ssm_gated_norm_fwd)

@@ -1,0 +1,223 @@
+"""Python binding of the block operators (include/ssmblock.h): norms, linear
+attention with a decay for each head, and products with 4-bit weights.
+
+As in the package's other calls: argument marshalling only, tensors are passed
+to the C ABI as device pointers on the current stream, and there is no
+fallback.  Functions carry the C names.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+from . import _check, _dtype_code, _load, _stream
+
+SSM_NORM_CENTER = 1
+SSM_NORM_GATE_LAST = 2
+
+_vp, _i64, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+_ARGS = {
+    "ssm_add_norm_fwd": [_vp, _i64, _vp, _vp, _vp, _vp, _f32, _f32, _int, _vp, _vp, _i64, _i64, _int, _int, _int, _vp],
+    "ssm_add_norm_bwd": [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _f32, _f32, _int, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                         _int, _int, _int, _vp],
+    "ssm_gated_norm_fwd": [_vp, _i64, _vp, _i64, _vp, _vp, _f32, _int, _vp, _i64, _i64, _i64, _int, _int, _vp],
+    "ssm_gated_norm_bwd": [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                           _int, _int, _vp],
+}
+_fns: dict = {}
+
+
+def _fn(name: str):
+    """The C function, with its argument types set on first use."""
+    f = _fns.get(name)
+    if f is None:
+        f = getattr(_load(), name)
+        f.argtypes, f.restype = _ARGS[name], ctypes.c_int
+        _fns[name] = f
+    return f
+
+
+def _want(t, name: str, shape, dtype, device):
+    """The pointer of a contiguous tensor of this shape, dtype (None: float32 or
+    bfloat16) and device, or of no tensor.  The C ABI trusts the sizes it is given,
+    so every tensor is checked before its pointer is passed."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is None:
+        _dtype_code(t)
+    elif t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, shape, dtype, device, inner: int = 1):
+    """(pointer, row stride) of a tensor whose last ``inner`` dimensions are
+    contiguous and whose leading ones are evenly spaced rows, such as a slice of a
+    packed projection's last dimension."""
+    if t is None:
+        return None, 0
+    if t.is_contiguous():
+        n = 1
+        for s in t.shape[t.dim() - inner:]:
+            n *= s
+        return _want(t, name, shape, dtype, device), n
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is None:
+        _dtype_code(t)
+    elif t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    lead, step = t.dim() - inner, 1
+    for d in range(t.dim() - 1, lead - 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != step:
+            raise ValueError(f"{name} must be contiguous in its last {inner} dimension(s)")
+        step *= t.shape[d]
+    row, expect = None, None
+    for d in range(lead - 1, -1, -1):
+        if t.shape[d] == 1:
+            continue
+        if row is None:
+            row = t.stride(d)
+        elif t.stride(d) != expect:
+            raise ValueError(f"{name} must have evenly spaced rows")
+        expect = t.stride(d) * t.shape[d]
+    return t.data_ptr(), step if row is None else row
+
+
+def _new(shape, dtype, device):
+    import torch
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, scale=None, alpha: float = 1.0, eps: float = 1e-5,
+                     center: bool = False, out=None, residual_out=None, out_dtype=None, stream=None):
+    """Residual add and norm before a block: r = alpha * residual + scale * x and
+    out = norm(r) * weight + bias over the last dimension (root mean square, or with
+    ``center`` mean and variance).  x, residual: [..., width] (float32 or bfloat16
+    each; x may be a slice of a packed tensor); weight, bias, scale: [width] float32.
+    ``residual_out`` (residual's dtype, or float32 without one) may be ``residual``.
+    Returns (out, residual_out)."""
+    import torch
+    dev, shape = x.device, x.shape
+    width = shape[-1]
+    rows = x.numel() // width if width else 0
+    xp, xs = _rows(x, "x", shape, None, dev)
+    rp = _want(residual, "residual", shape, None, dev)
+    if out is None:
+        out = _new(shape, out_dtype or x.dtype, dev)
+    if residual_out is None:
+        residual_out = _new(shape, torch.float32 if residual is None else residual.dtype, dev)
+    cols = (width,)
+    _check(_fn("ssm_add_norm_fwd")(
+        xp, xs, rp, _want(weight, "weight", cols, torch.float32, dev), _want(bias, "bias", cols, torch.float32, dev),
+        _want(scale, "scale", cols, torch.float32, dev), alpha, eps, SSM_NORM_CENTER if center else 0,
+        _want(out, "out", shape, None, dev),
+        _want(residual_out, "residual_out", shape, None if residual is None else residual.dtype, dev), rows, width,
+        _dtype_code(x), _dtype_code(residual_out), _dtype_code(out), _stream(stream)))
+    return out, residual_out
+
+
+def ssm_add_norm_bwd(dout, r, weight=None, dresidual_out=None, x=None, scale=None, alpha: float = 1.0,
+                     eps: float = 1e-5, center: bool = False, want_weight: bool = True, want_bias: bool = False,
+                     want_scale: Optional[bool] = None, dx_dtype=None, stream=None):
+    """Gradients of ``ssm_add_norm_fwd`` from r (its ``residual_out``), dout [..., width]
+    and, optionally, the gradient that arrives at the residual stream.  Returns a dict
+    with dx (``dx_dtype``, or x's or dout's dtype), dresidual (r's dtype) and, as asked,
+    dweight, dbias and dscale (wanted by default where ``scale`` and ``x`` are given)."""
+    import torch
+    dev, shape, f32 = dout.device, dout.shape, torch.float32
+    width = shape[-1]
+    rows = dout.numel() // width if width else 0
+    if want_scale is None:
+        want_scale = scale is not None and x is not None
+    if want_scale and x is None:
+        raise ValueError("dscale needs x")
+    xdt = x.dtype if x is not None else (dx_dtype or dout.dtype)
+    if dx_dtype is not None and dx_dtype != xdt:
+        raise TypeError("dx has x's dtype")
+    xp, xs = _rows(x, "x", shape, None, dev) if want_scale else (None, width)
+    cols = (width,)
+    g = {"dx": _new(shape, xdt, dev), "dresidual": _new(shape, r.dtype, dev)}
+    if want_weight:
+        g["dweight"] = _new(cols, f32, dev)
+    if want_bias:
+        g["dbias"] = _new(cols, f32, dev)
+    if want_scale:
+        g["dscale"] = _new(cols, f32, dev)
+    ptr = {k: v.data_ptr() for k, v in g.items()}
+    _check(_fn("ssm_add_norm_bwd")(
+        _want(dout, "dout", shape, None, dev), _want(r, "r", shape, None, dev), _want(weight, "weight", cols, f32, dev),
+        _want(dresidual_out, "dresidual_out", shape, r.dtype, dev), xp, xs, _want(scale, "scale", cols, f32, dev),
+        alpha, eps, SSM_NORM_CENTER if center else 0, ptr["dx"], ptr["dresidual"], ptr.get("dweight"),
+        ptr.get("dbias"), ptr.get("dscale"), rows, width, _dtype_code(g["dx"]), _dtype_code(r), _dtype_code(dout),
+        _stream(stream)))
+    return g
+
+
+def _norm_flags(center, gate_first):
+    return (SSM_NORM_CENTER if center else 0) | (0 if gate_first else SSM_NORM_GATE_LAST)
+
+
+def ssm_gated_norm_fwd(x, z=None, weight=None, bias=None, ngroups: int = 1, gate_first: bool = True,
+                       eps: float = 1e-5, center: bool = False, out=None, out_dtype=None, stream=None):
+    """The norm after a block's mixer over ``ngroups`` groups of the last dimension's
+    channels, gated by SiLU(z): norm(x * silu(z)) * weight + bias with ``gate_first``,
+    (norm(x) * weight + bias) * silu(z) without.  x, z: [..., width] of one dtype (each
+    may be a slice of a packed tensor); weight, bias: [width] float32.  Returns out."""
+    import torch
+    dev, shape, f32 = x.device, x.shape, torch.float32
+    width = shape[-1]
+    rows = x.numel() // width if width else 0
+    xp, xs = _rows(x, "x", shape, None, dev)
+    zp, zs = _rows(z, "z", shape, x.dtype, dev)
+    if out is None:
+        out = _new(shape, out_dtype or x.dtype, dev)
+    cols = (width,)
+    _check(_fn("ssm_gated_norm_fwd")(
+        xp, xs, zp, zs, _want(weight, "weight", cols, f32, dev), _want(bias, "bias", cols, f32, dev), eps,
+        _norm_flags(center, gate_first), _want(out, "out", shape, None, dev), rows, width, ngroups, _dtype_code(x),
+        _dtype_code(out), _stream(stream)))
+    return out
+
+
+def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1, gate_first: bool = True,
+                       eps: float = 1e-5, center: bool = False, want_weight: bool = True,
+                       want_bias: Optional[bool] = None, stream=None):
+    """Gradients of ``ssm_gated_norm_fwd`` from its inputs and dout.  Returns a dict with
+    dx, dz (where z is given), and dweight and dbias as asked (dbias by default where
+    ``bias`` is given)."""
+    import torch
+    dev, shape, f32 = x.device, x.shape, torch.float32
+    width = shape[-1]
+    rows = x.numel() // width if width else 0
+    if want_bias is None:
+        want_bias = bias is not None
+    xp, xs = _rows(x, "x", shape, None, dev)
+    zp, zs = _rows(z, "z", shape, x.dtype, dev)
+    cols = (width,)
+    g = {"dx": _new(shape, x.dtype, dev)}
+    if z is not None:
+        g["dz"] = _new(shape, x.dtype, dev)
+    if want_weight:
+        g["dweight"] = _new(cols, f32, dev)
+    if want_bias:
+        g["dbias"] = _new(cols, f32, dev)
+    ptr = {k: v.data_ptr() for k, v in g.items()}
+    _check(_fn("ssm_gated_norm_bwd")(
+        _want(dout, "dout", shape, None, dev), xp, xs, zp, zs, _want(weight, "weight", cols, f32, dev),
+        _want(bias, "bias", cols, f32, dev), eps, _norm_flags(center, gate_first), ptr["dx"], ptr.get("dz"),
+        ptr.get("dweight"), ptr.get("dbias"), rows, width, ngroups, _dtype_code(x), _dtype_code(dout),
+        _stream(stream)))
+    return g

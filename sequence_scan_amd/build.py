@@ -38,8 +38,11 @@ def _scan_units():
 
 
 DEVICE_UNITS = _scan_units() + [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("scan.hip", "conv.hip", "bwd.hip", "ssd.hip")]
-HOST_UNITS = [(os.path.join(CSRC, "api.cpp"), [], "api")]
-SOURCES = sorted({u[0] for u in DEVICE_UNITS + HOST_UNITS})
+# The block operators' kernels (include/ssmblock.h): units of their own, so that
+# the profiles of the scans stay keyed to the scans' code alone.
+BLOCK_UNITS = [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("norm_add.hip", "norm_gate.hip")]
+HOST_UNITS = [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("api.cpp", "api_block.cpp")]
+SOURCES = sorted({u[0] for u in DEVICE_UNITS + BLOCK_UNITS + HOST_UNITS})
 HEADERS = [os.path.join(CSRC, f) for f in ("internal.h", "device.h", "scan_kernel.h")] + [
     os.path.join(os.path.dirname(HERE), "include", "ssmscan.h")]
 LIB = os.path.join(HERE, "libssmscan.so")
@@ -83,7 +86,7 @@ def _code_tokens(text: str) -> bytes:
 
 
 def kernel_source_sha256() -> str:
-    """One hash over the code of every device source and header (in a fixed
+    """One hash over the code of the scans' device sources and headers (in a fixed
     order, comments and layout left out): the identity of the kernels that a
     profile was taken of."""
     import hashlib
@@ -119,7 +122,7 @@ def build(verbose: bool = False) -> str:
     """Compile unconditionally; returns the path of libssmscan.so."""
     tmp = LIB + f".tmp{os.getpid()}"
     with tempfile.TemporaryDirectory(prefix="ssmscan_build_") as od:
-        units = DEVICE_UNITS + HOST_UNITS
+        units = DEVICE_UNITS + BLOCK_UNITS + HOST_UNITS
         objs = [os.path.join(od, name + ".o") for _, _, name in units]
         comp = [f for f in FLAGS if f != "-shared"]
         _run_all([["hipcc", *comp, *defs, "-c", src, "-o", obj] for (src, defs, _), obj in zip(units, objs)], verbose)
@@ -136,10 +139,11 @@ def asm(out_path: str) -> str:
     """Write the gfx950 assembly of every device translation unit, concatenated
     (for inspection and the code-generation checks)."""
     with tempfile.TemporaryDirectory(prefix="ssmscan_asm_") as od:
-        outs = [os.path.join(od, name + ".s") for _, _, name in DEVICE_UNITS]
+        units = DEVICE_UNITS + BLOCK_UNITS
+        outs = [os.path.join(od, name + ".s") for _, _, name in units]
         flags = [f for f in FLAGS if f not in ("-shared", "-fPIC")]
         _run_all([["hipcc", *flags, *defs, "--cuda-device-only", "-S", src, "-o", o]
-                  for (src, defs, _), o in zip(DEVICE_UNITS, outs)], False)
+                  for (src, defs, _), o in zip(units, outs)], False)
         with open(out_path, "w") as f:
             for o in outs:
                 with open(o) as g:
