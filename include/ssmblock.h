@@ -111,6 +111,90 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
                               float* dweight, float* dbias, int64_t rows, int64_t width, int64_t ngroups,
                               ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream);
 
+/*
+ * Linear attention with a decay for each head:
+ *
+ *   S_t = exp(g[b,t,h]) S_{t-1} + v_t k_t^T          (S: [dv, dk] per head)
+ *   out_t = scale * S_t q_t
+ *
+ * computed for prompts chunk by chunk with matrix products (as the Mamba-2 scan
+ * of ssmscan.h, whose decay is tied to its input's coefficient, and which has no
+ * gradient), and for single tokens by the recurrence.
+ *   q, k      : [batch, seqlen, ngroups, dk] bf16: each of the ngroups serves
+ *               nheads / ngroups consecutive heads
+ *   v, out    : [batch, seqlen, nheads, dv]; v bf16, out in out_dtype
+ *   log_decay : [batch, seqlen, nheads] fp32, or with SSM_LINATTN_FIXED_DECAY
+ *               [nheads], the same for every step.  Decays are meant to be <= 0;
+ *               minus infinity forgets everything before its step.
+ *   initial_state, last_state: [batch, nheads, dv, dk] fp32, each NULL for zero or
+ *               not stored; last_state may be initial_state (in place).
+ * q, k and v may be slices of packed tensors: token (b, t)'s values start
+ * (b * seqlen + t) * q_row (k_row, v_row) elements after the first token's.
+ * dk and dv: multiples of 8 up to SSM_LINATTN_MAX_DIM; q, k, v 16-byte aligned,
+ * rows multiples of 8 elements and at most 2^24; nheads a multiple of ngroups,
+ * at most 65535; states and out 16-byte aligned.  The state, the sums and the
+ * decays are fp32; the products run on bf16 matrix cores with computed operands
+ * split into two bf16 terms (about 16 significant bits).  A value of v that is
+ * not finite makes its column not finite from its step on, one of q, k or the
+ * decays every column; earlier steps are not touched.
+ *
+ * Plans: as for ssm_ssd_fwd.  A workgroup walks 64 columns of one (batch row,
+ * head); where they are few, the sequence is cut into time chunks (chunk_len a
+ * multiple of 64 where it cuts, at most 65535 of them), which costs one more pass
+ * over k and v and a workspace of
+ * batch * n_chunks * nheads * (dk * dv + 1) * 4 bytes on `stream` (plus a copy of
+ * an in-place initial state).  plan may be NULL; its states_per_wave is ignored.
+ */
+#define SSM_LINATTN_FIXED_DECAY 1
+#define SSM_LINATTN_MAX_DIM 128
+
+ssm_status ssm_linattn_plan_query(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dk, int64_t dv,
+                                  ssm_plan* plan);
+
+ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                           const float* log_decay, int flags, float scale, const float* initial_state, void* out,
+                           float* last_state, int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups,
+                           int64_t dk, int64_t dv, ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream,
+                           const ssm_plan* plan);
+
+/*
+ * Its gradients, from the forward's inputs, dout [batch, seqlen, nheads, dv] bf16
+ * and, optionally, dlast_state = dL/dlast_state:
+ *   dq, dk        : [batch, seqlen, ngroups, dk] in grad_dtype (summed over the
+ *                   heads of a group in head order)
+ *   dv            : [batch, seqlen, nheads, dv] in grad_dtype
+ *   dlog_decay    : fp32, of log_decay's shape
+ *   dinitial_state: [batch, nheads, dv, dk] fp32, or NULL (not computed)
+ * The forward's outputs are not needed.  Sequences are cut into time chunks of at
+ * most 2048 steps.  Workspace, on `stream`:
+ * batch * seqlen * nheads * ceil(dk / 64) * 8 bytes, with more than one time chunk
+ * 8 * batch * n_chunks * nheads * (dk * dv + 1), with dlast_state
+ * batch * nheads * dk * dv * 4, with nheads > ngroups
+ * batch * seqlen * nheads * dk * 8 more.  Alignment and rows as above, gradients
+ * and dout 16-byte aligned.
+ */
+ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                           const float* log_decay, int flags, float scale, const float* initial_state,
+                           const void* dout, const float* dlast_state, void* dq, void* dk_, void* dv_,
+                           float* dlog_decay, float* dinitial_state, int64_t batch, int64_t seqlen, int64_t nheads,
+                           int64_t ngroups, int64_t dk, int64_t dv, ssm_dtype in_dtype, ssm_dtype grad_dtype,
+                           void* stream);
+
+/*
+ * One token for every (b, h): state_out = exp(g) state + v k^T and
+ * out = scale * state_out q.  state, state_out: [batch, nheads, dv, dk] fp32, which may
+ * be one buffer (in place) or two (the state before the token is kept).
+ * q, k: [batch, ngroups, dk]; v, out: [batch, nheads, dv]; log_decay: [batch, nheads],
+ * or [nheads] with SSM_LINATTN_FIXED_DECAY.  in_dtype fp32 or bf16; dk a multiple of
+ * 4 up to SSM_LINATTN_MAX_STEP_DK; dv >= 1; nheads and batch at most 65535.  States
+ * 16-byte aligned, q and k aligned to four elements.
+ */
+#define SSM_LINATTN_MAX_STEP_DK 256
+ssm_status ssm_linattn_state_update(const float* state, float* state_out, const void* q, const void* k, const void* v,
+                                    const float* log_decay, int flags, float scale, void* out, int64_t batch,
+                                    int64_t nheads, int64_t ngroups, int64_t dk, int64_t dv, ssm_dtype in_dtype,
+                                    ssm_dtype out_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

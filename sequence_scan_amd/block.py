@@ -10,10 +10,11 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import _check, _dtype_code, _load, _stream
+from . import _check, _dtype_code, _load, _stream, ssm_plan
 
 SSM_NORM_CENTER = 1
 SSM_NORM_GATE_LAST = 2
+SSM_LINATTN_FIXED_DECAY = 1
 
 _vp, _i64, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _ARGS = {
@@ -23,6 +24,12 @@ _ARGS = {
     "ssm_gated_norm_fwd": [_vp, _i64, _vp, _i64, _vp, _vp, _f32, _int, _vp, _i64, _i64, _i64, _int, _int, _vp],
     "ssm_gated_norm_bwd": [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _f32, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                            _int, _int, _vp],
+    "ssm_linattn_plan_query": [_i64] * 5 + [ctypes.POINTER(ssm_plan)],
+    "ssm_linattn_fwd": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _f32, _vp, _vp, _vp] + [_i64] * 6 +
+                       [_int, _int, _vp, ctypes.POINTER(ssm_plan)],
+    "ssm_linattn_bwd": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _f32] + [_vp] * 8 + [_i64] * 6 +
+                       [_int, _int, _vp],
+    "ssm_linattn_state_update": [_vp] * 6 + [_int, _f32, _vp] + [_i64] * 5 + [_int, _int, _vp],
 }
 _fns: dict = {}
 
@@ -221,3 +228,106 @@ def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1
         ptr.get("dweight"), ptr.get("dbias"), rows, width, ngroups, _dtype_code(x), _dtype_code(dout),
         _stream(stream)))
     return g
+
+
+def ssm_linattn_plan_query(batch: int, seqlen: int, nheads: int, dk: int = 128, dv: int = 128) -> dict:
+    """The time chunks ``ssm_linattn_fwd`` picks for these sizes."""
+    p = ssm_plan()
+    _check(_fn("ssm_linattn_plan_query")(batch, seqlen, nheads, dk, dv, ctypes.byref(p)))
+    return {"chunk_len": p.chunk_len, "n_chunks": p.n_chunks}
+
+
+def _la_shapes(q, v, tokens: int):
+    if q.dim() != tokens + 2 or v.dim() != tokens + 2:
+        lead = "batch, seqlen" if tokens == 2 else "batch"
+        raise ValueError(f"q must be [{lead}, ngroups, dk] and v [{lead}, nheads, dv]")
+    return q.shape[-2], q.shape[-1], v.shape[-2], v.shape[-1]
+
+
+def _la_decay(g, lead, nheads, device):
+    """(pointer, flags) of the log decay: [*lead, nheads], or [nheads] for a fixed one."""
+    import torch
+    fixed = g.dim() == 1
+    return (_want(g, "log_decay", (nheads,) if fixed else (*lead, nheads), torch.float32, device),
+            SSM_LINATTN_FIXED_DECAY if fixed else 0)
+
+
+def ssm_linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, initial_state=None, out=None, last_state=None,
+                    out_dtype=None, stream=None, plan: Optional[dict] = None):
+    """Linear attention with a decay for each head (see include/ssmblock.h): q, k
+    [batch, seqlen, ngroups, dk] and v [batch, seqlen, nheads, dv] bfloat16 (each may be a
+    slice of a packed tensor); log_decay [batch, seqlen, nheads] or [nheads] float32; scale
+    1 / sqrt(dk) by default; states [batch, nheads, dv, dk] float32 (last_state is written
+    where given, and may be initial_state).  Returns out [batch, seqlen, nheads, dv].
+    ``plan`` = {"chunk_len": ..} forces the time chunks."""
+    import torch
+    G, dk, H, dv = _la_shapes(q, v, 2)
+    B, L, dev, f32 = q.shape[0], q.shape[1], q.device, torch.float32
+    qs, vs, st = (B, L, G, dk), (B, L, H, dv), (B, H, dv, dk)
+    qp, qr = _rows(q, "q", qs, None, dev, 2)
+    kp, kr = _rows(k, "k", qs, q.dtype, dev, 2)
+    vp, vr = _rows(v, "v", vs, q.dtype, dev, 2)
+    gp, flags = _la_decay(log_decay, (B, L), H, dev)
+    if out is None:
+        out = _new(vs, out_dtype or v.dtype, dev)
+    p = None
+    if plan is not None:
+        p = ssm_plan()
+        p.chunk_len = int(plan["chunk_len"])
+        p = ctypes.byref(p)
+    _check(_fn("ssm_linattn_fwd")(
+        qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
+        _want(initial_state, "initial_state", st, f32, dev), _want(out, "out", vs, None, dev),
+        _want(last_state, "last_state", st, f32, dev), B, L, H, G, dk, dv, _dtype_code(q), _dtype_code(out),
+        _stream(stream), p))
+    return out
+
+
+def ssm_linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, initial_state=None, dlast_state=None,
+                    want_dinitial_state: bool = False, grad_dtype=None, stream=None):
+    """Gradients of ``ssm_linattn_fwd`` from its inputs, dout [batch, seqlen, nheads, dv]
+    (bfloat16) and, optionally, the gradient of the last state.  Returns a dict with dq, dk,
+    dv (``grad_dtype``, or q's dtype), dlog_decay (float32, of log_decay's shape) and, as
+    asked, dinitial_state."""
+    import torch
+    G, dk, H, dv = _la_shapes(q, v, 2)
+    B, L, dev, f32 = q.shape[0], q.shape[1], q.device, torch.float32
+    qs, vs, st = (B, L, G, dk), (B, L, H, dv), (B, H, dv, dk)
+    gdt = grad_dtype or q.dtype
+    qp, qr = _rows(q, "q", qs, None, dev, 2)
+    kp, kr = _rows(k, "k", qs, q.dtype, dev, 2)
+    vp, vr = _rows(v, "v", vs, q.dtype, dev, 2)
+    gp, flags = _la_decay(log_decay, (B, L), H, dev)
+    g = {"dq": _new(qs, gdt, dev), "dk": _new(qs, gdt, dev), "dv": _new(vs, gdt, dev),
+         "dlog_decay": _new(log_decay.shape, f32, dev)}
+    if want_dinitial_state:
+        g["dinitial_state"] = _new(st, f32, dev)
+    _check(_fn("ssm_linattn_bwd")(
+        qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
+        _want(initial_state, "initial_state", st, f32, dev), _want(dout, "dout", vs, q.dtype, dev),
+        _want(dlast_state, "dlast_state", st, f32, dev), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+        g["dlog_decay"].data_ptr(), g["dinitial_state"].data_ptr() if want_dinitial_state else None, B, L, H, G, dk,
+        dv, _dtype_code(q), _dtype_code(g["dq"]), _stream(stream)))
+    return g
+
+
+def ssm_linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = None, out=None, state_out=None,
+                             out_dtype=None, stream=None):
+    """One token of linear attention: state [batch, nheads, dv, dk] float32 moves on (in
+    place, or into ``state_out``, which keeps ``state``).  q, k: [batch, ngroups, dk]; v:
+    [batch, nheads, dv] (float32 or bfloat16); log_decay: [batch, nheads] or [nheads]
+    float32.  Returns out [batch, nheads, dv]."""
+    import torch
+    G, dk, H, dv = _la_shapes(q, v, 1)
+    B, dev, f32 = q.shape[0], q.device, torch.float32
+    qs, vs, st = (B, G, dk), (B, H, dv), (B, H, dv, dk)
+    gp, flags = _la_decay(log_decay, (B,), H, dev)
+    if out is None:
+        out = _new(vs, out_dtype or v.dtype, dev)
+    sp = _want(state, "state", st, f32, dev)
+    _check(_fn("ssm_linattn_state_update")(
+        sp, sp if state_out is None else _want(state_out, "state_out", st, f32, dev), _want(q, "q", qs, None, dev),
+        _want(k, "k", qs, q.dtype, dev), _want(v, "v", vs, q.dtype, dev), gp, flags,
+        dk ** -0.5 if scale is None else scale, _want(out, "out", vs, None, dev), B, H, G, dk, dv, _dtype_code(q),
+        _dtype_code(out), _stream(stream)))
+    return out

@@ -134,6 +134,116 @@ ssm_status zero_sums(float* const sums[3], int64_t width, hipStream_t s) {
   return ok();
 }
 
+// ------------------------------------------------------------ linear attention
+
+static_assert(ssm::kLaMaxDim == SSM_LINATTN_MAX_DIM && ssm::kLaMaxStepDk == SSM_LINATTN_MAX_STEP_DK,
+              "block.h and ssmblock.h agree");
+
+struct LaSizes {
+  int64_t rows;      // batch * seqlen
+  int64_t v;         // elements of v and out
+  int64_t qk;        // elements of q and k, packed
+  int64_t state;     // elements of a state
+  int64_t decay;     // elements of the decay
+};
+
+ssm_status la_check(int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups, int64_t dk, int64_t dv, int flags,
+                    float scale, std::initializer_list<ssm_dtype> types, LaSizes* sz) {
+  if (batch < 0 || seqlen < 0 || nheads < 0 || ngroups < 0 || dk < 0 || dv < 0)
+    return fail(SSM_ERR_BAD_SHAPE, "negative size (batch=%lld seqlen=%lld nheads=%lld ngroups=%lld dk=%lld dv=%lld)",
+                (long long)batch, (long long)seqlen, (long long)nheads, (long long)ngroups, (long long)dk, (long long)dv);
+  if (ngroups < 1 || nheads < 1 || nheads % ngroups != 0)
+    return fail(SSM_ERR_UNSUPPORTED, "nheads=%lld must be a positive multiple of ngroups=%lld", (long long)nheads,
+                (long long)ngroups);
+  if (nheads > 65535) return fail(SSM_ERR_UNSUPPORTED, "nheads=%lld exceeds 65535", (long long)nheads);
+  if (batch > 65535) return fail(SSM_ERR_UNSUPPORTED, "batch=%lld exceeds 65535", (long long)batch);
+  if (dk < 1 || dv < 1 || dv > INT32_MAX) return fail(SSM_ERR_UNSUPPORTED, "dk and dv must be positive");
+  if ((flags & ~SSM_LINATTN_FIXED_DECAY) != 0) return fail(SSM_ERR_UNSUPPORTED, "linear attention flags %d: unknown bits", flags);
+  if (!std::isfinite(scale)) return fail(SSM_ERR_UNSUPPORTED, "scale must be finite");
+  for (ssm_dtype t : types)
+    if (!valid_dtype(t)) return fail(SSM_ERR_UNSUPPORTED, "unknown dtype (%d)", (int)t);
+  int64_t t;
+  if (!mul_ok(batch, seqlen, &sz->rows) || !mul_ok(sz->rows, nheads, &sz->decay) || !mul_ok(sz->decay, dv, &sz->v) ||
+      !mul_ok(sz->v, 8, &t) || !mul_ok(sz->rows, ngroups, &t) || !mul_ok(t, dk, &sz->qk) || !mul_ok(sz->qk, 8, &t) ||
+      !mul_ok(sz->decay, dk, &t) || !mul_ok(t, 8, &t) || !mul_ok(batch * nheads, dk, &t) || !mul_ok(t, dv, &sz->state) ||
+      !mul_ok(sz->state, 8, &t))
+    return fail(SSM_ERR_BAD_SHAPE, "element count overflows int64");
+  if (flags & SSM_LINATTN_FIXED_DECAY) sz->decay = nheads;
+  return SSM_OK;
+}
+
+// What the chunked form needs besides.
+ssm_status la_check_chunked(int64_t batch, int64_t nheads, int64_t dk, int64_t dv, ssm_dtype in_dtype, int slots) {
+  if (in_dtype != SSM_BF16)
+    return fail(SSM_ERR_UNSUPPORTED, "chunked linear attention takes bf16 inputs (its products run on bf16 matrix cores)");
+  if (dk % 8 != 0 || dv % 8 != 0 || dk > SSM_LINATTN_MAX_DIM || dv > SSM_LINATTN_MAX_DIM)
+    return fail(SSM_ERR_UNSUPPORTED, "dk=%lld and dv=%lld must be multiples of 8, at most %d", (long long)dk, (long long)dv,
+                SSM_LINATTN_MAX_DIM);
+  if (batch * nheads * slots > INT32_MAX) return fail(SSM_ERR_UNSUPPORTED, "batch * nheads exceeds the grid");
+  return SSM_OK;
+}
+
+ssm_status la_rows(const char* name, int64_t rows, int64_t width, int64_t row, int64_t* bytes) {
+  *bytes = 0;
+  if (rows == 0) return SSM_OK;
+  if (row < width || row % 8 != 0 || row > (int64_t{1} << 24))
+    return fail(SSM_ERR_UNSUPPORTED, "%s rows are %lld elements apart: a multiple of 8 from %lld to 2^24 is supported", name,
+                (long long)row, (long long)width);
+  int64_t t;
+  if (!mul_ok(rows, row * 2, &t)) return fail(SSM_ERR_BAD_SHAPE, "%s extent overflows int64", name);
+  *bytes = ((rows - 1) * row + width) * 2;
+  return SSM_OK;
+}
+
+// Time chunks of a forward.  A workgroup walks 64 value columns of one (batch
+// row, head) and two fit a CU.
+void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, int simds, ssm_plan* p) {
+  const int64_t wgs = std::max<int64_t>(1, batch * nheads * ((dv + 63) / 64));
+  const int64_t cus = std::max(1, simds / 4);
+  int64_t chunks = 1;
+  if (wgs <= cus) chunks = std::min((4 * cus + wgs - 1) / wgs, std::max<int64_t>(1, seqlen / 512));
+  int64_t len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
+  if (chunks > 1) len = (len + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
+  *p = ssm_plan{};
+  p->chunk_len = std::max<int64_t>(1, len);
+  p->n_chunks = seqlen > 0 ? (seqlen + p->chunk_len - 1) / p->chunk_len : 0;
+}
+
+// Time chunks of a backward: at most kLaBwdChunk steps each, and more where its
+// three walks leave CUs idle.
+void choose_la_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t slots, int simds, ssm_plan* p) {
+  const int64_t wgs = std::max<int64_t>(1, batch * nheads * slots);
+  const int64_t cus = std::max(1, simds / 4);
+  int64_t chunks = (seqlen + ssm::kLaBwdChunk - 1) / ssm::kLaBwdChunk;
+  if (wgs <= cus) chunks = std::max(chunks, std::min((4 * cus + wgs - 1) / wgs, seqlen / 512));
+  chunks = std::max<int64_t>(1, chunks);
+  const int64_t len = ((seqlen + chunks - 1) / chunks + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
+  *p = ssm_plan{};
+  p->chunk_len = std::max<int64_t>(ssm::kLaQ, len);
+  p->n_chunks = (seqlen + p->chunk_len - 1) / p->chunk_len;
+}
+
+ssm::LaOperand la_operand(const void* p, int64_t row, int64_t dim, int64_t share) {
+  ssm::LaOperand o{};
+  o.p = static_cast<const uint16_t*>(p);
+  o.row = row;
+  o.head = (int32_t)dim;
+  o.share = (int32_t)share;
+  return o;
+}
+
+// Consecutive pieces of one workspace, each 16-byte aligned.
+struct Pieces {
+  int64_t floats = 0;
+  bool fits = true;
+  int64_t add(int64_t n) {
+    const int64_t at = floats;
+    if (n < 0 || n > (INT64_MAX / 4 - 4) - floats) fits = false;
+    else floats += (n + 3) / 4 * 4;
+    return at;
+  }
+};
+
 }  // namespace
 
 extern "C" {
@@ -310,6 +420,316 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
   a.gate_last = (flags & SSM_NORM_GATE_LAST) != 0;
   a.cus = device_simds() / 4;
   return norm_bwd_run(a, sums, [&](const ssm::NormArgs& n) { return ssm::launch_gated_norm_bwd(n, to_dt(in_dtype), to_dt(out_dtype), s); }, s);
+}
+
+ssm_status ssm_linattn_plan_query(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dk, int64_t dv,
+                                  ssm_plan* plan) {
+  if (plan == nullptr) return fail(SSM_ERR_NULL_ARG, "required pointer plan is NULL");
+  LaSizes sz;
+  ssm_status st = la_check(batch, seqlen, nheads, 1, dk, dv, 0, 1.0f, {}, &sz);
+  if (st == SSM_OK) st = la_check_chunked(batch, nheads, dk, dv, SSM_BF16, 2);
+  if (st != SSM_OK) return st;
+  choose_la_plan(batch, seqlen, nheads, dv, device_simds(), plan);
+  return ok();
+}
+
+ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                           const float* log_decay, int flags, float scale, const float* initial_state, void* out,
+                           float* last_state, int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups,
+                           int64_t dk, int64_t dv, ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream,
+                           const ssm_plan* plan_in) {
+  LaSizes sz;
+  ssm_status st = la_check(batch, seqlen, nheads, ngroups, dk, dv, flags, scale, {in_dtype, out_dtype}, &sz);
+  if (st == SSM_OK) st = la_check_chunked(batch, nheads, dk, dv, in_dtype, 2);
+  int64_t qb, kb, vb;
+  if (st == SSM_OK) st = la_rows("q", sz.rows, ngroups * dk, q_row, &qb);
+  if (st == SSM_OK) st = la_rows("k", sz.rows, ngroups * dk, k_row, &kb);
+  if (st == SSM_OK) st = la_rows("v", sz.rows, nheads * dv, v_row, &vb);
+  if (st != SSM_OK) return st;
+  const bool some = sz.rows > 0;
+  st = check_args({{"q", q, qb, 16, true},
+                   {"k", k, kb, 16, true},
+                   {"v", v, vb, 16, true},
+                   {"log_decay", log_decay, some ? sz.decay * 4 : 0, 4, true},
+                   {"initial_state", initial_state, sz.state * 4, 16, false}},
+                  {{"out", out, sz.v * esize(out_dtype), 16, true}, {"last_state", last_state, sz.state * 4, 16, false}},
+                  {{"last_state", "initial_state"}});
+  if (st != SSM_OK) return st;
+  ssm_plan plan;
+  if (plan_in != nullptr) {
+    plan = *plan_in;
+    if (plan.chunk_len < 1) return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len must be >= 1");
+    plan.n_chunks = seqlen > 0 ? (seqlen + plan.chunk_len - 1) / plan.chunk_len : 0;
+    if (plan.n_chunks > 1 && plan.chunk_len % ssm::kLaQ != 0)
+      return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len=%lld must be a multiple of %d when it cuts the sequence",
+                  (long long)plan.chunk_len, ssm::kLaQ);
+    if (plan.n_chunks > 65535) return fail(SSM_ERR_UNSUPPORTED, "plan gives more than 65535 chunks");
+  } else {
+    choose_la_plan(batch, seqlen, nheads, dv, device_simds(), &plan);
+  }
+  const int64_t K = std::max<int64_t>(1, plan.n_chunks);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool in_place = initial_state != nullptr && initial_state == last_state;
+  if (batch == 0) return ok();
+  hipError_t e = hipSuccess;
+  if (seqlen == 0) {
+    if (last_state != nullptr && !in_place)
+      e = initial_state ? ssm::launch_copy_f32(last_state, initial_state, sz.state, s)
+                        : ssm::launch_fill_zero(last_state, sz.state, s);
+    return e == hipSuccess ? ok() : fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  }
+  const bool fixed = (flags & SSM_LINATTN_FIXED_DECAY) != 0;
+  const int64_t share = nheads / ngroups;
+  ssm::LaWalk a{};
+  a.A = la_operand(q, q_row, dk, share);
+  a.B = la_operand(k, k_row, dk, share);
+  a.X = la_operand(v, v_row, dv, 1);
+  a.decay = log_decay;
+  a.decay_t = fixed ? 0 : nheads;
+  a.decay_b = fixed ? 0 : seqlen * nheads;
+  a.out = out;
+  a.first = initial_state;
+  a.last = last_state;
+  a.seqlen = seqlen;
+  a.chunk_len = K > 1 ? plan.chunk_len : seqlen;
+  a.st_x = dk;
+  a.st_c = 1;
+  a.n_chunks = (int32_t)K;
+  a.batch = (int32_t)batch;
+  a.nheads = (int32_t)nheads;
+  a.xdim = (int32_t)dv;
+  a.cdim = (int32_t)dk;
+  a.out_bf16 = out_dtype == SSM_BF16;
+  a.w_scale = scale;
+  a.row_scale = scale;
+  a.src_scale = 1.0f;
+  void* ws = nullptr;
+  if (K > 1) {
+    // the workgroups that read the initial state are then not those that write
+    // the last one: an in-place state is read from a copy
+    int64_t n_state, n_decay;
+    if (!mul_ok(sz.state, K, &n_state) || !mul_ok(batch * nheads, K, &n_decay))
+      return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
+    Pieces w;
+    const int64_t at_state = w.add(n_state), at_decay = w.add(n_decay), at_copy = w.add(in_place ? sz.state : 0);
+    if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
+    e = ws_alloc(&ws, w.floats * 4, s);
+    if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)(w.floats * 4), e);
+    float* f = static_cast<float*>(ws);
+    a.chunk_out = f + at_state;
+    a.chunk_states = a.chunk_out;
+    a.chunk_decay = f + at_decay;
+    if (in_place) {
+      e = ssm::launch_copy_f32(f + at_copy, initial_state, sz.state, s);
+      a.first = f + at_copy;
+    }
+    if (e == hipSuccess) e = ssm::launch_la_states(a, false, s);
+  }
+  if (e == hipSuccess) e = ssm::launch_la_fwd(a, s);
+  if (ws) {
+    const hipError_t e2 = hipFreeAsync(ws, s);
+    if (e == hipSuccess) e = e2;
+  }
+  if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                           const float* log_decay, int flags, float scale, const float* initial_state,
+                           const void* dout, const float* dlast_state, void* dq, void* dk_, void* dv_,
+                           float* dlog_decay, float* dinitial_state, int64_t batch, int64_t seqlen, int64_t nheads,
+                           int64_t ngroups, int64_t dk, int64_t dv, ssm_dtype in_dtype, ssm_dtype grad_dtype,
+                           void* stream) {
+  LaSizes sz;
+  ssm_status st = la_check(batch, seqlen, nheads, ngroups, dk, dv, flags, scale, {in_dtype, grad_dtype}, &sz);
+  if (st == SSM_OK) st = la_check_chunked(batch, nheads, dk, dv, in_dtype, 6);
+  int64_t qb, kb, vb;
+  if (st == SSM_OK) st = la_rows("q", sz.rows, ngroups * dk, q_row, &qb);
+  if (st == SSM_OK) st = la_rows("k", sz.rows, ngroups * dk, k_row, &kb);
+  if (st == SSM_OK) st = la_rows("v", sz.rows, nheads * dv, v_row, &vb);
+  if (st != SSM_OK) return st;
+  const int64_t sg = esize(grad_dtype);
+  const bool some = sz.rows > 0;
+  const bool fixed = (flags & SSM_LINATTN_FIXED_DECAY) != 0;
+  st = check_args({{"q", q, qb, 16, true},
+                   {"k", k, kb, 16, true},
+                   {"v", v, vb, 16, true},
+                   {"log_decay", log_decay, some ? sz.decay * 4 : 0, 4, true},
+                   {"initial_state", initial_state, sz.state * 4, 16, false},
+                   {"dout", dout, sz.v * 2, 16, true},
+                   {"dlast_state", dlast_state, sz.state * 4, 16, false}},
+                  {{"dq", dq, sz.qk * sg, 16, true},
+                   {"dk", dk_, sz.qk * sg, 16, true},
+                   {"dv", dv_, sz.v * sg, 16, true},
+                   {"dlog_decay", dlog_decay, sz.decay * 4, 4, true},
+                   {"dinitial_state", dinitial_state, sz.state * 4, 16, false}});
+  if (st != SSM_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (!some) {
+    if (fixed) e = ssm::launch_fill_zero(dlog_decay, sz.decay, s);
+    if (e == hipSuccess && dinitial_state != nullptr && sz.state > 0)
+      e = dlast_state ? ssm::launch_copy_f32(dinitial_state, dlast_state, sz.state, s)
+                      : ssm::launch_fill_zero(dinitial_state, sz.state, s);
+    return e == hipSuccess ? ok() : fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  }
+  const int64_t nk = (dk + 63) / 64, nv = (dv + 63) / 64, share = nheads / ngroups;
+  ssm_plan plan;
+  choose_la_bwd_plan(batch, seqlen, nheads, 2 * nk + nv, device_simds(), &plan);
+  const int64_t K = plan.n_chunks;
+  if (K > 65535) return fail(SSM_ERR_UNSUPPORTED, "seqlen=%lld gives more than 65535 time chunks", (long long)seqlen);
+  int64_t n_state, n_heads, n_part, n_grad;
+  if (!mul_ok(sz.state, K, &n_state) || !mul_ok(batch * nheads, K, &n_heads) || !mul_ok(sz.rows * nheads, nk, &n_part) ||
+      !mul_ok(sz.rows * nheads, dk, &n_grad))
+    return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
+  Pieces w;
+  const bool cut = K > 1;
+  const int64_t at_pq = w.add(n_part), at_pk = w.add(n_part), at_fwd = w.add(cut ? n_state : 0),
+                at_rev = w.add(cut ? n_state : 0), at_fd = w.add(cut ? n_heads : 0), at_rd = w.add(cut ? n_heads : 0),
+                at_last = w.add(dlast_state ? sz.state : 0), at_dq = w.add(share > 1 ? n_grad : 0),
+                at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? n_heads : 0);
+  if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
+  void* ws = nullptr;
+  e = ws_alloc(&ws, w.floats * 4, s);
+  if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)(w.floats * 4), e);
+  float* f = static_cast<float*>(ws);
+
+  const ssm::LaOperand oq = la_operand(q, q_row, dk, share), ok_ = la_operand(k, k_row, dk, share),
+                       ov = la_operand(v, v_row, dv, 1), od = la_operand(dout, nheads * dv, dv, 1);
+  ssm::LaWalk base{};
+  base.decay = log_decay;
+  base.decay_t = fixed ? 0 : nheads;
+  base.decay_b = fixed ? 0 : seqlen * nheads;
+  base.seqlen = seqlen;
+  base.chunk_len = plan.chunk_len;
+  base.n_chunks = (int32_t)K;
+  base.batch = (int32_t)batch;
+  base.nheads = (int32_t)nheads;
+  base.out_bf16 = grad_dtype == SSM_BF16;
+  base.w_scale = scale;
+  // the states at time chunk borders, values v (forward) and dout (back)
+  ssm::LaWalk fs = base, rs = base;
+  fs.B = ok_;
+  fs.X = ov;
+  fs.first = initial_state;
+  fs.chunk_out = f + at_fwd;
+  fs.chunk_decay = f + at_fd;
+  fs.src_scale = 1.0f;
+  rs.B = oq;
+  rs.X = od;
+  rs.first = dlast_state;
+  rs.chunk_out = f + at_rev;
+  rs.chunk_decay = f + at_rd;
+  rs.src_scale = scale;
+  for (ssm::LaWalk* p : {&fs, &rs}) {
+    p->xdim = (int32_t)dv;
+    p->cdim = (int32_t)dk;
+    p->st_x = dk;
+    p->st_c = 1;
+  }
+  ssm::LaBwd a{};
+  a.dq = base;
+  a.dq.A = od;
+  a.dq.B = ov;
+  a.dq.X = ok_;
+  a.dq.Z = oq;
+  a.dq.out = share > 1 ? static_cast<void*>(f + at_dq) : dq;
+  a.dq.first = initial_state;
+  a.dq.last = dlast_state ? f + at_last : nullptr;
+  a.dq.chunk_states = f + at_fwd;
+  a.dq.part = f + at_pq;
+  a.dq.row_scale = scale;
+  a.dq.src_scale = 1.0f;
+  a.dk = base;
+  a.dk.A = ov;
+  a.dk.B = od;
+  a.dk.X = oq;
+  a.dk.Z = ok_;
+  a.dk.out = share > 1 ? static_cast<void*>(f + at_dk) : dk_;
+  a.dk.first = dlast_state;
+  a.dk.chunk_states = f + at_rev;
+  a.dk.part = f + at_pk;
+  a.dk.row_scale = 1.0f;
+  a.dk.src_scale = scale;
+  for (ssm::LaWalk* p : {&a.dq, &a.dk}) {   // values k and q: states read transposed
+    p->xdim = (int32_t)dk;
+    p->cdim = (int32_t)dv;
+    p->st_x = 1;
+    p->st_c = dk;
+    if (share > 1) p->out_bf16 = 0;
+  }
+  a.dv = base;
+  a.dv.A = ok_;
+  a.dv.B = oq;
+  a.dv.X = od;
+  a.dv.out = dv_;
+  a.dv.first = dlast_state;
+  a.dv.last = dinitial_state;
+  a.dv.chunk_states = f + at_rev;
+  a.dv.row_scale = 1.0f;
+  a.dv.src_scale = scale;
+  a.dv.xdim = (int32_t)dv;
+  a.dv.cdim = (int32_t)dk;
+  a.dv.st_x = dk;
+  a.dv.st_c = 1;
+  a.fwd_states = f + at_fwd;
+  a.rev_states = f + at_rev;
+  a.last_state = f + at_last;
+  a.dlast = dlast_state;
+  a.ddecay = fixed ? f + at_dec : dlog_decay;
+  a.fixed_decay = fixed ? 1 : 0;
+  if (cut) e = ssm::launch_la_states(fs, false, s);
+  if (cut && e == hipSuccess) e = ssm::launch_la_states(rs, true, s);
+  if (e == hipSuccess) e = ssm::launch_la_bwd(a, s);
+  if (share > 1) {
+    const bool b16 = grad_dtype == SSM_BF16;
+    if (e == hipSuccess) e = ssm::launch_la_group_sum(f + at_dq, dq, b16, sz.rows, (int)ngroups, (int)share, (int)dk, s);
+    if (e == hipSuccess) e = ssm::launch_la_group_sum(f + at_dk, dk_, b16, sz.rows, (int)ngroups, (int)share, (int)dk, s);
+  }
+  if (fixed && e == hipSuccess) e = ssm::launch_la_decay_sum(f + at_dec, dlog_decay, batch * K, (int)nheads, s);
+  const hipError_t e2 = hipFreeAsync(ws, s);
+  if (e == hipSuccess) e = e2;
+  if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+ssm_status ssm_linattn_state_update(const float* state, float* state_out, const void* q, const void* k, const void* v,
+                                    const float* log_decay, int flags, float scale, void* out, int64_t batch,
+                                    int64_t nheads, int64_t ngroups, int64_t dk, int64_t dv, ssm_dtype in_dtype,
+                                    ssm_dtype out_dtype, void* stream) {
+  LaSizes sz;
+  ssm_status st = la_check(batch, 1, nheads, ngroups, dk, dv, flags, scale, {in_dtype, out_dtype}, &sz);
+  if (st != SSM_OK) return st;
+  if (dk % 4 != 0 || dk > SSM_LINATTN_MAX_STEP_DK)
+    return fail(SSM_ERR_UNSUPPORTED, "dk=%lld must be a multiple of 4, at most %d", (long long)dk, SSM_LINATTN_MAX_STEP_DK);
+  const int64_t si = esize(in_dtype);
+  st = check_args({{"state", state, sz.state * 4, 16, true},
+                   {"q", q, sz.qk * si, 4 * si, true},
+                   {"k", k, sz.qk * si, 4 * si, true},
+                   {"v", v, sz.v * si, si, true},
+                   {"log_decay", log_decay, batch > 0 ? sz.decay * 4 : 0, 4, true}},
+                  {{"state_out", state_out, sz.state * 4, 16, true}, {"out", out, sz.v * esize(out_dtype), esize(out_dtype), true}},
+                  {{"state_out", "state"}});
+  if (st != SSM_OK) return st;
+  if (batch == 0) return ok();
+  ssm::LaStep a{};
+  a.state = state;
+  a.state_out = state_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.decay = log_decay;
+  a.decay_b = (flags & SSM_LINATTN_FIXED_DECAY) ? 0 : nheads;
+  a.out = out;
+  a.scale = scale;
+  a.batch = (int32_t)batch;
+  a.nheads = (int32_t)nheads;
+  a.ngroups = (int32_t)ngroups;
+  a.dk = (int32_t)dk;
+  a.dv = (int32_t)dv;
+  const hipError_t e = ssm::launch_la_step(a, to_dt(in_dtype), to_dt(out_dtype), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  return ok();
 }
 
 }  // extern "C"

@@ -55,4 +55,80 @@ int norm_row_blocks(const NormArgs& a);
 hipError_t launch_norm_sums(const float* part, int blocks, int sums, int64_t width, float* const out[3],
                             hipStream_t s);
 
+// ------------------------------------------------------------ linear attention
+
+constexpr int kLaQ = 64;            // steps per matrix chunk
+constexpr int kLaBwdChunk = 2048;   // steps per time chunk of the backward, at most
+constexpr int kLaMaxDim = 128;      // dk and dv of the chunked form, multiples of 8
+constexpr int kLaMaxStepDk = 256;   // dk of the single-token step, a multiple of 4
+
+// A bf16 tensor of rows per token: head h of row (b, t) starts at
+// p + (b * seqlen + t) * row + (h / share) * head.
+struct LaOperand {
+  const uint16_t* p;
+  int64_t row;
+  int32_t head;
+  int32_t share;      // consecutive heads that read the same one
+};
+
+// One walk over the chunks (linattn_kernel.h): rows A, sources B, values X.
+// States are [batch, nheads, dv, dk] fp32 whatever the walk's values are: value x
+// and contracted column c of a head are at x * st_x + c * st_c.
+struct LaWalk {
+  LaOperand A, B, X, Z;
+  const float* decay;         // log decay of (b, t, h): decay[b * decay_b + t * decay_t + h]
+  int64_t decay_b, decay_t;
+  void* out;                  // [batch, seqlen, nheads, xdim]
+  const float* first;         // state that enters the walk (nullable)
+  float* last;                // state that leaves it (nullable)
+  const float* chunk_states;  // n_chunks > 1: [batch, n_chunks, nheads, ..], after the carry
+  float* chunk_out;           // state pass: each time chunk's end state
+  float* chunk_decay;         // state pass: [batch, n_chunks, nheads] summed log2 decay
+  float* part;                // dq and dk walks: [slices, batch, nheads, seqlen]
+  int64_t seqlen, chunk_len;
+  int64_t st_x, st_c;
+  int32_t n_chunks, batch, nheads;
+  int32_t xdim, cdim;
+  int32_t out_bf16;
+  float w_scale, row_scale, src_scale;
+};
+
+// The backward.  dq and dk walks write into fp32 workspaces where several heads
+// share q and k (share > 1), joined by launch_la_group_sum.
+struct LaBwd {
+  LaWalk dq, dk, dv;
+  const float* fwd_states;    // n_chunks > 1: state entering time chunk k + 1 in slot k
+  const float* rev_states;    // n_chunks > 1: gradient of the state entering time chunk k in slot k
+  const float* last_state;    // with dlast: the forward's last state
+  const float* dlast;         // nullable
+  float* ddecay;              // [batch, seqlen, nheads], or the partial sums [batch, n_chunks, nheads]
+  int32_t fixed_decay;
+};
+
+struct LaStep {
+  const float* state;
+  float* state_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* decay;         // of (b, h): decay[b * decay_b + h]
+  int64_t decay_b;
+  void* out;
+  float scale;
+  int32_t batch, nheads, ngroups, dk, dv;
+};
+
+// States entering every time chunk but the walk's first: the state pass and the
+// carry (rev: walking back in time).
+hipError_t launch_la_states(const LaWalk& a, bool rev, hipStream_t s);
+hipError_t launch_la_fwd(const LaWalk& a, hipStream_t s);
+// The three walks, then the decay's gradient (fixed_decay: its partial sums).
+hipError_t launch_la_bwd(const LaBwd& a, hipStream_t s);
+// out[row, g, d] = sum over the `share` heads of group g of in[row, g, i, d].
+hipError_t launch_la_group_sum(const float* in, void* out, bool out_bf16, int64_t rows, int ngroups, int share, int dim,
+                               hipStream_t s);
+// out[h] = sum over n rows of in[n, h].
+hipError_t launch_la_decay_sum(const float* in, float* out, int64_t n, int nheads, hipStream_t s);
+hipError_t launch_la_step(const LaStep& a, DT in, DT out, hipStream_t s);
+
 }  // namespace ssm
