@@ -57,7 +57,7 @@ hipError_t launch_norm_sums(const float* part, int blocks, int sums, int64_t wid
 
 // ------------------------------------------------------------ linear attention
 
-constexpr int kLaQ = 64;            // steps per matrix chunk
+constexpr int kLaQ = 32;            // steps per matrix chunk
 constexpr int kLaBwdChunk = 2048;   // steps per time chunk of the backward, at most
 constexpr int kLaMaxDim = 128;      // dk and dv of the chunked form, multiples of 8
 constexpr int kLaMaxStepDk = 256;   // dk of the single-token step, a multiple of 4

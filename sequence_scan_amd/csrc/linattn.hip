@@ -10,7 +10,7 @@ namespace ssm {
 namespace {
 
 template <int C>
-__global__ void __launch_bounds__(256, 2) la_fwd_kernel(LaWalk a) {
+__global__ void __launch_bounds__(256, 3) la_fwd_kernel(LaWalk a) {
   __shared__ LaTile<C, kWalkOut> s;
   int bh, slice;
   la_place(blockIdx.x, a.batch * a.nheads, (a.xdim + 63) / 64, &bh, &slice);
@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(256, 2) la_fwd_kernel(LaWalk a) {
 }
 
 template <int C, bool REV>
-__global__ void __launch_bounds__(256, 2) la_state_kernel(LaWalk a) {
+__global__ void __launch_bounds__(256, 3) la_state_kernel(LaWalk a) {
   __shared__ LaTile<C, kWalkState> s;
   int bh, slice;
   la_place(blockIdx.x, a.batch * a.nheads, (a.xdim + 63) / 64, &bh, &slice);

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaBwd a) {
   auto parts = [&](int c, float* da, float* db) SSM_INLINE {
     const int64_t t = (int64_t)c * kLaQ + l;
     *da = *db = 0.0f;
-    if (t < L)
+    if (l < kLaQ && t < L)
       for (int i = 0; i < nk; ++i) {
         *da += a.dq.part[i * plane + at0 + t];
         *db += a.dk.part[i * plane + at0 + t];
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaBwd a) {
     suf = __shfl(suf, 63 - l);
     const float g = suf + pre + X;
     const int64_t t = (int64_t)c * kLaQ + l;
-    if (t < L) {
+    if (l < kLaQ && t < L) {
       sum += g;
       if (!a.fixed_decay) a.ddecay[((int64_t)b * a.dq.seqlen + t_begin + t) * H + h] = g;
     }
