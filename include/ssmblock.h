@@ -195,6 +195,39 @@ ssm_status ssm_linattn_state_update(const float* state, float* state_out, const 
                                     int64_t nheads, int64_t ngroups, int64_t dk, int64_t dv, ssm_dtype in_dtype,
                                     ssm_dtype out_dtype, void* stream);
 
+/*
+ * Products of few rows with 4-bit weights and group scales, for the projections
+ * of a decode step:
+ *
+ *   out[m,n] = sum_k x[m,k] * (code[n,k] - zero[n,g]) * scale[n,g] + bias[n],  g = k / group
+ *
+ *   x      : [m, k] in in_dtype, rows x_row elements apart, 16-byte aligned and
+ *            rows multiples of 16 bytes
+ *   codes  : [n, k / 2] bytes, two codes (0..15) per byte, the lower k in the low
+ *            four bits; 16-byte aligned
+ *   scales : [n, k / group] fp32 or bf16 (scale_dtype)
+ *   zeros  : [n, k / group] bytes, or NULL: 8 for every group
+ *   bias   : [n] fp32, or NULL;   out: [m, n] in out_dtype
+ * group is 32, 64 or 128 and divides k; n, k < 2^31.  Any m; the kernel is made
+ * for up to about 64 rows, past which the codes are read again for every 64 (fp32
+ * x: 21).  Sums are fp32; x enters the matrix cores exactly (fp32 as three bf16
+ * terms).  A value of x that is not finite makes its row's outputs NaN.  With
+ * k = 0, out is the bias (or 0).
+ */
+ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                         const float* bias, void* out, int64_t m, int64_t n, int64_t k, int64_t group,
+                         ssm_dtype in_dtype, ssm_dtype scale_dtype, ssm_dtype out_dtype, void* stream);
+
+/*
+ * Quantises w [n, k] (w_dtype) into that form: per group,
+ * scale = (max(w, 0) - min(w, 0)) / 15 rounded to scale_dtype, zero = the nearest
+ * code to -min / scale, code = the nearest to w / scale + zero, within 0..15.
+ * |w - (code - zero) scale| is at most scale (half a step, and the rounding of
+ * the zero point) up to scale_dtype's rounding.  Finite weights only.
+ */
+ssm_status ssm_q4_quantize(const void* w, uint8_t* codes, void* scales, uint8_t* zeros, int64_t n, int64_t k,
+                           int64_t group, ssm_dtype w_dtype, ssm_dtype scale_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,8 @@ _ARGS = {
                        [_int, _int, _vp, ctypes.POINTER(ssm_plan)],
     "ssm_linattn_bwd": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _f32] + [_vp] * 8 + [_i64] * 6 +
                        [_int, _int, _vp],
+    "ssm_q4_matvec": [_vp, _i64] + [_vp] * 5 + [_i64] * 4 + [_int, _int, _int, _vp],
+    "ssm_q4_quantize": [_vp] * 4 + [_i64] * 3 + [_int, _int, _vp],
     "ssm_linattn_state_update": [_vp] * 6 + [_int, _f32, _vp] + [_i64] * 5 + [_int, _int, _vp],
 }
 _fns: dict = {}
@@ -330,4 +332,50 @@ def ssm_linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] =
         _want(k, "k", qs, q.dtype, dev), _want(v, "v", vs, q.dtype, dev), gp, flags,
         dk ** -0.5 if scale is None else scale, _want(out, "out", vs, None, dev), B, H, G, dk, dv, _dtype_code(q),
         _dtype_code(out), _stream(stream)))
+    return out
+
+
+def ssm_q4_quantize(w, group: int = 128, scale_dtype=None, stream=None):
+    """4-bit form of a weight matrix w [n, k] (float32 or bfloat16), k a multiple of
+    ``group`` (32, 64 or 128): codes [n, k // 2] uint8 (two per byte, the lower k in the low
+    bits), scales [n, k // group] (``scale_dtype``, float32 by default) and zeros
+    [n, k // group] uint8, with w close to (code - zero) * scale (see include/ssmblock.h)."""
+    import torch
+    if w.dim() != 2:
+        raise ValueError("w must be [n, k]")
+    n, k = w.shape
+    if group not in (32, 64, 128) or k % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide k={k}, got {group}")
+    dev, ng = w.device, k // group
+    codes, zeros = _new((n, k // 2), torch.uint8, dev), _new((n, ng), torch.uint8, dev)
+    scales = _new((n, ng), scale_dtype or torch.float32, dev)
+    _check(_fn("ssm_q4_quantize")(_want(w, "w", w.shape, None, dev), codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), n, k,
+                                  group, _dtype_code(w), _dtype_code(scales), _stream(stream)))
+    return codes, scales, zeros
+
+
+def ssm_q4_matvec(x, codes, scales, zeros=None, bias=None, out=None, out_dtype=None, stream=None):
+    """x W^T + bias for x [..., k] (float32 or bfloat16; rows may be slices of a packed
+    tensor) and 4-bit weights: codes [n, k // 2] uint8, scales [n, k // group] (float32 or
+    bfloat16), zeros [n, k // group] uint8 (None: 8), bias [n] float32.  Returns out
+    [..., n] (allocated if None, dtype ``out_dtype`` or x's)."""
+    import torch
+    dev = x.device
+    if codes.dim() != 2 or scales.dim() != 2 or x.dim() < 1:
+        raise ValueError("x must be [..., k], codes [n, k // 2] and scales [n, k // group]")
+    n, k = codes.shape[0], 2 * codes.shape[1]
+    ng = scales.shape[1]
+    group = k // ng if ng else 128
+    if x.shape[-1] != k or group * ng != k:
+        raise ValueError(f"x has {x.shape[-1]} columns, codes {k} and scales {ng} groups")
+    shape = (*x.shape[:-1], n)
+    if out is None:
+        out = _new(shape, out_dtype or x.dtype, dev)
+    xp, xr = _rows(x, "x", x.shape, None, dev)
+    m = x.numel() // k if k else out.numel() // n if n else 0
+    _check(_fn("ssm_q4_matvec")(
+        xp, xr, _want(codes, "codes", (n, k // 2), torch.uint8, dev), _want(scales, "scales", (n, ng), None, dev),
+        _want(zeros, "zeros", (n, ng), torch.uint8, dev), _want(bias, "bias", (n,), torch.float32, dev),
+        _want(out, "out", shape, None, dev), m, n, k, group, _dtype_code(x), _dtype_code(scales), _dtype_code(out),
+        _stream(stream)))
     return out

@@ -41,7 +41,7 @@ DEVICE_UNITS = _scan_units() + [(os.path.join(CSRC, f), [], f.split(".")[0]) for
 # The block operators' kernels (include/ssmblock.h): units of their own, so that
 # the profiles of the scans stay keyed to the scans' code alone.
 BLOCK_UNITS = [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("norm_add.hip", "norm_gate.hip", "linattn.hip",
-                                                                           "linattn_bwd.hip")]
+                                                                           "linattn_bwd.hip", "q4.hip")]
 HOST_UNITS = [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("api.cpp", "api_block.cpp")]
 SOURCES = sorted({u[0] for u in DEVICE_UNITS + BLOCK_UNITS + HOST_UNITS})
 HEADERS = [os.path.join(CSRC, f) for f in ("internal.h", "device.h", "scan_kernel.h")] + [

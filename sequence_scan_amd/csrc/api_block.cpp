@@ -232,6 +232,27 @@ ssm::LaOperand la_operand(const void* p, int64_t row, int64_t dim, int64_t share
   return o;
 }
 
+// ------------------------------------------------------------ 4-bit products
+
+ssm_status q4_check(int64_t m, int64_t n, int64_t k, int64_t group, std::initializer_list<ssm_dtype> types) {
+  if (m < 0 || n < 0 || k < 0 || group < 0)
+    return fail(SSM_ERR_BAD_SHAPE, "negative size (m=%lld n=%lld k=%lld group=%lld)", (long long)m, (long long)n, (long long)k,
+                (long long)group);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(SSM_ERR_UNSUPPORTED, "group=%lld is not supported (32, 64 or 128)", (long long)group);
+  if (k % group != 0) return fail(SSM_ERR_UNSUPPORTED, "k=%lld must be a multiple of group=%lld", (long long)k, (long long)group);
+  for (ssm_dtype t : types)
+    if (!valid_dtype(t)) return fail(SSM_ERR_UNSUPPORTED, "unknown dtype (%d)", (int)t);
+  int64_t t;
+  if (!mul_ok(n, k, &t) || !mul_ok(t, 8, &t) || !mul_ok(m, n, &t) || !mul_ok(t, 8, &t))
+    return fail(SSM_ERR_BAD_SHAPE, "element count overflows int64");
+  // (1024 columns of padding in the kernel's 32-bit indexes; 65535 blocks of 21 rows)
+  if (n > INT32_MAX - 1024 || k > INT32_MAX - 1024 || m > 65535ll * 5)
+    return fail(SSM_ERR_UNSUPPORTED, "m=%lld, n=%lld or k=%lld exceeds what the kernel indexes", (long long)m, (long long)n,
+                (long long)k);
+  return SSM_OK;
+}
+
 // Consecutive pieces of one workspace, each 16-byte aligned.
 struct Pieces {
   int64_t floats = 0;
@@ -728,6 +749,67 @@ ssm_status ssm_linattn_state_update(const float* state, float* state_out, const 
   a.dk = (int32_t)dk;
   a.dv = (int32_t)dv;
   const hipError_t e = ssm::launch_la_step(a, to_dt(in_dtype), to_dt(out_dtype), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                         const float* bias, void* out, int64_t m, int64_t n, int64_t k, int64_t group,
+                         ssm_dtype in_dtype, ssm_dtype scale_dtype, ssm_dtype out_dtype, void* stream) {
+  ssm_status st = q4_check(m, n, k, group, {in_dtype, scale_dtype, out_dtype});
+  if (st != SSM_OK) return st;
+  const int64_t si = esize(in_dtype), ss = esize(scale_dtype), so = esize(out_dtype);
+  int64_t xb = 0;
+  if (m > 0 && k > 0) {
+    int64_t t;
+    if (x_row < k || x_row * si % 16 != 0)
+      return fail(SSM_ERR_UNSUPPORTED, "x rows are %lld elements apart: at least k=%lld and a multiple of 16 bytes is supported",
+                  (long long)x_row, (long long)k);
+    if (!mul_ok(m, x_row, &t) || !mul_ok(t, 8, &t)) return fail(SSM_ERR_BAD_SHAPE, "x extent overflows int64");
+    xb = ((m - 1) * x_row + k) * si;
+  }
+  const bool some = m > 0 && n > 0;
+  st = check_args({{"x", x, xb, 16, some},
+                   {"codes", codes, n * k / 2, 16, some},
+                   {"scales", scales, n * (k / group) * ss, ss, some},
+                   {"zeros", zeros, n * (k / group), 1, false},
+                   {"bias", bias, n * 4, 4, false}},
+                  {{"out", out, m * n * so, so, true}});
+  if (st != SSM_OK) return st;
+  if (!some) return ok();
+  ssm::Q4Args a{};
+  a.x = x;
+  a.x_row = x_row;
+  a.codes = codes;
+  a.scales = scales;
+  a.zeros = zeros;
+  a.bias = bias;
+  a.out = out;
+  a.m = (int32_t)m;
+  a.n = (int32_t)n;
+  a.k = (int32_t)k;
+  a.group = (int32_t)group;
+  a.x_bf16 = in_dtype == SSM_BF16;
+  a.scale_bf16 = scale_dtype == SSM_BF16;
+  a.out_bf16 = out_dtype == SSM_BF16;
+  a.cus = device_simds() / 4;
+  const hipError_t e = ssm::launch_q4(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+ssm_status ssm_q4_quantize(const void* w, uint8_t* codes, void* scales, uint8_t* zeros, int64_t n, int64_t k,
+                           int64_t group, ssm_dtype w_dtype, ssm_dtype scale_dtype, void* stream) {
+  ssm_status st = q4_check(0, n, k, group, {w_dtype, scale_dtype});
+  if (st != SSM_OK) return st;
+  const int64_t sw = esize(w_dtype), ss = esize(scale_dtype), groups = n * (k / group);
+  if (groups / 256 > INT32_MAX - 1) return fail(SSM_ERR_UNSUPPORTED, "n * k / group exceeds the grid");
+  st = check_args({{"w", w, n * k * sw, sw, true}},
+                  {{"codes", codes, n * k / 2, 1, true}, {"scales", scales, groups * ss, ss, true}, {"zeros", zeros, groups, 1, true}});
+  if (st != SSM_OK) return st;
+  if (groups == 0) return ok();
+  const hipError_t e = ssm::launch_q4_quantize(w, w_dtype == SSM_BF16, codes, scales, scale_dtype == SSM_BF16, zeros, groups,
+                                               (int)group, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return ok();
 }

@@ -131,4 +131,25 @@ hipError_t launch_la_group_sum(const float* in, void* out, bool out_bf16, int64_
 hipError_t launch_la_decay_sum(const float* in, float* out, int64_t n, int nheads, hipStream_t s);
 hipError_t launch_la_step(const LaStep& a, DT in, DT out, hipStream_t s);
 
+// ------------------------------------------------------------ 4-bit products
+
+struct Q4Args {
+  const void* x;              // [m, k], rows x_row elements apart
+  int64_t x_row;
+  const uint8_t* codes;       // [n, k / 2], the low four bits first
+  const void* scales;         // [n, k / group]
+  const uint8_t* zeros;       // [n, k / group], or NULL: 8
+  const float* bias;          // [n], nullable
+  void* out;                  // [m, n]
+  int32_t m, n, k, group;
+  int32_t x_bf16, scale_bf16, out_bf16;
+  int32_t cus;
+  int32_t rows_per;           // set by the launcher: rows of x per workgroup
+};
+
+hipError_t launch_q4(const Q4Args& a, hipStream_t s);
+// groups: n * k / group.
+hipError_t launch_q4_quantize(const void* w, bool w_bf16, uint8_t* codes, void* scales, bool scale_bf16, uint8_t* zeros,
+                              int64_t groups, int group, hipStream_t s);
+
 }  // namespace ssm
