@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import _check, _dtype_code, _load, _stream, ssm_plan
+from . import SSM_BF16, SSM_F32, _check, _dtype_code, _load, ssm_plan
 
 SSM_NORM_CENTER = 1
 SSM_NORM_GATE_LAST = 2
@@ -34,24 +34,47 @@ _ARGS = {
     "ssm_linattn_state_update": [_vp] * 6 + [_int, _f32, _vp] + [_i64] * 5 + [_int, _int, _vp],
 }
 _fns: dict = {}
+_code: dict = {}            # torch dtype -> the C ABI's code
+_F32 = _U8 = _empty = _raw_stream = _device = None
 
 
 def _fn(name: str):
     """The C function, with its argument types set on first use."""
     f = _fns.get(name)
     if f is None:
+        _start()
         f = getattr(_load(), name)
         f.argtypes, f.restype = _ARGS[name], ctypes.c_int
         _fns[name] = f
     return f
 
 
-def _want(t, name: str, shape, dtype, device):
-    """The pointer of a contiguous tensor of this shape, dtype (None: float32 or
-    bfloat16) and device, or of no tensor.  The C ABI trusts the sizes it is given,
-    so every tensor is checked before its pointer is passed."""
-    if t is None:
-        return None
+def _start():
+    """What the wrappers use of PyTorch, looked up once: a decode step makes dozens of
+    these calls, and each microsecond of a wrapper counts."""
+    global _F32, _U8, _empty, _raw_stream, _device
+    import torch
+    _F32, _U8, _empty = torch.float32, torch.uint8, torch.empty
+    _code.update({torch.float32: SSM_F32, torch.bfloat16: SSM_BF16})
+    # the public form builds a Stream object first, 2.7 us against 0.1 us
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on(stream, device):
+    """The HIP stream to run on: the given one, or the current one of the tensors' device,
+    which has to be the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    i = device.index
+    if i != _device():
+        raise ValueError(f"tensors are on {device}, but the current device is cuda:{_device()}")
+    return _raw_stream(i)
+
+
+def _bad(t, name: str, shape, dtype, device):
+    """Raise for the first thing that is not as wanted."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is None:
@@ -62,8 +85,18 @@ def _want(t, name: str, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _want(t, name: str, shape, dtype, device):
+    """The pointer of a contiguous tensor of this shape, dtype (None: float32 or
+    bfloat16) and device, or of no tensor.  The C ABI trusts the sizes it is given,
+    so every tensor is checked before its pointer is passed."""
+    if t is None:
+        return None
+    if (t.shape != shape or (t.dtype not in _code if dtype is None else t.dtype is not dtype) or t.device != device
+            or not t.is_cuda or not t.is_contiguous()):
+        _bad(t, name, shape, dtype, device)
     return t.data_ptr()
 
 
@@ -74,20 +107,11 @@ def _rows(t, name: str, shape, dtype, device, inner: int = 1):
     if t is None:
         return None, 0
     if t.is_contiguous():
-        n = 1
-        for s in t.shape[t.dim() - inner:]:
-            n *= s
-        return _want(t, name, shape, dtype, device), n
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtype is None:
-        _dtype_code(t)
-    elif t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_cuda:
-        raise ValueError("tensors must be on the GPU")
+        row = shape[-1] if inner == 1 else shape[-1] * shape[-2]
+        return _want(t, name, shape, dtype, device), row
+    if (t.shape != shape or (t.dtype not in _code if dtype is None else t.dtype is not dtype) or t.device != device
+            or not t.is_cuda):
+        _bad(t, name, shape, dtype, device)
     lead, step = t.dim() - inner, 1
     for d in range(t.dim() - 1, lead - 1, -1):
         if t.shape[d] != 1 and t.stride(d) != step:
@@ -105,9 +129,15 @@ def _rows(t, name: str, shape, dtype, device, inner: int = 1):
     return t.data_ptr(), step if row is None else row
 
 
+def _kind(dtype) -> int:
+    """The C ABI's code of an output's dtype."""
+    if dtype not in _code:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return _code[dtype]
+
+
 def _new(shape, dtype, device):
-    import torch
-    return torch.empty(shape, dtype=dtype, device=device)
+    return _empty(shape, dtype=dtype, device=device)
 
 
 def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, scale=None, alpha: float = 1.0, eps: float = 1e-5,
@@ -118,7 +148,7 @@ def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, scale=None, alpha
     each; x may be a slice of a packed tensor); weight, bias, scale: [width] float32.
     ``residual_out`` (residual's dtype, or float32 without one) may be ``residual``.
     Returns (out, residual_out)."""
-    import torch
+    call = _fn("ssm_add_norm_fwd")
     dev, shape = x.device, x.shape
     width = shape[-1]
     rows = x.numel() // width if width else 0
@@ -127,14 +157,14 @@ def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, scale=None, alpha
     if out is None:
         out = _new(shape, out_dtype or x.dtype, dev)
     if residual_out is None:
-        residual_out = _new(shape, torch.float32 if residual is None else residual.dtype, dev)
+        residual_out = _new(shape, _F32 if residual is None else residual.dtype, dev)
     cols = (width,)
-    _check(_fn("ssm_add_norm_fwd")(
-        xp, xs, rp, _want(weight, "weight", cols, torch.float32, dev), _want(bias, "bias", cols, torch.float32, dev),
-        _want(scale, "scale", cols, torch.float32, dev), alpha, eps, SSM_NORM_CENTER if center else 0,
+    _check(call(
+        xp, xs, rp, _want(weight, "weight", cols, _F32, dev), _want(bias, "bias", cols, _F32, dev),
+        _want(scale, "scale", cols, _F32, dev), alpha, eps, SSM_NORM_CENTER if center else 0,
         _want(out, "out", shape, None, dev),
         _want(residual_out, "residual_out", shape, None if residual is None else residual.dtype, dev), rows, width,
-        _dtype_code(x), _dtype_code(residual_out), _dtype_code(out), _stream(stream)))
+        _code[x.dtype], _code[residual_out.dtype], _code[out.dtype], _on(stream, dev)))
     return out, residual_out
 
 
@@ -145,8 +175,8 @@ def ssm_add_norm_bwd(dout, r, weight=None, dresidual_out=None, x=None, scale=Non
     and, optionally, the gradient that arrives at the residual stream.  Returns a dict
     with dx (``dx_dtype``, or x's or dout's dtype), dresidual (r's dtype) and, as asked,
     dweight, dbias and dscale (wanted by default where ``scale`` and ``x`` are given)."""
-    import torch
-    dev, shape, f32 = dout.device, dout.shape, torch.float32
+    call = _fn("ssm_add_norm_bwd")
+    dev, shape = dout.device, dout.shape
     width = shape[-1]
     rows = dout.numel() // width if width else 0
     if want_scale is None:
@@ -156,22 +186,23 @@ def ssm_add_norm_bwd(dout, r, weight=None, dresidual_out=None, x=None, scale=Non
     xdt = x.dtype if x is not None else (dx_dtype or dout.dtype)
     if dx_dtype is not None and dx_dtype != xdt:
         raise TypeError("dx has x's dtype")
+    _kind(xdt)
     xp, xs = _rows(x, "x", shape, None, dev) if want_scale else (None, width)
     cols = (width,)
     g = {"dx": _new(shape, xdt, dev), "dresidual": _new(shape, r.dtype, dev)}
     if want_weight:
-        g["dweight"] = _new(cols, f32, dev)
+        g["dweight"] = _new(cols, _F32, dev)
     if want_bias:
-        g["dbias"] = _new(cols, f32, dev)
+        g["dbias"] = _new(cols, _F32, dev)
     if want_scale:
-        g["dscale"] = _new(cols, f32, dev)
+        g["dscale"] = _new(cols, _F32, dev)
     ptr = {k: v.data_ptr() for k, v in g.items()}
-    _check(_fn("ssm_add_norm_bwd")(
-        _want(dout, "dout", shape, None, dev), _want(r, "r", shape, None, dev), _want(weight, "weight", cols, f32, dev),
-        _want(dresidual_out, "dresidual_out", shape, r.dtype, dev), xp, xs, _want(scale, "scale", cols, f32, dev),
+    _check(call(
+        _want(dout, "dout", shape, None, dev), _want(r, "r", shape, None, dev), _want(weight, "weight", cols, _F32, dev),
+        _want(dresidual_out, "dresidual_out", shape, r.dtype, dev), xp, xs, _want(scale, "scale", cols, _F32, dev),
         alpha, eps, SSM_NORM_CENTER if center else 0, ptr["dx"], ptr["dresidual"], ptr.get("dweight"),
-        ptr.get("dbias"), ptr.get("dscale"), rows, width, _dtype_code(g["dx"]), _dtype_code(r), _dtype_code(dout),
-        _stream(stream)))
+        ptr.get("dbias"), ptr.get("dscale"), rows, width, _code[g["dx"].dtype], _code[r.dtype], _code[dout.dtype],
+        _on(stream, dev)))
     return g
 
 
@@ -185,8 +216,8 @@ def ssm_gated_norm_fwd(x, z=None, weight=None, bias=None, ngroups: int = 1, gate
     channels, gated by SiLU(z): norm(x * silu(z)) * weight + bias with ``gate_first``,
     (norm(x) * weight + bias) * silu(z) without.  x, z: [..., width] of one dtype (each
     may be a slice of a packed tensor); weight, bias: [width] float32.  Returns out."""
-    import torch
-    dev, shape, f32 = x.device, x.shape, torch.float32
+    call = _fn("ssm_gated_norm_fwd")
+    dev, shape = x.device, x.shape
     width = shape[-1]
     rows = x.numel() // width if width else 0
     xp, xs = _rows(x, "x", shape, None, dev)
@@ -194,10 +225,10 @@ def ssm_gated_norm_fwd(x, z=None, weight=None, bias=None, ngroups: int = 1, gate
     if out is None:
         out = _new(shape, out_dtype or x.dtype, dev)
     cols = (width,)
-    _check(_fn("ssm_gated_norm_fwd")(
-        xp, xs, zp, zs, _want(weight, "weight", cols, f32, dev), _want(bias, "bias", cols, f32, dev), eps,
-        _norm_flags(center, gate_first), _want(out, "out", shape, None, dev), rows, width, ngroups, _dtype_code(x),
-        _dtype_code(out), _stream(stream)))
+    _check(call(
+        xp, xs, zp, zs, _want(weight, "weight", cols, _F32, dev), _want(bias, "bias", cols, _F32, dev), eps,
+        _norm_flags(center, gate_first), _want(out, "out", shape, None, dev), rows, width, ngroups, _code[x.dtype],
+        _code[out.dtype], _on(stream, dev)))
     return out
 
 
@@ -207,8 +238,8 @@ def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1
     """Gradients of ``ssm_gated_norm_fwd`` from its inputs and dout.  Returns a dict with
     dx, dz (where z is given), and dweight and dbias as asked (dbias by default where
     ``bias`` is given)."""
-    import torch
-    dev, shape, f32 = x.device, x.shape, torch.float32
+    call = _fn("ssm_gated_norm_bwd")
+    dev, shape = x.device, x.shape
     width = shape[-1]
     rows = x.numel() // width if width else 0
     if want_bias is None:
@@ -220,22 +251,23 @@ def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1
     if z is not None:
         g["dz"] = _new(shape, x.dtype, dev)
     if want_weight:
-        g["dweight"] = _new(cols, f32, dev)
+        g["dweight"] = _new(cols, _F32, dev)
     if want_bias:
-        g["dbias"] = _new(cols, f32, dev)
+        g["dbias"] = _new(cols, _F32, dev)
     ptr = {k: v.data_ptr() for k, v in g.items()}
-    _check(_fn("ssm_gated_norm_bwd")(
-        _want(dout, "dout", shape, None, dev), xp, xs, zp, zs, _want(weight, "weight", cols, f32, dev),
-        _want(bias, "bias", cols, f32, dev), eps, _norm_flags(center, gate_first), ptr["dx"], ptr.get("dz"),
-        ptr.get("dweight"), ptr.get("dbias"), rows, width, ngroups, _dtype_code(x), _dtype_code(dout),
-        _stream(stream)))
+    _check(call(
+        _want(dout, "dout", shape, None, dev), xp, xs, zp, zs, _want(weight, "weight", cols, _F32, dev),
+        _want(bias, "bias", cols, _F32, dev), eps, _norm_flags(center, gate_first), ptr["dx"], ptr.get("dz"),
+        ptr.get("dweight"), ptr.get("dbias"), rows, width, ngroups, _code[x.dtype], _code[dout.dtype],
+        _on(stream, dev)))
     return g
 
 
 def ssm_linattn_plan_query(batch: int, seqlen: int, nheads: int, dk: int = 128, dv: int = 128) -> dict:
     """The time chunks ``ssm_linattn_fwd`` picks for these sizes."""
+    call = _fn("ssm_linattn_plan_query")
     p = ssm_plan()
-    _check(_fn("ssm_linattn_plan_query")(batch, seqlen, nheads, dk, dv, ctypes.byref(p)))
+    _check(call(batch, seqlen, nheads, dk, dv, ctypes.byref(p)))
     return {"chunk_len": p.chunk_len, "n_chunks": p.n_chunks}
 
 
@@ -248,9 +280,8 @@ def _la_shapes(q, v, tokens: int):
 
 def _la_decay(g, lead, nheads, device):
     """(pointer, flags) of the log decay: [*lead, nheads], or [nheads] for a fixed one."""
-    import torch
     fixed = g.dim() == 1
-    return (_want(g, "log_decay", (nheads,) if fixed else (*lead, nheads), torch.float32, device),
+    return (_want(g, "log_decay", (nheads,) if fixed else (*lead, nheads), _F32, device),
             SSM_LINATTN_FIXED_DECAY if fixed else 0)
 
 
@@ -262,9 +293,9 @@ def ssm_linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, initial_s
     1 / sqrt(dk) by default; states [batch, nheads, dv, dk] float32 (last_state is written
     where given, and may be initial_state).  Returns out [batch, seqlen, nheads, dv].
     ``plan`` = {"chunk_len": ..} forces the time chunks."""
-    import torch
+    call = _fn("ssm_linattn_fwd")
     G, dk, H, dv = _la_shapes(q, v, 2)
-    B, L, dev, f32 = q.shape[0], q.shape[1], q.device, torch.float32
+    B, L, dev = q.shape[0], q.shape[1], q.device
     qs, vs, st = (B, L, G, dk), (B, L, H, dv), (B, H, dv, dk)
     qp, qr = _rows(q, "q", qs, None, dev, 2)
     kp, kr = _rows(k, "k", qs, q.dtype, dev, 2)
@@ -277,11 +308,11 @@ def ssm_linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, initial_s
         p = ssm_plan()
         p.chunk_len = int(plan["chunk_len"])
         p = ctypes.byref(p)
-    _check(_fn("ssm_linattn_fwd")(
+    _check(call(
         qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
-        _want(initial_state, "initial_state", st, f32, dev), _want(out, "out", vs, None, dev),
-        _want(last_state, "last_state", st, f32, dev), B, L, H, G, dk, dv, _dtype_code(q), _dtype_code(out),
-        _stream(stream), p))
+        _want(initial_state, "initial_state", st, _F32, dev), _want(out, "out", vs, None, dev),
+        _want(last_state, "last_state", st, _F32, dev), B, L, H, G, dk, dv, _code[q.dtype], _code[out.dtype],
+        _on(stream, dev), p))
     return out
 
 
@@ -291,25 +322,26 @@ def ssm_linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, ini
     (bfloat16) and, optionally, the gradient of the last state.  Returns a dict with dq, dk,
     dv (``grad_dtype``, or q's dtype), dlog_decay (float32, of log_decay's shape) and, as
     asked, dinitial_state."""
-    import torch
+    call = _fn("ssm_linattn_bwd")
     G, dk, H, dv = _la_shapes(q, v, 2)
-    B, L, dev, f32 = q.shape[0], q.shape[1], q.device, torch.float32
+    B, L, dev = q.shape[0], q.shape[1], q.device
     qs, vs, st = (B, L, G, dk), (B, L, H, dv), (B, H, dv, dk)
     gdt = grad_dtype or q.dtype
+    _kind(gdt)
     qp, qr = _rows(q, "q", qs, None, dev, 2)
     kp, kr = _rows(k, "k", qs, q.dtype, dev, 2)
     vp, vr = _rows(v, "v", vs, q.dtype, dev, 2)
     gp, flags = _la_decay(log_decay, (B, L), H, dev)
     g = {"dq": _new(qs, gdt, dev), "dk": _new(qs, gdt, dev), "dv": _new(vs, gdt, dev),
-         "dlog_decay": _new(log_decay.shape, f32, dev)}
+         "dlog_decay": _new(log_decay.shape, _F32, dev)}
     if want_dinitial_state:
-        g["dinitial_state"] = _new(st, f32, dev)
-    _check(_fn("ssm_linattn_bwd")(
+        g["dinitial_state"] = _new(st, _F32, dev)
+    _check(call(
         qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
-        _want(initial_state, "initial_state", st, f32, dev), _want(dout, "dout", vs, q.dtype, dev),
-        _want(dlast_state, "dlast_state", st, f32, dev), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+        _want(initial_state, "initial_state", st, _F32, dev), _want(dout, "dout", vs, q.dtype, dev),
+        _want(dlast_state, "dlast_state", st, _F32, dev), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
         g["dlog_decay"].data_ptr(), g["dinitial_state"].data_ptr() if want_dinitial_state else None, B, L, H, G, dk,
-        dv, _dtype_code(q), _dtype_code(g["dq"]), _stream(stream)))
+        dv, _code[q.dtype], _code[g["dq"].dtype], _on(stream, dev)))
     return g
 
 
@@ -319,19 +351,19 @@ def ssm_linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] =
     place, or into ``state_out``, which keeps ``state``).  q, k: [batch, ngroups, dk]; v:
     [batch, nheads, dv] (float32 or bfloat16); log_decay: [batch, nheads] or [nheads]
     float32.  Returns out [batch, nheads, dv]."""
-    import torch
+    call = _fn("ssm_linattn_state_update")
     G, dk, H, dv = _la_shapes(q, v, 1)
-    B, dev, f32 = q.shape[0], q.device, torch.float32
+    B, dev = q.shape[0], q.device
     qs, vs, st = (B, G, dk), (B, H, dv), (B, H, dv, dk)
     gp, flags = _la_decay(log_decay, (B,), H, dev)
     if out is None:
         out = _new(vs, out_dtype or v.dtype, dev)
-    sp = _want(state, "state", st, f32, dev)
-    _check(_fn("ssm_linattn_state_update")(
-        sp, sp if state_out is None else _want(state_out, "state_out", st, f32, dev), _want(q, "q", qs, None, dev),
+    sp = _want(state, "state", st, _F32, dev)
+    _check(call(
+        sp, sp if state_out is None else _want(state_out, "state_out", st, _F32, dev), _want(q, "q", qs, None, dev),
         _want(k, "k", qs, q.dtype, dev), _want(v, "v", vs, q.dtype, dev), gp, flags,
-        dk ** -0.5 if scale is None else scale, _want(out, "out", vs, None, dev), B, H, G, dk, dv, _dtype_code(q),
-        _dtype_code(out), _stream(stream)))
+        dk ** -0.5 if scale is None else scale, _want(out, "out", vs, None, dev), B, H, G, dk, dv, _code[q.dtype],
+        _code[out.dtype], _on(stream, dev)))
     return out
 
 
@@ -340,17 +372,18 @@ def ssm_q4_quantize(w, group: int = 128, scale_dtype=None, stream=None):
     ``group`` (32, 64 or 128): codes [n, k // 2] uint8 (two per byte, the lower k in the low
     bits), scales [n, k // group] (``scale_dtype``, float32 by default) and zeros
     [n, k // group] uint8, with w close to (code - zero) * scale (see include/ssmblock.h)."""
-    import torch
+    call = _fn("ssm_q4_quantize")
     if w.dim() != 2:
         raise ValueError("w must be [n, k]")
     n, k = w.shape
     if group not in (32, 64, 128) or k % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide k={k}, got {group}")
     dev, ng = w.device, k // group
-    codes, zeros = _new((n, k // 2), torch.uint8, dev), _new((n, ng), torch.uint8, dev)
-    scales = _new((n, ng), scale_dtype or torch.float32, dev)
-    _check(_fn("ssm_q4_quantize")(_want(w, "w", w.shape, None, dev), codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), n, k,
-                                  group, _dtype_code(w), _dtype_code(scales), _stream(stream)))
+    codes, zeros = _new((n, k // 2), _U8, dev), _new((n, ng), _U8, dev)
+    scales = _new((n, ng), scale_dtype or _F32, dev)
+    _kind(scales.dtype)
+    _check(call(_want(w, "w", w.shape, None, dev), codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), n, k,
+                                  group, _code[w.dtype], _code[scales.dtype], _on(stream, dev)))
     return codes, scales, zeros
 
 
@@ -359,7 +392,7 @@ def ssm_q4_matvec(x, codes, scales, zeros=None, bias=None, out=None, out_dtype=N
     tensor) and 4-bit weights: codes [n, k // 2] uint8, scales [n, k // group] (float32 or
     bfloat16), zeros [n, k // group] uint8 (None: 8), bias [n] float32.  Returns out
     [..., n] (allocated if None, dtype ``out_dtype`` or x's)."""
-    import torch
+    call = _fn("ssm_q4_matvec")
     dev = x.device
     if codes.dim() != 2 or scales.dim() != 2 or x.dim() < 1:
         raise ValueError("x must be [..., k], codes [n, k // 2] and scales [n, k // group]")
@@ -373,9 +406,9 @@ def ssm_q4_matvec(x, codes, scales, zeros=None, bias=None, out=None, out_dtype=N
         out = _new(shape, out_dtype or x.dtype, dev)
     xp, xr = _rows(x, "x", x.shape, None, dev)
     m = x.numel() // k if k else out.numel() // n if n else 0
-    _check(_fn("ssm_q4_matvec")(
-        xp, xr, _want(codes, "codes", (n, k // 2), torch.uint8, dev), _want(scales, "scales", (n, ng), None, dev),
-        _want(zeros, "zeros", (n, ng), torch.uint8, dev), _want(bias, "bias", (n,), torch.float32, dev),
-        _want(out, "out", shape, None, dev), m, n, k, group, _dtype_code(x), _dtype_code(scales), _dtype_code(out),
-        _stream(stream)))
+    _check(call(
+        xp, xr, _want(codes, "codes", (n, k // 2), _U8, dev), _want(scales, "scales", (n, ng), None, dev),
+        _want(zeros, "zeros", (n, ng), _U8, dev), _want(bias, "bias", (n,), _F32, dev),
+        _want(out, "out", shape, None, dev), m, n, k, group, _code[x.dtype], _code[scales.dtype], _code[out.dtype],
+        _on(stream, dev)))
     return out
