@@ -168,8 +168,8 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
  * The forward's outputs are not needed.  Sequences are cut into time chunks of at
  * most 2048 steps.  Workspace, on `stream`:
  * batch * seqlen * nheads * ceil(dk / 64) * 8 bytes, with more than one time chunk
- * 8 * batch * n_chunks * nheads * (dk * dv + 1), with dlast_state
- * batch * nheads * dk * dv * 4, with nheads > ngroups
+ * 8 * batch * n_chunks * nheads * (dk * dv + 1), with dlast_state and
+ * with initial_state batch * nheads * dk * dv * 4 each, with nheads > ngroups
  * batch * seqlen * nheads * dk * 8 more.  Alignment and rows as above, gradients
  * and dout 16-byte aligned.
  */

@@ -607,7 +607,8 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   const bool cut = K > 1;
   const int64_t at_pq = w.add(n_part), at_pk = w.add(n_part), at_fwd = w.add(cut ? n_state : 0),
                 at_rev = w.add(cut ? n_state : 0), at_fd = w.add(cut ? n_heads : 0), at_rd = w.add(cut ? n_heads : 0),
-                at_last = w.add(dlast_state ? sz.state : 0), at_dq = w.add(share > 1 ? n_grad : 0),
+                at_last = w.add(dlast_state ? sz.state : 0),
+                at_init = w.add(initial_state ? sz.state : 0), at_dq = w.add(share > 1 ? n_grad : 0),
                 at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? n_heads : 0);
   if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
   void* ws = nullptr;
@@ -697,6 +698,9 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   a.rev_states = f + at_rev;
   a.last_state = f + at_last;
   a.dlast = dlast_state;
+  a.initial = initial_state;
+  a.dinitial = f + at_init;
+  a.dk.last = initial_state ? f + at_init : nullptr;
   a.ddecay = fixed ? f + at_dec : dlog_decay;
   a.fixed_decay = fixed ? 1 : 0;
   if (cut) e = ssm::launch_la_states(fs, false, s);

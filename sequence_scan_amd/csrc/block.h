@@ -101,6 +101,8 @@ struct LaBwd {
   const float* rev_states;    // n_chunks > 1: gradient of the state entering time chunk k in slot k
   const float* last_state;    // with dlast: the forward's last state
   const float* dlast;         // nullable
+  const float* initial;       // nullable: the forward's initial state, and with it
+  const float* dinitial;      // ... its gradient (left by the dk walk)
   float* ddecay;              // [batch, seqlen, nheads], or the partial sums [batch, n_chunks, nheads]
   int32_t fixed_decay;
 };

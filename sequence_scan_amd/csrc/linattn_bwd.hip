@@ -11,9 +11,9 @@
 // The first sum is a suffix sum of M's row sums less its column sums, whose terms
 // are fp32 and exact products, so that no difference of rounded values enters it;
 // a and b are by-products of the dq and dk walks' readouts.  X follows from chunk
-// to chunk: <S, R> at a chunk's end is X + sum b, at its start X + sum a; it
-// is a plain dot product of two states where the walks end or a time chunk
-// does, which bounds how far rounding travels.
+// to chunk: <S, R> at a chunk's end is X + sum b, at its start X + sum a; it is a
+// plain dot product of two states where the walks or a time chunk start and end,
+// which bounds how far rounding travels.
 #include <algorithm>
 
 #include "linattn_kernel.h"
@@ -43,11 +43,16 @@ __global__ void __launch_bounds__(256, 2) la_bwd_kernel(LaBwd a) {
 __device__ __forceinline__ float wave_total(float v) { return la_rows_sum(la_row_sum(v)); }
 
 constexpr int kLaDecayChunks = kLaBwdChunk / kLaQ;   // matrix chunks per time chunk, at most
+constexpr int kDecayWaves = 16, kDecayEach = kLaDecayChunks / kDecayWaves;
 
 // The decay's gradient of one (batch row, head) and time chunk, from the walks'
-// per-step parts.
-__global__ void __launch_bounds__(256) la_decay_kernel(LaBwd a) {
-  __shared__ float sA[kLaDecayChunks], sB[kLaDecayChunks], sdot[4], ssum[4];
+// per-step parts: a wavefront per matrix chunk, a lane per step, all parts loaded
+// first.  The recursion for <S, R> runs from the time chunk's end; at its start it
+// has to arrive at <S, R> there, which is known too.  What it misses by is the
+// rounding that it gathered, and is taken off each chunk in proportion to its
+// distance from the end.
+__global__ void __launch_bounds__(64 * kDecayWaves) la_decay_kernel(LaBwd a) {
+  __shared__ float sA[kLaDecayChunks], sB[kLaDecayChunks], sdot[2][kDecayWaves], ssum[kDecayWaves];
   const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
   const int H = a.dq.nheads, K = a.dq.n_chunks;
   const int b = blockIdx.x / H, h = blockIdx.x % H, kt = blockIdx.y;
@@ -55,50 +60,69 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaBwd a) {
   const int64_t L = min(a.dq.chunk_len, a.dq.seqlen - t_begin);
   const int chunks = (int)((L + kLaQ - 1) / kLaQ);
   const int64_t per = (int64_t)a.dq.xdim * a.dq.cdim;
-  const float* S = kt < K - 1 ? a.fwd_states + ((int64_t)(b * K + kt) * H + h) * per
-                   : a.dlast != nullptr ? a.last_state + ((int64_t)b * H + h) * per : nullptr;
-  const float* R = kt < K - 1 ? a.rev_states + ((int64_t)(b * K + kt + 1) * H + h) * per
-                   : a.dlast != nullptr ? a.dlast + ((int64_t)b * H + h) * per : nullptr;
-  float dot = 0.0f;
-  if (S != nullptr)
-    for (int64_t e = tid; e < per; e += 256) dot = __builtin_fmaf(S[e], R[e], dot);
-  dot = wave_total(dot);
-  if (l == 0) sdot[w] = dot;
   const int nk = (a.dq.xdim + 63) / 64;
   const int64_t plane = (int64_t)a.dq.batch * H * a.dq.seqlen;
   const int64_t at0 = ((int64_t)b * H + h) * a.dq.seqlen + t_begin;
-  auto parts = [&](int c, float* da, float* db) SSM_INLINE {
-    const int64_t t = (int64_t)c * kLaQ + l;
-    *da = *db = 0.0f;
+  float da[kDecayEach], db[kDecayEach];
+#pragma unroll
+  for (int i = 0; i < kDecayEach; ++i) {
+    const int64_t t = (int64_t)(w + kDecayWaves * i) * kLaQ + l;
+    da[i] = db[i] = 0.0f;
     if (l < kLaQ && t < L)
-      for (int i = 0; i < nk; ++i) {
-        *da += a.dq.part[i * plane + at0 + t];
-        *db += a.dk.part[i * plane + at0 + t];
+      for (int n = 0; n < nk; ++n) {
+        da[i] += a.dq.part[n * plane + at0 + t];
+        db[i] += a.dk.part[n * plane + at0 + t];
       }
-  };
-  for (int c = w; c < chunks; c += 4) {
-    float da, db;
-    parts(c, &da, &db);
-    da = wave_total(da);
-    db = wave_total(db);
+  }
+  // <S, R> where the time chunk ends and where it starts
+  const float* S[2];
+  const float* R[2];
+  const int64_t bh = ((int64_t)b * H + h) * per;
+  auto slot = [&](int k) SSM_INLINE { return ((int64_t)(b * K + k) * H + h) * per; };
+  S[0] = kt < K - 1 ? a.fwd_states + slot(kt) : a.dlast != nullptr ? a.last_state + bh : nullptr;
+  R[0] = kt < K - 1 ? a.rev_states + slot(kt + 1) : a.dlast != nullptr ? a.dlast + bh : nullptr;
+  S[1] = kt > 0 ? a.fwd_states + slot(kt - 1) : a.initial != nullptr ? a.initial + bh : nullptr;
+  R[1] = kt > 0 ? a.rev_states + slot(kt) : a.initial != nullptr ? a.dinitial + bh : nullptr;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float dot = 0.0f;
+    if (S[e] != nullptr)
+      for (int64_t i = 4 * tid; i < per; i += 4 * 64 * kDecayWaves) {   // per is a multiple of 64
+        const float4 x = *reinterpret_cast<const float4*>(S[e] + i), y = *reinterpret_cast<const float4*>(R[e] + i);
+        dot = __builtin_fmaf(x.x, y.x, __builtin_fmaf(x.y, y.y, __builtin_fmaf(x.z, y.z, __builtin_fmaf(x.w, y.w, dot))));
+      }
+    dot = wave_total(dot);
+    if (l == 0) sdot[e][w] = dot;
+  }
+#pragma unroll
+  for (int i = 0; i < kDecayEach; ++i) {
+    const float A = wave_total(da[i]), B = wave_total(db[i]);
     if (l == 0) {
-      sA[c] = da;
-      sB[c] = db;
+      sA[w + kDecayWaves * i] = A;
+      sB[w + kDecayWaves * i] = B;
     }
   }
   block_sync();
-  const float end = sdot[0] + sdot[1] + sdot[2] + sdot[3];
+  float end = 0.0f, miss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kDecayWaves; ++i) {
+    end += sdot[0][i];
+    miss -= sdot[1][i];
+  }
+  miss += end;
+  for (int i = chunks - 1; i >= 0; --i) miss += sA[i] - sB[i];
   float sum = 0.0f;
-  for (int c = w; c < chunks; c += 4) {
+#pragma unroll
+  for (int n = 0; n < kDecayEach; ++n) {
+    const int c = w + kDecayWaves * n;
+    if (c >= chunks) continue;
     float X = end;
     for (int i = chunks - 1; i > c; --i) X += sA[i] - sB[i];
-    X -= sB[c];
-    float da, db;
-    parts(c, &da, &db);
-    float one = 1.0f, pre = db;
+    X -= sB[c] + miss * ((float)(chunks - c) - 0.5f) / (float)chunks;
+    float one = 1.0f, pre = db[n];
     affine_wave_scan(one, pre);
-    pre -= db;                                   // sum of b before this step
-    float suf = __shfl(da, 63 - l);              // steps in reverse order
+    pre -= db[n];                                // sum of b before this step
+    float suf = __shfl(da[n], 63 - l);           // steps in reverse order
     one = 1.0f;
     affine_wave_scan(one, suf);
     suf = __shfl(suf, 63 - l);
@@ -113,7 +137,12 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaBwd a) {
     sum = wave_total(sum);
     if (l == 0) ssum[w] = sum;
     block_sync();
-    if (tid == 0) a.ddecay[(int64_t)(b * K + kt) * H + h] = ssum[0] + ssum[1] + ssum[2] + ssum[3];
+    if (tid == 0) {
+      float r = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kDecayWaves; ++i) r += ssum[i];
+      a.ddecay[(int64_t)(b * K + kt) * H + h] = r;
+    }
   }
 }
 
@@ -154,7 +183,8 @@ hipError_t launch_la_bwd(const LaBwd& a, hipStream_t s) {
   else if (wk) hipLaunchKernelGGL((la_bwd_kernel<128, 64>), grid, dim3(256), 0, s, a);
   else if (wv) hipLaunchKernelGGL((la_bwd_kernel<64, 128>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((la_bwd_kernel<64, 64>), grid, dim3(256), 0, s, a);
-  hipLaunchKernelGGL(la_decay_kernel, dim3((unsigned)(a.dq.batch * a.dq.nheads), (unsigned)a.dq.n_chunks), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(la_decay_kernel, dim3((unsigned)(a.dq.batch * a.dq.nheads), (unsigned)a.dq.n_chunks),
+                     dim3(64 * kDecayWaves), 0, s, a);
   return hipGetLastError();
 }
 
