@@ -42,13 +42,49 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
+// Tiles of bf16 in LDS, W bytes per row (128 or 256), in units of 16 bytes.  They
+// are filled by loads that go straight to LDS, 1024 consecutive bytes per
+// wavefront, so rows cannot be padded; instead the unit u of row r lies at
+// position u ^ f(r), f(r) = 2 (r & 3) + (r >> 2 & 1).  Eight consecutive rows
+// then hold one unit in eight different bank groups (row reads), and four
+// consecutive rows two neighbouring units in eight (transposing reads).
+__device__ __forceinline__ uint32_t la_flip(int row) { return (uint32_t)(((row & 3) << 1) | ((row >> 2) & 1)) * 16u; }
+
+template <int W>
+struct LaRows {
+  char* p;
+  // Sixteen bytes: row, unit.  (The unit's bits flip independently, so that with a
+  // constant part of it the address is one xor or an immediate offset away.)
+  __device__ __forceinline__ char* at(int row, int byte) const { return p + row * W + ((uint32_t)byte ^ la_flip(row)); }
+  // Eight columns from 8 u.
+  __device__ __forceinline__ bf16x8_t op(int row, int u) const { return *reinterpret_cast<const bf16x8_t*>(at(row, 16 * u)); }
+  // Columns c .. c + 3 and c + 16 .. c + 19 (c a multiple of 4).
+  __device__ __forceinline__ bf16x8_t op2(int row, int c) const {
+    const bf16x4_t a = *reinterpret_cast<const bf16x4_t*>(at(row, 2 * c));
+    const bf16x4_t b = *reinterpret_cast<const bf16x4_t*>(at(row, 2 * c + 32));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  __device__ __forceinline__ uint2 four(int row, int c) const { return *reinterpret_cast<const uint2*>(at(row, 2 * c)); }
+};
+
 __device__ __forceinline__ bf16x8_t la_op(const uint16_t* p) { return *reinterpret_cast<const bf16x8_t*>(p); }
 
-__device__ __forceinline__ bf16x8_t la_op2(const uint16_t* p0, const uint16_t* p1) {
-  const bf16x4_t a = *reinterpret_cast<const bf16x4_t*>(p0);
-  const bf16x4_t b = *reinterpret_cast<const bf16x4_t*>(p1);
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+// A wavefront's load of 64 x 16 bytes to LDS: lane l's come from base + off and go
+// to `to` + 16 l.  (Of lanes that are off, nothing is written.)  Completion is the
+// wavefront's to wait for: la_loaded(), then a barrier.  Written as an
+// instruction: of the compiler's own form every later LDS read waits, which
+// would serialise a chunk's loads with the arithmetic of the one before.
+__device__ __forceinline__ void la_load_lds(const char* base, uint32_t off, void* to) {
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)static_cast<char*>(to);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
+      : "memory");   // (m0 is a scratch register: whoever needs it sets it)
 }
+__device__ __forceinline__ void la_loaded() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Transposing read: within 16 lanes, lane i gets element i % 4 of the 8-byte
 // pieces addressed by lanes 4 e + i / 4, e = 0..3.
@@ -56,12 +92,13 @@ __device__ __forceinline__ i16x4_t la_tr(const uint16_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p));
 }
 
-// Rows r0 .. r0 + 7 of column c0 + (lane % 16) of a row-major tile.
-__device__ __forceinline__ bf16x8_t la_col8(const uint16_t* tile, int stride, int r0, int c0, int l) {
+// Rows r0 .. r0 + 7 (r0 a multiple of 8) of column c0 + (lane % 16).
+template <int W>
+__device__ __forceinline__ bf16x8_t la_col8(const LaRows<W>& tile, int r0, int c0, int l) {
   const int k = l & 15;
-  const uint16_t* a0 = tile + (r0 + (k >> 2)) * stride + c0 + 4 * (k & 3);
-  const i16x4_t lo = la_tr(a0);
-  const i16x4_t hi = la_tr(a0 + 4 * stride);
+  const int row = r0 + (k >> 2), byte = 2 * c0 + 8 * (k & 3);
+  const i16x4_t lo = la_tr(reinterpret_cast<const uint16_t*>(tile.at(row, byte)));
+  const i16x4_t hi = la_tr(reinterpret_cast<const uint16_t*>(tile.at(row + 4, byte)));
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -132,50 +169,46 @@ __device__ __forceinline__ float la_rows_sum(float v) {
   return __uint_as_float(u[0]) + __uint_as_float(u[1]);
 }
 
-// Whether the 8-column vector `vec` of a row lies within `dim` columns.
-__device__ __forceinline__ bool la_in(int vec, int dim) { return vec * 8 < dim; }
-
 constexpr int kWalkOut = 0;     // the products alone
 constexpr int kWalkState = 1;   // no rows and no output: the state at the end of the time chunk
 constexpr int kWalkDq = 2;      // with the decay gradient's parts of dq: Z = q
 constexpr int kWalkDk = 3;      // ... of dk: Z = k
 
-// LDS of one walk (C: contracted columns, 64 or 128).  What both phases of a
-// chunk read is held twice, so that the next chunk is staged while the current
-// one's second phase runs.
+// LDS of one walk (C: contracted columns, 64 or 128).  B and X, which both
+// phases of a chunk read, are held twice: the next chunk's are loaded from the
+// chunk's start; A and Z, which only the first phase reads, from its middle.
 template <int C, int KIND>
 struct LaTile {
-  static constexpr int SA = C + 8, SB = C + 16, SX = 64 + 16, SZ = 64 + 8, SW = kLaQ + 8;
+  static constexpr int SW = kLaQ + 8;
+  static constexpr bool kOut = KIND != kWalkState;
   static constexpr bool kZ = KIND == kWalkDq || KIND == kWalkDk;
   static constexpr int kBlk = kLaQ / 16;
-  uint16_t B[2][kLaQ * SB] __attribute__((aligned(16)));
-  uint16_t X[2][kLaQ * SX] __attribute__((aligned(16)));
-  uint16_t A[KIND == kWalkState ? 8 : kLaQ * SA] __attribute__((aligned(16)));
-  uint16_t Z[kZ ? kLaQ * SZ : 8] __attribute__((aligned(16)));
-  uint16_t W[2][KIND == kWalkState ? 8 : kLaQ * SW] __attribute__((aligned(16)));   // hi, lo
+  char B[2][kLaQ * 2 * C] __attribute__((aligned(1024)));
+  char X[2][kLaQ * 128] __attribute__((aligned(1024)));
+  char A[kOut ? kLaQ * 2 * C : 16] __attribute__((aligned(1024)));
+  char Z[kZ ? kLaQ * 128 : 16] __attribute__((aligned(1024)));
+  uint16_t W[2][kOut ? kLaQ * SW : 8] __attribute__((aligned(16)));   // hi, lo
   float cum[2][kLaQ] __attribute__((aligned(16)));   // log2 decay summed from the chunk's first step, inclusive
   float low[2][kLaQ] __attribute__((aligned(16)));   // what it lacks of the 64-bit sum
   float row[2][kLaQ];                                // factor of A S^T
   float src[2][kLaQ] __attribute__((aligned(16)));   // factor of X in the state update
   float end[2];                                      // exp(c_end)
   int bad[2];                                        // the chunk's X holds a value that is not finite
-  int badstep[2][64];                                // column's first (REV: last) such step
   float dot[kZ ? 4 : 1][kLaQ];                       // per wavefront: Z . (diag(row) A S^T)
   float rs[KIND == kWalkDq ? kBlk : 1][kLaQ];        // row sums of M by column block
   float cs[KIND == kWalkDq ? kBlk : 1][kLaQ] __attribute__((aligned(16)));   // column sums of M by row block
 };
 
-// One walk.  `h`, `b`: head and batch row; `x0`: first value column of the
-// slice; `kt`: time chunk.
+// One walk.  `h`, `b`: head and batch row; `slice`: its 64 value columns; `kt`:
+// time chunk.
 template <int C, int KIND, bool REV>
 __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int b, int h, int slice, int kt) {
   using T = LaTile<C, KIND>;
   constexpr int NT = C / 16;                  // 16 x 16 state tiles per wavefront
   constexpr int NB = kLaQ / 16;               // 16-step blocks per chunk
   static_assert(NB == 2, "the products over a chunk's steps are one instruction deep");
-  constexpr int NR = kLaQ * C / 8 / 256;      // 16-byte vectors of A and B per thread and chunk
-  constexpr int NX = kLaQ * 64 / 8 / 256;     // ... of X and Z
-  constexpr bool kOut = KIND != kWalkState;
+  constexpr int NR = kLaQ * 2 * C / 4096;     // loads of A and B per wavefront and chunk (of X and Z: one)
+  constexpr bool kOut = T::kOut;
   constexpr bool kZ = T::kZ;
   constexpr int kTerms = kZ ? 3 : 2;          // bf16 terms of the state in the readout
   const int tid = threadIdx.x, l = tid & 63;
@@ -185,112 +218,69 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   const int K = a.n_chunks;
   const int64_t t_begin = (int64_t)kt * a.chunk_len;
   const int64_t L = min(a.chunk_len, a.seqlen - t_begin);
-  auto base = [&](const LaOperand& o, int col) SSM_INLINE {
-    return o.p + ((int64_t)b * a.seqlen + t_begin) * o.row + (int64_t)(h / o.share) * o.head + col;
-  };
-  const uint16_t* Ab = kOut ? base(a.A, 0) : nullptr;
-  const uint16_t* Bb = base(a.B, 0);
-  const uint16_t* Xb = base(a.X, x0);
-  const uint16_t* Zb = kZ ? base(a.Z, x0) : nullptr;
-  const float* gb = a.decay + (int64_t)b * a.decay_b + t_begin * a.decay_t + h;
+  const int chunks = (int)((L + kLaQ - 1) / kLaQ);
   const int xdim = min(64, a.xdim - x0);      // value columns of this slice that exist
   const int p = 16 * w + lr;                  // this lane's value column in the slice
+  auto start_of = [&](int ch) SSM_INLINE { return (int64_t)(REV ? chunks - 1 - ch : ch) * kLaQ; };
+  auto steps_of = [&](int ch) SSM_INLINE { return (int)min((int64_t)kLaQ, L - start_of(ch)); };
 
-  // Rows of 16-byte vectors; rows past the sequence's last step re-read that step
-  // (their X, Z and decay are then zero), columns past the tensor's width read its
-  // first vector and are not staged (zero in LDS from the start).  Addresses are
-  // a chunk's base, uniform across the workgroup, plus a 32-bit byte offset: one
-  // chunk of any tensor spans less than 2^31 bytes (checked on the host).
-  struct Bank {
-    u32x4_t A[kOut ? NR : 1], B[NR], X[NX], Z[kZ ? NX : 1];
+  // Loads: each operand's next chunk is a running base, uniform across the
+  // workgroup, plus 32-bit lane offsets that are the same for every full chunk
+  // (one chunk of any tensor spans less than 2^31 bytes: checked on the host).
+  // Rows past the sequence's last step re-read that step; lanes whose columns lie
+  // past the tensor's width stay off, and those columns zero from the start.
+  auto base = [&](const LaOperand& o, int col) SSM_INLINE {
+    return reinterpret_cast<const char*>(o.p + ((int64_t)b * a.seqlen + t_begin + start_of(0)) * o.row +
+                                         (int64_t)(h / o.share) * o.head + col);
   };
-  Bank bank;
-  struct Offsets {
-    uint32_t A[kOut ? NR : 1], B[NR], X[NX], Z[kZ ? NX : 1];
-  };
-  auto offsets = [&](int nt) SSM_INLINE {
-    Offsets o;
+  auto hop = [&](const LaOperand& o) SSM_INLINE { return (REV ? -2 : 2) * kLaQ * o.row; };   // bytes
+  const char* nA = kOut ? base(a.A, 0) : nullptr;
+  const char* nB = base(a.B, 0);
+  const char* nX = base(a.X, x0);
+  const char* nZ = kZ ? base(a.Z, x0) : nullptr;
+  constexpr int kPer = 1024 / (2 * C);        // rows of A and B per load
+  // lane l of load r: row, and the source's byte in it
+  auto wide_row = [&](int r) SSM_INLINE { return (w * NR + r) * kPer + l / (64 / kPer); };
+  auto wide_byte = [&](int r) SSM_INLINE { return (uint32_t)(l % (64 / kPer)) * 16u ^ la_flip(wide_row(r)); };
+  const int xrow = 8 * w + l / 8;
+  const uint32_t xbyte = (uint32_t)(l % 8) * 16u ^ la_flip(xrow);
+  const bool xin = (int)xbyte < 2 * xdim;
+  uint32_t offA[kOut ? NR : 1], offB[NR], offX, offZ = 0u;
+  auto set_offsets = [&](int nt) SSM_INLINE {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int v = tid + 256 * r;
-      const uint32_t row = (uint32_t)min(v / (C / 8), nt - 1), c16 = la_in(v % (C / 8), a.cdim) ? v % (C / 8) * 16u : 0u;
-      if constexpr (kOut) o.A[r] = row * ((uint32_t)a.A.row * 2u) + c16;
-      o.B[r] = row * ((uint32_t)a.B.row * 2u) + c16;
+      const uint32_t row = (uint32_t)min(wide_row(r), nt - 1);
+      if constexpr (kOut) offA[r] = row * ((uint32_t)a.A.row * 2u) + wide_byte(r);
+      offB[r] = row * ((uint32_t)a.B.row * 2u) + wide_byte(r);
     }
-#pragma unroll
-    for (int r = 0; r < NX; ++r) {
-      const int v = tid + 256 * r;
-      const uint32_t row = (uint32_t)min(v >> 3, nt - 1), c16 = la_in(v & 7, xdim) ? (v & 7) * 16u : 0u;
-      o.X[r] = row * ((uint32_t)a.X.row * 2u) + c16;
-      if constexpr (kZ) o.Z[r] = row * ((uint32_t)a.Z.row * 2u) + c16;
-    }
-    return o;
+    const uint32_t row = (uint32_t)min(xrow, nt - 1);
+    offX = row * ((uint32_t)a.X.row * 2u) + xbyte;
+    if constexpr (kZ) offZ = row * ((uint32_t)a.Z.row * 2u) + xbyte;
   };
-  auto load = [&](int64_t t0, const Offsets& o) SSM_INLINE {
-    auto at = [&](const uint16_t* p, const LaOperand& t, uint32_t off) SSM_INLINE {
-      return *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(p + t0 * t.row) + off);
-    };
+  // (the ragged chunk is a forward walk's last and a backward walk's first)
+  auto load_bx = [&](int to) SSM_INLINE {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      if constexpr (kOut) bank.A[r] = at(Ab, a.A, o.A[r]);
-      bank.B[r] = at(Bb, a.B, o.B[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < NX; ++r) {
-      bank.X[r] = at(Xb, a.X, o.X[r]);
-      if constexpr (kZ) bank.Z[r] = at(Zb, a.Z, o.Z[r]);
-    }
+    for (int r = 0; r < NR; ++r)
+      if ((int)wide_byte(r) < 2 * a.cdim) la_load_lds(nB, offB[r], &s.B[to][(w * NR + r) * 1024]);
+    if (xin) la_load_lds(nX, offX, &s.X[to][w * 1024]);
+    nB += hop(a.B);
+    nX += hop(a.X);
   };
-  const Offsets whole = offsets(kLaQ);
-  auto issue = [&](int64_t t0, int nt) SSM_INLINE {
-    if (nt == kLaQ) load(t0, whole);
-    else load(t0, offsets(nt));
-  };
-
-  auto stage = [&](int nt, int to) SSM_INLINE {
+  auto load_az = [&]() SSM_INLINE {
+    if constexpr (kOut) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int v = tid + 256 * r;
-      const int row = v / (C / 8), c8 = v % (C / 8);
-      if (la_in(c8, a.cdim)) {
-        if constexpr (kOut) *reinterpret_cast<u32x4_t*>(&s.A[row * T::SA + c8 * 8]) = bank.A[r];
-        *reinterpret_cast<u32x4_t*>(&s.B[to][row * T::SB + c8 * 8]) = bank.B[r];
-      }
+      for (int r = 0; r < NR; ++r)
+        if ((int)wide_byte(r) < 2 * a.cdim) la_load_lds(nA, offA[r], &s.A[(w * NR + r) * 1024]);
+      nA += hop(a.A);
     }
-#pragma unroll
-    for (int r = 0; r < NX; ++r) {
-      const int v = tid + 256 * r;
-      const int row = v >> 3, c8 = v & 7;
-      if (!la_in(c8, xdim)) continue;
-      u32x4_t x = bank.X[r];
-      if (nt < kLaQ && row >= nt) {
-        x = u32x4_t{0u, 0u, 0u, 0u};
-        if constexpr (kZ) bank.Z[r] = x;   // M's rows past the end
-      }
-      // W is zero where j comes after i, and zero times a value that is not
-      // finite is not zero: such values of X are taken out here and put back
-      // into the rows and the state that they reach (poison, below)
-      auto mag = [&](int e) SSM_INLINE { return __builtin_bit_cast(u16x2_t, x[e] & 0x7fff7fffu); };
-      const uint32_t top = __builtin_bit_cast(
-          uint32_t, __builtin_elementwise_max(__builtin_elementwise_max(mag(0), mag(1)), __builtin_elementwise_max(mag(2), mag(3))));
-      if (((top + 0x00800080u) & 0x80008000u) != 0u) {   // an exponent of all ones
-        s.bad[to] = 1;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t half = (e & 1) ? 0xffff0000u : 0x0000ffffu;
-          if ((x[e >> 1] & half & 0x7f807f80u) == (half & 0x7f807f80u)) {
-            if (REV) atomicMax(&s.badstep[to][c8 * 8 + e], row);
-            else atomicMin(&s.badstep[to][c8 * 8 + e], row);
-            x[e >> 1] &= ~half;
-          }
-        }
-      }
-      *reinterpret_cast<u32x4_t*>(&s.X[to][row * T::SX + c8 * 8]) = x;
-      if constexpr (kZ) *reinterpret_cast<u32x4_t*>(&s.Z[row * T::SZ + c8 * 8]) = bank.Z[r];
+    if constexpr (kZ) {
+      if (xin) la_load_lds(nZ, offZ, &s.Z[w * 1024]);
+      nZ += hop(a.Z);
     }
   };
 
   // The last wavefront sums the decays, a chunk ahead.
+  const float* gb = a.decay + (int64_t)b * a.decay_b + t_begin * a.decay_t + h;
   float g = 0.0f;      // this lane's step
   float csum = 0.0f;   // log2 decay of the whole time chunk
   auto get_decay = [&](int64_t t0, int nt) SSM_INLINE { g = gb[(t0 + min(l, nt - 1)) * a.decay_t]; };
@@ -342,16 +332,15 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     }
   }
 
-  if (tid < 128) s.badstep[tid >> 6][tid & 63] = REV ? -1 : kLaQ;
   if (tid < 2) s.bad[tid] = 0;
-  // columns past the tensors' widths are never staged
   if (a.cdim < C || xdim < 64) {
-    for (int e = tid; e < 2 * kLaQ * T::SB; e += 256) s.B[0][e] = 0;
-    for (int e = tid; e < 2 * kLaQ * T::SX; e += 256) s.X[0][e] = 0;
-    if constexpr (kOut)
-      for (int e = tid; e < kLaQ * T::SA; e += 256) s.A[e] = 0;
-    if constexpr (kZ)
-      for (int e = tid; e < kLaQ * T::SZ; e += 256) s.Z[e] = 0;
+    auto clear = [&](char* t, int bytes) SSM_INLINE {
+      for (int e = 16 * tid; e < bytes; e += 16 * 256) *reinterpret_cast<u32x4_t*>(t + e) = u32x4_t{0u, 0u, 0u, 0u};
+    };
+    clear(s.B[0], sizeof(s.B));
+    clear(s.X[0], sizeof(s.X));
+    if constexpr (kOut) clear(s.A, sizeof(s.A));
+    if constexpr (kZ) clear(s.Z, sizeof(s.Z));
   }
   if constexpr (kOut) {
     // W's block beyond the triangle
@@ -362,31 +351,74 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   }
   block_sync();
 
-  const int64_t chunks = (L + kLaQ - 1) / kLaQ;
-  auto start_of = [&](int64_t ch) SSM_INLINE { return (REV ? chunks - 1 - ch : ch) * kLaQ; };
-  auto steps_of = [&](int64_t ch) SSM_INLINE { return (int)min((int64_t)kLaQ, L - start_of(ch)); };
-  issue(start_of(0), steps_of(0));
+  set_offsets(steps_of(0));
+  load_bx(0);
+  load_az();
   if (w == 3) {
     get_decay(start_of(0), steps_of(0));
     sum_decay(steps_of(0), 0);
     if (chunks > 1) get_decay(start_of(1), steps_of(1));
   }
-  stage(steps_of(0), 0);
-  if (chunks > 1) issue(start_of(1), steps_of(1));
+  la_loaded();
   block_sync();
-  for (int64_t ch = 0; ch < chunks; ++ch) {
+
+  f32x4_t accY[kOut ? NB : 1];
+  // Stores of chunk ch: four consecutive columns of step 16 n + lr per lane
+  // (xdim is a multiple of 8).
+  auto store = [&](int ch) SSM_INLINE {
     const int64_t t0 = start_of(ch);
     const int nt = steps_of(ch);
-    const int cur = (int)(ch & 1);
+    const int64_t o0 = (((int64_t)b * a.seqlen + t_begin + t0) * a.nheads + h) * a.xdim + x0;
+    const int py = 16 * w + 4 * q;
+    if (py < xdim) {
+      auto put = [&](auto type) SSM_INLINE {
+        using To = decltype(type);
+        char* const to = reinterpret_cast<char*>(static_cast<To*>(a.out) + o0);
+        const uint32_t rowb = (uint32_t)a.nheads * (uint32_t)a.xdim * (uint32_t)sizeof(To);
+        const uint32_t at = (uint32_t)lr * rowb + (uint32_t)py * (uint32_t)sizeof(To);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+          if (nt == kLaQ || 16 * n + lr < nt) {
+            const float y[4] = {accY[n][0], accY[n][1], accY[n][2], accY[n][3]};
+            store_row<To, 4>(reinterpret_cast<To*>(to + (at + 16u * (uint32_t)n * rowb)), y);
+          }
+      };
+      if (a.out_bf16) put(uint16_t{});
+      else put(float{});
+    }
+  };
+  float part = 0.0f;
+  auto store_part = [&](int ch) SSM_INLINE {
+    if (tid < steps_of(ch)) {
+      if (s.bad[ch & 1] != 0) part = __builtin_nanf("");
+      a.part[(((int64_t)slice * a.batch + b) * a.nheads + h) * a.seqlen + t_begin + start_of(ch) + tid] = part;
+    }
+    if (tid == 0) s.bad[ch & 1] = 0;
+  };
+
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int nt = steps_of(ch);
+    const int cur = ch & 1;
     const bool more = ch + 1 < chunks;
+    const LaRows<2 * C> tA{s.A}, tB{s.B[cur]};
+    const LaRows<128> tX{s.X[cur]}, tZ{s.Z};
+    // The previous chunk's stores, then the next one's loads: what is waited for
+    // at the chunk's end has had the chunk's time.
+    if constexpr (kOut) {
+      if (ch > 0) {
+        store(ch - 1);
+        if constexpr (kZ) store_part(ch - 1);
+      }
+    }
+    if (more) {
+      if (REV ? ch == 0 : ch + 2 == chunks) set_offsets(steps_of(ch + 1));
+      load_bx(cur ^ 1);
+    }
     if (w == 3 && more) {
       sum_decay(steps_of(ch + 1), cur ^ 1);
       if (ch + 2 < chunks) get_decay(start_of(ch + 2), steps_of(ch + 2));
     }
-    const uint16_t* const tB = s.B[cur];
-    const uint16_t* const tX = s.X[cur];
 
-    f32x4_t accY[kOut ? NB : 1];
     if constexpr (kOut) {
       // Phase 1.  The triangle's three 16 x 16 tiles of G, one each for the first
       // three wavefronts (the last one sums decays), transposed: lane (q, lr)
@@ -397,8 +429,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       if (w < 3) {
         f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < C / 32; ++m)
-          acc = la_mfma(la_op(&tB[(16 * jb + lr) * T::SB + 32 * m + 8 * q]), la_op(&s.A[i * T::SA + 32 * m + 8 * q]), acc);
+        for (int m = 0; m < C / 32; ++m) acc = la_mfma(tB.op(16 * jb + lr, 4 * m + q), tA.op(i, 4 * m + q), acc);
         const float ci = s.cum[cur][i], li = s.low[cur][i];
         const f32x4_t cj = *reinterpret_cast<const f32x4_t*>(&s.cum[cur][j0]);
         const f32x4_t lj = *reinterpret_cast<const f32x4_t*>(&s.low[cur][j0]);
@@ -416,13 +447,12 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
           // and k: its row and column sums, in fp32 from exact products
           f32x4_t pk = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            pk = la_mfma(la_op(&tX[(16 * jb + lr) * T::SX + 32 * m + 8 * q]), la_op(&s.Z[i * T::SZ + 32 * m + 8 * q]), pk);
+          for (int m = 0; m < 2; ++m) pk = la_mfma(tX.op(16 * jb + lr, 4 * m + q), tZ.op(i, 4 * m + q), pk);
           float rowsum = 0.0f;
           f32x4_t colsum;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float m = j0 + r < i ? v[r] * pk[r] : 0.0f;
+            const float m = j0 + r < i && i < nt ? v[r] * pk[r] : 0.0f;
             rowsum += m;
             colsum[r] = la_row_sum(m);
           }
@@ -431,9 +461,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
           if (lr == 0) *reinterpret_cast<f32x4_t*>(&s.cs[ib][j0]) = colsum;
         }
       }
-      // The entering state as operands of the readout: tiles 2 m and 2 m + 1 give
-      // the eight k slots of product m (columns 32 m + 4 q + 0..3 and
-      // 32 m + 16 + 4 q + 0..3), and A is read in the same order.
+      // The entering state's readout: tiles 2 m and 2 m + 1 give the eight k slots
+      // of product m (columns 32 m + 4 q + 0..3 and 32 m + 16 + 4 q + 0..3), and
+      // A is read in the same order.
 #pragma unroll
       for (int n = 0; n < NB; ++n) accY[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -448,24 +478,22 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          const uint16_t* arow = &s.A[(16 * n + lr) * T::SA + 32 * m + 4 * q];
-          const bf16x8_t av = la_op2(arow, arow + 16);
+          const bf16x8_t av = tA.op2(16 * n + lr, 32 * m + 4 * q);
 #pragma unroll
           for (int e = 0; e < kTerms; ++e) accY[n] = la_mfma(__builtin_bit_cast(bf16x8_t, t[e]), av, accY[n]);
         }
       }
-      float rowf[NB];
 #pragma unroll
-      for (int n = 0; n < NB; ++n) rowf[n] = s.row[cur][16 * n + lr];
+      for (int n = 0; n < NB; ++n) {
+        const float f = s.row[cur][16 * n + lr];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) accY[n][r] *= rowf[n];
+        for (int r = 0; r < 4; ++r) accY[n][r] *= f;
+      }
       if constexpr (kZ) {
         // Z . readout over this wavefront's 16 columns
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          const uint2 z = *reinterpret_cast<const uint2*>(&s.Z[(16 * n + lr) * T::SZ + 16 * w + 4 * q]);
+          const uint2 z = tZ.four(16 * n + lr, 16 * w + 4 * q);
           float d = accY[n][0] * __uint_as_float(z.x << 16);
           d = __builtin_fmaf(accY[n][1], __uint_as_float(z.x & 0xffff0000u), d);
           d = __builtin_fmaf(accY[n][2], __uint_as_float(z.y << 16), d);
@@ -475,19 +503,52 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
         }
       }
       block_sync();
+      if (more) load_az();
     }
 
-    // Phase 2: Y += W X, stored; the state moves past the chunk, and the next
-    // chunk is staged (A and Z, which only phase 1 reads, in place).
-    const bool poison = s.bad[cur] != 0;
-    const int bad_at = s.badstep[cur][p];
+    // Phase 2: Y += W X; the state moves past the chunk.
     const float e_end = s.end[cur];
-    const bf16x8_t xo = la_col8(tX, T::SX, 8 * q, 16 * w, l);   // X[8 q .. 8 q + 7][p]
+    u32x4_t xw = __builtin_bit_cast(u32x4_t, la_col8(tX, 8 * q, 16 * w, l));   // X[8 q .. 8 q + 7][p]
     const f32x4_t f0 = *reinterpret_cast<const f32x4_t*>(&s.src[cur][8 * q]);
     const f32x4_t f1 = *reinterpret_cast<const f32x4_t*>(&s.src[cur][8 * q + 4]);
+    if (nt < kLaQ) {   // steps past the end
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * q + e >= nt) xw[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+    }
+    // W is zero where j comes after i, and zero times a value that is not finite
+    // is not zero: such values of X are taken out here and put back into the
+    // rows and the state that they reach (poison, below).
+    auto mag = [&](int e) SSM_INLINE { return __builtin_bit_cast(u16x2_t, xw[e] & 0x7fff7fffu); };
+    const uint32_t top = __builtin_bit_cast(
+        uint32_t, __builtin_elementwise_max(__builtin_elementwise_max(mag(0), mag(1)), __builtin_elementwise_max(mag(2), mag(3))));
+    const bool poison = __any(((top + 0x00800080u) & 0x80008000u) != 0u);   // an exponent of all ones
+    int bad_at = REV ? -1 : kLaQ;               // column p's first (REV: last) such step
+    if (poison) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t half = (e & 1) ? 0xffff0000u : 0x0000ffffu;
+        if ((xw[e >> 1] & half & 0x7f807f80u) == (half & 0x7f807f80u)) {
+          bad_at = REV ? max(bad_at, 8 * q + e) : min(bad_at, 8 * q + e);
+          xw[e >> 1] &= ~half;
+        }
+      }
+#pragma unroll
+      for (int d = 16; d < 64; d *= 2) {
+        const int o = __shfl_xor(bad_at, d);
+        bad_at = REV ? max(bad_at, o) : min(bad_at, o);
+      }
+      if (kZ && l == 0) s.bad[cur] = 1;
+    }
+    if constexpr (kOut) {
+      const bf16x8_t xo = __builtin_bit_cast(bf16x8_t, xw);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) accY[n] = la_mfma(xo, la_op(&s.W[e][(16 * n + lr) * T::SW + 8 * q]), accY[n]);
+    }
     bf16x8_t xs[3];
     {
-      const u32x4_t xw = __builtin_bit_cast(u32x4_t, xo);
       u32x4_t t[3];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -499,81 +560,46 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
 #pragma unroll
       for (int k = 0; k < 3; ++k) xs[k] = __builtin_bit_cast(bf16x8_t, t[k]);
     }
-    if constexpr (kOut) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-          accY[n] = la_mfma(xo, la_op(&s.W[e][(16 * n + lr) * T::SW + 8 * q]), accY[n]);
-    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) accS[t][r] *= e_end;
-      const bf16x8_t bt = la_col8(tB, T::SB, 8 * q, 16 * t, l);
+      const bf16x8_t bt = la_col8(tB, 8 * q, 16 * t, l);
 #pragma unroll
       for (int k = 0; k < 3; ++k) accS[t] = la_mfma(bt, xs[k], accS[t]);
     }
-    if (poison && (REV ? bad_at >= 0 : bad_at < kLaQ)) {
+    if (poison) {
+      if (REV ? bad_at >= 0 : bad_at < kLaQ) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) accS[t][r] = __builtin_nanf("");
-    }
-    // The next chunk is staged before this one's stores are issued: loads and
-    // stores complete in order, and waiting for the loads must not mean waiting
-    // for younger stores.
-    if (more) stage(steps_of(ch + 1), cur ^ 1);
-    if constexpr (kOut) {
-      if (poison) {
+          for (int r = 0; r < 4; ++r) accS[t][r] = __builtin_nanf("");
+      }
+      if constexpr (kOut) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int at = s.badstep[cur][16 * w + 4 * q + r];
+          const int at = __shfl(bad_at, 4 * q + r);      // of column 16 w + 4 q + r
 #pragma unroll
-          for (int ib = 0; ib < NB; ++ib)
-            if (REV ? 16 * ib + lr <= at : 16 * ib + lr >= at) accY[ib][r] = __builtin_nanf("");
-        }
-      }
-      // four consecutive columns of step 16 ib + lr (xdim is a multiple of 8)
-      const int64_t o0 = (((int64_t)b * a.seqlen + t_begin + t0) * a.nheads + h) * a.xdim + x0;
-      const int py = 16 * w + 4 * q;
-      if (py < xdim) {
-        auto store = [&](auto type) SSM_INLINE {
-          using To = decltype(type);
-          char* const base = reinterpret_cast<char*>(static_cast<To*>(a.out) + o0);
-          const uint32_t rowb = (uint32_t)a.nheads * (uint32_t)a.xdim * (uint32_t)sizeof(To);
-          const uint32_t at = (uint32_t)lr * rowb + (uint32_t)py * (uint32_t)sizeof(To);
-#pragma unroll
-          for (int ib = 0; ib < NB; ++ib)
-            if (nt == kLaQ || 16 * ib + lr < nt) {
-              const float y[4] = {accY[ib][0], accY[ib][1], accY[ib][2], accY[ib][3]};
-              store_row<To, 4>(reinterpret_cast<To*>(base + (at + 16u * (uint32_t)ib * rowb)), y);
-            }
-        };
-        if (a.out_bf16) store(uint16_t{});
-        else store(float{});
-      }
-      if constexpr (kZ) {
-        if (tid < nt) {
-          float d = s.dot[0][tid] + s.dot[1][tid] + s.dot[2][tid] + s.dot[3][tid];
-          if constexpr (KIND == kWalkDq) {
-            float m = 0.0f;
-            for (int k = 0; k <= tid >> 4; ++k) m += s.rs[k][tid];
-            for (int k = tid >> 4; k < NB; ++k) m -= s.cs[k][tid];
-            d += m;
-          }
-          if (poison) d = __builtin_nanf("");
-          a.part[(((int64_t)slice * a.batch + b) * a.nheads + h) * a.seqlen + t_begin + t0 + tid] = d;
+          for (int n = 0; n < NB; ++n)
+            if (REV ? 16 * n + lr <= at : 16 * n + lr >= at) accY[n][r] = __builtin_nanf("");
         }
       }
     }
-    if (ch + 2 < chunks) issue(start_of(ch + 2), steps_of(ch + 2));
+    if constexpr (kZ) {
+      if (tid < nt) {
+        part = s.dot[0][tid] + s.dot[1][tid] + s.dot[2][tid] + s.dot[3][tid];
+        if constexpr (KIND == kWalkDq) {
+          for (int k = 0; k <= tid >> 4; ++k) part += s.rs[k][tid];
+          for (int k = tid >> 4; k < NB; ++k) part -= s.cs[k][tid];
+        }
+      }
+    }
+    la_loaded();
     block_sync();
-    if (poison) {
-      if (tid < 64) s.badstep[cur][tid] = REV ? -1 : kLaQ;
-      if (tid == 0) s.bad[cur] = 0;
-      block_sync();
-    }
+  }
+  if constexpr (kOut) {
+    store(chunks - 1);
+    if constexpr (kZ) store_part(chunks - 1);
   }
 
   const int far = REV ? 0 : K - 1;
