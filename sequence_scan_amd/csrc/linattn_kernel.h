@@ -134,7 +134,8 @@ __device__ __forceinline__ LaSplit<N> la_split(float v0, float v1) {
   return r;
 }
 
-// Prefix sums over a wavefront in 64 bits (row shifts, then the rows' totals).
+// Prefix sums over each half of a wavefront in 64 bits (row shifts, then the first
+// row's total into the second).
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double la_dpp(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -142,13 +143,12 @@ __device__ __forceinline__ double la_dpp(double v) {
   const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
   return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
-__device__ __forceinline__ double la_prefix(double v) {
+__device__ __forceinline__ double la_prefix32(double v) {
   v += la_dpp<0x111, 0xf>(v);   // row_shr:1
   v += la_dpp<0x112, 0xf>(v);   // row_shr:2
   v += la_dpp<0x114, 0xf>(v);   // row_shr:4
   v += la_dpp<0x118, 0xf>(v);   // row_shr:8
   v += la_dpp<0x142, 0xa>(v);   // row_bcast:15 into rows 1 and 3
-  v += la_dpp<0x143, 0xc>(v);   // row_bcast:31 into rows 2 and 3
   return v;
 }
 
@@ -183,16 +183,17 @@ struct LaTile {
   static constexpr bool kOut = KIND != kWalkState;
   static constexpr bool kZ = KIND == kWalkDq || KIND == kWalkDk;
   static constexpr int kBlk = kLaQ / 16;
+  static constexpr int kRing = 16;            // chunks whose decays are at hand
   char B[2][kLaQ * 2 * C] __attribute__((aligned(1024)));
   char X[2][kLaQ * 128] __attribute__((aligned(1024)));
   char A[kOut ? kLaQ * 2 * C : 16] __attribute__((aligned(1024)));
   char Z[kZ ? kLaQ * 128 : 16] __attribute__((aligned(1024)));
   uint16_t W[2][kOut ? kLaQ * SW : 8] __attribute__((aligned(16)));   // hi, lo
-  float cum[2][kLaQ] __attribute__((aligned(16)));   // log2 decay summed from the chunk's first step, inclusive
-  float low[2][kLaQ] __attribute__((aligned(16)));   // what it lacks of the 64-bit sum
-  float row[2][kLaQ];                                // factor of A S^T
-  float src[2][kLaQ] __attribute__((aligned(16)));   // factor of X in the state update
-  float end[2];                                      // exp(c_end)
+  float cum[kRing][kLaQ] __attribute__((aligned(16)));   // log2 decay summed from the chunk's first step, inclusive
+  float low[kRing][kLaQ] __attribute__((aligned(16)));   // what it lacks of the 64-bit sum
+  float row[kRing][kLaQ];                                // factor of A S^T
+  float src[kRing][kLaQ] __attribute__((aligned(16)));   // factor of X in the state update
+  float end[kRing];                                  // exp(c_end)
   int bad[2];                                        // the chunk's X holds a value that is not finite
   float dot[kZ ? 4 : 1][kLaQ];                       // per wavefront: Z . (diag(row) A S^T)
   float rs[KIND == kWalkDq ? kBlk : 1][kLaQ];        // row sums of M by column block
@@ -279,31 +280,34 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     }
   };
 
-  // The last wavefront sums the decays, a chunk ahead.
+  // Decays.  Every eight chunks each wavefront sums those of two, one in each
+  // half: eight chunks ahead, of eight steps loaded eight chunks before that.
   const float* gb = a.decay + (int64_t)b * a.decay_b + t_begin * a.decay_t + h;
   float g = 0.0f;      // this lane's step
-  float csum = 0.0f;   // log2 decay of the whole time chunk
-  auto get_decay = [&](int64_t t0, int nt) SSM_INLINE { g = gb[(t0 + min(l, nt - 1)) * a.decay_t]; };
-  auto sum_decay = [&](int nt, int to) SSM_INLINE {
+  float csum = 0.0f;   // log2 decay of this half's chunks
+  const int half = l >> 5, step = l & 31;
+  static_assert(kLaQ == 32, "two chunks' decays fit a wavefront");
+  auto get_decays = [&](int first) SSM_INLINE {
+    const int ch = first + 2 * w + half;
+    const int nt = ch < chunks ? steps_of(ch) : 0;
+    g = step < nt ? gb[(start_of(ch) + step) * a.decay_t] : 0.0f;
+  };
+  auto sum_decays = [&](int first) SSM_INLINE {
     // exp2 of anything below -150 is 0 in fp32: decays are held above -160, so
     // that a decay of minus infinity (forget everything) leaves the differences
     // of sums finite.  Sums are held as two floats (from 64 bits): W needs
     // their differences, which one float would give to 2^-24 of the sums only.
+    const int to = (first + 2 * w + half) % T::kRing;
     const float one = g * kLog2e;
-    const double c = la_prefix(l < nt ? (double)(one < -160.0f ? -160.0f : one) : 0.0);
-    const uint64_t cb = __builtin_bit_cast(uint64_t, c);
-    const uint32_t e0 = __builtin_amdgcn_readlane((uint32_t)cb, kLaQ - 1);
-    const uint32_t e1 = __builtin_amdgcn_readlane((uint32_t)(cb >> 32), kLaQ - 1);
-    const double c_end = __builtin_bit_cast(double, (uint64_t)e0 | ((uint64_t)e1 << 32));
+    const double c = la_prefix32((double)(one < -160.0f ? -160.0f : one));
+    const double c_end = __shfl(c, 31, 32);
+    const float hi = (float)c, rest = (float)(c_end - c);
     csum += (float)c_end;
-    if (l < kLaQ) {
-      const float hi = (float)c, rest = (float)(c_end - c);
-      s.cum[to][l] = hi;
-      s.low[to][l] = (float)(c - (double)hi);
-      s.row[to][l] = __builtin_amdgcn_exp2f(REV ? rest : hi) * a.row_scale;
-      s.src[to][l] = __builtin_amdgcn_exp2f(REV ? hi : rest) * a.src_scale;
-    }
-    if (l == 0) s.end[to] = __builtin_amdgcn_exp2f((float)c_end);
+    s.cum[to][step] = hi;
+    s.low[to][step] = (float)(c - (double)hi);
+    s.row[to][step] = __builtin_amdgcn_exp2f(REV ? rest : hi) * a.row_scale;
+    s.src[to][step] = __builtin_amdgcn_exp2f(REV ? hi : rest) * a.src_scale;
+    if (step == 0) s.end[to] = __builtin_amdgcn_exp2f((float)c_end);
   };
 
   // S^T: tile t holds contracted columns [16 t, 16 t + 16) x this wavefront's 16
@@ -354,11 +358,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   set_offsets(steps_of(0));
   load_bx(0);
   load_az();
-  if (w == 3) {
-    get_decay(start_of(0), steps_of(0));
-    sum_decay(steps_of(0), 0);
-    if (chunks > 1) get_decay(start_of(1), steps_of(1));
-  }
+  get_decays(0);
+  sum_decays(0);
+  if (chunks > 8) get_decays(8);
   la_loaded();
   block_sync();
 
@@ -398,7 +400,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
 
   for (int ch = 0; ch < chunks; ++ch) {
     const int nt = steps_of(ch);
-    const int cur = ch & 1;
+    const int cur = ch & 1, dec = ch % T::kRing;
     const bool more = ch + 1 < chunks;
     const LaRows<2 * C> tA{s.A}, tB{s.B[cur]};
     const LaRows<128> tX{s.X[cur]}, tZ{s.Z};
@@ -414,14 +416,14 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       if (REV ? ch == 0 : ch + 2 == chunks) set_offsets(steps_of(ch + 1));
       load_bx(cur ^ 1);
     }
-    if (w == 3 && more) {
-      sum_decay(steps_of(ch + 1), cur ^ 1);
-      if (ch + 2 < chunks) get_decay(start_of(ch + 2), steps_of(ch + 2));
+    if (ch % 8 == 0 && ch + 8 < chunks) {
+      sum_decays(ch + 8);
+      if (ch + 16 < chunks) get_decays(ch + 16);
     }
 
     if constexpr (kOut) {
       // Phase 1.  The triangle's three 16 x 16 tiles of G, one each for the first
-      // three wavefronts (the last one sums decays), transposed: lane (q, lr)
+      // three wavefronts, transposed: lane (q, lr)
       // holds row i = 16 ib + lr, columns j = 16 jb + 4 q + r.
       const int ib = REV ? (w == 2 ? 1 : 0) : (w == 0 ? 0 : 1);
       const int jb = REV ? (w == 0 ? 0 : 1) : (w == 2 ? 1 : 0);
@@ -430,9 +432,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
         f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < C / 32; ++m) acc = la_mfma(tB.op(16 * jb + lr, 4 * m + q), tA.op(i, 4 * m + q), acc);
-        const float ci = s.cum[cur][i], li = s.low[cur][i];
-        const f32x4_t cj = *reinterpret_cast<const f32x4_t*>(&s.cum[cur][j0]);
-        const f32x4_t lj = *reinterpret_cast<const f32x4_t*>(&s.low[cur][j0]);
+        const float ci = s.cum[dec][i], li = s.low[dec][i];
+        const f32x4_t cj = *reinterpret_cast<const f32x4_t*>(&s.cum[dec][j0]);
+        const f32x4_t lj = *reinterpret_cast<const f32x4_t*>(&s.low[dec][j0]);
         float v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -485,7 +487,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       }
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const float f = s.row[cur][16 * n + lr];
+        const float f = s.row[dec][16 * n + lr];
 #pragma unroll
         for (int r = 0; r < 4; ++r) accY[n][r] *= f;
       }
@@ -507,10 +509,10 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     }
 
     // Phase 2: Y += W X; the state moves past the chunk.
-    const float e_end = s.end[cur];
+    const float e_end = s.end[dec];
     u32x4_t xw = __builtin_bit_cast(u32x4_t, la_col8(tX, 8 * q, 16 * w, l));   // X[8 q .. 8 q + 7][p]
-    const f32x4_t f0 = *reinterpret_cast<const f32x4_t*>(&s.src[cur][8 * q]);
-    const f32x4_t f1 = *reinterpret_cast<const f32x4_t*>(&s.src[cur][8 * q + 4]);
+    const f32x4_t f0 = *reinterpret_cast<const f32x4_t*>(&s.src[dec][8 * q]);
+    const f32x4_t f1 = *reinterpret_cast<const f32x4_t*>(&s.src[dec][8 * q + 4]);
     if (nt < kLaQ) {   // steps past the end
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -618,7 +620,18 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       }
     }
   }
-  if (KIND == kWalkState && slice == 0 && w == 3 && l == 0) a.chunk_decay[(int64_t)(b * K + kt) * a.nheads + h] = csum;
+  if constexpr (KIND == kWalkState) {
+    // the time chunk's log2 decay: the halves of all wavefronts, in order
+    float* const sums = &s.row[0][0];
+    block_sync();
+    if (step == 0) sums[2 * w + half] = csum;
+    block_sync();
+    if (slice == 0 && tid == 0) {
+      float r = 0.0f;
+      for (int i = 0; i < 8; ++i) r += sums[i];
+      a.chunk_decay[(int64_t)(b * K + kt) * a.nheads + h] = r;
+    }
+  }
 }
 
 // Heads and slots (value slices, or slices of several walks) of a flat grid:
