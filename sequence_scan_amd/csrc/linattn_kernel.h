@@ -42,20 +42,27 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
-// Tiles of bf16 in LDS, W bytes per row (128 or 256), in units of 16 bytes.  They
-// are filled by loads that go straight to LDS, 1024 consecutive bytes per
-// wavefront, so rows cannot be padded; instead the unit u of row r lies at
-// position u ^ f(r), f(r) = 2 (r & 3) + (r >> 2 & 1).  Eight consecutive rows
-// then hold one unit in eight different bank groups (row reads), and four
-// consecutive rows two neighbouring units in eight (transposing reads).
-__device__ __forceinline__ uint32_t la_flip(int row) { return (uint32_t)(((row & 3) << 1) | ((row >> 2) & 1)) * 16u; }
+// Tiles of bf16 in LDS, W bytes per row, in units of 16 bytes.  They are filled by
+// loads that go straight to LDS, 1024 consecutive bytes per wavefront, so rows
+// cannot be padded; instead unit u of row r lies at position u ^ f(r).  A cycle
+// serves 64 banks, 16 units: the eight rows of half a wavefront's transposing read
+// (r, r + 1 .. r + 3, r + 8 .. r + 11, two neighbouring units each) and the 16 rows
+// of its 8-byte reads (one unit) then lie in different banks.  (Reads of 16 bytes
+// from 16 rows take two cycles in place of one with the wider tiles.)
+template <int W>
+__device__ __forceinline__ uint32_t la_flip(int row) {
+  const uint32_t b0 = row & 1, b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1;
+  if constexpr (W == 256) return 16u * (b2 | b0 << 1 | b1 << 2 | b3 << 3);
+  else if constexpr (W == 128) return 16u * (b2 | b1 << 1 | b3 << 2);
+  else return 16u * (b2 | (b2 ^ b3) << 1);     // 64
+}
 
 template <int W>
 struct LaRows {
   char* p;
-  // Sixteen bytes: row, unit.  (The unit's bits flip independently, so that with a
-  // constant part of it the address is one xor or an immediate offset away.)
-  __device__ __forceinline__ char* at(int row, int byte) const { return p + row * W + ((uint32_t)byte ^ la_flip(row)); }
+  // (The position's bits flip independently, so that with a constant part of it the
+  // address is one xor or an immediate offset away.)
+  __device__ __forceinline__ char* at(int row, int byte) const { return p + row * W + ((uint32_t)byte ^ la_flip<W>(row)); }
   // Eight columns from 8 u.
   __device__ __forceinline__ bf16x8_t op(int row, int u) const { return *reinterpret_cast<const bf16x8_t*>(at(row, 16 * u)); }
   // Columns c .. c + 3 and c + 16 .. c + 19 (c a multiple of 4).
@@ -66,8 +73,6 @@ struct LaRows {
   }
   __device__ __forceinline__ uint2 four(int row, int c) const { return *reinterpret_cast<const uint2*>(at(row, 2 * c)); }
 };
-
-__device__ __forceinline__ bf16x8_t la_op(const uint16_t* p) { return *reinterpret_cast<const bf16x8_t*>(p); }
 
 // A wavefront's load of 64 x 16 bytes to LDS: lane l's come from base + off and go
 // to `to` + 16 l.  (Of lanes that are off, nothing is written.)  Completion is the
@@ -179,7 +184,6 @@ constexpr int kWalkDk = 3;      // ... of dk: Z = k
 // chunk's start; A and Z, which only the first phase reads, from its middle.
 template <int C, int KIND>
 struct LaTile {
-  static constexpr int SW = kLaQ + 8;
   static constexpr bool kOut = KIND != kWalkState;
   static constexpr bool kZ = KIND == kWalkDq || KIND == kWalkDk;
   static constexpr int kBlk = kLaQ / 16;
@@ -188,7 +192,7 @@ struct LaTile {
   char X[2][kLaQ * 128] __attribute__((aligned(1024)));
   char A[kOut ? kLaQ * 2 * C : 16] __attribute__((aligned(1024)));
   char Z[kZ ? kLaQ * 128 : 16] __attribute__((aligned(1024)));
-  uint16_t W[2][kOut ? kLaQ * SW : 8] __attribute__((aligned(16)));   // hi, lo
+  char W[2][kOut ? kLaQ * 64 : 16] __attribute__((aligned(16)));   // hi, lo
   float cum[kRing][kLaQ] __attribute__((aligned(16)));   // log2 decay summed from the chunk's first step, inclusive
   float low[kRing][kLaQ] __attribute__((aligned(16)));   // what it lacks of the 64-bit sum
   float row[kRing][kLaQ];                                // factor of A S^T
@@ -242,9 +246,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   constexpr int kPer = 1024 / (2 * C);        // rows of A and B per load
   // lane l of load r: row, and the source's byte in it
   auto wide_row = [&](int r) SSM_INLINE { return (w * NR + r) * kPer + l / (64 / kPer); };
-  auto wide_byte = [&](int r) SSM_INLINE { return (uint32_t)(l % (64 / kPer)) * 16u ^ la_flip(wide_row(r)); };
+  auto wide_byte = [&](int r) SSM_INLINE { return (uint32_t)(l % (64 / kPer)) * 16u ^ la_flip<2 * C>(wide_row(r)); };
   const int xrow = 8 * w + l / 8;
-  const uint32_t xbyte = (uint32_t)(l % 8) * 16u ^ la_flip(xrow);
+  const uint32_t xbyte = (uint32_t)(l % 8) * 16u ^ la_flip<128>(xrow);
   const bool xin = (int)xbyte < 2 * xdim;
   uint32_t offA[kOut ? NR : 1], offB[NR], offX, offZ = 0u;
   auto set_offsets = [&](int nt) SSM_INLINE {
@@ -350,7 +354,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     // W's block beyond the triangle
     for (int e = tid; e < 2 * 256; e += 256) {
       const int k = e >> 8, i = (e >> 4) & 15, j = e & 15;
-      s.W[k][(i + (REV ? 16 : 0)) * T::SW + j + (REV ? 0 : 16)] = 0;
+      *reinterpret_cast<uint16_t*>(LaRows<64>{s.W[k]}.at(i + (REV ? 16 : 0), 2 * (j + (REV ? 0 : 16)))) = 0;
     }
   }
   block_sync();
@@ -442,8 +446,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
           v[r] = (REV ? j0 + r >= i : j0 + r <= i) ? acc[r] * d : 0.0f;
         }
         const LaSplit<2> s0 = la_split<2>(v[0], v[1]), s1 = la_split<2>(v[2], v[3]);
-        *reinterpret_cast<uint2*>(&s.W[0][i * T::SW + j0]) = make_uint2(s0.t[0], s1.t[0]);
-        *reinterpret_cast<uint2*>(&s.W[1][i * T::SW + j0]) = make_uint2(s0.t[1], s1.t[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) *reinterpret_cast<uint2*>(LaRows<64>{s.W[e]}.at(i, 2 * j0)) = make_uint2(s0.t[e], s1.t[e]);
         if constexpr (KIND == kWalkDq) {
           // M = W o (q k^T) below the diagonal, over this slice's columns of q
           // and k: its row and column sums, in fp32 from exact products
@@ -547,7 +551,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) accY[n] = la_mfma(xo, la_op(&s.W[e][(16 * n + lr) * T::SW + 8 * q]), accY[n]);
+        for (int n = 0; n < NB; ++n) accY[n] = la_mfma(xo, LaRows<64>{s.W[e]}.op(16 * n + lr, q), accY[n]);
     }
     bf16x8_t xs[3];
     {
