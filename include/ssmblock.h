@@ -210,7 +210,8 @@ ssm_status ssm_linattn_state_update(const float* state, float* state_out, const 
  *   bias   : [n] fp32, or NULL;   out: [m, n] in out_dtype
  * group is 32, 64 or 128 and divides k; n, k < 2^31.  Any m; the kernel is made
  * for up to about 64 rows, past which the codes are read again for every 64 (fp32
- * x: 21).  Sums are fp32; x enters the matrix cores exactly (fp32 as three bf16
+ * x: 21).  Above 16 rows (5) x is laid out in a workspace of about 2 m k bytes (6) on
+ * `stream`.  Sums are fp32; x enters the matrix cores exactly (fp32 as three bf16
  * terms).  A value of x that is not finite makes its row's outputs NaN.  With
  * k = 0, out is the bias (or 0).
  */

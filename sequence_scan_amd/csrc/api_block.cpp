@@ -797,7 +797,19 @@ ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, con
   a.scale_bf16 = scale_dtype == SSM_BF16;
   a.out_bf16 = out_dtype == SSM_BF16;
   a.cus = device_simds() / 4;
-  const hipError_t e = ssm::launch_q4(a, static_cast<hipStream_t>(stream));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  void* ws = nullptr;
+  hipError_t e = hipSuccess;
+  if (const int64_t bytes = ssm::q4_image_bytes(a)) {
+    e = ws_alloc(&ws, bytes, s);
+    if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)bytes, e);
+    a.image = static_cast<char*>(ws);
+  }
+  e = ssm::launch_q4(a, s);
+  if (ws) {
+    const hipError_t e2 = hipFreeAsync(ws, s);
+    if (e == hipSuccess) e = e2;
+  }
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return ok();
 }

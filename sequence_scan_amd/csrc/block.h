@@ -146,9 +146,12 @@ struct Q4Args {
   int32_t m, n, k, group;
   int32_t x_bf16, scale_bf16, out_bf16;
   int32_t cus;
+  char* image;                // q4_image_bytes bytes of workspace, 16-byte aligned
   int32_t rows_per;           // set by the launcher: rows of x per workgroup
+  int32_t terms;              // ... bf16 terms of x
 };
 
+int64_t q4_image_bytes(const Q4Args& a);
 hipError_t launch_q4(const Q4Args& a, hipStream_t s);
 // groups: n * k / group.
 hipError_t launch_q4_quantize(const void* w, bool w_bf16, uint8_t* codes, void* scales, bool scale_bf16, uint8_t* zeros,

@@ -31,7 +31,7 @@
 #define SSMSCAN_LINATTN_KERNEL_H
 
 #include "block.h"
-#include "device.h"
+#include "lds_load.h"
 
 namespace ssm {
 namespace {
@@ -73,23 +73,6 @@ struct LaRows {
   }
   __device__ __forceinline__ uint2 four(int row, int c) const { return *reinterpret_cast<const uint2*>(at(row, 2 * c)); }
 };
-
-// A wavefront's load of 64 x 16 bytes to LDS: lane l's come from base + off and go
-// to `to` + 16 l.  (Of lanes that are off, nothing is written.)  Completion is the
-// wavefront's to wait for: la_loaded(), then a barrier.  Written as an
-// instruction: of the compiler's own form every later LDS read waits, which
-// would serialise a chunk's loads with the arithmetic of the one before.
-__device__ __forceinline__ void la_load_lds(const char* base, uint32_t off, void* to) {
-  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)static_cast<char*>(to);
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %1, %2"
-      :
-      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
-      : "memory");   // (m0 is a scratch register: whoever needs it sets it)
-}
-__device__ __forceinline__ void la_loaded() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Transposing read: within 16 lanes, lane i gets element i % 4 of the 8-byte
 // pieces addressed by lanes 4 e + i / 4, e = 0..3.
@@ -266,8 +249,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   auto load_bx = [&](int to) SSM_INLINE {
 #pragma unroll
     for (int r = 0; r < NR; ++r)
-      if ((int)wide_byte(r) < 2 * a.cdim) la_load_lds(nB, offB[r], &s.B[to][(w * NR + r) * 1024]);
-    if (xin) la_load_lds(nX, offX, &s.X[to][w * 1024]);
+      if ((int)wide_byte(r) < 2 * a.cdim) load_lds(nB, offB[r], &s.B[to][(w * NR + r) * 1024]);
+    if (xin) load_lds(nX, offX, &s.X[to][w * 1024]);
     nB += hop(a.B);
     nX += hop(a.X);
   };
@@ -275,11 +258,11 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     if constexpr (kOut) {
 #pragma unroll
       for (int r = 0; r < NR; ++r)
-        if ((int)wide_byte(r) < 2 * a.cdim) la_load_lds(nA, offA[r], &s.A[(w * NR + r) * 1024]);
+        if ((int)wide_byte(r) < 2 * a.cdim) load_lds(nA, offA[r], &s.A[(w * NR + r) * 1024]);
       nA += hop(a.A);
     }
     if constexpr (kZ) {
-      if (xin) la_load_lds(nZ, offZ, &s.Z[w * 1024]);
+      if (xin) load_lds(nZ, offZ, &s.Z[w * 1024]);
       nZ += hop(a.Z);
     }
   };
@@ -365,7 +348,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   get_decays(0);
   sum_decays(0);
   if (chunks > 8) get_decays(8);
-  la_loaded();
+  loaded<0>();
   block_sync();
 
   f32x4_t accY[kOut ? NB : 1];
@@ -381,7 +364,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
         using To = decltype(type);
         char* const to = reinterpret_cast<char*>(static_cast<To*>(a.out) + o0);
         const uint32_t rowb = (uint32_t)a.nheads * (uint32_t)a.xdim * (uint32_t)sizeof(To);
-        const uint32_t at = (uint32_t)lr * rowb + (uint32_t)py * (uint32_t)sizeof(To);
+        uint32_t lane = (uint32_t)lr;
+        asm("" : "+v"(lane));   // (the offset is formed anew, not held through the chunk)
+        const uint32_t at = lane * rowb + (uint32_t)py * (uint32_t)sizeof(To);
 #pragma unroll
         for (int n = 0; n < NB; ++n)
           if (nt == kLaQ || 16 * n + lr < nt) {
@@ -600,7 +585,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
         }
       }
     }
-    la_loaded();
+    loaded<0>();
     block_sync();
   }
   if constexpr (kOut) {

@@ -19,12 +19,17 @@
 // 32 codes of one row, so 16 rows x 128 codes per load.  For groups below 128
 // the four lanes of a row exchange words (a 4 x 4 transpose by row swaps), which
 // makes every product cover 32 consecutive codes, one group's; for groups of
-// 128 the order does not matter and x is read in the same order instead.  Loads
-// of the next slab are issued before the current one's arithmetic.
+// 128 the order does not matter and x is read in the same order instead.
+//
+// Two forms.  Up to 16 rows of x (its terms counted) every workgroup rounds, orders
+// and sums its slab of x itself (q4_kernel).  Above, that would cost each of
+// them as much as its products, so a small kernel lays x out once
+// (q4_rows_kernel) as the LDS images of all slabs, and the workgroups load them
+// straight to LDS, a slab ahead, and the codes three slabs ahead (q4_wide_kernel).
 #include <algorithm>
 
 #include "block.h"
-#include "device.h"
+#include "lds_load.h"
 
 namespace ssm {
 namespace {
@@ -53,9 +58,40 @@ __device__ __forceinline__ u32x4_t q4_transpose(u32x4_t w) {
 // Rows of x that MT tiles of 16 hold: all of them in bf16, a third in fp32.
 constexpr int q4_rows(int mt, bool xf32) { return xf32 ? 16 * mt / 3 : 16 * mt; }
 
-// MT: 16-row tiles of x (its terms counted as rows).
-template <int MT, int GROUP, int NH, bool XF32>
-__global__ void __launch_bounds__(kThreads, MT <= 2 ? 4 : 2) q4_kernel(Q4Args a) {
+// The codes' pair order of eight consecutive bf16.
+__device__ __forceinline__ u32x4_t q4_pairs(u32x4_t p) {
+  return u32x4_t{__builtin_amdgcn_perm(p[2], p[0], 0x05040100u), __builtin_amdgcn_perm(p[2], p[0], 0x07060302u),
+                 __builtin_amdgcn_perm(p[3], p[1], 0x05040100u), __builtin_amdgcn_perm(p[3], p[1], 0x07060302u)};
+}
+
+// Eight values of a row of x: their sum over the group's lanes (a lane holds
+// eight consecutive k), and per term the bf16 operand (f keeps the rest).
+template <int GROUP>
+__device__ __forceinline__ float q4_group_sum(const float* f) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum += f[e];
+  sum += SSM_DPP(0.0f, sum, 0xB1, 0xf);                                // quad_perm [1,0,3,2]
+  sum += SSM_DPP(0.0f, sum, 0x4E, 0xf);                                // quad_perm [2,3,0,1]
+  if constexpr (GROUP >= 64) sum += SSM_DPP(0.0f, sum, 0x141, 0xf);    // row_half_mirror
+  if constexpr (GROUP >= 128) sum += SSM_DPP(0.0f, sum, 0x140, 0xf);   // row_mirror
+  return sum;
+}
+__device__ __forceinline__ u32x4_t q4_term(float* f) {
+  u32x4_t p;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    p[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+    f[2 * e] -= __uint_as_float(p[e] << 16);
+    f[2 * e + 1] -= __uint_as_float(p[e] & 0xffff0000u);
+  }
+  return q4_pairs(p);
+}
+
+// Up to 16 rows of x, its terms counted.
+template <int GROUP, int NH, bool XF32>
+__global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
+  constexpr int MT = 1;
   constexpr int kTerms = XF32 ? 3 : 1;
   constexpr int KQ = kWaves / NH;            // 128-wide pieces of a slab
   constexpr int kSlab = 128 * KQ;
@@ -129,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 4 : 2) q4_kernel(Q4Args a)
       const int v = tid + kThreads * i;
       const int row = v / kVec, c = v % kVec;
       if (row < mrows) {     // whole wavefronts: a row is one or two of them
-        float f[8], sum = 0.0f;
+        float f[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (XF32) {
@@ -140,30 +176,11 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 4 : 2) q4_kernel(Q4Args a)
             f[2 * e + 1] = __uint_as_float(xv[i][0][e] & 0xffff0000u);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += f[e];
-        sum += SSM_DPP(0.0f, sum, 0xB1, 0xf);                                // quad_perm [1,0,3,2]
-        sum += SSM_DPP(0.0f, sum, 0x4E, 0xf);                                // quad_perm [2,3,0,1]
-        if constexpr (GROUP >= 64) sum += SSM_DPP(0.0f, sum, 0x141, 0xf);    // row_half_mirror
-        if constexpr (GROUP >= 128) sum += SSM_DPP(0.0f, sum, 0x140, 0xf);   // row_mirror
+        const float sum = q4_group_sum<GROUP>(f);
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {
-          u32x4_t p;
-          if constexpr (XF32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
-              f[2 * e] -= __uint_as_float(p[e] << 16);
-              f[2 * e + 1] -= __uint_as_float(p[e] & 0xffff0000u);
-            }
-          } else {
-            p = xv[i][0];
-          }
-          // the codes' pair order
-          const u32x4_t o = {__builtin_amdgcn_perm(p[2], p[0], 0x05040100u), __builtin_amdgcn_perm(p[2], p[0], 0x07060302u),
-                             __builtin_amdgcn_perm(p[3], p[1], 0x05040100u), __builtin_amdgcn_perm(p[3], p[1], 0x07060302u)};
           const int to = t * mrows + row;      // terms of one row lie mrows apart
-          *reinterpret_cast<u32x4_t*>(&s.x[to * SX + c * 8]) = o;
+          *reinterpret_cast<u32x4_t*>(&s.x[to * SX + c * 8]) = XF32 ? q4_term(f) : q4_pairs(xv[i][0]);
           if (c % (GROUP / 8) == 0) s.sum[c / (GROUP / 8)][to] = t == 0 ? sum : 0.0f;
         }
       }
@@ -254,6 +271,223 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 4 : 2) q4_kernel(Q4Args a)
   }
 }
 
+// ---------------------------------------------------------- more rows than 16
+
+constexpr int kWideSlab = 512, kWideCols = 64, kWideSplit = 4;   // k, columns, pieces of a slab
+
+// A slab's LDS image: `live` rows of 1024 bytes, 16-byte unit u of row r at
+// position u ^ (r & 15) (then 16 rows' reads of one unit use all banks), and the
+// groups' sums [kG][kRows], padded to 1024 bytes.
+template <int MT, int GROUP>
+struct Q4Image {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kG = kWideSlab / GROUP;
+  static constexpr int kSums = (kG * kRows * 4 + 1023) / 1024;      // units of 1024 bytes
+  static __host__ __device__ int64_t bytes(int live) { return (int64_t)(live + kSums) * 1024; }
+};
+
+// One vector of eight k per thread, a wavefront per row and slab: x's terms in the
+// codes' order and the sums, zero past k.  grid: slabs, rows of x, blocks of rows.
+template <int MT, int GROUP, bool XF32>
+__global__ void __launch_bounds__(64) q4_rows_kernel(Q4Args a) {
+  using I = Q4Image<MT, GROUP>;
+  constexpr int kTerms = XF32 ? 3 : 1;
+  const int l = threadIdx.x, slab = blockIdx.x, row = blockIdx.y;
+  const int m0 = (int)blockIdx.z * a.rows_per;
+  const int mrows = min(a.rows_per, a.m - m0);
+  if (row >= mrows) return;
+  const int64_t image = I::bytes(a.rows_per * kTerms);     // one size for all blocks
+  char* to = a.image + ((int64_t)blockIdx.z * gridDim.x + slab) * image;
+  const int live = mrows * kTerms;
+  const int k = slab * kWideSlab + 8 * l;
+  float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4_t p = {0u, 0u, 0u, 0u};
+  if (k < a.k) {
+    const int64_t at = (int64_t)(m0 + row) * a.x_row + k;
+    if constexpr (XF32) {
+      const float4 v0 = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + at);
+      const float4 v1 = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + at + 4);
+      f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
+      f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
+    } else {
+      p = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(p[e] << 16);
+        f[2 * e + 1] = __uint_as_float(p[e] & 0xffff0000u);
+      }
+    }
+  }
+  const float sum = q4_group_sum<GROUP>(f);
+  float* const sums = reinterpret_cast<float*>(to + (int64_t)live * 1024);
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    const int r = t * mrows + row;
+    *reinterpret_cast<u32x4_t*>(to + (int64_t)r * 1024 + 16 * (l ^ (r & 15))) = XF32 ? q4_term(f) : q4_pairs(p);
+    if (l % (GROUP / 8) == 0) sums[l / (GROUP / 8) * I::kRows + r] = t == 0 ? sum : 0.0f;
+  }
+}
+
+template <int MT, int GROUP>
+__global__ void __launch_bounds__(kThreads, 2) q4_wide_kernel(Q4Args a) {
+  using I = Q4Image<MT, GROUP>;
+  constexpr int kRows = I::kRows, kG = I::kG;
+  constexpr int NS = kWideCols * kG / kThreads;     // scales per thread
+  static_assert(NS * kThreads == kWideCols * kG || kWideCols * kG < kThreads, "scales fill the workgroup");
+  constexpr int kS = NS > 0 ? NS : 1;
+  struct Lds {
+    char x[2][(kRows + I::kSums) * 1024] __attribute__((aligned(1024)));
+    float2 sc[2][kG][kWideCols];                    // scale, 16 + zero
+  };
+  constexpr int kJoin = kWideSplit * kRows * (kWideCols + 1) * 4;
+  static_assert(sizeof(Lds) >= kJoin, "the join fits the slabs' place");
+  __shared__ Lds s;
+
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nh = w & 1, kq = w >> 1;
+  const int lr = l & 15, q = l >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * kWideCols;
+  const int m0 = (int)blockIdx.y * a.rows_per;
+  const int mrows = min(a.rows_per, a.m - m0);
+  const int live = mrows * a.terms;
+  const int groups = a.k / GROUP;
+  const int slabs = (a.k + kWideSlab - 1) / kWideSlab;
+  const int64_t kb = a.k / 2;
+  const int64_t image = I::bytes(a.rows_per * a.terms);
+  const char* img = a.image + (int64_t)blockIdx.y * slabs * image;
+
+  const uint8_t* cw[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) cw[t] = a.codes + min(n0 + 32 * nh + 16 * t + lr, (int64_t)a.n - 1) * kb;
+  auto get_codes = [&](int slab, u32x4_t (&c)[2]) SSM_INLINE {
+    const int64_t off = min(slab * kWideSlab + 128 * kq + 32 * q, a.k - 32) / 2;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) c[t] = *reinterpret_cast<const u32x4_t*>(cw[t] + off);
+  };
+  const int units = live + I::kSums;
+  auto load_image = [&](int slab, int to) SSM_INLINE {
+    const char* from = img + slab * image;
+    for (int u = w; u < units; u += kWaves) load_lds(from + u * 1024, 16u * l, &s.x[to][u * 1024]);
+  };
+  const int sc_col = tid / kG, sc_g = tid % kG;     // (several per thread: kThreads / kG columns apart)
+  float sv[kS];
+  int zv[kS];
+  auto get_scales = [&](int slab) SSM_INLINE {
+#pragma unroll
+    for (int i = 0; i < kS; ++i) {
+      const int64_t at = min(n0 + min(sc_col + i * (kThreads / kG), kWideCols - 1), (int64_t)a.n - 1) * groups +
+                         min(slab * kG + sc_g, groups - 1);
+      sv[i] = a.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.scales)[at]) : static_cast<const float*>(a.scales)[at];
+      zv[i] = a.zeros != nullptr ? a.zeros[at] : 8;
+    }
+  };
+  auto put_scales = [&](int to) SSM_INLINE {
+#pragma unroll
+    for (int i = 0; i < kS; ++i) {
+      const int c = sc_col + i * (kThreads / kG);
+      if (c < kWideCols) s.sc[to][sc_g][c] = make_float2(sv[i], (float)(16 + zv[i]));
+    }
+  };
+
+  f32x4_t acc[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  int xrow[MT];      // this lane's rows of x in LDS; rows past the last repeat it
+#pragma unroll
+  for (int m = 0; m < MT; ++m) xrow[m] = min(16 * m + lr, live - 1);
+
+  u32x4_t code[3][2];
+  load_image(0, 0);
+  get_scales(0);
+  put_scales(0);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) get_codes(i, code[i]);
+  loaded<6>();
+  block_sync();
+  for (int slab = 0; slab < slabs; ++slab) {
+    const int cur = slab & 1;
+    // This slab's codes are taken out of their loads before the next slab's loads
+    // are issued, which the wait for them would otherwise include.
+    u32x4_t c[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      c[t] = GROUP < 128 ? q4_transpose(code[0][t]) : code[0][t];
+      asm volatile("" : "+v"(c[t]));
+      code[0][t] = code[1][t];
+      code[1][t] = code[2][t];
+    }
+    const bool more = slab + 1 < slabs;
+    if (more) {
+      load_image(slab + 1, cur ^ 1);
+      get_scales(slab + 1);
+    }
+    get_codes(slab + 3, code[2]);
+    const char* const tile = s.x[cur];
+    const float* const sums = reinterpret_cast<const float*>(tile + live * 1024);
+    f32x4_t d[MT][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      constexpr int kPer = GROUP / 32;
+      const int u = 16 * kq + (GROUP < 128 ? 4 * j + q : 4 * q + j);     // unit of this lane's eight k
+      bf16x8_t xo[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        xo[m] = *reinterpret_cast<const bf16x8_t*>(tile + xrow[m] * 1024 + 16 * (u ^ (xrow[m] & 15)));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const bf16x8_t wo = q4_decode(c[t][j]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (j % kPer == 0) d[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          d[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo[m], wo, d[m][t], 0, 0, 0);
+        }
+      }
+      if (j % kPer == kPer - 1) {
+        const int g = 128 * kq / GROUP + j / kPer;
+        float2 sc[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) sc[t] = s.sc[cur][g][32 * nh + 16 * t + lr];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(&sums[g * kRows + 16 * m + 4 * q]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][t][r] = __builtin_fmaf(sc[t].x, __builtin_fmaf(-sc[t].y, xs[r], d[m][t][r]), acc[m][t][r]);
+        }
+      }
+    }
+    if (more) put_scales(cur ^ 1);
+    loaded<2>();       // all but this slab's two loads of codes
+    block_sync();
+  }
+
+  float(*part)[kRows][kWideCols + 1] = reinterpret_cast<float(*)[kRows][kWideCols + 1]>(&s);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[kq][16 * m + 4 * q + r][32 * nh + 16 * t + lr] = acc[m][t][r];
+  block_sync();
+  for (int e = tid; e < mrows * kWideCols; e += kThreads) {
+    const int m = e / kWideCols, c = e % kWideCols;
+    if (n0 + c >= a.n) continue;
+    float y = 0.0f;
+    for (int t = 0; t < a.terms; ++t)
+#pragma unroll
+      for (int k = 0; k < kWideSplit; ++k) y += part[k][t * mrows + m][c];
+    if (a.bias != nullptr) y += a.bias[n0 + c];
+    const int64_t at = (int64_t)(m0 + m) * a.n + n0 + c;
+    if (a.out_bf16) Io<uint16_t>::store(a.out, at, y);
+    else Io<float>::store(a.out, at, y);
+  }
+}
+
 // One group per thread: scale = (max - min) / 15 over the group's values and 0,
 // rounded to the scales' type; zero = the code of 0; codes to the nearest step.
 template <typename Tw>
@@ -290,35 +524,72 @@ __global__ void __launch_bounds__(256) q4_quantize_kernel(const Tw* w, uint8_t* 
   }
 }
 
-template <int GROUP, bool XF32>
-void launch_q4_g(const Q4Args& a, int mt, int nh, dim3 grid, hipStream_t s) {
-  if (mt == 1 && nh == 1) hipLaunchKernelGGL((q4_kernel<1, GROUP, 1, XF32>), grid, dim3(kThreads), 0, s, a);
-  else if (mt == 1) hipLaunchKernelGGL((q4_kernel<1, GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
-  else if (mt == 2) hipLaunchKernelGGL((q4_kernel<2, GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
-  else if (mt == 3) hipLaunchKernelGGL((q4_kernel<3, GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((q4_kernel<4, GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
+// 16-row tiles of x for a call of m rows, and rows of x per workgroup.
+struct Q4Shape {
+  int mt, rows_per, terms, slabs, blocks;
+};
+Q4Shape q4_shape(const Q4Args& a) {
+  Q4Shape h{1, 0, a.x_bf16 ? 1 : 3, 0, 0};
+  while (h.mt < 4 && q4_rows(h.mt, !a.x_bf16) < a.m) ++h.mt;
+  h.rows_per = std::min(a.m, q4_rows(h.mt, !a.x_bf16));
+  h.slabs = (a.k + kWideSlab - 1) / kWideSlab;
+  h.blocks = (a.m + h.rows_per - 1) / h.rows_per;
+  return h;
 }
 
-template <bool XF32>
-void launch_q4_x(const Q4Args& args, hipStream_t s) {
+template <int GROUP, bool XF32>
+void launch_q4_x(const Q4Args& args, const Q4Shape& h, hipStream_t s) {
   Q4Args a = args;
-  int mt = 1;
-  while (mt < 4 && q4_rows(mt, XF32) < a.m) ++mt;
-  a.rows_per = q4_rows(mt, XF32);
-  // 64 columns per workgroup where that gives every CU one, or where several
-  // tiles of x have to be shared by as many columns as possible; else 32
-  const int nh = mt == 1 && (int64_t)a.n < 64ll * a.cus ? 1 : 2;
-  const dim3 grid((unsigned)((a.n + 32 * nh - 1) / (32 * nh)), (unsigned)((a.m + a.rows_per - 1) / a.rows_per));
-  if (a.group == 32) launch_q4_g<32, XF32>(a, mt, nh, grid, s);
-  else if (a.group == 64) launch_q4_g<64, XF32>(a, mt, nh, grid, s);
-  else launch_q4_g<128, XF32>(a, mt, nh, grid, s);
+  a.rows_per = h.rows_per;
+  a.terms = h.terms;
+  if (h.mt == 1 || a.k == 0) {
+    // 64 columns per workgroup where that gives every CU one, else 32
+    if (h.mt == 1) a.rows_per = q4_rows(1, XF32);
+    const int nh = (int64_t)a.n < 64ll * a.cus ? 1 : 2;
+    const dim3 grid((unsigned)((a.n + 32 * nh - 1) / (32 * nh)), (unsigned)((a.m + a.rows_per - 1) / a.rows_per));
+    if (nh == 1) hipLaunchKernelGGL((q4_kernel<GROUP, 1, XF32>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((q4_kernel<GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
+    return;
+  }
+  const dim3 rows((unsigned)h.slabs, (unsigned)h.rows_per, (unsigned)h.blocks);
+  const dim3 grid((unsigned)((a.n + kWideCols - 1) / kWideCols), (unsigned)h.blocks);
+  auto run = [&](auto mt) {
+    constexpr int MT = decltype(mt)::value;
+    hipLaunchKernelGGL((q4_rows_kernel<MT, GROUP, XF32>), rows, dim3(64), 0, s, a);
+    hipLaunchKernelGGL((q4_wide_kernel<MT, GROUP>), grid, dim3(kThreads), 0, s, a);
+  };
+  if (h.mt == 2) run(std::integral_constant<int, 2>());
+  else if (h.mt == 3) run(std::integral_constant<int, 3>());
+  else run(std::integral_constant<int, 4>());
+}
+
+template <int GROUP>
+int64_t image_bytes(const Q4Shape& h) {
+  const int64_t live = (int64_t)h.rows_per * h.terms;
+  const int64_t one = h.mt == 2 ? Q4Image<2, GROUP>::bytes((int)live)
+                      : h.mt == 3 ? Q4Image<3, GROUP>::bytes((int)live) : Q4Image<4, GROUP>::bytes((int)live);
+  return one * h.slabs * h.blocks;
 }
 
 }  // namespace
 
+int64_t q4_image_bytes(const Q4Args& a) {
+  const Q4Shape h = q4_shape(a);
+  if (h.mt == 1 || a.k == 0) return 0;
+  return a.group == 32 ? image_bytes<32>(h) : a.group == 64 ? image_bytes<64>(h) : image_bytes<128>(h);
+}
+
 hipError_t launch_q4(const Q4Args& a, hipStream_t s) {
-  if (a.x_bf16) launch_q4_x<false>(a, s);
-  else launch_q4_x<true>(a, s);
+  const Q4Shape h = q4_shape(a);
+  if (a.x_bf16) {
+    if (a.group == 32) launch_q4_x<32, false>(a, h, s);
+    else if (a.group == 64) launch_q4_x<64, false>(a, h, s);
+    else launch_q4_x<128, false>(a, h, s);
+  } else {
+    if (a.group == 32) launch_q4_x<32, true>(a, h, s);
+    else if (a.group == 64) launch_q4_x<64, true>(a, h, s);
+    else launch_q4_x<128, true>(a, h, s);
+  }
   return hipGetLastError();
 }
 
