@@ -12,20 +12,25 @@
 // does.  fp32 x enters as three bf16 terms, as rows of their own that the
 // epilogue adds (all 24 bits).
 //
-// A workgroup of eight wavefronts owns 32 NH columns of W and all of K.  It takes
-// K in slabs; x's slab, the groups' sums and the slab's scales go through LDS,
-// shared by the wavefronts, which split the slab into 128-wide pieces (and the
-// columns in NH parts of 32).  Codes go from HBM to registers, 16 bytes per lane:
-// 32 codes of one row, so 16 rows x 128 codes per load.  For groups below 128
-// the four lanes of a row exchange words (a 4 x 4 transpose by row swaps), which
-// makes every product cover 32 consecutive codes, one group's; for groups of
-// 128 the order does not matter and x is read in the same order instead.
+// Codes go from HBM to registers, 16 bytes per lane: 32 codes of one row, so 16
+// rows x 128 codes (a "piece") per load of a wavefront.  For groups below 128 the
+// four lanes of a row exchange words (a 4 x 4 transpose by row swaps), which makes
+// every product cover 32 consecutive codes, one group's; for groups of 128 the
+// order does not matter and x is read in the same order instead.  A workgroup owns
+// some columns of out and all of K; its wavefronts split K in pieces and are joined
+// in order at the end (no atomics: a call gives the same bits every time).
 //
-// Two forms.  Up to 16 rows of x (its terms counted) every workgroup rounds, orders
-// and sums its slab of x itself (q4_kernel).  Above, that would cost each of
-// them as much as its products, so a small kernel lays x out once
-// (q4_rows_kernel) as the LDS images of all slabs, and the workgroups load them
-// straight to LDS, a slab ahead, and the codes three slabs ahead (q4_wide_kernel).
+// Three forms.  Up to 16 rows of x (its terms counted) every workgroup rounds,
+// orders and sums x itself: all of it at once, where it fits (q4_fits_kernel), or in
+// slabs (q4_slabs_kernel).  Above, that would cost each of them as much as its
+// products, so a small kernel lays x out once (q4_rows_kernel) as the LDS images of
+// all slabs, and the workgroups load them straight to LDS, a slab ahead, and the
+// codes three slabs ahead (q4_wide_kernel).
+//
+// Measured: one row x 10576 x 2560 (13.5 MB of codes) 8.4 us, of which a launch and
+// the wait for the first bytes are about half; 48 rows x 16384 x 8192 37 us, where
+// the vector instructions that decode, address and scale are what bounds it (145
+// per wavefront and slab, half of the time, against 12 MFMA).
 #include <algorithm>
 
 #include "block.h"
@@ -64,6 +69,24 @@ __device__ __forceinline__ u32x4_t q4_pairs(u32x4_t p) {
                  __builtin_amdgcn_perm(p[3], p[1], 0x05040100u), __builtin_amdgcn_perm(p[3], p[1], 0x07060302u)};
 }
 
+// Eight values of x from element `at` on, as floats and (bf16) as they are.
+template <bool XF32>
+__device__ __forceinline__ void q4_x(const void* x, int64_t at, float* f, u32x4_t& p) {
+  if constexpr (XF32) {
+    const float4 v0 = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 v1 = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4);
+    f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
+    f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
+  } else {
+    p = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(x) + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(p[e] << 16);
+      f[2 * e + 1] = __uint_as_float(p[e] & 0xffff0000u);
+    }
+  }
+}
+
 // Eight values of a row of x: their sum over the group's lanes (a lane holds
 // eight consecutive k), and per term the bf16 operand (f keeps the rest).
 template <int GROUP>
@@ -88,10 +111,138 @@ __device__ __forceinline__ u32x4_t q4_term(float* f) {
   return q4_pairs(p);
 }
 
-// Up to 16 rows of x, its terms counted.
+// The same where all of x, its sums and the columns' scales fit the LDS (q4_fits):
+// one row of 2560, say.  They are staged once, and the wavefronts then walk their
+// pieces of K without a barrier, codes kAhead pieces ahead.  With slabs, such a
+// call would wait for memory once a slab, with little to do in between.
+constexpr int kFitsBytes = 64 * 1024;
+constexpr int kAhead = 4;
+
+// LDS: x [live][pieces * 128 + 8], sums [pieces * 128 / GROUP][16], scales
+// [..][16]; the join takes its place.
+struct Q4Fit {
+  int64_t x, sums, bytes;
+};
+inline __host__ __device__ Q4Fit q4_fit(int live, int k, int group) {
+  Q4Fit f;
+  const int64_t wide = (k + 127) / 128 * 128, groups = wide / group;
+  f.x = (int64_t)live * (wide + 8) * 2;
+  f.sums = f.x + groups * 16 * 4;
+  f.bytes = f.sums + groups * 16 * 8;
+  const int64_t join = (int64_t)kWaves * 16 * 17 * 4;
+  if (f.bytes < join) f.bytes = join;
+  return f;
+}
+
+template <int GROUP, bool XF32>
+__global__ void __launch_bounds__(kThreads, 4) q4_fits_kernel(Q4Args a) {
+  constexpr int kTerms = XF32 ? 3 : 1;
+  extern __shared__ __attribute__((aligned(16))) char raw[];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = l & 15, q = l >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int live = a.m * kTerms;                            // rows of LDS in use
+  const int groups = a.k / GROUP;
+  const int pieces = (a.k + 127) / 128;
+  const int wide = pieces * 128, SX = wide + 8;
+  const Q4Fit fit = q4_fit(live, a.k, GROUP);
+  uint16_t* const sx = reinterpret_cast<uint16_t*>(raw);
+  float* const ssum = reinterpret_cast<float*>(raw + fit.x);
+  float2* const ssc = reinterpret_cast<float2*>(raw + fit.sums);
+
+  // This lane's row of codes (a column of out); past n the last one again.  A
+  // wavefront's pieces are w, w + 8, ..; past its last it loads the row's end
+  // again.
+  const int mine = (pieces - w + kWaves - 1) / kWaves;
+  const uint8_t* const cw = a.codes + min(n0 + lr, (int64_t)a.n - 1) * (a.k / 2);
+  u32x4_t code[kAhead];
+  auto get_codes = [&](int i) SSM_INLINE {
+    return *reinterpret_cast<const u32x4_t*>(cw + min((w + kWaves * i) * 128 + 32 * q, a.k - 32) / 2);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) code[i] = get_codes(i);
+
+  // x, a vector of eight k per thread.  A row's vectors are a multiple of 16 (wide
+  // is one of 128), so the lanes that share a group's sum are in one row of x.
+  const int vecs = wide / 8;
+  for (int v = tid; v < a.m * vecs; v += kThreads) {
+    const int row = v / vecs, c = v % vecs;
+    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4_t p = {0u, 0u, 0u, 0u};
+    if (8 * c < a.k) q4_x<XF32>(a.x, (int64_t)row * a.x_row + 8 * c, f, p);
+    const float sum = q4_group_sum<GROUP>(f);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      const int to = t * a.m + row;
+      *reinterpret_cast<u32x4_t*>(&sx[to * SX + 8 * c]) = XF32 ? q4_term(f) : q4_pairs(p);
+      if (c % (GROUP / 8) == 0) ssum[c / (GROUP / 8) * 16 + to] = t == 0 ? sum : 0.0f;
+    }
+  }
+  for (int e = tid; e < 16 * groups; e += kThreads) {
+    const int c = e / groups, g = e % groups;
+    const int64_t at = min(n0 + c, (int64_t)a.n - 1) * groups + g;
+    const float sc = a.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.scales)[at]) : static_cast<const float*>(a.scales)[at];
+    ssc[g * 16 + c] = make_float2(sc, (float)(16 + (a.zeros != nullptr ? a.zeros[at] : 8)));
+  }
+  for (int e = 16 * groups + tid; e < 16 * (wide / GROUP); e += kThreads) ssc[e] = make_float2(0.0f, 0.0f);   // past k
+  block_sync();
+
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint16_t* const xrow = sx + min(lr, live - 1) * SX;     // rows past the last repeat it
+  for (int i0 = 0; i0 < mine; i0 += kAhead) {
+#pragma unroll
+    for (int ii = 0; ii < kAhead; ++ii) {
+      const int i = i0 + ii;
+      if (i >= mine) break;
+      const u32x4_t c = GROUP < 128 ? q4_transpose(code[ii]) : code[ii];
+      if (i + kAhead < mine) code[ii] = get_codes(i + kAhead);
+      const int piece = w + kWaves * i;
+      f32x4_t d;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        constexpr int kPer = GROUP / 32;       // products per group
+        // product j's codes of lane row q: 32 j + 8 q + 0..7 of the piece (groups
+        // of 128: 32 q + 8 j + 0..7)
+        const bf16x8_t xo = *reinterpret_cast<const bf16x8_t*>(xrow + 128 * piece + (GROUP < 128 ? 32 * j + 8 * q : 32 * q + 8 * j));
+        if (j % kPer == 0) d = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, q4_decode(c[j]), d, 0, 0, 0);
+        if (j % kPer == kPer - 1) {
+          const int g = (128 / GROUP) * piece + j / kPer;
+          const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(&ssum[g * 16 + 4 * q]);
+          const float2 sc = ssc[g * 16 + lr];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(sc.x, __builtin_fmaf(-sc.y, xs[r], d[r]), acc[r]);
+        }
+      }
+    }
+  }
+  block_sync();
+  // Join the wavefronts' parts, in order, and the terms of x.
+  float(*part)[16][17] = reinterpret_cast<float(*)[16][17]>(raw);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) part[w][4 * q + r][lr] = acc[r];
+  block_sync();
+  for (int e = tid; e < a.m * 16; e += kThreads) {
+    const int m = e / 16, c = e % 16;
+    if (n0 + c >= a.n) continue;
+    float y = 0.0f;
+    for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) y += part[k][t * a.m + m][c];
+    if (a.bias != nullptr) y += a.bias[n0 + c];
+    const int64_t at = (int64_t)m * a.n + n0 + c;
+    if (a.out_bf16) Io<uint16_t>::store(a.out, at, y);
+    else Io<float>::store(a.out, at, y);
+  }
+}
+
+// ----------------------------------------------- up to 16 rows, x in slabs
+//
+// x's slab, its sums and the slab's scales go through LDS, loaded a slab ahead
+// into registers; NH wavefronts share a piece, 32 columns each.
 template <int GROUP, int NH, bool XF32>
-__global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
-  constexpr int MT = 1;
+__global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
   constexpr int kTerms = XF32 ? 3 : 1;
   constexpr int KQ = kWaves / NH;            // 128-wide pieces of a slab
   constexpr int kSlab = 128 * KQ;
@@ -99,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
   constexpr int kVec = kSlab / 8;            // 16-byte vectors of an x row
   constexpr int SX = kSlab + 8;              // row stride of x in LDS
   constexpr int kG = kSlab / GROUP;          // groups of a slab
-  constexpr int kRows = 16 * MT;
-  constexpr int NX = (q4_rows(MT, XF32) * kVec + kThreads - 1) / kThreads;   // x vectors per thread
+  constexpr int kRows = 16;
+  constexpr int NX = (q4_rows(1, XF32) * kVec + kThreads - 1) / kThreads;   // x vectors per thread
   constexpr int NS = (kCols * kG + kThreads - 1) / kThreads;   // scales per thread
   struct Lds {
     uint16_t x[kRows * SX] __attribute__((aligned(16)));
@@ -192,11 +343,9 @@ __global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
     }
   };
 
-  f32x4_t acc[MT][2];
+  f32x4_t acc[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < 2; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   if (slabs > 0) issue(0);
   for (int slab = 0; slab < slabs; ++slab) {
     stage();
@@ -207,41 +356,27 @@ __global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) cur[t] = q4_transpose(cur[t]);
     }
-    f32x4_t d[MT][2];
+    f32x4_t d[2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       constexpr int kPer = GROUP / 32;       // products per group
       // product j's codes of lane row q: 32 j + 8 q + 0..7 of the piece (groups
       // of 128: 32 q + 8 j + 0..7)
       const int k = 128 * kq + (GROUP < 128 ? 32 * j + 8 * q : 32 * q + 8 * j);
-      bf16x8_t xo[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int row = min(16 * m + lr, live - 1);     // rows past the last repeat it
-        xo[m] = *reinterpret_cast<const bf16x8_t*>(&s.x[row * SX + k]);
-      }
+      const bf16x8_t xo = *reinterpret_cast<const bf16x8_t*>(&s.x[min(lr, live - 1) * SX + k]);   // (rows past the last repeat it)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const bf16x8_t wo = q4_decode(cur[t][j]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (j % kPer == 0) d[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          d[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo[m], wo, d[m][t], 0, 0, 0);
-        }
+        if (j % kPer == 0) d[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, q4_decode(cur[t][j]), d[t], 0, 0, 0);
       }
       if (j % kPer == kPer - 1) {
         const int g = 128 * kq / GROUP + j / kPer;
-        float2 sc[2];
+        const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(&s.sum[g][4 * q]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) sc[t] = s.sc[g][32 * nh + 16 * t + lr];
+        for (int t = 0; t < 2; ++t) {
+          const float2 sc = s.sc[g][32 * nh + 16 * t + lr];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(&s.sum[g][16 * m + 4 * q]);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[m][t][r] = __builtin_fmaf(sc[t].x, __builtin_fmaf(-sc[t].y, xs[r], d[m][t][r]), acc[m][t][r]);
+          for (int r = 0; r < 4; ++r) acc[t][r] = __builtin_fmaf(sc.x, __builtin_fmaf(-sc.y, xs[r], d[t][r]), acc[t][r]);
         }
       }
     }
@@ -251,11 +386,9 @@ __global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
   // Join the wavefronts' parts, in order, and the terms of x.
   float(*part)[kRows][kCols + 1] = reinterpret_cast<float(*)[kRows][kCols + 1]>(raw);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[kq][16 * m + 4 * q + r][32 * nh + 16 * t + lr] = acc[m][t][r];
+    for (int r = 0; r < 4; ++r) part[kq][4 * q + r][32 * nh + 16 * t + lr] = acc[t][r];
   block_sync();
   for (int e = tid; e < mrows * kCols; e += kThreads) {
     const int m = e / kCols, c = e % kCols;
@@ -274,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_kernel(Q4Args a) {
 // ---------------------------------------------------------- more rows than 16
 
 constexpr int kWideSlab = 512, kWideCols = 64, kWideSplit = 4;   // k, columns, pieces of a slab
+constexpr int kWideThreads = 64 * kWideSplit * (kWideCols / 16);   // a wavefront per piece and 16 columns
 
 // A slab's LDS image: `live` rows of 1024 bytes, 16-byte unit u of row r at
 // position u ^ (r & 15) (then 16 rows' reads of one unit use all banks), and the
@@ -302,22 +436,7 @@ __global__ void __launch_bounds__(64) q4_rows_kernel(Q4Args a) {
   const int k = slab * kWideSlab + 8 * l;
   float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   u32x4_t p = {0u, 0u, 0u, 0u};
-  if (k < a.k) {
-    const int64_t at = (int64_t)(m0 + row) * a.x_row + k;
-    if constexpr (XF32) {
-      const float4 v0 = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + at);
-      const float4 v1 = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + at + 4);
-      f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
-      f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
-    } else {
-      p = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + at);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[2 * e] = __uint_as_float(p[e] << 16);
-        f[2 * e + 1] = __uint_as_float(p[e] & 0xffff0000u);
-      }
-    }
-  }
+  if (k < a.k) q4_x<XF32>(a.x, (int64_t)(m0 + row) * a.x_row + k, f, p);
   const float sum = q4_group_sum<GROUP>(f);
   float* const sums = reinterpret_cast<float*>(to + (int64_t)live * 1024);
 #pragma unroll
@@ -329,11 +448,11 @@ __global__ void __launch_bounds__(64) q4_rows_kernel(Q4Args a) {
 }
 
 template <int MT, int GROUP>
-__global__ void __launch_bounds__(kThreads, 2) q4_wide_kernel(Q4Args a) {
+__global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
   using I = Q4Image<MT, GROUP>;
   constexpr int kRows = I::kRows, kG = I::kG;
-  constexpr int NS = kWideCols * kG / kThreads;     // scales per thread
-  static_assert(NS * kThreads == kWideCols * kG || kWideCols * kG < kThreads, "scales fill the workgroup");
+  constexpr int NS = kWideCols * kG / kWideThreads;     // scales per thread
+  static_assert(NS * kWideThreads == kWideCols * kG || kWideCols * kG < kWideThreads, "scales fill the workgroup");
   constexpr int kS = NS > 0 ? NS : 1;
   struct Lds {
     char x[2][(kRows + I::kSums) * 1024] __attribute__((aligned(1024)));
@@ -345,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_wide_kernel(Q4Args a) {
 
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nh = w & 1, kq = w >> 1;
+  const int nt = w & 3, kq = w >> 2;     // 16-column tile, piece of the slab
   const int lr = l & 15, q = l >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * kWideCols;
   const int m0 = (int)blockIdx.y * a.rows_per;
@@ -357,26 +476,28 @@ __global__ void __launch_bounds__(kThreads, 2) q4_wide_kernel(Q4Args a) {
   const int64_t image = I::bytes(a.rows_per * a.terms);
   const char* img = a.image + (int64_t)blockIdx.y * slabs * image;
 
-  const uint8_t* cw[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) cw[t] = a.codes + min(n0 + 32 * nh + 16 * t + lr, (int64_t)a.n - 1) * kb;
-  auto get_codes = [&](int slab, u32x4_t (&c)[2]) SSM_INLINE {
-    const int64_t off = min(slab * kWideSlab + 128 * kq + 32 * q, a.k - 32) / 2;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) c[t] = *reinterpret_cast<const u32x4_t*>(cw[t] + off);
+  // Workgroups start at different slabs: at one time their rows' codes then lie at
+  // different offsets, spread over the memory's channels.
+  const int first = (int)blockIdx.x % slabs;
+  auto slab_at = [&](int i) SSM_INLINE { return i + first < slabs ? i + first : i + first - slabs; };
+  const uint8_t* const cw = a.codes + min(n0 + 16 * nt + lr, (int64_t)a.n - 1) * kb;
+  auto get_codes = [&](int i) SSM_INLINE {
+    const int slab = slab_at(min(i, slabs - 1));
+    return *reinterpret_cast<const u32x4_t*>(cw + min(slab * kWideSlab + 128 * kq + 32 * q, a.k - 32) / 2);
   };
   const int units = live + I::kSums;
-  auto load_image = [&](int slab, int to) SSM_INLINE {
-    const char* from = img + slab * image;
-    for (int u = w; u < units; u += kWaves) load_lds(from + u * 1024, 16u * l, &s.x[to][u * 1024]);
+  auto load_image = [&](int i, int to) SSM_INLINE {
+    const char* from = img + slab_at(i) * image;
+    for (int u = w; u < units; u += kWideThreads / 64) load_lds(from + u * 1024, 16u * l, &s.x[to][u * 1024]);
   };
-  const int sc_col = tid / kG, sc_g = tid % kG;     // (several per thread: kThreads / kG columns apart)
+  const int sc_col = tid / kG, sc_g = tid % kG;     // (several per thread: kWideThreads / kG columns apart)
   float sv[kS];
   int zv[kS];
-  auto get_scales = [&](int slab) SSM_INLINE {
+  auto get_scales = [&](int n) SSM_INLINE {
+    const int slab = slab_at(n);
 #pragma unroll
     for (int i = 0; i < kS; ++i) {
-      const int64_t at = min(n0 + min(sc_col + i * (kThreads / kG), kWideCols - 1), (int64_t)a.n - 1) * groups +
+      const int64_t at = min(n0 + min(sc_col + i * (kWideThreads / kG), kWideCols - 1), (int64_t)a.n - 1) * groups +
                          min(slab * kG + sc_g, groups - 1);
       sv[i] = a.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.scales)[at]) : static_cast<const float*>(a.scales)[at];
       zv[i] = a.zeros != nullptr ? a.zeros[at] : 8;
@@ -385,96 +506,102 @@ __global__ void __launch_bounds__(kThreads, 2) q4_wide_kernel(Q4Args a) {
   auto put_scales = [&](int to) SSM_INLINE {
 #pragma unroll
     for (int i = 0; i < kS; ++i) {
-      const int c = sc_col + i * (kThreads / kG);
+      const int c = sc_col + i * (kWideThreads / kG);
       if (c < kWideCols) s.sc[to][sc_g][c] = make_float2(sv[i], (float)(16 + zv[i]));
     }
   };
 
-  f32x4_t acc[MT][2];
+  f32x4_t acc[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m) acc[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // This lane's operands of x in a slab: product j's, of row tile m, at
+  // at[m] ^ 64 j' (j' = j, or for groups of 128 its place within the unit's bits);
+  // rows past the last repeat it.
+  uint32_t at[MT];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  int xrow[MT];      // this lane's rows of x in LDS; rows past the last repeat it
-#pragma unroll
-  for (int m = 0; m < MT; ++m) xrow[m] = min(16 * m + lr, live - 1);
+  for (int m = 0; m < MT; ++m) {
+    const int row = min(16 * m + lr, live - 1);
+    at[m] = (uint32_t)(row * 1024 + 16 * ((16 * kq + (GROUP < 128 ? q : 4 * q)) ^ (row & 15)));
+  }
+  uint32_t sum_at = (uint32_t)(live * 1024 + (kq * (128 / GROUP) * kRows + 4 * q) * 4);
+  constexpr uint32_t kHop = GROUP < 128 ? 64 : 16;
 
-  u32x4_t code[3][2];
+  u32x4_t code[3];
   load_image(0, 0);
   get_scales(0);
   put_scales(0);
 #pragma unroll
-  for (int i = 0; i < 3; ++i) get_codes(i, code[i]);
-  loaded<6>();
+  for (int i = 0; i < 3; ++i) code[i] = get_codes(i);
+  loaded<3>();
   block_sync();
-  for (int slab = 0; slab < slabs; ++slab) {
-    const int cur = slab & 1;
+  auto step = [&](int slab, auto buffer) SSM_INLINE {
+    const int cur = buffer;
     // This slab's codes are taken out of their loads before the next slab's loads
     // are issued, which the wait for them would otherwise include.
-    u32x4_t c[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      c[t] = GROUP < 128 ? q4_transpose(code[0][t]) : code[0][t];
-      asm volatile("" : "+v"(c[t]));
-      code[0][t] = code[1][t];
-      code[1][t] = code[2][t];
-    }
+    u32x4_t c = GROUP < 128 ? q4_transpose(code[0]) : code[0];
+    asm volatile("" : "+v"(c));
+    code[0] = code[1];
+    code[1] = code[2];
     const bool more = slab + 1 < slabs;
     if (more) {
       load_image(slab + 1, cur ^ 1);
       get_scales(slab + 1);
     }
-    get_codes(slab + 3, code[2]);
+    code[2] = get_codes(slab + 3);
     const char* const tile = s.x[cur];
-    const float* const sums = reinterpret_cast<const float*>(tile + live * 1024);
-    f32x4_t d[MT][2];
+    // Many tiles or groups: addresses are computed again in every slab, or they
+    // would all be kept and spill.
+    if constexpr (MT * kG >= 32) {
+      asm volatile("" : "+v"(sum_at));
+#pragma unroll
+      for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(at[m]));
+    }
+    f32x4_t d[MT];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       constexpr int kPer = GROUP / 32;
-      const int u = 16 * kq + (GROUP < 128 ? 4 * j + q : 4 * q + j);     // unit of this lane's eight k
-      bf16x8_t xo[MT];
+      const bf16x8_t wo = q4_decode(c[j]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        xo[m] = *reinterpret_cast<const bf16x8_t*>(tile + xrow[m] * 1024 + 16 * (u ^ (xrow[m] & 15)));
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const bf16x8_t wo = q4_decode(c[t][j]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (j % kPer == 0) d[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-          d[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo[m], wo, d[m][t], 0, 0, 0);
-        }
+      for (int m = 0; m < MT; ++m) {
+        const bf16x8_t xo = *reinterpret_cast<const bf16x8_t*>(tile + (at[m] ^ (kHop * j)));
+        if (j % kPer == 0) d[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, wo, d[m], 0, 0, 0);
       }
       if (j % kPer == kPer - 1) {
-        const int g = 128 * kq / GROUP + j / kPer;
-        float2 sc[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) sc[t] = s.sc[cur][g][32 * nh + 16 * t + lr];
+        const int g = kq * (128 / GROUP) + j / kPer;
+        const float2 sc = s.sc[cur][g][16 * nt + lr];
+        const float* const sums = reinterpret_cast<const float*>(tile + sum_at) + (j / kPer) * kRows;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(&sums[g * kRows + 16 * m + 4 * q]);
+          const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(sums + 16 * m);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[m][t][r] = __builtin_fmaf(sc[t].x, __builtin_fmaf(-sc[t].y, xs[r], d[m][t][r]), acc[m][t][r]);
+          for (int r = 0; r < 4; ++r)
+            acc[m][r] = __builtin_fmaf(sc.x, __builtin_fmaf(-sc.y, xs[r], d[m][r]), acc[m][r]);
         }
       }
+      if constexpr (MT > 2) __builtin_amdgcn_sched_barrier(0);   // (one product's operands at a time: 128 registers)
     }
     if (more) put_scales(cur ^ 1);
-    loaded<2>();       // all but this slab's two loads of codes
+    loaded<1>();       // all but this slab's load of codes
     block_sync();
+  };
+  if constexpr (MT * kG >= 48) {
+#pragma unroll 1
+    for (int slab = 0; slab < slabs; ++slab) step(slab, slab & 1);
+  } else {
+    for (int slab = 0; slab < slabs; slab += 2) {
+      step(slab, std::integral_constant<int, 0>());
+      if (slab + 1 < slabs) step(slab + 1, std::integral_constant<int, 1>());
+    }
   }
 
   float(*part)[kRows][kWideCols + 1] = reinterpret_cast<float(*)[kRows][kWideCols + 1]>(&s);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[kq][16 * m + 4 * q + r][32 * nh + 16 * t + lr] = acc[m][t][r];
+    for (int r = 0; r < 4; ++r) part[kq][16 * m + 4 * q + r][16 * nt + lr] = acc[m][r];
   block_sync();
-  for (int e = tid; e < mrows * kWideCols; e += kThreads) {
+  for (int e = tid; e < mrows * kWideCols; e += kWideThreads) {
     const int m = e / kWideCols, c = e % kWideCols;
     if (n0 + c >= a.n) continue;
     float y = 0.0f;
@@ -537,18 +664,32 @@ Q4Shape q4_shape(const Q4Args& a) {
   return h;
 }
 
+// The form for up to 16 rows.  All of x in LDS, 16 columns per workgroup, against
+// slabs of x, 32 or 64 columns per workgroup (one row, microseconds):
+//   2560 x 5120: 6.2, 9.5   10576 x 2560: 8.4, 9.0   8192 x 8192: 14.9, 18.4
+//   20480 x 5120: 19.2, 22.2   32768 x 8192: 37.4, 34.5   65536 x 2560: 30.8, 28.8
+// From 128 columns per CU on the slabs' wider workgroups, which stage x less
+// often, are ahead.  In slabs, 64 columns where that gives every CU a workgroup.
+bool q4_fits(const Q4Shape& h, const Q4Args& a) {
+  return h.mt == 1 && a.k > 0 && (int64_t)a.n < 128ll * a.cus && q4_fit(a.m * h.terms, a.k, a.group).bytes <= kFitsBytes;
+}
+
 template <int GROUP, bool XF32>
 void launch_q4_x(const Q4Args& args, const Q4Shape& h, hipStream_t s) {
   Q4Args a = args;
   a.rows_per = h.rows_per;
   a.terms = h.terms;
+  if (q4_fits(h, a)) {
+    const dim3 grid((unsigned)((a.n + 15) / 16));
+    hipLaunchKernelGGL((q4_fits_kernel<GROUP, XF32>), grid, dim3(kThreads), (uint32_t)q4_fit(a.m * h.terms, a.k, GROUP).bytes, s, a);
+    return;
+  }
   if (h.mt == 1 || a.k == 0) {
-    // 64 columns per workgroup where that gives every CU one, else 32
-    if (h.mt == 1) a.rows_per = q4_rows(1, XF32);
     const int nh = (int64_t)a.n < 64ll * a.cus ? 1 : 2;
+    if (h.mt > 1) a.rows_per = q4_rows(1, XF32);       // (k = 0: the bias alone)
     const dim3 grid((unsigned)((a.n + 32 * nh - 1) / (32 * nh)), (unsigned)((a.m + a.rows_per - 1) / a.rows_per));
-    if (nh == 1) hipLaunchKernelGGL((q4_kernel<GROUP, 1, XF32>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((q4_kernel<GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
+    if (nh == 1) hipLaunchKernelGGL((q4_slabs_kernel<GROUP, 1, XF32>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((q4_slabs_kernel<GROUP, 2, XF32>), grid, dim3(kThreads), 0, s, a);
     return;
   }
   const dim3 rows((unsigned)h.slabs, (unsigned)h.rows_per, (unsigned)h.blocks);
@@ -556,7 +697,7 @@ void launch_q4_x(const Q4Args& args, const Q4Shape& h, hipStream_t s) {
   auto run = [&](auto mt) {
     constexpr int MT = decltype(mt)::value;
     hipLaunchKernelGGL((q4_rows_kernel<MT, GROUP, XF32>), rows, dim3(64), 0, s, a);
-    hipLaunchKernelGGL((q4_wide_kernel<MT, GROUP>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((q4_wide_kernel<MT, GROUP>), grid, dim3(kWideThreads), 0, s, a);
   };
   if (h.mt == 2) run(std::integral_constant<int, 2>());
   else if (h.mt == 3) run(std::integral_constant<int, 3>());
