@@ -36,7 +36,8 @@ extern "C" {
 #define SSM_NORM_CENTER 1
 #define SSM_NORM_GATE_LAST 2
 
-/* Largest width that one norm runs over (width, or width / ngroups). */
+/* Largest width that one norm runs over (width, or width / ngroups, of at most
+ * 65535 groups and 2^24 channels in all). */
 #define SSM_NORM_MAX_WIDTH 8192
 
 /*
@@ -132,7 +133,8 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
  * (b * seqlen + t) * q_row (k_row, v_row) elements after the first token's.
  * dk and dv: multiples of 8 up to SSM_LINATTN_MAX_DIM; q, k, v 16-byte aligned,
  * rows multiples of 8 elements and at most 2^24; nheads a multiple of ngroups,
- * at most 65535; states and out 16-byte aligned.  The state, the sums and the
+ * at most 65535, as batch, and batch * nheads below 2^23 (backward: 2.7 million);
+ * states and out 16-byte aligned.  The state, the sums and the
  * decays are fp32; the products run on bf16 matrix cores with computed operands
  * split into two bf16 terms (about 16 significant bits).  A value of v that is
  * not finite makes its column not finite from its step on, one of q, k or the
@@ -140,7 +142,7 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
  *
  * Plans: as for ssm_ssd_fwd.  A workgroup walks 64 columns of one (batch row,
  * head); where they are few, the sequence is cut into time chunks (chunk_len a
- * multiple of 64 where it cuts, at most 65535 of them), which costs one more pass
+ * multiple of 32 where it cuts, at most 65535 of them), which costs one more pass
  * over k and v and a workspace of
  * batch * n_chunks * nheads * (dk * dv + 1) * 4 bytes on `stream` (plus a copy of
  * an in-place initial state).  plan may be NULL; its states_per_wave is ignored.
@@ -186,7 +188,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
  * be one buffer (in place) or two (the state before the token is kept).
  * q, k: [batch, ngroups, dk]; v, out: [batch, nheads, dv]; log_decay: [batch, nheads],
  * or [nheads] with SSM_LINATTN_FIXED_DECAY.  in_dtype fp32 or bf16; dk a multiple of
- * 4 up to SSM_LINATTN_MAX_STEP_DK; dv >= 1; nheads and batch at most 65535.  States
+ * 4 up to SSM_LINATTN_MAX_STEP_DK; dv from 1 to 2^24; nheads and batch at most 65535.  States
  * 16-byte aligned, q and k aligned to four elements.
  */
 #define SSM_LINATTN_MAX_STEP_DK 256
@@ -208,8 +210,8 @@ ssm_status ssm_linattn_state_update(const float* state, float* state_out, const 
  *   scales : [n, k / group] fp32 or bf16 (scale_dtype)
  *   zeros  : [n, k / group] bytes, or NULL: 8 for every group
  *   bias   : [n] fp32, or NULL;   out: [m, n] in out_dtype
- * group is 32, 64 or 128 and divides k; n, k < 2^31.  Any m; the kernel is made
- * for up to about 64 rows, past which the codes are read again for every 64 (fp32
+ * group is 32, 64 or 128 and divides k; n < 2^28 - 1024, k < 2^31 - 1024,
+ * m at most 327675.  The kernel is made for up to about 64 rows, past which the codes are read again for every 64 (fp32
  * x: 21).  Above 16 rows (5) x is laid out in a workspace of about 2 m k bytes (6) on
  * `stream`.  Sums are fp32; x enters the matrix cores exactly (fp32 as three bf16
  * terms).  A value of x that is not finite makes its row's outputs NaN.  With

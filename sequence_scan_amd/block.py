@@ -63,14 +63,16 @@ def _start():
 
 
 def _on(stream, device):
-    """The HIP stream to run on: the given one, or the current one of the tensors' device,
+    """The HIP stream to run on: the given one, or the current one, of the tensors' device,
     which has to be the current device."""
-    if stream is not None:
-        return stream.cuda_stream
     i = device.index
     if i != _device():
         raise ValueError(f"tensors are on {device}, but the current device is cuda:{_device()}")
-    return _raw_stream(i)
+    if stream is None:
+        return _raw_stream(i)
+    if stream.device_index != i:
+        raise ValueError(f"tensors are on {device}, but the stream is on cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def _bad(t, name: str, shape, dtype, device):

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 
 #include "../../include/ssmblock.h"
@@ -46,7 +47,7 @@ ssm_status check_args(std::initializer_list<Arg> ins, std::initializer_list<Arg>
     for (const Arg& i : ins) {
       bool allowed = false;
       for (const Same& s : same)
-        allowed |= o.p == i.p && o.bytes == i.bytes && std::string(s.out) == o.name && std::string(s.in) == i.name;
+        allowed |= o.p == i.p && o.bytes == i.bytes && std::strcmp(s.out, o.name) == 0 && std::strcmp(s.in, i.name) == 0;
       if (!allowed && overlaps(ro, range(i.name, i.p, i.bytes)))
         return fail(SSM_ERR_UNSUPPORTED, "%s overlaps input %s", o.name, i.name);
     }
@@ -58,6 +59,11 @@ ssm_status check_args(std::initializer_list<Arg> ins, std::initializer_list<Arg>
 }
 
 // ----------------------------------------------------------------------- norms
+
+// A grid dimension holds fewer than 2^32 threads (16 per channel in the kernel
+// that joins the column sums).
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1024;
+constexpr int64_t kMaxNormChannels = int64_t{1} << 24;
 
 struct NormSizes {
   int64_t elems;   // rows * width
@@ -74,6 +80,8 @@ ssm_status norm_check(int64_t rows, int64_t width, int64_t ngroups, float eps, i
     return fail(SSM_ERR_UNSUPPORTED, "a norm over %lld channels is not supported (at most %d)",
                 (long long)(width / ngroups), SSM_NORM_MAX_WIDTH);
   if (ngroups > 65535) return fail(SSM_ERR_UNSUPPORTED, "ngroups=%lld exceeds 65535", (long long)ngroups);
+  if (width > kMaxNormChannels)
+    return fail(SSM_ERR_UNSUPPORTED, "width=%lld exceeds %lld", (long long)width, (long long)kMaxNormChannels);
   if (!(eps >= 0.0f) || std::isinf(eps)) return fail(SSM_ERR_UNSUPPORTED, "eps must be finite and not negative");
   if ((flags & ~allowed) != 0) return fail(SSM_ERR_UNSUPPORTED, "norm flags %d: unknown bits for this call", flags);
   for (ssm_dtype t : types)
@@ -157,7 +165,8 @@ ssm_status la_check(int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngrou
                 (long long)ngroups);
   if (nheads > 65535) return fail(SSM_ERR_UNSUPPORTED, "nheads=%lld exceeds 65535", (long long)nheads);
   if (batch > 65535) return fail(SSM_ERR_UNSUPPORTED, "batch=%lld exceeds 65535", (long long)batch);
-  if (dk < 1 || dv < 1 || dv > INT32_MAX) return fail(SSM_ERR_UNSUPPORTED, "dk and dv must be positive");
+  if (dk < 1 || dv < 1 || dv > (1 << 24))
+    return fail(SSM_ERR_UNSUPPORTED, "dk=%lld and dv=%lld must be positive, dv at most 2^24", (long long)dk, (long long)dv);
   if ((flags & ~SSM_LINATTN_FIXED_DECAY) != 0) return fail(SSM_ERR_UNSUPPORTED, "linear attention flags %d: unknown bits", flags);
   if (!std::isfinite(scale)) return fail(SSM_ERR_UNSUPPORTED, "scale must be finite");
   for (ssm_dtype t : types)
@@ -179,7 +188,8 @@ ssm_status la_check_chunked(int64_t batch, int64_t nheads, int64_t dk, int64_t d
   if (dk % 8 != 0 || dv % 8 != 0 || dk > SSM_LINATTN_MAX_DIM || dv > SSM_LINATTN_MAX_DIM)
     return fail(SSM_ERR_UNSUPPORTED, "dk=%lld and dv=%lld must be multiples of 8, at most %d", (long long)dk, (long long)dv,
                 SSM_LINATTN_MAX_DIM);
-  if (batch * nheads * slots > INT32_MAX) return fail(SSM_ERR_UNSUPPORTED, "batch * nheads exceeds the grid");
+  if (batch * nheads * slots * 256 > kMaxThreads)
+    return fail(SSM_ERR_UNSUPPORTED, "batch * nheads = %lld exceeds the grid", (long long)(batch * nheads));
   return SSM_OK;
 }
 
@@ -246,8 +256,9 @@ ssm_status q4_check(int64_t m, int64_t n, int64_t k, int64_t group, std::initial
   int64_t t;
   if (!mul_ok(n, k, &t) || !mul_ok(t, 8, &t) || !mul_ok(m, n, &t) || !mul_ok(t, 8, &t))
     return fail(SSM_ERR_BAD_SHAPE, "element count overflows int64");
-  // (1024 columns of padding in the kernel's 32-bit indexes; 65535 blocks of 21 rows)
-  if (n > INT32_MAX - 1024 || k > INT32_MAX - 1024 || m > 65535ll * 5)
+  // (16 threads per column in a grid; 1024 of padding in 32-bit indexes; 65535
+  // blocks of 5 rows)
+  if (n > (1 << 28) - 1024 || k > INT32_MAX - 1024 || m > 65535ll * 5)
     return fail(SSM_ERR_UNSUPPORTED, "m=%lld, n=%lld or k=%lld exceeds what the kernel indexes", (long long)m, (long long)n,
                 (long long)k);
   return SSM_OK;
@@ -599,6 +610,8 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   choose_la_bwd_plan(batch, seqlen, nheads, 2 * nk + nv, device_simds(), &plan);
   const int64_t K = plan.n_chunks;
   if (K > 65535) return fail(SSM_ERR_UNSUPPORTED, "seqlen=%lld gives more than 65535 time chunks", (long long)seqlen);
+  if (share > 1 && sz.qk / 4 > kMaxThreads)
+    return fail(SSM_ERR_UNSUPPORTED, "q and k of %lld elements exceed the grid that sums their heads' gradients", (long long)sz.qk);
   int64_t n_state, n_heads, n_part, n_grad;
   if (!mul_ok(sz.state, K, &n_state) || !mul_ok(batch * nheads, K, &n_heads) || !mul_ok(sz.rows * nheads, nk, &n_part) ||
       !mul_ok(sz.rows * nheads, dk, &n_grad))
@@ -819,7 +832,7 @@ ssm_status ssm_q4_quantize(const void* w, uint8_t* codes, void* scales, uint8_t*
   ssm_status st = q4_check(0, n, k, group, {w_dtype, scale_dtype});
   if (st != SSM_OK) return st;
   const int64_t sw = esize(w_dtype), ss = esize(scale_dtype), groups = n * (k / group);
-  if (groups / 256 > INT32_MAX - 1) return fail(SSM_ERR_UNSUPPORTED, "n * k / group exceeds the grid");
+  if (groups > kMaxThreads) return fail(SSM_ERR_UNSUPPORTED, "n * k / group exceeds the grid");
   st = check_args({{"w", w, n * k * sw, sw, true}},
                   {{"codes", codes, n * k / 2, 1, true}, {"scales", scales, groups * ss, ss, true}, {"zeros", zeros, groups, 1, true}});
   if (st != SSM_OK) return st;
