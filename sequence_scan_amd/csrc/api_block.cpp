@@ -206,12 +206,22 @@ ssm_status la_rows(const char* name, int64_t rows, int64_t width, int64_t row, i
 }
 
 // Time chunks of a forward.  A workgroup walks 64 value columns of one (batch
-// row, head) and two fit a CU.
+// row, head), and three fit a CU: one round of them, as long as time chunks keep
+// 1024 steps; with shorter ones two per CU, of at least 128 steps, since a time
+// chunk costs a fixed part and the carry between them runs over all (microseconds,
+// dk = dv = 128 where not said):
+//   1 x 65537, 16 heads of 64 x 128: 16 chunks 371, 24 321, 32 326, 48 342
+//   1 x 16384, 32 heads: 8 chunks 256, 12 246, 16 264    1 x 8192, 8 heads: 16 66, 32 56, 48 60
+//   1 x 2048, 8 heads: 4 chunks 59, 16 36, 32 36         1 x 131072, 2 heads of 128 x 64: 256 138, 384 165
+// More workgroups than CUs are not cut: 8 x 2048, 40 heads: 1 chunk 222, 2 275.
 void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, int simds, ssm_plan* p) {
   const int64_t wgs = std::max<int64_t>(1, batch * nheads * ((dv + 63) / 64));
   const int64_t cus = std::max(1, simds / 4);
   int64_t chunks = 1;
-  if (wgs <= cus) chunks = std::min((4 * cus + wgs - 1) / wgs, std::max<int64_t>(1, seqlen / 512));
+  if (wgs <= cus) {
+    chunks = 3 * cus / wgs;
+    if (seqlen / chunks < 1024) chunks = std::min(2 * cus / wgs, std::max<int64_t>(1, seqlen / 128));
+  }
   int64_t len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
   if (chunks > 1) len = (len + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
   *p = ssm_plan{};
@@ -220,12 +230,15 @@ void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, i
 }
 
 // Time chunks of a backward: at most kLaBwdChunk steps each, and more where its
-// three walks leave CUs idle.
+// three walks leave CUs idle.  The walks differ in length, so six workgroups per CU
+// (two fit) even them out better than two, down to 256 steps (microseconds, dk = dv
+// = 128, 2 and 6 per CU): 1 x 4096, 40 heads 379, 317; 1 x 8192, 8 heads 177, 170;
+// with at least 512 steps in place of 256: 1 x 2048, 8 heads 108, 80.
 void choose_la_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t slots, int simds, ssm_plan* p) {
   const int64_t wgs = std::max<int64_t>(1, batch * nheads * slots);
   const int64_t cus = std::max(1, simds / 4);
   int64_t chunks = (seqlen + ssm::kLaBwdChunk - 1) / ssm::kLaBwdChunk;
-  if (wgs <= cus) chunks = std::max(chunks, std::min((4 * cus + wgs - 1) / wgs, seqlen / 512));
+  if (wgs <= cus) chunks = std::max(chunks, std::min(6 * cus / wgs, seqlen / 256));
   chunks = std::max<int64_t>(1, chunks);
   const int64_t len = ((seqlen + chunks - 1) / chunks + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
   *p = ssm_plan{};
