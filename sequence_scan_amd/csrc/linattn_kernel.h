@@ -94,32 +94,35 @@ __device__ __forceinline__ f32x4_t la_mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// Two fp32 values as sums of N pairs of bf16 terms: a value's rounding, the
-// rest's rounding, ...; the first value in the low half.  The rest v - bf16(v) is
-// exact in fp32; the two-term dot product forms it in one instruction, from the
-// packed pair (a half that is not finite spoils its neighbour's too: they are of
-// one value column, which is lost then anyway).
+// Eight fp32 values as sums of N bf16 operands: their roundings, the rests'
+// roundings, ...  The rest v - bf16(v) is exact in fp32; the two-term dot product
+// with (-1, 0) or (0, -1) forms it in one instruction, from the packed pair (a half
+// that is not finite spoils its neighbour's too: they are of one value column,
+// which is lost then anyway).
 template <int N>
-struct LaSplit {
-  uint32_t t[N];
-};
-template <int N>
-__device__ __forceinline__ LaSplit<N> la_split(float v0, float v1) {
-  LaSplit<N> r;
-  // (-1, 0) and (0, -1), kept in registers: as an instruction's own constant, -1.0
-  // does not mean the packed pair that the compiler takes it for
+__device__ __forceinline__ void la_split8(float* v, u32x4_t* t) {
+  // (kept in registers: as an instruction's own constant, -1.0 does not mean the
+  // packed pair that the compiler takes it for)
   uint32_t first = 0x0000bf80u, second = 0xbf800000u;
   asm("" : "+s"(first), "+s"(second));
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    r.t[i] = pack_bf16x2(v0, v1);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t[i][r] = pack_bf16x2(v[2 * r], v[2 * r + 1]);
     if (i + 1 < N) {
-      const bf16x2_t p = __builtin_bit_cast(bf16x2_t, r.t[i]);
-      v0 = __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2_t, first), v0, false);
-      v1 = __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2_t, second), v1, false);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // (by itself: out of the operand of eight, the compiler takes the first pair
+        // for every one of the four)
+        uint32_t pair = t[i][r];
+        asm("" : "+v"(pair));
+        t[i][r] = pair;
+        const bf16x2_t p = __builtin_bit_cast(bf16x2_t, pair);
+        v[2 * r] = __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2_t, first), v[2 * r], false);
+        v[2 * r + 1] = __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2_t, second), v[2 * r + 1], false);
+      }
     }
   }
-  return r;
 }
 
 // Prefix sums over each half of a wavefront in 64 bits (row shifts, then the first
@@ -430,9 +433,11 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
           const float d = __builtin_amdgcn_exp2f(REV ? cj[r] - ci + (lj[r] - li) : ci - cj[r] + (li - lj[r])) * a.w_scale;
           v[r] = (REV ? j0 + r >= i : j0 + r <= i) ? acc[r] * d : 0.0f;
         }
-        const LaSplit<2> s0 = la_split<2>(v[0], v[1]), s1 = la_split<2>(v[2], v[3]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) *reinterpret_cast<uint2*>(LaRows<64>{s.W[e]}.at(i, 2 * j0)) = make_uint2(s0.t[e], s1.t[e]);
+        const uint2 hi = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        *reinterpret_cast<uint2*>(LaRows<64>{s.W[0]}.at(i, 2 * j0)) = hi;
+        const uint2 lo = make_uint2(pack_bf16x2(v[0] - __uint_as_float(hi.x << 16), v[1] - __uint_as_float(hi.x & 0xffff0000u)),
+                                    pack_bf16x2(v[2] - __uint_as_float(hi.y << 16), v[3] - __uint_as_float(hi.y & 0xffff0000u)));
+        *reinterpret_cast<uint2*>(LaRows<64>{s.W[1]}.at(i, 2 * j0)) = lo;
         if constexpr (KIND == kWalkDq) {
           // M = W o (q k^T) below the diagonal, over this slice's columns of q
           // and k: its row and column sums, in fp32 from exact products
@@ -460,15 +465,15 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
 #pragma unroll
       for (int m = 0; m < C / 32; ++m) {
         u32x4_t t[kTerms];
+        float v[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const f32x4_t& tile = accS[2 * m + r / 2];
-          const LaSplit<kTerms> sp = la_split<kTerms>(tile[2 * (r & 1)], tile[2 * (r & 1) + 1]);
-#pragma unroll
-          for (int e = 0; e < kTerms; ++e) t[e][r] = sp.t[e];
-        }
+        for (int r = 0; r < 8; ++r) v[r] = accS[2 * m + r / 4][r % 4];
+        la_split8<kTerms>(v, t);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
+          // (apart: the compiler would fetch halves of two operands with one
+          // instruction, and move them into place with six)
+          asm volatile("" ::: "memory");
           const bf16x8_t av = tA.op2(16 * n + lr, 32 * m + 4 * q);
 #pragma unroll
           for (int e = 0; e < kTerms; ++e) accY[n] = la_mfma(__builtin_bit_cast(bf16x8_t, t[e]), av, accY[n]);
@@ -541,13 +546,13 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     bf16x8_t xs[3];
     {
       u32x4_t t[3];
+      float v[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float g0 = e < 2 ? f0[2 * e] : f1[2 * e - 4], g1 = e < 2 ? f0[2 * e + 1] : f1[2 * e - 3];
-        const LaSplit<3> sp = la_split<3>(__uint_as_float(xw[e] << 16) * g0, __uint_as_float(xw[e] & 0xffff0000u) * g1);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) t[k][e] = sp.t[k];
+        v[2 * e] = __uint_as_float(xw[e] << 16) * (e < 2 ? f0[2 * e] : f1[2 * e - 4]);
+        v[2 * e + 1] = __uint_as_float(xw[e] & 0xffff0000u) * (e < 2 ? f0[2 * e + 1] : f1[2 * e - 3]);
       }
+      la_split8<3>(v, t);
 #pragma unroll
       for (int k = 0; k < 3; ++k) xs[k] = __builtin_bit_cast(bf16x8_t, t[k]);
     }
