@@ -30,6 +30,8 @@
 #ifndef SSMSCAN_LINATTN_KERNEL_H
 #define SSMSCAN_LINATTN_KERNEL_H
 
+#include <type_traits>
+
 #include "block.h"
 #include "lds_load.h"
 
@@ -398,9 +400,10 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     if (tid == 0) s.bad[ch & 1] = 0;
   };
 
-  for (int ch = 0; ch < chunks; ++ch) {
+  auto chunk = [&](int ch, auto buffer) SSM_INLINE {
     const int nt = steps_of(ch);
-    const int cur = ch & 1, dec = ch % T::kRing;
+    constexpr int cur = decltype(buffer)::value;
+    const int dec = ch % T::kRing;
     const bool more = ch + 1 < chunks;
     const LaRows<2 * C> tA{s.A}, tB{s.B[cur]};
     const LaRows<128> tX{s.X[cur]}, tZ{s.Z};
@@ -601,6 +604,10 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     }
     loaded<0>();
     block_sync();
+  };
+  for (int ch = 0; ch < chunks; ch += 2) {
+    chunk(ch, std::integral_constant<int, 0>());
+    if (ch + 1 < chunks) chunk(ch + 1, std::integral_constant<int, 1>());
   }
   if constexpr (kOut) {
     store(chunks - 1);
