@@ -60,6 +60,16 @@ __device__ __forceinline__ u32x4_t q4_transpose(u32x4_t w) {
   return u32x4_t{c[0], c[1], d[0], d[1]};
 }
 
+// A scale as it is stored, and its value: apart, so that the wait for the load
+// falls where the value is used, a slab later.
+__device__ __forceinline__ uint32_t q4_scale_bits(const Q4Args& a, int64_t at) {
+  uint32_t bits;
+  if (a.scale_bf16) bits = static_cast<const uint16_t*>(a.scales)[at];
+  else bits = static_cast<const uint32_t*>(a.scales)[at];
+  return bits;
+}
+__device__ __forceinline__ float q4_scale(const Q4Args& a, uint32_t bits) { return __uint_as_float(a.scale_bf16 ? bits << 16 : bits); }
+
 // Rows of x that MT tiles of 16 hold: all of them in bf16, a third in fp32.
 constexpr int q4_rows(int mt, bool xf32) { return xf32 ? 16 * mt / 3 : 16 * mt; }
 
@@ -182,8 +192,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_fits_kernel(Q4Args a) {
   for (int e = tid; e < 16 * groups; e += kThreads) {
     const int c = e / groups, g = e % groups;
     const int64_t at = min(n0 + c, (int64_t)a.n - 1) * groups + g;
-    const float sc = a.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.scales)[at]) : static_cast<const float*>(a.scales)[at];
-    ssc[g * 16 + c] = make_float2(sc, (float)(16 + (a.zeros != nullptr ? a.zeros[at] : 8)));
+    ssc[g * 16 + c] = make_float2(q4_scale(a, q4_scale_bits(a, at)), (float)(16 + (a.zeros != nullptr ? a.zeros[at] : 8)));
   }
   for (int e = 16 * groups + tid; e < 16 * (wide / GROUP); e += kThreads) ssc[e] = make_float2(0.0f, 0.0f);   // past k
   block_sync();
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
   for (int t = 0; t < 2; ++t) cw[t] = a.codes + min(n0 + 32 * nh + 16 * t + lr, (int64_t)a.n - 1) * kb;
 
   u32x4_t code[2], xv[NX][XF32 ? 2 : 1];
-  float sv[NS];
+  uint32_t sv[NS];
   int zv[NS];
   auto issue = [&](int slab) SSM_INLINE {
     const int k0 = slab * kSlab + 128 * kq + 32 * q;
@@ -291,14 +300,14 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
     for (int i = 0; i < NX; ++i) {
       const int v = tid + kThreads * i;
       const int row = v / kVec, k = slab * kSlab + (v % kVec) * 8;
-      const bool in = row < mrows && k < a.k;
-      const int64_t at = in ? (int64_t)(m0 + row) * a.x_row + k : 0;
+      // (past the row's end, its last vector again: staged as zero)
+      const int64_t at = (int64_t)(m0 + min(row, mrows - 1)) * a.x_row + min(k, a.k - 8);
       if constexpr (XF32) {
         const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const float*>(a.x) + at);
-        xv[i][0] = in ? p[0] : u32x4_t{0u, 0u, 0u, 0u};
-        xv[i][1] = in ? p[1] : u32x4_t{0u, 0u, 0u, 0u};
+        xv[i][0] = p[0];
+        xv[i][1] = p[1];
       } else {
-        xv[i][0] = in ? *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + at) : u32x4_t{0u, 0u, 0u, 0u};
+        xv[i][0] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + at);
       }
     }
 #pragma unroll
@@ -306,16 +315,20 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
       const int e = tid + kThreads * i;
       const int c = min(e / kG, kCols - 1), g = min(slab * kG + e % kG, groups - 1);
       const int64_t at = min(n0 + c, (int64_t)a.n - 1) * groups + g;
-      sv[i] = a.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.scales)[at]) : static_cast<const float*>(a.scales)[at];
+      sv[i] = q4_scale_bits(a, at);
       zv[i] = a.zeros != nullptr ? a.zeros[at] : 8;
     }
   };
-  auto stage = [&]() SSM_INLINE {
+  auto stage = [&](int slab) SSM_INLINE {
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int v = tid + kThreads * i;
       const int row = v / kVec, c = v % kVec;
       if (row < mrows) {     // whole wavefronts: a row is one or two of them
+        if (slab * kSlab + c * 8 >= a.k) {
+#pragma unroll
+          for (int e = 0; e < (XF32 ? 2 : 1); ++e) xv[i][e] = u32x4_t{0u, 0u, 0u, 0u};
+        }
         float f[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int e = tid + kThreads * i;
-      if (e < kCols * kG) s.sc[e % kG][e / kG] = make_float2(sv[i], (float)(16 + zv[i]));
+      if (e < kCols * kG) s.sc[e % kG][e / kG] = make_float2(q4_scale(a, sv[i]), (float)(16 + zv[i]));
     }
   };
 
@@ -348,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
   for (int t = 0; t < 2; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   if (slabs > 0) issue(0);
   for (int slab = 0; slab < slabs; ++slab) {
-    stage();
+    stage(slab);
     u32x4_t cur[2] = {code[0], code[1]};
     if (slab + 1 < slabs) issue(slab + 1);
     block_sync();
@@ -491,7 +504,7 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
     for (int u = w; u < units; u += kWideThreads / 64) load_lds(from + u * 1024, 16u * l, &s.x[to][u * 1024]);
   };
   const int sc_col = tid / kG, sc_g = tid % kG;     // (several per thread: kWideThreads / kG columns apart)
-  float sv[kS];
+  uint32_t sv[kS];
   int zv[kS];
   auto get_scales = [&](int n) SSM_INLINE {
     const int slab = slab_at(n);
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
     for (int i = 0; i < kS; ++i) {
       const int64_t at = min(n0 + min(sc_col + i * (kWideThreads / kG), kWideCols - 1), (int64_t)a.n - 1) * groups +
                          min(slab * kG + sc_g, groups - 1);
-      sv[i] = a.scale_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(a.scales)[at]) : static_cast<const float*>(a.scales)[at];
+      sv[i] = q4_scale_bits(a, at);
       zv[i] = a.zeros != nullptr ? a.zeros[at] : 8;
     }
   };
@@ -507,7 +520,7 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
 #pragma unroll
     for (int i = 0; i < kS; ++i) {
       const int c = sc_col + i * (kWideThreads / kG);
-      if (c < kWideCols) s.sc[to][sc_g][c] = make_float2(sv[i], (float)(16 + zv[i]));
+      if (c < kWideCols) s.sc[to][sc_g][c] = make_float2(q4_scale(a, sv[i]), (float)(16 + zv[i]));
     }
   };
 
