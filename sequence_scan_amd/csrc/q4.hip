@@ -45,8 +45,15 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 
 // Eight codes as bf16 pairs of 16 + code, in the order (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ bf16x8_t q4_decode(uint32_t w) {
-  const uint32_t mask = 0x00780078u, base = 0x41804180u;
+// The mask comes in a vector register (q4_mask): with that, and-or is one
+// instruction, which takes one constant from elsewhere, not two.
+__device__ __forceinline__ uint32_t q4_mask() {
+  uint32_t mask = 0x00780078u;
+  asm("" : "+v"(mask));
+  return mask;
+}
+__device__ __forceinline__ bf16x8_t q4_decode(uint32_t w, uint32_t mask) {
+  const uint32_t base = 0x41804180u;
   const u32x4_t t = {((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base, ((w >> 9) & mask) | base};
   return __builtin_bit_cast(bf16x8_t, t);
 }
@@ -197,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_fits_kernel(Q4Args a) {
   for (int e = 16 * groups + tid; e < 16 * (wide / GROUP); e += kThreads) ssc[e] = make_float2(0.0f, 0.0f);   // past k
   block_sync();
 
+  const uint32_t mask = q4_mask();
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
   const uint16_t* const xrow = sx + min(lr, live - 1) * SX;     // rows past the last repeat it
   for (int i0 = 0; i0 < mine; i0 += kAhead) {
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_fits_kernel(Q4Args a) {
         // of 128: 32 q + 8 j + 0..7)
         const bf16x8_t xo = *reinterpret_cast<const bf16x8_t*>(xrow + 128 * piece + (GROUP < 128 ? 32 * j + 8 * q : 32 * q + 8 * j));
         if (j % kPer == 0) d = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, q4_decode(c[j]), d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, q4_decode(c[j], mask), d, 0, 0, 0);
         if (j % kPer == kPer - 1) {
           const int g = (128 / GROUP) * piece + j / kPer;
           const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(&ssum[g * 16 + 4 * q]);
@@ -356,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
     }
   };
 
+  const uint32_t mask = q4_mask();
   f32x4_t acc[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (j % kPer == 0) d[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, q4_decode(cur[t][j]), d[t], 0, 0, 0);
+        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, q4_decode(cur[t][j], mask), d[t], 0, 0, 0);
       }
       if (j % kPer == kPer - 1) {
         const int g = 128 * kq / GROUP + j / kPer;
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
   constexpr int kS = NS > 0 ? NS : 1;
   struct Lds {
     char x[2][(kRows + I::kSums) * 1024] __attribute__((aligned(1024)));
-    float2 sc[2][kG][kWideCols];                    // scale, 16 + zero
+    float2 sc[2][kG][kWideCols];                    // scale, -(16 + zero) scale
   };
   constexpr int kJoin = kWideSplit * kRows * (kWideCols + 1) * 4;
   static_assert(sizeof(Lds) >= kJoin, "the join fits the slabs' place");
@@ -520,10 +529,12 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
 #pragma unroll
     for (int i = 0; i < kS; ++i) {
       const int c = sc_col + i * (kWideThreads / kG);
-      if (c < kWideCols) s.sc[to][sc_g][c] = make_float2(q4_scale(a, sv[i]), (float)(16 + zv[i]));
+      const float sc = q4_scale(a, sv[i]);
+      if (c < kWideCols) s.sc[to][sc_g][c] = make_float2(sc, -(float)(16 + zv[i]) * sc);
     }
   };
 
+  const uint32_t mask = q4_mask();
   f32x4_t acc[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) acc[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -536,7 +547,8 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
     const int row = min(16 * m + lr, live - 1);
     at[m] = (uint32_t)(row * 1024 + 16 * ((16 * kq + (GROUP < 128 ? q : 4 * q)) ^ (row & 15)));
   }
-  uint32_t sum_at = (uint32_t)(live * 1024 + (kq * (128 / GROUP) * kRows + 4 * q) * 4);
+  constexpr int kPiece = 128 / GROUP;                 // groups of a piece
+  uint32_t sum_at = (uint32_t)(live * 1024 + ((kq * kPiece + (q < kPiece ? q : 0)) * kRows + lr) * 4);
   constexpr uint32_t kHop = GROUP < 128 ? 64 : 16;
 
   u32x4_t code[3];
@@ -569,11 +581,22 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(at[m]));
     }
+    // What the codes' 16 and zero points add, taken off for the piece's groups at
+    // once: -(16 + zero) scale times the groups' sums, an fp32 product of depth 4
+    // (lane row q: group q, where there are so many).
+    {
+      const int g = kq * kPiece + (q < kPiece ? q : 0);
+      const float off = s.sc[cur][g][16 * nt + lr].y;
+      const float co = q < kPiece ? off : 0.0f;
+      const float* const sums = reinterpret_cast<const float*>(tile + sum_at);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(sums[16 * m], co, acc[m], 0, 0, 0);
+    }
     f32x4_t d[MT];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       constexpr int kPer = GROUP / 32;
-      const bf16x8_t wo = q4_decode(c[j]);
+      const bf16x8_t wo = q4_decode(c[j], mask);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const bf16x8_t xo = *reinterpret_cast<const bf16x8_t*>(tile + (at[m] ^ (kHop * j)));
@@ -581,16 +604,11 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
         d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, wo, d[m], 0, 0, 0);
       }
       if (j % kPer == kPer - 1) {
-        const int g = kq * (128 / GROUP) + j / kPer;
-        const float2 sc = s.sc[cur][g][16 * nt + lr];
-        const float* const sums = reinterpret_cast<const float*>(tile + sum_at) + (j / kPer) * kRows;
+        const float sc = s.sc[cur][kq * kPiece + j / kPer][16 * nt + lr].x;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const f32x4_t xs = *reinterpret_cast<const f32x4_t*>(sums + 16 * m);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[m][r] = __builtin_fmaf(sc.x, __builtin_fmaf(-sc.y, xs[r], d[m][r]), acc[m][r]);
-        }
+          for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(sc, d[m][r], acc[m][r]);
       }
       if constexpr (MT > 2) __builtin_amdgcn_sched_barrier(0);   // (one product's operands at a time: 128 registers)
     }
