@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
     at[m] = (uint32_t)(row * 1024 + 16 * ((16 * kq + (GROUP < 128 ? q : 4 * q)) ^ (row & 15)));
   }
   constexpr int kPiece = 128 / GROUP;                 // groups of a piece
-  uint32_t sum_at = (uint32_t)(live * 1024 + ((kq * kPiece + (q < kPiece ? q : 0)) * kRows + lr) * 4);
+  const uint32_t sum_at = (uint32_t)(live * 1024 + ((kq * kPiece + (q < kPiece ? q : 0)) * kRows + lr) * 4);
   constexpr uint32_t kHop = GROUP < 128 ? 64 : 16;
 
   u32x4_t code[3];
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
   loaded<3>();
   block_sync();
   auto step = [&](int slab, auto buffer) SSM_INLINE {
-    const int cur = buffer;
+    constexpr int cur = decltype(buffer)::value;
     // This slab's codes are taken out of their loads before the next slab's loads
     // are issued, which the wait for them would otherwise include.
     u32x4_t c = GROUP < 128 ? q4_transpose(code[0]) : code[0];
@@ -574,10 +574,9 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
     }
     code[2] = get_codes(slab + 3);
     const char* const tile = s.x[cur];
-    // Many tiles or groups: addresses are computed again in every slab, or they
-    // would all be kept and spill.
-    if constexpr (MT * kG >= 32) {
-      asm volatile("" : "+v"(sum_at));
+    // Four tiles in groups of 32: addresses are computed again in every slab, or they
+    // would all be kept, past the registers that there are.
+    if constexpr (MT * kG >= 64) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(at[m]));
     }
@@ -616,14 +615,9 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
     loaded<1>();       // all but this slab's load of codes
     block_sync();
   };
-  if constexpr (MT * kG >= 48) {
-#pragma unroll 1
-    for (int slab = 0; slab < slabs; ++slab) step(slab, slab & 1);
-  } else {
-    for (int slab = 0; slab < slabs; slab += 2) {
-      step(slab, std::integral_constant<int, 0>());
-      if (slab + 1 < slabs) step(slab + 1, std::integral_constant<int, 1>());
-    }
+  for (int slab = 0; slab < slabs; slab += 2) {
+    step(slab, std::integral_constant<int, 0>());
+    if (slab + 1 < slabs) step(slab + 1, std::integral_constant<int, 1>());
   }
 
   float(*part)[kRows][kWideCols + 1] = reinterpret_cast<float(*)[kRows][kWideCols + 1]>(&s);
