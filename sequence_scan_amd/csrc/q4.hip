@@ -25,7 +25,7 @@
 // slabs (q4_slabs_kernel).  Above, that would cost each of them as much as its
 // products, so a small kernel lays x out once (q4_rows_kernel) as the LDS images of
 // all slabs, and the workgroups load them straight to LDS, a slab ahead, and the
-// codes three slabs ahead (q4_wide_kernel).
+// codes two slabs ahead (q4_wide_kernel).
 //
 // Measured: one row x 10576 x 2560 (13.5 MB of codes) 8.4 us, of which a launch and
 // the wait for the first bytes are about half; 48 rows x 16384 x 8192 37 us, where
@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(kThreads, 4) q4_fits_kernel(Q4Args a) {
 // ----------------------------------------------- up to 16 rows, x in slabs
 //
 // x's slab, its sums and the slab's scales go through LDS, loaded a slab ahead
-// into registers; NH wavefronts share a piece, 32 columns each.
+// into registers, and codes two slabs ahead (each slab of a pair has registers of its
+// own: to move a load's result is to wait for it); NH wavefronts share a piece, 32
+// columns each.
 template <int GROUP, int NH, bool XF32>
 __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
   constexpr int kTerms = XF32 ? 3 : 1;
@@ -296,14 +298,15 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) cw[t] = a.codes + min(n0 + 32 * nh + 16 * t + lr, (int64_t)a.n - 1) * kb;
 
-  u32x4_t code[2], xv[NX][XF32 ? 2 : 1];
+  u32x4_t code[2][2], xv[NX][XF32 ? 2 : 1];
   uint32_t sv[NS];
   int zv[NS];
-  auto issue = [&](int slab) SSM_INLINE {
-    const int k0 = slab * kSlab + 128 * kq + 32 * q;
-    const int64_t off = min(k0, a.k - 32) / 2;
+  auto get_codes = [&](int slab, u32x4_t* to) SSM_INLINE {
+    const int64_t off = min(min(slab, slabs - 1) * kSlab + 128 * kq + 32 * q, a.k - 32) / 2;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) code[t] = *reinterpret_cast<const u32x4_t*>(cw[t] + off);
+    for (int t = 0; t < 2; ++t) to[t] = *reinterpret_cast<const u32x4_t*>(cw[t] + off);
+  };
+  auto issue = [&](int slab) SSM_INLINE {
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int v = tid + kThreads * i;
@@ -368,16 +371,22 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
   f32x4_t acc[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  if (slabs > 0) issue(0);
-  for (int slab = 0; slab < slabs; ++slab) {
-    stage(slab);
-    u32x4_t cur[2] = {code[0], code[1]};
-    if (slab + 1 < slabs) issue(slab + 1);
-    block_sync();
-    if constexpr (GROUP < 128) {
+  if (slabs > 0) {
+    issue(0);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) cur[t] = q4_transpose(cur[t]);
+    for (int i = 0; i < 2; ++i) get_codes(i, code[i]);
+  }
+  auto step = [&](int slab, auto half) SSM_INLINE {
+    stage(slab);
+    u32x4_t cur[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      cur[t] = GROUP < 128 ? q4_transpose(code[half][t]) : code[half][t];
+      asm volatile("" : "+v"(cur[t]));     // (taken before the loads below are issued)
     }
+    if (slab + 1 < slabs) issue(slab + 1);
+    if (slab + 2 < slabs) get_codes(slab + 2, code[half]);
+    block_sync();
     f32x4_t d[2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -403,6 +412,10 @@ __global__ void __launch_bounds__(kThreads, 4) q4_slabs_kernel(Q4Args a) {
       }
     }
     block_sync();
+  };
+  for (int slab = 0; slab < slabs; slab += 2) {
+    step(slab, std::integral_constant<int, 0>());
+    if (slab + 1 < slabs) step(slab + 1, std::integral_constant<int, 1>());
   }
 
   // Join the wavefronts' parts, in order, and the terms of x.
@@ -551,28 +564,26 @@ __global__ void __launch_bounds__(kWideThreads) q4_wide_kernel(Q4Args a) {
   const uint32_t sum_at = (uint32_t)(live * 1024 + ((kq * kPiece + (q < kPiece ? q : 0)) * kRows + lr) * 4);
   constexpr uint32_t kHop = GROUP < 128 ? 64 : 16;
 
-  u32x4_t code[3];
+  u32x4_t code[2];
   load_image(0, 0);
   get_scales(0);
   put_scales(0);
 #pragma unroll
-  for (int i = 0; i < 3; ++i) code[i] = get_codes(i);
-  loaded<3>();
+  for (int i = 0; i < 2; ++i) code[i] = get_codes(i);
+  loaded<2>();
   block_sync();
   auto step = [&](int slab, auto buffer) SSM_INLINE {
     constexpr int cur = decltype(buffer)::value;
     // This slab's codes are taken out of their loads before the next slab's loads
     // are issued, which the wait for them would otherwise include.
-    u32x4_t c = GROUP < 128 ? q4_transpose(code[0]) : code[0];
+    u32x4_t c = GROUP < 128 ? q4_transpose(code[cur]) : code[cur];
     asm volatile("" : "+v"(c));
-    code[0] = code[1];
-    code[1] = code[2];
     const bool more = slab + 1 < slabs;
     if (more) {
       load_image(slab + 1, cur ^ 1);
       get_scales(slab + 1);
     }
-    code[2] = get_codes(slab + 3);
+    code[cur] = get_codes(slab + 2);
     const char* const tile = s.x[cur];
     // Four tiles in groups of 32: addresses are computed again in every slab, or they
     // would all be kept, past the registers that there are.
