@@ -27,10 +27,11 @@
 // all slabs, and the workgroups load them straight to LDS, a slab ahead, and the
 // codes two slabs ahead (q4_wide_kernel).
 //
-// Measured: one row x 10576 x 2560 (13.5 MB of codes) 8.4 us, of which a launch and
-// the wait for the first bytes are about half; 48 rows x 16384 x 8192 37 us, where
-// the vector instructions that decode, address and scale are what bounds it (145
-// per wavefront and slab, half of the time, against 12 MFMA).
+// Measured: one row x 10576 x 2560 (13.5 MB of codes) 8.1 us, of which the launch and
+// the wait for the first bytes are about half; 2 rows x 16384 x 16384 (134 MB) 37 us,
+// 3.6 TB/s; 48 rows x 16384 x 8192 (67 MB) 31 us and 3 us for x.  There no one thing
+// bounds it: without its loads, its matrix products or its reads of x it takes 23,
+// 31 and 31 us, since the 16 wavefronts that a CU holds meet at a barrier every slab.
 #include <algorithm>
 
 #include "block.h"
@@ -128,10 +129,11 @@ __device__ __forceinline__ u32x4_t q4_term(float* f) {
   return q4_pairs(p);
 }
 
-// The same where all of x, its sums and the columns' scales fit the LDS (q4_fits):
-// one row of 2560, say.  They are staged once, and the wavefronts then walk their
-// pieces of K without a barrier, codes kAhead pieces ahead.  With slabs, such a
-// call would wait for memory once a slab, with little to do in between.
+// ------------------------------------------------ few rows, x in LDS at once
+//
+// All of x, its sums and the columns' scales are staged once (q4_fits says where), and
+// the wavefronts then walk their pieces of K without a barrier, codes kAhead pieces
+// ahead.
 constexpr int kFitsBytes = 64 * 1024;
 constexpr int kAhead = 4;
 
@@ -700,14 +702,20 @@ Q4Shape q4_shape(const Q4Args& a) {
   return h;
 }
 
-// The form for up to 16 rows.  All of x in LDS, 16 columns per workgroup, against
-// slabs of x, 32 or 64 columns per workgroup (one row, microseconds):
-//   2560 x 5120: 6.2, 9.5   10576 x 2560: 8.4, 9.0   8192 x 8192: 14.9, 18.4
-//   20480 x 5120: 19.2, 22.2   32768 x 8192: 37.4, 34.5   65536 x 2560: 30.8, 28.8
-// From 128 columns per CU on the slabs' wider workgroups, which stage x less
-// often, are ahead.  In slabs, 64 columns where that gives every CU a workgroup.
+// Columns per workgroup of the form in slabs: 64 where that gives every CU a
+// workgroup, else 32.
+int q4_slab_cols(const Q4Args& a) { return (int64_t)a.n < 64ll * a.cus ? 32 : 64; }
+
+// All of x in LDS, 16 columns per workgroup: for up to four rows (terms counted;
+// each workgroup stages them all), where the workgroups of the form in slabs would
+// leave a quarter of their last round of CUs idle or more.  Measured, all of x against
+// slabs, one row (microseconds): 2560 x 5120 6.1, 7.6; 10576 x 2560 8.1, 9.1; 20480 x
+// 5120 17.6, 21.2; but 8192 x 8192 14.6, 13.5; 16384 x 8192 25.2, 23.3; 65536 x 2560
+// 31.1, 25.8.  10576 x 2560 by rows: 2 8.3, 9.2; 4 9.3, 9.7; 8 11.4, 10.3.
 bool q4_fits(const Q4Shape& h, const Q4Args& a) {
-  return h.mt == 1 && a.k > 0 && (int64_t)a.n < 128ll * a.cus && q4_fit(a.m * h.terms, a.k, a.group).bytes <= kFitsBytes;
+  const int cols = q4_slab_cols(a);
+  const int64_t wgs = ((int64_t)a.n + cols - 1) / cols, places = (wgs + a.cus - 1) / a.cus * a.cus;
+  return a.k > 0 && a.m * h.terms <= 4 && 4 * wgs <= 3 * places && q4_fit(a.m * h.terms, a.k, a.group).bytes <= kFitsBytes;
 }
 
 template <int GROUP, bool XF32>
@@ -721,7 +729,7 @@ void launch_q4_x(const Q4Args& args, const Q4Shape& h, hipStream_t s) {
     return;
   }
   if (h.mt == 1 || a.k == 0) {
-    const int nh = (int64_t)a.n < 64ll * a.cus ? 1 : 2;
+    const int nh = q4_slab_cols(a) / 32;
     if (h.mt > 1) a.rows_per = q4_rows(1, XF32);       // (k = 0: the bias alone)
     const dim3 grid((unsigned)((a.n + 32 * nh - 1) / (32 * nh)), (unsigned)((a.m + a.rows_per - 1) / a.rows_per));
     if (nh == 1) hipLaunchKernelGGL((q4_slabs_kernel<GROUP, 1, XF32>), grid, dim3(kThreads), 0, s, a);
