@@ -69,6 +69,23 @@ __device__ __forceinline__ void put8(uint16_t* p, const float* v) {
   *reinterpret_cast<u32x4_any*>(p) = a;
 }
 
+// Eight elements as they are, and their values: apart, for loads a row ahead.
+template <typename T>
+struct Raw8 {
+  u32x4_any q[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = *reinterpret_cast<const u32x4_any*>(p + 4 * i);
+  }
+  __device__ __forceinline__ void values(float* o) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) o[i] = __uint_as_float(q[i / 4][i % 4]);
+      else o[i] = __uint_as_float((i & 1) ? q[0][i / 2] & 0xffff0000u : q[0][i / 2] << 16);
+    }
+  }
+};
+
 // Up to eight elements (TINY: the first n, the rest 0).
 template <bool TINY, typename T>
 __device__ __forceinline__ void get(const T* p, int n, float* o) {
@@ -222,21 +239,40 @@ __global__ void __launch_bounds__(T > 0 ? 64 * kNormWaves : 1024) norm_fwd_kerne
     for (int j = 0; j < 8; ++j) w[v][j] = 1.0f;
     if (a.w != nullptr) get<TINY>(a.w + gbase + at.e0[v], n, w[v]);
   }
+  // In the workgroup layout a row's loads are issued a row ahead: its wavefronts wait
+  // for each other in every row, and would all wait for memory after that (gated norm
+  // of 16384 x 5120: 114 us without, 103 with; the add norm, which stores twice as
+  // much as it loads ahead, has gained little or lost: 65536 x 1280 182, 194).
+  constexpr bool kAhead = T == 0 && MODE != kModeAdd;
+  Raw8<Tx> nx, nz;
+  auto fetch = [&](int64_t row) SSM_INLINE {
+    nx.load(x + row * a.x_stride + at.e0[0]);
+    if (z != nullptr) nz.load(z + row * a.z_stride + at.e0[0]);
+  };
+  if constexpr (kAhead)
+    if (at.row0 < a.rows) fetch(at.row0);
   for (int64_t base = at.row0; base < a.rows; base += at.step) {
     const int64_t row = min(base + at.rslot, a.rows - 1);
     const bool live = T == 0 || (base + at.rslot < a.rows && at.glive);
     // every load of the row first
     float r[NV][8], gate[NV][8], xv[NV][8], zr[NV][8];
+    if constexpr (kAhead) {
+      static_assert(NV == 1, "one step per lane");
+      nx.values(xv[0]);
+      if (z != nullptr) nz.values(zr[0]);
+      if (base + at.step < a.rows) fetch(base + at.step);
+    } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      get<TINY>(x + row * a.x_stride + at.e0[v], n, xv[v]);
-      if constexpr (MODE != kModeAdd)
-        if (z != nullptr) get<TINY>(z + row * a.z_stride + at.e0[v], n, zr[v]);
-    }
-    if constexpr (MODE == kModeAdd) {
-      if (res != nullptr) {
+      for (int v = 0; v < NV; ++v) {
+        get<TINY>(x + row * a.x_stride + at.e0[v], n, xv[v]);
+        if constexpr (MODE != kModeAdd)
+          if (z != nullptr) get<TINY>(z + row * a.z_stride + at.e0[v], n, zr[v]);
+      }
+      if constexpr (MODE == kModeAdd) {
+        if (res != nullptr) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) get<TINY>(res + row * wide + at.e0[v], n, r[v]);
+          for (int v = 0; v < NV; ++v) get<TINY>(res + row * wide + at.e0[v], n, r[v]);
+        }
       }
     }
 #pragma unroll
@@ -344,18 +380,38 @@ __global__ void __launch_bounds__(T > 0 ? 64 * kNormWaves : 1024) norm_bwd_kerne
     }
     if (a.w != nullptr) get<TINY>(a.w + gbase + at.e0[v], n, w[v]);
   }
+  // (as in the forward: gated 16384 x 5120 184 us without, 167 with; the add norm's
+  // three column sums leave too few registers, 16384 x 2560 131, 172)
+  constexpr bool kAhead = T == 0 && MODE != kModeAdd;
+  Raw8<Td> nd;
+  Raw8<Tx> nx, nz;
+  auto fetch = [&](int64_t row) SSM_INLINE {
+    nd.load(dout + row * wide + at.e0[0]);
+    nx.load(x + row * a.x_stride + at.e0[0]);
+    if (z != nullptr) nz.load(z + row * a.z_stride + at.e0[0]);
+  };
+  if constexpr (kAhead)
+    if (at.row0 < a.rows) fetch(at.row0);
   for (int64_t base = at.row0; base < a.rows; base += at.step) {
     const int64_t row = min(base + at.rslot, a.rows - 1);
     const bool live = T == 0 || (base + at.rslot < a.rows && at.glive);
     float x_[NV][8], dy_[NV][8], gate[NV][8], slope[NV][8];
+    if constexpr (kAhead) {
+      static_assert(NV == 1, "one step per lane");
+      nd.values(dy_[0]);
+      nx.values(x_[0]);
+      if (z != nullptr) nz.values(gate[0]);
+      if (base + at.step < a.rows) fetch(base + at.step);
+    } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      get<TINY>(dout + row * wide + at.e0[v], n, dy_[v]);
-      if constexpr (MODE == kModeAdd) {
-        get<TINY>(static_cast<const Tr*>(a.res) + row * wide + at.e0[v], n, x_[v]);
-      } else {
-        get<TINY>(x + row * a.x_stride + at.e0[v], n, x_[v]);
-        if (z != nullptr) get<TINY>(z + row * a.z_stride + at.e0[v], n, gate[v]);
+      for (int v = 0; v < NV; ++v) {
+        get<TINY>(dout + row * wide + at.e0[v], n, dy_[v]);
+        if constexpr (MODE == kModeAdd) {
+          get<TINY>(static_cast<const Tr*>(a.res) + row * wide + at.e0[v], n, x_[v]);
+        } else {
+          get<TINY>(x + row * a.x_stride + at.e0[v], n, x_[v]);
+          if (z != nullptr) get<TINY>(z + row * a.z_stride + at.e0[v], n, gate[v]);
+        }
       }
     }
     if constexpr (MODE != kModeAdd) {
