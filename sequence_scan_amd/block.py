@@ -62,20 +62,21 @@ def _start():
     _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _on(stream, device):
-    """The HIP stream to run on: the given one, or the current one, of the tensors' device,
-    which has to be the current device."""
-    i = device.index
-    if i != _device():
-        raise ValueError(f"tensors are on {device}, but the current device is cuda:{_device()}")
+def _on(stream, dev: int):
+    """The HIP stream to run on: the given one, or the current one, of the tensors' device
+    (its index), which has to be the current device."""
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    if dev != _device():
+        raise ValueError(f"tensors are on cuda:{dev}, but the current device is cuda:{_device()}")
     if stream is None:
-        return _raw_stream(i)
-    if stream.device_index != i:
-        raise ValueError(f"tensors are on {device}, but the stream is on cuda:{stream.device_index}")
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"tensors are on cuda:{dev}, but the stream is on cuda:{stream.device_index}")
     return stream.cuda_stream
 
 
-def _bad(t, name: str, shape, dtype, device):
+def _bad(t, name: str, shape, dtype, dev: int):
     """Raise for the first thing that is not as wanted."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -83,37 +84,34 @@ def _bad(t, name: str, shape, dtype, device):
         _dtype_code(t)
     elif t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_cuda:
-        raise ValueError("tensors must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {'cuda:%d' % dev if dev >= 0 else 'the CPU'}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _want(t, name: str, shape, dtype, device):
+def _want(t, name: str, shape, dtype, dev: int):
     """The pointer of a contiguous tensor of this shape, dtype (None: float32 or
-    bfloat16) and device, or of no tensor.  The C ABI trusts the sizes it is given,
-    so every tensor is checked before its pointer is passed."""
+    bfloat16) and device index, or of no tensor.  The C ABI trusts the sizes it is given,
+    so every tensor is checked before its pointer is passed (that the device is a GPU:
+    ``_on``)."""
     if t is None:
         return None
-    if (t.shape != shape or (t.dtype not in _code if dtype is None else t.dtype is not dtype) or t.device != device
-            or not t.is_cuda or not t.is_contiguous()):
-        _bad(t, name, shape, dtype, device)
+    if (t.shape != shape or (t.dtype not in _code if dtype is None else t.dtype is not dtype) or t.get_device() != dev
+            or not t.is_contiguous()):
+        _bad(t, name, shape, dtype, dev)
     return t.data_ptr()
 
 
-def _rows(t, name: str, shape, dtype, device, inner: int = 1):
+def _rows(t, name: str, shape, dtype, dev: int, inner: int = 1):
     """(pointer, row stride) of a tensor whose last ``inner`` dimensions are
     contiguous and whose leading ones are evenly spaced rows, such as a slice of a
     packed projection's last dimension."""
     if t is None:
         return None, 0
+    if t.shape != shape or (t.dtype not in _code if dtype is None else t.dtype is not dtype) or t.get_device() != dev:
+        _bad(t, name, shape, dtype, dev)
     if t.is_contiguous():
-        row = shape[-1] if inner == 1 else shape[-1] * shape[-2]
-        return _want(t, name, shape, dtype, device), row
-    if (t.shape != shape or (t.dtype not in _code if dtype is None else t.dtype is not dtype) or t.device != device
-            or not t.is_cuda):
-        _bad(t, name, shape, dtype, device)
+        return t.data_ptr(), shape[-1] if inner == 1 else shape[-1] * shape[-2]
     lead, step = t.dim() - inner, 1
     for d in range(t.dim() - 1, lead - 1, -1):
         if t.shape[d] != 1 and t.stride(d) != step:
@@ -138,8 +136,8 @@ def _kind(dtype) -> int:
     return _code[dtype]
 
 
-def _new(shape, dtype, device):
-    return _empty(shape, dtype=dtype, device=device)
+def _new(shape, dtype, like):
+    return _empty(shape, dtype=dtype, device=like.device)
 
 
 def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, scale=None, alpha: float = 1.0, eps: float = 1e-5,
@@ -151,15 +149,15 @@ def ssm_add_norm_fwd(x, residual=None, weight=None, bias=None, scale=None, alpha
     ``residual_out`` (residual's dtype, or float32 without one) may be ``residual``.
     Returns (out, residual_out)."""
     call = _fn("ssm_add_norm_fwd")
-    dev, shape = x.device, x.shape
+    dev, shape = x.get_device(), x.shape
     width = shape[-1]
     rows = x.numel() // width if width else 0
     xp, xs = _rows(x, "x", shape, None, dev)
     rp = _want(residual, "residual", shape, None, dev)
     if out is None:
-        out = _new(shape, out_dtype or x.dtype, dev)
+        out = _new(shape, out_dtype or x.dtype, x)
     if residual_out is None:
-        residual_out = _new(shape, _F32 if residual is None else residual.dtype, dev)
+        residual_out = _new(shape, _F32 if residual is None else residual.dtype, x)
     cols = (width,)
     _check(call(
         xp, xs, rp, _want(weight, "weight", cols, _F32, dev), _want(bias, "bias", cols, _F32, dev),
@@ -178,7 +176,7 @@ def ssm_add_norm_bwd(dout, r, weight=None, dresidual_out=None, x=None, scale=Non
     with dx (``dx_dtype``, or x's or dout's dtype), dresidual (r's dtype) and, as asked,
     dweight, dbias and dscale (wanted by default where ``scale`` and ``x`` are given)."""
     call = _fn("ssm_add_norm_bwd")
-    dev, shape = dout.device, dout.shape
+    dev, shape = dout.get_device(), dout.shape
     width = shape[-1]
     rows = dout.numel() // width if width else 0
     if want_scale is None:
@@ -191,13 +189,13 @@ def ssm_add_norm_bwd(dout, r, weight=None, dresidual_out=None, x=None, scale=Non
     _kind(xdt)
     xp, xs = _rows(x, "x", shape, None, dev) if want_scale else (None, width)
     cols = (width,)
-    g = {"dx": _new(shape, xdt, dev), "dresidual": _new(shape, r.dtype, dev)}
+    g = {"dx": _new(shape, xdt, dout), "dresidual": _new(shape, r.dtype, dout)}
     if want_weight:
-        g["dweight"] = _new(cols, _F32, dev)
+        g["dweight"] = _new(cols, _F32, dout)
     if want_bias:
-        g["dbias"] = _new(cols, _F32, dev)
+        g["dbias"] = _new(cols, _F32, dout)
     if want_scale:
-        g["dscale"] = _new(cols, _F32, dev)
+        g["dscale"] = _new(cols, _F32, dout)
     ptr = {k: v.data_ptr() for k, v in g.items()}
     _check(call(
         _want(dout, "dout", shape, None, dev), _want(r, "r", shape, None, dev), _want(weight, "weight", cols, _F32, dev),
@@ -219,13 +217,13 @@ def ssm_gated_norm_fwd(x, z=None, weight=None, bias=None, ngroups: int = 1, gate
     (norm(x) * weight + bias) * silu(z) without.  x, z: [..., width] of one dtype (each
     may be a slice of a packed tensor); weight, bias: [width] float32.  Returns out."""
     call = _fn("ssm_gated_norm_fwd")
-    dev, shape = x.device, x.shape
+    dev, shape = x.get_device(), x.shape
     width = shape[-1]
     rows = x.numel() // width if width else 0
     xp, xs = _rows(x, "x", shape, None, dev)
     zp, zs = _rows(z, "z", shape, x.dtype, dev)
     if out is None:
-        out = _new(shape, out_dtype or x.dtype, dev)
+        out = _new(shape, out_dtype or x.dtype, x)
     cols = (width,)
     _check(call(
         xp, xs, zp, zs, _want(weight, "weight", cols, _F32, dev), _want(bias, "bias", cols, _F32, dev), eps,
@@ -241,7 +239,7 @@ def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1
     dx, dz (where z is given), and dweight and dbias as asked (dbias by default where
     ``bias`` is given)."""
     call = _fn("ssm_gated_norm_bwd")
-    dev, shape = x.device, x.shape
+    dev, shape = x.get_device(), x.shape
     width = shape[-1]
     rows = x.numel() // width if width else 0
     if want_bias is None:
@@ -249,13 +247,13 @@ def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1
     xp, xs = _rows(x, "x", shape, None, dev)
     zp, zs = _rows(z, "z", shape, x.dtype, dev)
     cols = (width,)
-    g = {"dx": _new(shape, x.dtype, dev)}
+    g = {"dx": _new(shape, x.dtype, dout)}
     if z is not None:
-        g["dz"] = _new(shape, x.dtype, dev)
+        g["dz"] = _new(shape, x.dtype, dout)
     if want_weight:
-        g["dweight"] = _new(cols, _F32, dev)
+        g["dweight"] = _new(cols, _F32, dout)
     if want_bias:
-        g["dbias"] = _new(cols, _F32, dev)
+        g["dbias"] = _new(cols, _F32, dout)
     ptr = {k: v.data_ptr() for k, v in g.items()}
     _check(call(
         _want(dout, "dout", shape, None, dev), xp, xs, zp, zs, _want(weight, "weight", cols, _F32, dev),
@@ -280,10 +278,10 @@ def _la_shapes(q, v, tokens: int):
     return q.shape[-2], q.shape[-1], v.shape[-2], v.shape[-1]
 
 
-def _la_decay(g, lead, nheads, device):
+def _la_decay(g, lead, nheads, dev):
     """(pointer, flags) of the log decay: [*lead, nheads], or [nheads] for a fixed one."""
     fixed = g.dim() == 1
-    return (_want(g, "log_decay", (nheads,) if fixed else (*lead, nheads), _F32, device),
+    return (_want(g, "log_decay", (nheads,) if fixed else (*lead, nheads), _F32, dev),
             SSM_LINATTN_FIXED_DECAY if fixed else 0)
 
 
@@ -297,14 +295,14 @@ def ssm_linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, initial_s
     ``plan`` = {"chunk_len": ..} forces the time chunks."""
     call = _fn("ssm_linattn_fwd")
     G, dk, H, dv = _la_shapes(q, v, 2)
-    B, L, dev = q.shape[0], q.shape[1], q.device
+    B, L, dev = q.shape[0], q.shape[1], q.get_device()
     qs, vs, st = (B, L, G, dk), (B, L, H, dv), (B, H, dv, dk)
     qp, qr = _rows(q, "q", qs, None, dev, 2)
     kp, kr = _rows(k, "k", qs, q.dtype, dev, 2)
     vp, vr = _rows(v, "v", vs, q.dtype, dev, 2)
     gp, flags = _la_decay(log_decay, (B, L), H, dev)
     if out is None:
-        out = _new(vs, out_dtype or v.dtype, dev)
+        out = _new(vs, out_dtype or v.dtype, q)
     p = None
     if plan is not None:
         p = ssm_plan()
@@ -326,7 +324,7 @@ def ssm_linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, ini
     asked, dinitial_state."""
     call = _fn("ssm_linattn_bwd")
     G, dk, H, dv = _la_shapes(q, v, 2)
-    B, L, dev = q.shape[0], q.shape[1], q.device
+    B, L, dev = q.shape[0], q.shape[1], q.get_device()
     qs, vs, st = (B, L, G, dk), (B, L, H, dv), (B, H, dv, dk)
     gdt = grad_dtype or q.dtype
     _kind(gdt)
@@ -334,10 +332,10 @@ def ssm_linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, ini
     kp, kr = _rows(k, "k", qs, q.dtype, dev, 2)
     vp, vr = _rows(v, "v", vs, q.dtype, dev, 2)
     gp, flags = _la_decay(log_decay, (B, L), H, dev)
-    g = {"dq": _new(qs, gdt, dev), "dk": _new(qs, gdt, dev), "dv": _new(vs, gdt, dev),
-         "dlog_decay": _new(log_decay.shape, _F32, dev)}
+    g = {"dq": _new(qs, gdt, q), "dk": _new(qs, gdt, q), "dv": _new(vs, gdt, q),
+         "dlog_decay": _new(log_decay.shape, _F32, q)}
     if want_dinitial_state:
-        g["dinitial_state"] = _new(st, _F32, dev)
+        g["dinitial_state"] = _new(st, _F32, q)
     _check(call(
         qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
         _want(initial_state, "initial_state", st, _F32, dev), _want(dout, "dout", vs, q.dtype, dev),
@@ -355,11 +353,11 @@ def ssm_linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] =
     float32.  Returns out [batch, nheads, dv]."""
     call = _fn("ssm_linattn_state_update")
     G, dk, H, dv = _la_shapes(q, v, 1)
-    B, dev = q.shape[0], q.device
+    B, dev = q.shape[0], q.get_device()
     qs, vs, st = (B, G, dk), (B, H, dv), (B, H, dv, dk)
     gp, flags = _la_decay(log_decay, (B,), H, dev)
     if out is None:
-        out = _new(vs, out_dtype or v.dtype, dev)
+        out = _new(vs, out_dtype or v.dtype, q)
     sp = _want(state, "state", st, _F32, dev)
     _check(call(
         sp, sp if state_out is None else _want(state_out, "state_out", st, _F32, dev), _want(q, "q", qs, None, dev),
@@ -380,9 +378,9 @@ def ssm_q4_quantize(w, group: int = 128, scale_dtype=None, stream=None):
     n, k = w.shape
     if group not in (32, 64, 128) or k % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide k={k}, got {group}")
-    dev, ng = w.device, k // group
-    codes, zeros = _new((n, k // 2), _U8, dev), _new((n, ng), _U8, dev)
-    scales = _new((n, ng), scale_dtype or _F32, dev)
+    dev, ng = w.get_device(), k // group
+    codes, zeros = _new((n, k // 2), _U8, w), _new((n, ng), _U8, w)
+    scales = _new((n, ng), scale_dtype or _F32, w)
     _kind(scales.dtype)
     _check(call(_want(w, "w", w.shape, None, dev), codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), n, k,
                                   group, _code[w.dtype], _code[scales.dtype], _on(stream, dev)))
@@ -395,7 +393,7 @@ def ssm_q4_matvec(x, codes, scales, zeros=None, bias=None, out=None, out_dtype=N
     bfloat16), zeros [n, k // group] uint8 (None: 8), bias [n] float32.  Returns out
     [..., n] (allocated if None, dtype ``out_dtype`` or x's)."""
     call = _fn("ssm_q4_matvec")
-    dev = x.device
+    dev = x.get_device()
     if codes.dim() != 2 or scales.dim() != 2 or x.dim() < 1:
         raise ValueError("x must be [..., k], codes [n, k // 2] and scales [n, k // group]")
     n, k = codes.shape[0], 2 * codes.shape[1]
@@ -405,7 +403,7 @@ def ssm_q4_matvec(x, codes, scales, zeros=None, bias=None, out=None, out_dtype=N
         raise ValueError(f"x has {x.shape[-1]} columns, codes {k} and scales {ng} groups")
     shape = (*x.shape[:-1], n)
     if out is None:
-        out = _new(shape, out_dtype or x.dtype, dev)
+        out = _new(shape, out_dtype or x.dtype, x)
     xp, xr = _rows(x, "x", x.shape, None, dev)
     m = x.numel() // k if k else out.numel() // n if n else 0
     _check(call(
