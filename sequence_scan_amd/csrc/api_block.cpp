@@ -206,21 +206,22 @@ ssm_status la_rows(const char* name, int64_t rows, int64_t width, int64_t row, i
 }
 
 // Time chunks of a forward.  A workgroup walks 64 value columns of one (batch
-// row, head), and three fit a CU: one round of them, as long as time chunks keep
-// 1024 steps; with shorter ones two per CU, of at least 128 steps, since a time
-// chunk costs a fixed part and the carry between them runs over all (microseconds,
-// dk = dv = 128 where not said):
-//   1 x 65537, 16 heads of 64 x 128: 16 chunks 371, 24 321, 32 326, 48 342
-//   1 x 16384, 32 heads: 8 chunks 256, 12 246, 16 264    1 x 8192, 8 heads: 16 66, 32 56, 48 60
-//   1 x 2048, 8 heads: 4 chunks 59, 16 36, 32 36         1 x 131072, 2 heads of 128 x 64: 256 138, 384 165
-// More workgroups than CUs are not cut: 8 x 2048, 40 heads: 1 chunk 222, 2 275.
+// row, head), and three fit a CU: one round of them, up to 24 time chunks of at
+// least 256 steps; past that two per CU, of at least 128 steps, since a time chunk
+// costs a fixed part and the carry runs over all of them (microseconds, dk = dv =
+// 128 where not said):
+//   1 x 65537, 16 heads of 64 x 128: 16 chunks 344, 24 297, 32 291, 48 300
+//   1 x 16384, 32 heads: 8 chunks 241, 12 236, 16 252    4 x 2048, 32 heads: 1 chunk 126, 2 130, 3 119, 4 135
+//   1 x 8192, 8 heads: 16 chunks 61, 32 50, 48 56         1 x 2048, 8 heads: 4 chunks 59, 16 34, 32 34
+//   1 x 131072, 2 heads of 128 x 64: 256 chunks 98, 384 108
+// More workgroups than CUs are not cut: 4 x 2048, 40 heads: 1 chunk 148, 2 165.
 void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, int simds, ssm_plan* p) {
   const int64_t wgs = std::max<int64_t>(1, batch * nheads * ((dv + 63) / 64));
   const int64_t cus = std::max(1, simds / 4);
   int64_t chunks = 1;
   if (wgs <= cus) {
     chunks = 3 * cus / wgs;
-    if (seqlen / chunks < 1024) chunks = std::min(2 * cus / wgs, std::max<int64_t>(1, seqlen / 128));
+    if (chunks > 24 || seqlen / chunks < 256) chunks = std::min(2 * cus / wgs, std::max<int64_t>(1, seqlen / 128));
   }
   int64_t len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
   if (chunks > 1) len = (len + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;

@@ -36,11 +36,24 @@ __global__ void __launch_bounds__(256) la_carry_kernel(LaWalk a) {
   const int h = blockIdx.y;
   const int64_t b = blockIdx.z;
   const int K = a.n_chunks;
+  constexpr int kAhead = 8;      // slots loaded before the first of them is stored
   float S = 0.0f;
-  for (int i = 0; i + 1 < K; ++i) {
-    const int64_t slot = (b * K + (REV ? K - 1 - i : i)) * a.nheads + h;
-    S = __builtin_fmaf(__builtin_amdgcn_exp2f(a.chunk_decay[slot]), S, a.chunk_out[slot * per + e]);
-    a.chunk_out[slot * per + e] = S;
+  for (int i0 = 0; i0 + 1 < K; i0 += kAhead) {
+    float end[kAhead], decay[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i + 1 >= K) break;
+      const int64_t slot = (b * K + (REV ? K - 1 - i0 - i : i0 + i)) * a.nheads + h;
+      end[i] = a.chunk_out[slot * per + e];
+      decay[i] = a.chunk_decay[slot];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i + 1 >= K) break;
+      const int64_t slot = (b * K + (REV ? K - 1 - i0 - i : i0 + i)) * a.nheads + h;
+      S = __builtin_fmaf(__builtin_amdgcn_exp2f(decay[i]), S, end[i]);
+      a.chunk_out[slot * per + e] = S;
+    }
   }
 }
 
