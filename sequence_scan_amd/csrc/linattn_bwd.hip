@@ -14,6 +14,11 @@
 // to chunk: <S, R> at a chunk's end is X + sum b, at its start X + sum a; it is a
 // plain dot product of two states where the walks or a time chunk start and end,
 // which bounds how far rounding travels.
+//
+// Measured: 4 x 2048, 40 heads of 128 x 128, 420 us, of which the decay's kernel is
+// 18 us; the bytes that have to move would take 114 us at a copy's rate.  The walks'
+// registers (the decay's gradient takes a third term of the state's rounding) leave
+// two workgroups per CU, so that the chunks' chains bound it as in the forward.
 #include <algorithm>
 
 #include "linattn_kernel.h"

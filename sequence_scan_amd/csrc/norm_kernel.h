@@ -9,6 +9,10 @@
 //             S2 = sum u (r - m) gives both 1 / std and mean(u n):
 //             dr = (u - [mean u] - (r - m) S2 / (W std^2)) / std
 // Memory is what bounds it: a few operations per element against 4 to 20 bytes.
+// Measured (a copy of 1 GiB runs at 5.2 TB/s): add norm of 16384 x 2560, bf16 into an
+// fp32 residual, 95 us, 5.3 TB/s, its backward with all three column sums 144 + 5 us,
+// 5.2 TB/s; gated norm of 16384 x 5120 102 us, 4.9 TB/s; the backward over 80 heads of
+// 64 164 + 4 us, 5.1 TB/s.  One row of 2560 takes 2.2 us, a launch's own time.
 //
 // Two layouts.  Up to 512 channels, T lanes of a wavefront (8, 16, 32 or 64)
 // hold one norm, and the sums stay within the wavefront (DPP and the row
@@ -16,7 +20,8 @@
 // wavefront then covers 64 / T norms: neighbouring groups of one row first,
 // which are contiguous in memory, rows after that.  Above 1024, a workgroup of
 // up to 16 wavefronts holds one norm and joins its wavefronts' sums in LDS.
-// Workgroups walk the rows with the stride of the grid.
+// Workgroups walk the rows with the stride of the grid, 8 (backward: 4, whose column
+// sums are a row of workspace each) of four wavefronts per CU.
 //
 // Widths need not be multiples of eight: the last active lane's eight channels
 // end at the width and overlap its neighbour's; the repeated ones are left out
