@@ -626,9 +626,12 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   if (K > 65535) return fail(SSM_ERR_UNSUPPORTED, "seqlen=%lld gives more than 65535 time chunks", (long long)seqlen);
   if (share > 1 && sz.qk / 4 > kMaxThreads)
     return fail(SSM_ERR_UNSUPPORTED, "q and k of %lld elements exceed the grid that sums their heads' gradients", (long long)sz.qk);
-  int64_t n_state, n_heads, n_part, n_grad;
+  const int64_t q_chunks = (std::min(seqlen, plan.chunk_len) + ssm::kLaQ - 1) / ssm::kLaQ;
+  const int64_t snap_slots = fixed ? (q_chunks - 1) / ssm::kLaSnap : 0;
+  int64_t n_state, n_heads, n_part, n_grad, n_snap;
   if (!mul_ok(sz.state, K, &n_state) || !mul_ok(batch * nheads, K, &n_heads) || !mul_ok(sz.rows * nheads, nk, &n_part) ||
-      !mul_ok(sz.rows * nheads, dk, &n_grad))
+      !mul_ok(sz.rows * nheads, dk, &n_grad) ||
+      !mul_ok(n_heads, snap_slots * nk * (dv > 64 ? 8192 : 4096), &n_snap))
     return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
   Pieces w;
   const bool cut = K > 1;
@@ -636,7 +639,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
                 at_rev = w.add(cut ? n_state : 0), at_fd = w.add(cut ? n_heads : 0), at_rd = w.add(cut ? n_heads : 0),
                 at_last = w.add(dlast_state ? sz.state : 0),
                 at_init = w.add(initial_state ? sz.state : 0), at_dq = w.add(share > 1 ? n_grad : 0),
-                at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? n_heads : 0);
+                at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? n_heads : 0), at_sq = w.add(n_snap), at_sk = w.add(n_snap);
   if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
   void* ws = nullptr;
   e = ws_alloc(&ws, w.floats * 4, s);
@@ -656,6 +659,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   base.nheads = (int32_t)nheads;
   base.out_bf16 = grad_dtype == SSM_BF16;
   base.w_scale = scale;
+  base.snap_slots = (int32_t)snap_slots;
   // the states at time chunk borders, values v (forward) and dout (back)
   ssm::LaWalk fs = base, rs = base;
   fs.B = ok_;
@@ -687,6 +691,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   a.dq.last = dlast_state ? f + at_last : nullptr;
   a.dq.chunk_states = f + at_fwd;
   a.dq.part = f + at_pq;
+  a.dq.snaps = snap_slots > 0 ? f + at_sq : nullptr;
   a.dq.row_scale = scale;
   a.dq.src_scale = 1.0f;
   a.dk = base;
@@ -698,6 +703,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
   a.dk.first = dlast_state;
   a.dk.chunk_states = f + at_rev;
   a.dk.part = f + at_pk;
+  a.dk.snaps = snap_slots > 0 ? f + at_sk : nullptr;
   a.dk.row_scale = 1.0f;
   a.dk.src_scale = scale;
   for (ssm::LaWalk* p : {&a.dq, &a.dk}) {   // values k and q: states read transposed

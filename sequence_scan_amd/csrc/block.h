@@ -59,6 +59,8 @@ hipError_t launch_norm_sums(const float* part, int blocks, int sums, int64_t wid
 
 constexpr int kLaQ = 32;            // steps per matrix chunk
 constexpr int kLaBwdChunk = 2048;   // steps per time chunk of the backward, at most
+constexpr int kLaSnap = 8;          // matrix chunks between two states kept for a fixed decay's gradient
+constexpr int kLaSnapParts = kLaBwdChunk / kLaQ / kLaSnap;   // parts of a time chunk between them, at most
 constexpr int kLaMaxDim = 128;      // dk and dv of the chunked form, multiples of 8
 constexpr int kLaMaxStepDk = 256;   // dk of the single-token step, a multiple of 4
 
@@ -84,12 +86,14 @@ struct LaWalk {
   const float* chunk_states;  // n_chunks > 1: [batch, n_chunks, nheads, ..], after the carry
   float* chunk_out;           // state pass: each time chunk's end state
   float* chunk_decay;         // state pass: [batch, n_chunks, nheads] summed log2 decay
+  float* snaps;               // dq and dk walks, fixed decay: [batch, nheads, n_chunks, snap_slots, slices, 4096 or 8192]
   float* part;                // dq and dk walks: [slices, batch, nheads, seqlen]
   int64_t seqlen, chunk_len;
   int64_t st_x, st_c;
   int32_t n_chunks, batch, nheads;
   int32_t xdim, cdim;
   int32_t out_bf16;
+  int32_t snap_slots;         // states kept within a time chunk: one less than its parts of kLaSnap matrix chunks
   float w_scale, row_scale, src_scale;
 };
 

@@ -156,6 +156,25 @@ __device__ __forceinline__ double la_prefix32(double v) {
   return v;
 }
 
+// 2^c rounded to fp32 once: the power series of e^(f ln 2) to its seventh power, for
+// the rest f of c to the nearest integer (the eighth is below 2^-27).  The hardware's
+// exponential is off by up to an ulp, and with a fixed decay by the same in every
+// chunk, which adds up over a state's memory and in the decay's gradient.
+__device__ __forceinline__ float la_exp2(double c) {
+  constexpr double kLn2 = 0.6931471805599453;
+  constexpr double c1 = kLn2, c2 = c1 * kLn2 / 2, c3 = c2 * kLn2 / 3, c4 = c3 * kLn2 / 4, c5 = c4 * kLn2 / 5, c6 = c5 * kLn2 / 6,
+                   c7 = c6 * kLn2 / 7;
+  const double n = __builtin_rint(c), f = c - n;
+  double p = __builtin_fma(c7, f, c6);
+  p = __builtin_fma(p, f, c5);
+  p = __builtin_fma(p, f, c4);
+  p = __builtin_fma(p, f, c3);
+  p = __builtin_fma(p, f, c2);
+  p = __builtin_fma(p, f, c1);
+  p = __builtin_fma(p, f, 1.0);
+  return __builtin_amdgcn_ldexpf((float)p, (int)n);
+}
+
 // The sum over the 16 lanes of a DPP row, in all of them.
 __device__ __forceinline__ float la_row_sum(float v) {
   v += SSM_DPP(0.0f, v, 0xB1, 0xf);    // quad_perm [1,0,3,2]
@@ -305,13 +324,14 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     const float one = g * kLog2e;
     const double c = la_prefix32((double)(one < -160.0f ? -160.0f : one));
     const double c_end = __shfl(c, 31, 32);
-    const float hi = (float)c, rest = (float)(c_end - c);
+    const float hi = (float)c;
+    const float to_here = la_exp2(c), to_end = la_exp2(c_end - c);
     csum += (float)c_end;
     s.cum[to][step] = hi;
     s.low[to][step] = (float)(c - (double)hi);
-    s.row[to][step] = __builtin_amdgcn_exp2f(REV ? rest : hi) * a.row_scale;
-    s.src[to][step] = __builtin_amdgcn_exp2f(REV ? hi : rest) * a.src_scale;
-    if (step == 0) s.end[to] = __builtin_amdgcn_exp2f((float)c_end);
+    s.row[to][step] = (REV ? to_end : to_here) * a.row_scale;
+    s.src[to][step] = (REV ? to_here : to_end) * a.src_scale;
+    if (step == 31) s.end[to] = to_here;
   };
 
   // S^T: tile t holds contracted columns [16 t, 16 t + 16) x this wavefront's 16
@@ -402,6 +422,18 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
         }
     }
   };
+  // The state at every kLaSnap chunks from the sequence's start on, as the wavefronts
+  // hold it, for the decay's gradient.  The dq walk passes a border between two chunks
+  // before the later one, the dk walk before the earlier one.
+  auto store_snap = [&](int ch) SSM_INLINE {
+    const int border = REV ? chunks - ch : ch;
+    if (a.snaps == nullptr || border % kLaSnap != 0) return;
+    constexpr int kTiles = NT * 256;        // float4 of a wavefront's tiles, all four of them
+    const int64_t slot = (((int64_t)b * a.nheads + h) * K + kt) * a.snap_slots + border / kLaSnap - 1;
+    f32x4_t* to = reinterpret_cast<f32x4_t*>(a.snaps) + (slot * ((a.xdim + 63) / 64) + slice) * kTiles + tid;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) to[t * 256] = accS[t];
+  };
   float part = 0.0f;
   auto store_part = [&](int ch) SSM_INLINE {
     if (tid < steps_of(ch)) {
@@ -430,9 +462,11 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       if (REV ? ch == 0 : ch + 2 == chunks) set_offsets(steps_of(ch + 1));
       load_bx(cur ^ 1);
     }
-    if (ch % 8 == 0 && ch + 8 < chunks) {
-      sum_decays(ch + 8);
-      if (ch + 16 < chunks) get_decays(ch + 16);
+    if constexpr (cur == 0) {      // (every eighth chunk is even)
+      if (ch % 8 == 0 && ch + 8 < chunks) {
+        sum_decays(ch + 8);
+        if (ch + 16 < chunks) get_decays(ch + 16);
+      }
     }
 
     if constexpr (kOut) {
@@ -617,8 +651,12 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     block_sync();
   };
   for (int ch = 0; ch < chunks; ch += 2) {
+    if constexpr (kZ)
+      if (ch > 0) store_snap(ch);
     chunk(ch, std::integral_constant<int, 0>());
-    if (ch + 1 < chunks) chunk(ch + 1, std::integral_constant<int, 1>());
+    if (ch + 1 >= chunks) break;
+    if constexpr (kZ && REV) store_snap(ch + 1);     // (forward, a border is even)
+    chunk(ch + 1, std::integral_constant<int, 1>());
   }
   if constexpr (kOut) {
     store(chunks - 1);
@@ -628,16 +666,21 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   const int far = REV ? 0 : K - 1;
   float* dst = KIND == kWalkState ? a.chunk_out + ((int64_t)(b * K + kt) * a.nheads + h) * per
               : kt == far && a.last != nullptr ? a.last + ((int64_t)b * a.nheads + h) * per : nullptr;
-  if (dst != nullptr && p < xdim) {
+  // (the lane's place is formed anew, not held through the chunks)
+  int lane = threadIdx.x & 63;
+  asm("" : "+v"(lane));
+  const int px = 16 * w + lane % 16;
+  const uint32_t at = (uint32_t)(x0 + px) * (uint32_t)a.st_x;
+  if (dst != nullptr && px < xdim) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int c = 16 * t + 4 * q;
+      const int c = 16 * t + 4 * (lane / 16);
       if (c >= a.cdim) continue;
       if (a.st_c == 1) {
-        *reinterpret_cast<f32x4_t*>(dst + sx + c) = accS[t];
+        *reinterpret_cast<f32x4_t*>(dst + at + c) = accS[t];
       } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dst[sx + (uint32_t)(c + r) * (uint32_t)a.st_c] = accS[t][r];
+        for (int r = 0; r < 4; ++r) dst[at + (uint32_t)(c + r) * (uint32_t)a.st_c] = accS[t][r];
       }
     }
   }

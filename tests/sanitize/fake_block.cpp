@@ -156,6 +156,10 @@ hipError_t launch_la_bwd(const LaBwd& a, hipStream_t) {
     touch("initial", a.initial, state, 4);
     touch("dinitial", a.dinitial, state, 4);
   }
+  const int64_t kept = bn * q.n_chunks * q.snap_slots * ((q.xdim + 63) / 64) * (q.cdim > 64 ? 8192 : 4096);
+  if (!a.fixed_decay && q.snap_slots > 0) std::abort();
+  touch("dq snaps", a.dq.snaps, kept, 4);
+  touch("dk snaps", a.dk.snaps, kept, 4);
   touch("ddecay", a.ddecay, a.fixed_decay ? bn * q.n_chunks : bn * q.seqlen, 4);
   return hipSuccess;
 }
