@@ -639,7 +639,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
                 at_rev = w.add(cut ? n_state : 0), at_fd = w.add(cut ? n_heads : 0), at_rd = w.add(cut ? n_heads : 0),
                 at_last = w.add(dlast_state ? sz.state : 0),
                 at_init = w.add(initial_state ? sz.state : 0), at_dq = w.add(share > 1 ? n_grad : 0),
-                at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? n_heads : 0), at_sq = w.add(n_snap), at_sk = w.add(n_snap);
+                at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? 2 * n_heads : 0), at_sq = w.add(n_snap), at_sk = w.add(n_snap);
   if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
   void* ws = nullptr;
   e = ws_alloc(&ws, w.floats * 4, s);

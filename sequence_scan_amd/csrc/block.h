@@ -107,7 +107,7 @@ struct LaBwd {
   const float* dlast;         // nullable
   const float* initial;       // nullable: the forward's initial state, and with it
   const float* dinitial;      // ... its gradient (left by the dk walk)
-  float* ddecay;              // [batch, seqlen, nheads], or the partial sums [batch, n_chunks, nheads]
+  float* ddecay;              // [batch, seqlen, nheads], or the partial sums [batch, n_chunks, nheads, 2]
   int32_t fixed_decay;
 };
 
@@ -133,7 +133,7 @@ hipError_t launch_la_bwd(const LaBwd& a, hipStream_t s);
 // out[row, g, d] = sum over the `share` heads of group g of in[row, g, i, d].
 hipError_t launch_la_group_sum(const float* in, void* out, bool out_bf16, int64_t rows, int ngroups, int share, int dim,
                                hipStream_t s);
-// out[h] = sum over n rows of in[n, h].
+// out[h] = sum over n rows of in[n, h, 0] + in[n, h, 1].
 hipError_t launch_la_decay_sum(const float* in, float* out, int64_t n, int nheads, hipStream_t s);
 hipError_t launch_la_step(const LaStep& a, DT in, DT out, hipStream_t s);
 

@@ -163,7 +163,10 @@ __global__ void __launch_bounds__(64 * kDecayWaves) la_decay_kernel(LaBwd a) {
       double r = 0.0;
 #pragma unroll
       for (int i = 0; i < kDecayWaves; ++i) r += ssum[i];
-      a.ddecay[(int64_t)(b * K + kt) * H + h] = (float)r;
+      // (as two floats: the time chunks' parts can be much larger than their sum)
+      const int64_t at = ((int64_t)(b * K + kt) * H + h) * 2;
+      a.ddecay[at] = (float)r;
+      a.ddecay[at + 1] = (float)(r - (double)(float)r);
     }
   }
 }
@@ -190,9 +193,12 @@ __global__ void __launch_bounds__(256) la_group_sum_kernel(const float* in, Tout
 __global__ void __launch_bounds__(256) la_decay_sum_kernel(const float* in, float* out, int64_t n, int nheads) {
   const int h = (int)(blockIdx.x * 256 + threadIdx.x);
   if (h >= nheads) return;
-  float s = 0.0f;
-  for (int64_t i = 0; i < n; ++i) s += in[i * nheads + h];
-  out[h] = s;
+  double s = 0.0;
+  for (int64_t i = 0; i < n; ++i) {
+    const float2 p = *reinterpret_cast<const float2*>(in + (i * nheads + h) * 2);
+    s += (double)p.x + (double)p.y;
+  }
+  out[h] = (float)s;
 }
 
 }  // namespace

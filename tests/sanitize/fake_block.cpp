@@ -160,7 +160,7 @@ hipError_t launch_la_bwd(const LaBwd& a, hipStream_t) {
   if (!a.fixed_decay && q.snap_slots > 0) std::abort();
   touch("dq snaps", a.dq.snaps, kept, 4);
   touch("dk snaps", a.dk.snaps, kept, 4);
-  touch("ddecay", a.ddecay, a.fixed_decay ? bn * q.n_chunks : bn * q.seqlen, 4);
+  touch("ddecay", a.ddecay, a.fixed_decay ? bn * q.n_chunks * 2 : bn * q.seqlen, 4);
   return hipSuccess;
 }
 
@@ -172,7 +172,7 @@ hipError_t launch_la_group_sum(const float* in, void* out, bool out_bf16, int64_
 }
 
 hipError_t launch_la_decay_sum(const float* in, float* out, int64_t n, int nheads, hipStream_t) {
-  touch("in", in, n * nheads, 4);
+  touch("in", in, n * nheads * 2, 4);
   touch("out", out, nheads, 4);
   ++g_block_launches;
   return hipSuccess;
