@@ -173,7 +173,7 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
  * 8 * batch * n_chunks * nheads * (dk * dv + 1), with dlast_state and
  * with initial_state batch * nheads * dk * dv * 4 each, with nheads > ngroups
  * batch * seqlen * nheads * dk * 8 more, with a fixed decay 8 * dk * dv (each
- * rounded up to 64 or 128) for every 256 steps of a head.  Alignment and rows as above, gradients
+ * rounded up to 64 or 128) for every 128 steps of a head.  Alignment and rows as above, gradients
  * and dout 16-byte aligned.
  */
 ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,

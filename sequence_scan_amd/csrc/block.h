@@ -59,7 +59,7 @@ hipError_t launch_norm_sums(const float* part, int blocks, int sums, int64_t wid
 
 constexpr int kLaQ = 32;            // steps per matrix chunk
 constexpr int kLaBwdChunk = 2048;   // steps per time chunk of the backward, at most
-constexpr int kLaSnap = 8;          // matrix chunks between two states kept for a fixed decay's gradient
+constexpr int kLaSnap = 4;          // matrix chunks between two states kept for a fixed decay's gradient
 constexpr int kLaSnapParts = kLaBwdChunk / kLaQ / kLaSnap;   // parts of a time chunk between them, at most
 constexpr int kLaMaxDim = 128;      // dk and dv of the chunked form, multiples of 8
 constexpr int kLaMaxStepDk = 256;   // dk of the single-token step, a multiple of 4
