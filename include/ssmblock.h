@@ -28,6 +28,19 @@ extern "C" {
 #endif
 
 /*
+ * A call whose comment names a workspace takes it from the library's pool of the
+ * device, which costs tens of microseconds of the host's time.  ssm_workspace
+ * offers memory of the caller's for the calling thread's next such call, of at least
+ * ssm_workspace_bytes() bytes, 16-byte aligned, that nothing but the call's stream uses
+ * until the call's kernels have run; the call takes from the pool what does not
+ * fit.  The offer ends with that call, also if it is refused; NULL withdraws it.
+ * ssm_workspace_bytes: what the thread's last such call wanted (0: nothing); it
+ * depends on the call's sizes, types, flags and absent tensors alone.
+ */
+ssm_status ssm_workspace(void* memory, int64_t bytes);
+int64_t ssm_workspace_bytes(void);
+
+/*
  * Bits of the norm calls' flags:
  *   SSM_NORM_CENTER     subtract the mean first (layer norm); without it the
  *                       rows are divided by their root mean square.

@@ -549,4 +549,4 @@ def ssm_ssd_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, so
 from .block import (SSM_LINATTN_FIXED_DECAY, SSM_NORM_CENTER, SSM_NORM_GATE_LAST,  # noqa: E402,F401
                     ssm_add_norm_bwd, ssm_add_norm_fwd, ssm_gated_norm_bwd, ssm_gated_norm_fwd, ssm_linattn_bwd,
                     ssm_linattn_fwd, ssm_linattn_plan_query, ssm_linattn_state_update, ssm_q4_matvec,
-                    ssm_q4_quantize)
+                    ssm_q4_quantize, ssm_workspace, ssm_workspace_bytes)

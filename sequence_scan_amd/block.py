@@ -31,6 +31,8 @@ _ARGS = {
                        [_int, _int, _vp],
     "ssm_q4_matvec": [_vp, _i64] + [_vp] * 5 + [_i64] * 4 + [_int, _int, _int, _vp],
     "ssm_q4_quantize": [_vp] * 4 + [_i64] * 3 + [_int, _int, _vp],
+    "ssm_workspace": [_vp, _i64],
+    "ssm_workspace_bytes": [],
     "ssm_linattn_state_update": [_vp] * 6 + [_int, _f32, _vp] + [_i64] * 5 + [_int, _int, _vp],
 }
 _fns: dict = {}
@@ -44,7 +46,7 @@ def _fn(name: str):
     if f is None:
         _start()
         f = getattr(_load(), name)
-        f.argtypes, f.restype = _ARGS[name], ctypes.c_int
+        f.argtypes, f.restype = _ARGS[name], _i64 if name == "ssm_workspace_bytes" else ctypes.c_int
         _fns[name] = f
     return f
 
@@ -197,13 +199,45 @@ def ssm_add_norm_bwd(dout, r, weight=None, dresidual_out=None, x=None, scale=Non
     if want_scale:
         g["dscale"] = _new(cols, _F32, dout)
     ptr = {k: v.data_ptr() for k, v in g.items()}
-    _check(call(
+    key = ("add", rows, width, r.dtype, dout.dtype, want_weight, want_bias, want_scale, dev)
+    _with_workspace(call, key, dout, stream, (
         _want(dout, "dout", shape, None, dev), _want(r, "r", shape, None, dev), _want(weight, "weight", cols, _F32, dev),
         _want(dresidual_out, "dresidual_out", shape, r.dtype, dev), xp, xs, _want(scale, "scale", cols, _F32, dev),
         alpha, eps, SSM_NORM_CENTER if center else 0, ptr["dx"], ptr["dresidual"], ptr.get("dweight"),
         ptr.get("dbias"), ptr.get("dscale"), rows, width, _code[g["dx"].dtype], _code[r.dtype], _code[dout.dtype],
         _on(stream, dev)))
     return g
+
+
+_wanted: dict = {}          # sizes and kind of a call -> bytes of workspace that it wants
+
+
+def ssm_workspace(memory, nbytes: int):
+    """Offer device memory (a pointer, or None) for this thread's next call that needs a
+    workspace (include/ssmblock.h).  The calls below do so themselves."""
+    _check(_fn("ssm_workspace")(memory, nbytes))
+
+
+def ssm_workspace_bytes() -> int:
+    """Bytes of workspace that this thread's last call wanted."""
+    return _fn("ssm_workspace_bytes")()
+
+
+def _with_workspace(call, key, like, stream, args):
+    """The call, with memory of PyTorch's for its workspace: 2 us in place of the 28 us that
+    the library's own allocation takes.  What a call of these sizes wants is known
+    after the first one.  A caller's own stream is not PyTorch's current one: there
+    the library allocates."""
+    n = _wanted.get(key)
+    if n and stream is None:
+        t = _empty((n,), dtype=_U8, device=like.device)
+        _fn("ssm_workspace")(t.data_ptr(), n)
+    status = call(*args)
+    if n is None and status == 0:
+        if len(_wanted) >= 4096:
+            _wanted.clear()
+        _wanted[key] = _fn("ssm_workspace_bytes")()
+    _check(status)
 
 
 def _norm_flags(center, gate_first):
@@ -255,7 +289,8 @@ def ssm_gated_norm_bwd(dout, x, z=None, weight=None, bias=None, ngroups: int = 1
     if want_bias:
         g["dbias"] = _new(cols, _F32, dout)
     ptr = {k: v.data_ptr() for k, v in g.items()}
-    _check(call(
+    key = ("gate", rows, width, ngroups, x.dtype, dout.dtype, want_weight, want_bias, dev)
+    _with_workspace(call, key, dout, stream, (
         _want(dout, "dout", shape, None, dev), xp, xs, zp, zs, _want(weight, "weight", cols, _F32, dev),
         _want(bias, "bias", cols, _F32, dev), eps, _norm_flags(center, gate_first), ptr["dx"], ptr.get("dz"),
         ptr.get("dweight"), ptr.get("dbias"), rows, width, ngroups, _code[x.dtype], _code[dout.dtype],
@@ -308,7 +343,9 @@ def ssm_linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, initial_s
         p = ssm_plan()
         p.chunk_len = int(plan["chunk_len"])
         p = ctypes.byref(p)
-    _check(call(
+    in_place = initial_state is not None and initial_state is last_state
+    key = ("la", B, L, H, dk, dv, 0 if plan is None else plan["chunk_len"], in_place, dev)
+    _with_workspace(call, key, q, stream, (
         qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
         _want(initial_state, "initial_state", st, _F32, dev), _want(out, "out", vs, None, dev),
         _want(last_state, "last_state", st, _F32, dev), B, L, H, G, dk, dv, _code[q.dtype], _code[out.dtype],
@@ -336,7 +373,8 @@ def ssm_linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, ini
          "dlog_decay": _new(log_decay.shape, _F32, q)}
     if want_dinitial_state:
         g["dinitial_state"] = _new(st, _F32, q)
-    _check(call(
+    key = ("la_bwd", B, L, H, G, dk, dv, flags, initial_state is None, dlast_state is None, dev)
+    _with_workspace(call, key, q, stream, (
         qp, qr, kp, kr, vp, vr, gp, flags, dk ** -0.5 if scale is None else scale,
         _want(initial_state, "initial_state", st, _F32, dev), _want(dout, "dout", vs, q.dtype, dev),
         _want(dlast_state, "dlast_state", st, _F32, dev), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
@@ -406,7 +444,7 @@ def ssm_q4_matvec(x, codes, scales, zeros=None, bias=None, out=None, out_dtype=N
         out = _new(shape, out_dtype or x.dtype, x)
     xp, xr = _rows(x, "x", x.shape, None, dev)
     m = x.numel() // k if k else out.numel() // n if n else 0
-    _check(call(
+    _with_workspace(call, ("q4", m, n, k, group, x.dtype, dev), x, stream, (
         xp, xr, _want(codes, "codes", (n, k // 2), _U8, dev), _want(scales, "scales", (n, ng), None, dev),
         _want(zeros, "zeros", (n, ng), _U8, dev), _want(bias, "bias", (n,), _F32, dev),
         _want(out, "out", shape, None, dev), m, n, k, group, _code[x.dtype], _code[scales.dtype], _code[out.dtype],

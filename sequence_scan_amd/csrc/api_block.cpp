@@ -58,6 +58,43 @@ ssm_status check_args(std::initializer_list<Arg> ins, std::initializer_list<Arg>
   return SSM_OK;
 }
 
+// The memory that the calling thread offered for its next call (ssm_workspace),
+// and what its last call wanted.
+struct Offer {
+  void* p;
+  int64_t bytes;
+  int64_t wanted;
+};
+thread_local Offer g_offer{nullptr, 0, 0};
+
+// A call's workspace: the offered memory, where it is large enough, or memory of
+// the library's pool.  An offer is for one call, whatever comes of it.
+class Workspace {
+ public:
+  Workspace() : offer_(g_offer) { g_offer = Offer{nullptr, 0, 0}; }
+  hipError_t get(void** p, int64_t bytes, hipStream_t s) {
+    g_offer.wanted = bytes;
+    if (offer_.p != nullptr && bytes <= offer_.bytes) {
+      *p = offer_.p;
+      return hipSuccess;
+    }
+    const hipError_t e = ws_alloc(&own_, bytes, s);
+    *p = own_;
+    return e;
+  }
+  // After the call's launches: their status, or that of the release.
+  hipError_t done(hipError_t launched, hipStream_t s) {
+    if (own_ == nullptr) return launched;
+    const hipError_t e = hipFreeAsync(own_, s);
+    own_ = nullptr;
+    return launched == hipSuccess ? e : launched;
+  }
+
+ private:
+  Offer offer_;
+  void* own_ = nullptr;
+};
+
 // ----------------------------------------------------------------------- norms
 
 // A grid dimension holds fewer than 2^32 threads (16 per channel in the kernel
@@ -107,7 +144,7 @@ ssm_status norm_extent(const char* name, int64_t rows, int64_t width, int64_t st
 
 // The backward's launches: the kernel, then the join of its column sums.
 template <typename Launch>
-ssm_status norm_bwd_run(ssm::NormArgs& a, float* const sums[3], Launch launch, hipStream_t s) {
+ssm_status norm_bwd_run(Workspace& work, ssm::NormArgs& a, float* const sums[3], Launch launch, hipStream_t s) {
   const int64_t width = (int64_t)a.groups * a.width;
   const bool want = sums[0] || sums[1] || sums[2];
   a.sums = sums[2] ? 3 : 2;
@@ -118,16 +155,13 @@ ssm_status norm_bwd_run(ssm::NormArgs& a, float* const sums[3], Launch launch, h
     blocks = ssm::norm_row_blocks(a);
     int64_t bytes;
     if (!mul_ok((int64_t)blocks * a.sums, width * 4, &bytes)) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
-    e = ws_alloc(&ws, bytes, s);
+    e = work.get(&ws, bytes, s);
     if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)bytes, e);
     a.part = static_cast<float*>(ws);
   }
   e = launch(a);
   if (e == hipSuccess && want) e = ssm::launch_norm_sums(a.part, blocks, a.sums, width, sums, s);
-  if (ws) {
-    const hipError_t e2 = hipFreeAsync(ws, s);
-    if (e == hipSuccess) e = e2;
-  }
+  e = work.done(e, s);
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return ok();
 }
@@ -294,6 +328,17 @@ struct Pieces {
 
 extern "C" {
 
+ssm_status ssm_workspace(void* memory, int64_t bytes) {
+  g_offer = Offer{nullptr, 0, 0};
+  if (bytes < 0) return fail(SSM_ERR_BAD_SHAPE, "negative size (bytes=%lld)", (long long)bytes);
+  const ssm_status st = check_align("memory", memory, 16);
+  if (st != SSM_OK) return st;
+  if (memory != nullptr) g_offer = Offer{memory, bytes, 0};
+  return ok();
+}
+
+int64_t ssm_workspace_bytes(void) { return g_offer.wanted; }
+
 ssm_status ssm_add_norm_fwd(const void* x, int64_t x_stride, const void* residual, const float* weight,
                             const float* bias, const float* scale, float alpha, float eps, int flags, void* out,
                             void* residual_out, int64_t rows, int64_t width, ssm_dtype x_dtype,
@@ -340,6 +385,7 @@ ssm_status ssm_add_norm_bwd(const void* dout, const void* r, const float* weight
                             void* dx, void* dresidual, float* dweight, float* dbias, float* dscale, int64_t rows,
                             int64_t width, ssm_dtype x_dtype, ssm_dtype res_dtype, ssm_dtype out_dtype,
                             void* stream) {
+  Workspace work;
   NormSizes sz;
   ssm_status st = norm_check(rows, width, 1, eps, flags, SSM_NORM_CENTER, {x_dtype, res_dtype, out_dtype}, &sz);
   if (st != SSM_OK) return st;
@@ -380,7 +426,7 @@ ssm_status ssm_add_norm_bwd(const void* dout, const void* r, const float* weight
   a.center = (flags & SSM_NORM_CENTER) != 0;
   a.x_bf16 = x_dtype == SSM_BF16;
   a.cus = device_simds() / 4;
-  return norm_bwd_run(a, sums, [&](const ssm::NormArgs& n) { return ssm::launch_add_norm_bwd(n, to_dt(out_dtype), to_dt(res_dtype), s); }, s);
+  return norm_bwd_run(work, a, sums, [&](const ssm::NormArgs& n) { return ssm::launch_add_norm_bwd(n, to_dt(out_dtype), to_dt(res_dtype), s); }, s);
 }
 
 ssm_status ssm_gated_norm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const float* weight,
@@ -426,6 +472,7 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
                               const float* weight, const float* bias, float eps, int flags, void* dx, void* dz,
                               float* dweight, float* dbias, int64_t rows, int64_t width, int64_t ngroups,
                               ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream) {
+  Workspace work;
   NormSizes sz;
   ssm_status st = norm_check(rows, width, ngroups, eps, flags, SSM_NORM_CENTER | SSM_NORM_GATE_LAST,
                              {in_dtype, out_dtype}, &sz);
@@ -465,7 +512,7 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
   a.center = (flags & SSM_NORM_CENTER) != 0;
   a.gate_last = (flags & SSM_NORM_GATE_LAST) != 0;
   a.cus = device_simds() / 4;
-  return norm_bwd_run(a, sums, [&](const ssm::NormArgs& n) { return ssm::launch_gated_norm_bwd(n, to_dt(in_dtype), to_dt(out_dtype), s); }, s);
+  return norm_bwd_run(work, a, sums, [&](const ssm::NormArgs& n) { return ssm::launch_gated_norm_bwd(n, to_dt(in_dtype), to_dt(out_dtype), s); }, s);
 }
 
 ssm_status ssm_linattn_plan_query(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dk, int64_t dv,
@@ -484,6 +531,7 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
                            float* last_state, int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups,
                            int64_t dk, int64_t dv, ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream,
                            const ssm_plan* plan_in) {
+  Workspace work;
   LaSizes sz;
   ssm_status st = la_check(batch, seqlen, nheads, ngroups, dk, dv, flags, scale, {in_dtype, out_dtype}, &sz);
   if (st == SSM_OK) st = la_check_chunked(batch, nheads, dk, dv, in_dtype, 2);
@@ -559,7 +607,7 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
     Pieces w;
     const int64_t at_state = w.add(n_state), at_decay = w.add(n_decay), at_copy = w.add(in_place ? sz.state : 0);
     if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
-    e = ws_alloc(&ws, w.floats * 4, s);
+    e = work.get(&ws, w.floats * 4, s);
     if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)(w.floats * 4), e);
     float* f = static_cast<float*>(ws);
     a.chunk_out = f + at_state;
@@ -572,10 +620,7 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
     if (e == hipSuccess) e = ssm::launch_la_states(a, false, s);
   }
   if (e == hipSuccess) e = ssm::launch_la_fwd(a, s);
-  if (ws) {
-    const hipError_t e2 = hipFreeAsync(ws, s);
-    if (e == hipSuccess) e = e2;
-  }
+  e = work.done(e, s);
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return ok();
 }
@@ -586,6 +631,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
                            float* dlog_decay, float* dinitial_state, int64_t batch, int64_t seqlen, int64_t nheads,
                            int64_t ngroups, int64_t dk, int64_t dv, ssm_dtype in_dtype, ssm_dtype grad_dtype,
                            void* stream) {
+  Workspace work;
   LaSizes sz;
   ssm_status st = la_check(batch, seqlen, nheads, ngroups, dk, dv, flags, scale, {in_dtype, grad_dtype}, &sz);
   if (st == SSM_OK) st = la_check_chunked(batch, nheads, dk, dv, in_dtype, 6);
@@ -642,7 +688,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
                 at_dk = w.add(share > 1 ? n_grad : 0), at_dec = w.add(fixed ? 2 * n_heads : 0), at_sq = w.add(n_snap), at_sk = w.add(n_snap);
   if (!w.fits) return fail(SSM_ERR_BAD_SHAPE, "workspace size overflows int64");
   void* ws = nullptr;
-  e = ws_alloc(&ws, w.floats * 4, s);
+  e = work.get(&ws, w.floats * 4, s);
   if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)(w.floats * 4), e);
   float* f = static_cast<float*>(ws);
 
@@ -745,8 +791,7 @@ ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t 
     if (e == hipSuccess) e = ssm::launch_la_group_sum(f + at_dk, dk_, b16, sz.rows, (int)ngroups, (int)share, (int)dk, s);
   }
   if (fixed && e == hipSuccess) e = ssm::launch_la_decay_sum(f + at_dec, dlog_decay, batch * K, (int)nheads, s);
-  const hipError_t e2 = hipFreeAsync(ws, s);
-  if (e == hipSuccess) e = e2;
+  e = work.done(e, s);
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return ok();
 }
@@ -793,6 +838,7 @@ ssm_status ssm_linattn_state_update(const float* state, float* state_out, const 
 ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, const void* scales, const uint8_t* zeros,
                          const float* bias, void* out, int64_t m, int64_t n, int64_t k, int64_t group,
                          ssm_dtype in_dtype, ssm_dtype scale_dtype, ssm_dtype out_dtype, void* stream) {
+  Workspace work;
   ssm_status st = q4_check(m, n, k, group, {in_dtype, scale_dtype, out_dtype});
   if (st != SSM_OK) return st;
   const int64_t si = esize(in_dtype), ss = esize(scale_dtype), so = esize(out_dtype);
@@ -834,15 +880,12 @@ ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, con
   void* ws = nullptr;
   hipError_t e = hipSuccess;
   if (const int64_t bytes = ssm::q4_image_bytes(a)) {
-    e = ws_alloc(&ws, bytes, s);
+    e = work.get(&ws, bytes, s);
     if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)bytes, e);
     a.image = static_cast<char*>(ws);
   }
   e = ssm::launch_q4(a, s);
-  if (ws) {
-    const hipError_t e2 = hipFreeAsync(ws, s);
-    if (e == hipSuccess) e = e2;
-  }
+  e = work.done(e, s);
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return ok();
 }

@@ -49,6 +49,22 @@ void rejected(const char* what, ssm_status want, F call) {
   }
 }
 
+// The call with its workspace offered: exactly what it wants, and too little.
+template <typename F>
+void offered(const char* what, F call) {
+  expect(what, call(), SSM_OK);
+  const int64_t n = ssm_workspace_bytes();
+  if (n == 0) return;
+  for (int64_t room : {n, n - 1}) {
+    expect(what, ssm_workspace(buf(room, 1), room), SSM_OK);
+    expect(what, call(), SSM_OK);
+    if (ssm_workspace_bytes() != n) {
+      std::fprintf(stderr, "%s: wants %lld bytes, then %lld\n", what, (long long)n, (long long)ssm_workspace_bytes());
+      ++g_failures;
+    }
+  }
+}
+
 const ssm_dtype kTypes[] = {SSM_F32, SSM_BF16};
 
 void add_norm(int64_t rows, int64_t width) {
@@ -69,7 +85,7 @@ void add_norm(int64_t rows, int64_t width) {
         auto bwd = [&](void* dro, void* dres, float* w1, float* b1, float* s1, void* px) {
           return ssm_add_norm_bwd(out, r, w, dro, x, stride, sc, 0.5f, 1e-5f, 0, px, dres, w1, b1, s1, rows, width, xt, rt, ot, nullptr);
         };
-        expect("add_norm_bwd", bwd(ro, dr, dw, db, ds, dx), SSM_OK);
+        offered("add_norm_bwd", [&] { return bwd(ro, dr, dw, db, ds, dx); });
         expect("add_norm_bwd in place", bwd(ro, ro, dw, nullptr, nullptr, dx), SSM_OK);
         expect("add_norm_bwd bare", bwd(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr), SSM_OK);
         if (n > 0) {
@@ -98,7 +114,7 @@ void gated_norm(int64_t rows, int64_t width, int64_t groups) {
           auto bwd = [&](float* w1, float* b1) {
             return ssm_gated_norm_bwd(out, x, sx, g, sz, w, b, 1e-5f, flags, dx, g ? dz : nullptr, w1, b1, rows, width, groups, it, ot, nullptr);
           };
-          expect("gated_norm_bwd", bwd(dw, db), SSM_OK);
+          offered("gated_norm_bwd", [&] { return bwd(dw, db); });
           expect("gated_norm_bwd without sums", bwd(nullptr, nullptr), SSM_OK);
         }
         if (n > 0) {
@@ -135,7 +151,7 @@ void linattn(int64_t B, int64_t L, int64_t H, int64_t G, int64_t K, int64_t V) {
       ssm_plan p{};
       for (int64_t c : {32, 64, 96}) {
         p.chunk_len = c;
-        expect("linattn plan", fwd(st, st, &p), SSM_OK);
+        offered("linattn plan", [&] { return fwd(st, st, &p); });
         expect("linattn plan", fwd(nullptr, st2, &p), SSM_OK);
       }
       if (L > 32 && B > 0) {
@@ -153,7 +169,7 @@ void linattn(int64_t B, int64_t L, int64_t H, int64_t G, int64_t K, int64_t V) {
         return ssm_linattn_bwd(q, row, k, row, v, row, g, flags, 0.5f, first, dout, dlast, dq, dk, dv, dg, dfirst, B, L, H, G, K, V,
                                SSM_BF16, ot, nullptr);
       };
-      expect("linattn_bwd", bwd(st, st2, st3), SSM_OK);
+      offered("linattn_bwd", [&] { return bwd(st, st2, st3); });
       expect("linattn_bwd bare", bwd(nullptr, nullptr, nullptr), SSM_OK);
       expect("linattn_bwd dlast", bwd(nullptr, st2, nullptr), SSM_OK);
       expect("linattn_bwd initial", bwd(st, nullptr, st3), SSM_OK);
@@ -187,7 +203,7 @@ void q4(int64_t m, int64_t n, int64_t k, int64_t group) {
         auto call = [&](const uint8_t* z, const float* b) {
           return ssm_q4_matvec(x, row, codes, sc, z, b, out, m, n, k, group, it, st, ot, nullptr);
         };
-        expect("q4", call(zeros, bias), SSM_OK);
+        offered("q4", [&] { return call(zeros, bias); });
         expect("q4 bare", call(nullptr, nullptr), SSM_OK);
         expect("q4 quantize", ssm_q4_quantize(w, codes, sc, zeros, n, k, group, it, st, nullptr), SSM_OK);
         if (m > 16 && n > 0 && k > 0) {

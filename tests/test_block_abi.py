@@ -28,7 +28,7 @@ def declared():
 def test_every_declared_function_is_exported_and_bound():
     lib = ssm.library()
     names = declared()
-    assert len(names) == 10
+    assert len(names) == 12
     for n in names:
         assert hasattr(lib, n), f"{n} is declared in ssmblock.h but not exported"
         assert n in block._ARGS
@@ -149,6 +149,15 @@ BAD = [
 def test_refusal(call, kw, status, says):
     assert call(**kw) == status, ssm.ssm_last_error()
     assert says in ssm.ssm_last_error()
+
+
+def test_workspace_offers():
+    offer = block._fn("ssm_workspace")
+    assert offer(ptr(0), 4096) == ssm.SSM_OK and ssm.ssm_workspace_bytes() == 0
+    assert offer(ptr(0) + 8, 4096) == UNSUPPORTED and offer(ptr(0), -1) == SHAPE
+    assert offer(None, 0) == ssm.SSM_OK
+    assert offer(ptr(0), 4096) == ssm.SSM_OK
+    assert la_bwd(batch=-1) == SHAPE and ssm.ssm_workspace_bytes() == 0     # (a refused call ends the offer)
 
 
 @pytest.mark.parametrize("chunk_len", [-1, 0, 31, 33])

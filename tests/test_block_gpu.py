@@ -119,6 +119,21 @@ def test_another_stream(name):
         assert torch.equal(a, b)
 
 
+def test_workspace_from_either_side():
+    """A shape's first call takes its workspace from the library, later ones from PyTorch."""
+    from sequence_scan_amd import block
+    for name, call in operators().items():
+        block._wanted.clear()
+        first = [t.clone() for t in call()]
+        wants = any(block._wanted.values())
+        assert wants == (name in ("add_norm_bwd", "gated_norm_bwd", "linattn", "linattn in time chunks", "linattn_bwd",
+                                  "linattn_bwd, fixed decay", "q4, rows laid out")), name
+        for _ in range(2):
+            torch.empty(1 << 20, device="cuda").fill_(float("nan"))
+            for a, b in zip(call(), first):
+                assert torch.equal(a, b), name
+
+
 def test_given_stream():
     x, w = randn(64, 256), randn(256, dtype=F32, seed=1)
     want, _ = ssm.ssm_add_norm_fwd(x, None, w)
