@@ -20,8 +20,8 @@
 // every eight chunks and by 7e-7 with every four; 4 x 2048, 40 heads then take 427, 464
 // and 514 us.
 //
-// Measured: 4 x 2048, 40 heads of 128 x 128, 420 us, of which the decay's kernel is
-// 18 us; the bytes that have to move would take 114 us at a copy's rate.  The walks'
+// Measured: 4 x 2048, 40 heads of 128 x 128, 421 us, of which the decay's kernel is
+// 14 us; the bytes that have to move would take 114 us at a copy's rate.  The walks'
 // registers (the decay's gradient takes a third term of the state's rounding) leave
 // two workgroups per CU, so that the chunks' chains bound it as in the forward.
 #include <algorithm>

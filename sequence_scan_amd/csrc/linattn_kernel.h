@@ -30,7 +30,7 @@
 // ds_read_b64_tr_b16.
 //
 // Chunks of 32 steps: chunks of 64 halve the work on the state (its rounding for the
-// readout and its scaling, two thirds of a wavefront's vector instructions here), but
+// readout and its scaling, two fifths of a wavefront's vector instructions here), but
 // hold twice the LDS, so two workgroups per CU in place of three.
 //
 // What bounds it: prompts of 8 x 2048, 40 heads of 128 x 128, take 207 us, 3.4 TB/s of
