@@ -172,7 +172,8 @@ __device__ __forceinline__ float la_exp2(double c) {
   p = __builtin_fma(p, f, c2);
   p = __builtin_fma(p, f, c1);
   p = __builtin_fma(p, f, 1.0);
-  return __builtin_amdgcn_ldexpf((float)p, (int)n);
+  // (held within an int; NaN stays in p)
+  return __builtin_amdgcn_ldexpf((float)p, (int)__builtin_fmin(__builtin_fmax(n, -2000.0), 2000.0));
 }
 
 // The sum over the 16 lanes of a DPP row, in all of them.

@@ -325,3 +325,23 @@ def test_example_block():
     assert errors["residual"] == 0.0
     for name, e in errors.items():
         assert e <= (9.4e-2 if name.startswith("d ") else 4.7e-2), (name, e)
+
+
+@pytest.mark.parametrize("plan", [None, {"chunk_len": 64}])
+@pytest.mark.parametrize("which", ["decay", "q", "k"])
+def test_values_that_are_not_finite_reach_their_head_only(which, plan):
+    """A NaN of a decay or of k at step t of one head: its outputs are NaN from there on
+    (of q: that step's alone); earlier steps and other heads and batch rows keep their bits."""
+    d = draw(2, 200, 3, 3, 64, 72, seed=9)
+    q, k, v, g = (d[n][0] for n in ("q", "k", "v", "g"))
+    clean = ssm.ssm_linattn_fwd(q, k, v, g, plan=plan)
+    b, t, h = 1, 77, 1
+    if which == "decay":
+        g[b, t, h] = float("nan")
+    else:
+        (q if which == "q" else k)[b, t, h, 5] = float("nan")
+    got = ssm.ssm_linattn_fwd(q, k, v, g, plan=plan)
+    hit = torch.zeros(got.shape[:3], dtype=torch.bool, device="cuda")
+    hit[b, t:t + 1 if which == "q" else None, h] = True
+    assert torch.isnan(got[hit]).all()
+    assert torch.equal(got[~hit], clean[~hit])
