@@ -214,7 +214,9 @@ _wanted: dict = {}          # sizes and kind of a call -> bytes of workspace tha
 
 def ssm_workspace(memory, nbytes: int):
     """Offer device memory (a pointer, or None) for this thread's next call that needs a
-    workspace (include/ssmblock.h).  The calls below do so themselves."""
+    workspace (include/ssmblock.h).  The calls of this module do so themselves, except on a
+    stream of the caller's.  An offer is the caller's to withdraw where the call that it was for
+    raises before the library is entered (a tensor of the wrong shape or type)."""
     _check(_fn("ssm_workspace")(memory, nbytes))
 
 
@@ -231,8 +233,16 @@ def _with_workspace(call, key, like, stream, args):
     n = _wanted.get(key)
     if n and stream is None:
         t = _empty((n,), dtype=_U8, device=like.device)
-        _fn("ssm_workspace")(t.data_ptr(), n)
-    status = call(*args)
+        try:
+            _fn("ssm_workspace")(t.data_ptr(), n)
+            status = call(*args)
+        except BaseException:
+            # the library may not have been entered (an argument that ctypes cannot
+            # convert): the offer must not outlive t, for a later call to write into
+            _fn("ssm_workspace")(None, 0)
+            raise
+    else:
+        status = call(*args)
     if n is None and status == 0:
         if len(_wanted) >= 4096:
             _wanted.clear()
