@@ -59,21 +59,24 @@ ssm_status check_args(std::initializer_list<Arg> ins, std::initializer_list<Arg>
 }
 
 // The memory that the calling thread offered for its next call (ssm_workspace),
-// and what its last call wanted.
+// and the bytes that its last call wanted.
 struct Offer {
   void* p;
   int64_t bytes;
-  int64_t wanted;
 };
-thread_local Offer g_offer{nullptr, 0, 0};
+thread_local Offer g_offer{nullptr, 0};
+thread_local int64_t g_wanted = 0;
 
 // A call's workspace: the offered memory, where it is large enough, or memory of
 // the library's pool.  An offer is for one call, whatever comes of it.
 class Workspace {
  public:
-  Workspace() : offer_(g_offer) { g_offer = Offer{nullptr, 0, 0}; }
+  Workspace() : offer_(g_offer) {
+    g_offer = Offer{nullptr, 0};
+    g_wanted = 0;
+  }
   hipError_t get(void** p, int64_t bytes, hipStream_t s) {
-    g_offer.wanted = bytes;
+    g_wanted = bytes;
     if (offer_.p != nullptr && bytes <= offer_.bytes) {
       *p = offer_.p;
       return hipSuccess;
@@ -329,15 +332,15 @@ struct Pieces {
 extern "C" {
 
 ssm_status ssm_workspace(void* memory, int64_t bytes) {
-  g_offer = Offer{nullptr, 0, 0};
+  g_offer = Offer{nullptr, 0};
   if (bytes < 0) return fail(SSM_ERR_BAD_SHAPE, "negative size (bytes=%lld)", (long long)bytes);
   const ssm_status st = check_align("memory", memory, 16);
   if (st != SSM_OK) return st;
-  if (memory != nullptr) g_offer = Offer{memory, bytes, 0};
+  if (memory != nullptr) g_offer = Offer{memory, bytes};
   return ok();
 }
 
-int64_t ssm_workspace_bytes(void) { return g_offer.wanted; }
+int64_t ssm_workspace_bytes(void) { return g_wanted; }
 
 ssm_status ssm_add_norm_fwd(const void* x, int64_t x_stride, const void* residual, const float* weight,
                             const float* bias, const float* scale, float alpha, float eps, int flags, void* out,

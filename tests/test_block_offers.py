@@ -99,3 +99,21 @@ def test_no_offer_outlives_a_call_that_the_library_refuses(fake):
     with pytest.raises(ssm.SSMError):
         block._with_workspace(call, "key", like, None, [*args[:8], -1.0, *args[9:]])
     assert takes_from_pool(fake, keep, args)
+
+
+def test_bytes_are_those_of_the_last_call_whatever_is_offered(fake):
+    """ssm_workspace_bytes answers for the thread's last call: an offer, or its withdrawal, is none."""
+    args, keep = add_norm_bwd_args()
+    assert block._fn("ssm_add_norm_bwd")(*args) == ssm.SSM_OK
+    n = ssm.ssm_workspace_bytes()
+    assert n > 0
+    memory = torch.zeros(n + 16, dtype=torch.uint8)
+    ssm.ssm_workspace(memory.data_ptr() + -memory.data_ptr() % 16, n)
+    assert ssm.ssm_workspace_bytes() == n
+    ssm.ssm_workspace(None, 0)
+    assert ssm.ssm_workspace_bytes() == n
+    with pytest.raises(ssm.SSMError):
+        ssm.ssm_workspace(memory.data_ptr() + 1, n)
+    assert ssm.ssm_workspace_bytes() == n
+    assert block._fn("ssm_add_norm_bwd")(*args[:8], -1.0, *args[9:]) == ssm.SSM_ERR_UNSUPPORTED
+    assert ssm.ssm_workspace_bytes() == 0           # (a refused call wants nothing)
