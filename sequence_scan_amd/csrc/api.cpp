@@ -35,7 +35,7 @@ void choose_plan(int64_t batch, int64_t seqlen, int64_t d_inner, int simds, ssm_
     chunks = (3 * cus + blocks - 1) / blocks;
     chunks = std::min(chunks, std::max<int64_t>(1, seqlen / 512));
   }
-  int64_t chunk_len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
+  int64_t chunk_len = seqlen > 0 ? ceil_div(seqlen, chunks) : 1;
   // a cut sequence is cut at multiples of the kernel's 32-step tile, so that
   // only the last chunk can have a ragged tile
   if (chunks > 1) chunk_len = (chunk_len + 31) / 32 * 32;
@@ -43,7 +43,7 @@ void choose_plan(int64_t batch, int64_t seqlen, int64_t d_inner, int simds, ssm_
   p->states_per_wave = 4;
   p->reserved0 = 0;
   p->chunk_len = chunk_len;
-  p->n_chunks = seqlen > 0 ? (seqlen + chunk_len - 1) / chunk_len : 0;
+  p->n_chunks = ceil_div(seqlen, chunk_len);
   for (auto& r : p->reserved) r = 0;
 }
 
@@ -77,13 +77,13 @@ void choose_bwd_plan(int64_t batch, int64_t seqlen, int64_t d_inner, int simds, 
     chunks = (24 * cus + blocks - 1) / blocks;
     chunks = std::min(chunks, std::max<int64_t>(1, seqlen / 512));
   }
-  int64_t chunk_len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
+  int64_t chunk_len = seqlen > 0 ? ceil_div(seqlen, chunks) : 1;
   if (chunks > 1) chunk_len = (chunk_len + ssm::kBwdTile - 1) / ssm::kBwdTile * ssm::kBwdTile;
   if (chunk_len < 1) chunk_len = 1;
   p->states_per_wave = 4;
   p->reserved0 = 0;
   p->chunk_len = chunk_len;
-  p->n_chunks = seqlen > 0 ? (seqlen + chunk_len - 1) / chunk_len : 0;
+  p->n_chunks = ceil_div(seqlen, chunk_len);
   for (auto& r : p->reserved) r = 0;
 }
 
@@ -101,13 +101,13 @@ void choose_ssd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int simds, s
     chunks = (12 * cus + wgs - 1) / wgs;
     chunks = std::min(chunks, std::max<int64_t>(1, seqlen / 1024));
   }
-  int64_t chunk_len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
+  int64_t chunk_len = seqlen > 0 ? ceil_div(seqlen, chunks) : 1;
   if (chunks > 1) chunk_len = (chunk_len + 31) / 32 * 32;
   if (chunk_len < 1) chunk_len = 1;
   p->states_per_wave = 0;
   p->reserved0 = 0;
   p->chunk_len = chunk_len;
-  p->n_chunks = seqlen > 0 ? (seqlen + chunk_len - 1) / chunk_len : 0;
+  p->n_chunks = ceil_div(seqlen, chunk_len);
   for (auto& r : p->reserved) r = 0;
 }
 
@@ -219,7 +219,7 @@ ssm_status scan_impl(const void* x, const void* delta, const float* A, const voi
     if (ns != 1 && ns != 2 && ns != 4 && ns != 8 && ns != 16)
       return fail(SSM_ERR_UNSUPPORTED, "plan.states_per_wave=%d not in {1,2,4,8,16}", ns);
     if (plan.chunk_len < 1) return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len must be >= 1");
-    plan.n_chunks = seqlen > 0 ? (seqlen + plan.chunk_len - 1) / plan.chunk_len : 0;
+    plan.n_chunks = ceil_div(seqlen, plan.chunk_len);
     if (plan.n_chunks > 65535) return fail(SSM_ERR_UNSUPPORTED, "plan gives more than 65535 chunks");
   } else {
     choose_plan(batch, seqlen, d_inner, device_simds(), &plan);
@@ -516,7 +516,7 @@ static ssm_status bwd_impl(const void* x, const void* delta, const float* A, con
       return fail(SSM_ERR_UNSUPPORTED, "plan.states_per_wave=%d: the backward carries 4 states per wavefront",
                   plan.states_per_wave);
     if (plan.chunk_len < 1) return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len must be >= 1");
-    plan.n_chunks = seqlen > 0 ? (seqlen + plan.chunk_len - 1) / plan.chunk_len : 0;
+    plan.n_chunks = ceil_div(seqlen, plan.chunk_len);
     if (plan.n_chunks > 1 && plan.chunk_len % ssm::kBwdTile != 0)
       return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len=%lld must be a multiple of %d when it cuts the sequence",
                   (long long)plan.chunk_len, ssm::kBwdTile);
@@ -805,7 +805,7 @@ static ssm_status ssd_impl(const void* x, const void* dt, const float* A, const 
   if (plan_in) {
     plan = *plan_in;
     if (plan.chunk_len < 1) return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len must be >= 1");
-    plan.n_chunks = seqlen > 0 ? (seqlen + plan.chunk_len - 1) / plan.chunk_len : 0;
+    plan.n_chunks = ceil_div(seqlen, plan.chunk_len);
     if (plan.n_chunks > 1 && plan.chunk_len % 32 != 0)
       return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len=%lld must be a multiple of 32 when it cuts the sequence",
                   (long long)plan.chunk_len);

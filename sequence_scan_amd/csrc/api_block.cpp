@@ -260,11 +260,11 @@ void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, i
     chunks = 3 * cus / wgs;
     if (chunks > 24 || seqlen / chunks < 256) chunks = std::min(2 * cus / wgs, std::max<int64_t>(1, seqlen / 128));
   }
-  int64_t len = seqlen > 0 ? (seqlen + chunks - 1) / chunks : 1;
+  int64_t len = seqlen > 0 ? ceil_div(seqlen, chunks) : 1;
   if (chunks > 1) len = (len + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
   *p = ssm_plan{};
   p->chunk_len = std::max<int64_t>(1, len);
-  p->n_chunks = seqlen > 0 ? (seqlen + p->chunk_len - 1) / p->chunk_len : 0;
+  p->n_chunks = ceil_div(seqlen, p->chunk_len);
 }
 
 // Time chunks of a backward: at most kLaBwdChunk steps each, and more where its
@@ -275,13 +275,13 @@ void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, i
 void choose_la_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t slots, int simds, ssm_plan* p) {
   const int64_t wgs = std::max<int64_t>(1, batch * nheads * slots);
   const int64_t cus = std::max(1, simds / 4);
-  int64_t chunks = (seqlen + ssm::kLaBwdChunk - 1) / ssm::kLaBwdChunk;
+  int64_t chunks = ceil_div(seqlen, ssm::kLaBwdChunk);
   if (wgs <= cus) chunks = std::max(chunks, std::min(6 * cus / wgs, seqlen / 256));
   chunks = std::max<int64_t>(1, chunks);
-  const int64_t len = ((seqlen + chunks - 1) / chunks + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
+  const int64_t len = (ceil_div(seqlen, chunks) + ssm::kLaQ - 1) / ssm::kLaQ * ssm::kLaQ;
   *p = ssm_plan{};
   p->chunk_len = std::max<int64_t>(ssm::kLaQ, len);
-  p->n_chunks = (seqlen + p->chunk_len - 1) / p->chunk_len;
+  p->n_chunks = ceil_div(seqlen, p->chunk_len);
 }
 
 ssm::LaOperand la_operand(const void* p, int64_t row, int64_t dim, int64_t share) {
@@ -556,7 +556,7 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
   if (plan_in != nullptr) {
     plan = *plan_in;
     if (plan.chunk_len < 1) return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len must be >= 1");
-    plan.n_chunks = seqlen > 0 ? (seqlen + plan.chunk_len - 1) / plan.chunk_len : 0;
+    plan.n_chunks = ceil_div(seqlen, plan.chunk_len);
     if (plan.n_chunks > 1 && plan.chunk_len % ssm::kLaQ != 0)
       return fail(SSM_ERR_UNSUPPORTED, "plan.chunk_len=%lld must be a multiple of %d when it cuts the sequence",
                   (long long)plan.chunk_len, ssm::kLaQ);

@@ -128,6 +128,9 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t* r) {
   return true;
 }
 
+// ceil(n / parts) for n >= 0 and parts >= 1, over their whole range.
+inline int64_t ceil_div(int64_t n, int64_t parts) { return n / parts + (n % parts != 0); }
+
 inline int64_t esize(ssm_dtype t) { return t == SSM_BF16 ? 2 : 4; }
 
 inline bool valid_dtype(ssm_dtype t) { return t == SSM_F32 || t == SSM_BF16; }
