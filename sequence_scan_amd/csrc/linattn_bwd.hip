@@ -40,7 +40,9 @@ __global__ void __launch_bounds__(256, 2) la_bwd_kernel(LaBwd a) {
     LaTile<CV, kWalkDk> dk;
     LaTile<CK, kWalkOut> dv;
   };
-  __shared__ __attribute__((aligned(16))) char raw[sizeof(Tiles)];
+  // (the tiles' own alignment: their swizzled addresses are formed by it)
+  __shared__ __attribute__((aligned(alignof(Tiles)))) char raw[sizeof(Tiles)];
+  static_assert(__alignof__(raw) == alignof(Tiles) && alignof(Tiles) == 1024, "the tiles' place");
   const int nk = (a.dq.xdim + 63) / 64, nv = (a.dv.xdim + 63) / 64;
   int bh, slot;
   la_place(blockIdx.x, a.dq.batch * a.dq.nheads, 2 * nk + nv, &bh, &slot);
