@@ -21,7 +21,7 @@ __device__ __forceinline__ void load_lds(const char* base, uint32_t off, void* t
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
-      : "memory", "m0");
+      : "memory");   // (m0 is a scratch register: whoever needs it sets it)
 }
 // Waits until at most N of the wavefront's loads and stores, the youngest, are
 // still under way.
