@@ -148,8 +148,9 @@ ssm_status ssm_gated_norm_bwd(const void* dout, const void* x, int64_t x_stride,
  * rows multiples of 8 elements and at most 2^24; nheads a multiple of ngroups,
  * at most 65535, as batch, and batch * nheads below 2^23 (backward: 2.7 million);
  * states and out 16-byte aligned.  The state, the sums and the
- * decays are fp32; the products run on bf16 matrix cores with computed operands
- * split into two bf16 terms (about 16 significant bits).  A value of v that is
+ * decays are fp32; the products run on bf16 matrix cores with fp32 sums, computed
+ * operands split into three bf16 terms (all 24 bits), so that fp32 outputs, gradients and
+ * states are off by fp32 roundings alone.  A value of v that is
  * not finite makes its column not finite from its step on, one of q, k or the
  * decays every column; earlier steps are not touched.
  *

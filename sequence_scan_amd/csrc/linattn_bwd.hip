@@ -17,13 +17,13 @@
 // steps, in which the errors of X that neighbouring steps share add up: there the dq
 // and dk walks keep S and R every four chunks, and X starts anew from each pair.  Of 6
 // x 5926 steps of 5 heads, the sums were off by 2.6e-6 without, by 1.6e-6 with states
-// every eight chunks and by 7e-7 with every four; 4 x 2048, 40 heads then take 427, 464
-// and 514 us.
+// every eight chunks and by 7e-7 with every four; 4 x 2048, 40 heads took 427, 464
+// and 514 us then.
 //
-// Measured: 4 x 2048, 40 heads of 128 x 128, 421 us, of which the decay's kernel is
-// 14 us; the bytes that have to move would take 114 us at a copy's rate.  The walks'
-// registers (the decay's gradient takes a third term of the state's rounding) leave
-// two workgroups per CU, so that the chunks' chains bound it as in the forward.
+// Measured: 4 x 2048, 40 heads of 128 x 128, 433 us (a fixed decay: 522), of which the
+// decay's kernel is 14 us; the bytes that have to move would take 114 us at a copy's
+// rate.  The walks' registers leave two workgroups per CU, so that the chunks' chains bound
+// it as in the forward.
 #include <algorithm>
 
 #include "linattn_kernel.h"

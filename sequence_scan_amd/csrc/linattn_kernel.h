@@ -13,12 +13,10 @@
 //
 // Per chunk, on v_mfma_f32_16x16x32_bf16 with fp32 accumulation:
 //   G = A B^T;  W = G o decay;  Y = diag(row) A S^T + W X;  S^T += B^T diag(src) X
-// A, B and X are bf16 inputs, exact as operands.  Computed operands are fp32 and
-// enter as sums of bf16 terms (v's rounding, the rest's rounding, ...): W and the
-// state in the readout as two, 2^-18 of the value off, which out's own rounding
-// hides; the scaled X of the state update as three, all its bits, since states
-// are kept and handed on in fp32.  The readout takes three terms too where the
-// decay's gradient comes of it, which adds up differences of such sums.
+// A, B and X are bf16 inputs, exact as operands.  Computed operands (W, the state in
+// the readout, the scaled X of the state update) are fp32 and enter as sums of three
+// bf16 terms (v's rounding, the rest's rounding, and its rest's), all their bits: outputs
+// may be fp32, and are then within fp32's own roundings of the exact sums.
 //
 // A workgroup of four wavefronts owns 64 value columns of one (batch row, head)
 // and walks its chunks of kLaQ steps; wavefront w holds columns 16 w .. 16 w + 15
@@ -33,11 +31,14 @@
 // readout and its scaling, two fifths of a wavefront's vector instructions here), but
 // hold twice the LDS, so two workgroups per CU in place of three.
 //
-// What bounds it: prompts of 8 x 2048, 40 heads of 128 x 128, take 207 us, 3.4 TB/s of
-// the bytes that they have to move (135 us at a copy's rate).  Without loads they take
-// 174 us, without stores 197 (of 226 then): a chunk's chain of products, roundings and
+// What bounds it: prompts of 8 x 2048, 40 heads of 128 x 128, take 231 us, 3.0 TB/s of
+// the bytes that they have to move (135 us at a copy's rate).  Of 226 us, before W and the
+// readout's state had their third term, they took 174 without loads and 197 without
+// stores: a chunk's chain of products, roundings and
 // two barriers is what its three wavefronts per SIMD wait for, and memory overlaps it
-// only in part.
+// only in part.  The third terms, 10 of a chunk's 58 products and an eighth of its vector
+// instructions, cost 205 -> 231 us here and 420 -> 433 us in the gradients; without them
+// fp32 outputs were off by 2.0e-6 to 2.5e-6 of their norm, with them by 1.3e-7.
 #ifndef SSMSCAN_LINATTN_KERNEL_H
 #define SSMSCAN_LINATTN_KERNEL_H
 
@@ -198,6 +199,8 @@ constexpr int kWalkState = 1;   // no rows and no output: the state at the end o
 constexpr int kWalkDq = 2;      // with the decay gradient's parts of dq: Z = q
 constexpr int kWalkDk = 3;      // ... of dk: Z = k
 
+constexpr int kLaTerms = 3;     // bf16 terms of an fp32 operand
+
 // LDS of one walk (C: contracted columns, 64 or 128).  B and X, which both
 // phases of a chunk read, are held twice: the next chunk's are loaded from the
 // chunk's start; A and Z, which only the first phase reads, from its middle.
@@ -211,7 +214,7 @@ struct LaTile {
   char X[2][kLaQ * 128] __attribute__((aligned(1024)));
   char A[kOut ? kLaQ * 2 * C : 16] __attribute__((aligned(1024)));
   char Z[kZ ? kLaQ * 128 : 16] __attribute__((aligned(1024)));
-  char W[2][kOut ? kLaQ * 64 : 16] __attribute__((aligned(16)));   // hi, lo
+  char W[kLaTerms][kOut ? kLaQ * 64 : 16] __attribute__((aligned(16)));   // by terms
   char Y[kOut ? kLaQ * 128 : 16] __attribute__((aligned(16)));     // bf16 output
   float cum[kRing][kLaQ] __attribute__((aligned(16)));   // log2 decay summed from the chunk's first step, inclusive
   float low[kRing][kLaQ] __attribute__((aligned(16)));   // what it lacks of the 64-bit sum
@@ -235,7 +238,6 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   constexpr int NR = kLaQ * 2 * C / 4096;     // loads of A and B per wavefront and chunk (of X and Z: one)
   constexpr bool kOut = T::kOut;
   constexpr bool kZ = T::kZ;
-  constexpr int kTerms = kZ ? 3 : 2;          // bf16 terms of the state in the readout
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = l & 15, q = l >> 4;
@@ -373,7 +375,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
   }
   if constexpr (kOut) {
     // W's block beyond the triangle
-    for (int e = tid; e < 2 * 256; e += 256) {
+    for (int e = tid; e < kLaTerms * 256; e += 256) {
       const int k = e >> 8, i = (e >> 4) & 15, j = e & 15;
       *reinterpret_cast<uint16_t*>(LaRows<64>{s.W[k]}.at(i + (REV ? 16 : 0), 2 * (j + (REV ? 0 : 16)))) = 0;
     }
@@ -490,11 +492,16 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
           const float d = __builtin_amdgcn_exp2f(REV ? cj[r] - ci + (lj[r] - li) : ci - cj[r] + (li - lj[r])) * a.w_scale;
           v[r] = (REV ? j0 + r >= i : j0 + r <= i) ? acc[r] * d : 0.0f;
         }
-        const uint2 hi = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        *reinterpret_cast<uint2*>(LaRows<64>{s.W[0]}.at(i, 2 * j0)) = hi;
-        const uint2 lo = make_uint2(pack_bf16x2(v[0] - __uint_as_float(hi.x << 16), v[1] - __uint_as_float(hi.x & 0xffff0000u)),
-                                    pack_bf16x2(v[2] - __uint_as_float(hi.y << 16), v[3] - __uint_as_float(hi.y & 0xffff0000u)));
-        *reinterpret_cast<uint2*>(LaRows<64>{s.W[1]}.at(i, 2 * j0)) = lo;
+        float rest[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int e = 0; e < kLaTerms; ++e) {
+          const uint2 term = make_uint2(pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
+          *reinterpret_cast<uint2*>(LaRows<64>{s.W[e]}.at(i, 2 * j0)) = term;
+          rest[0] -= __uint_as_float(term.x << 16);
+          rest[1] -= __uint_as_float(term.x & 0xffff0000u);
+          rest[2] -= __uint_as_float(term.y << 16);
+          rest[3] -= __uint_as_float(term.y & 0xffff0000u);
+        }
         if constexpr (KIND == kWalkDq) {
           // M = W o (q k^T) below the diagonal, over this slice's columns of q
           // and k: its row and column sums, in fp32 from exact products
@@ -521,11 +528,11 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       for (int n = 0; n < NB; ++n) accY[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int m = 0; m < C / 32; ++m) {
-        u32x4_t t[kTerms];
+        u32x4_t t[kLaTerms];
         float v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) v[r] = accS[2 * m + r / 4][r % 4];
-        la_split8<kTerms>(v, t);
+        la_split8<kLaTerms>(v, t);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           // (apart: the compiler would fetch halves of two operands with one
@@ -533,7 +540,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
           asm volatile("" ::: "memory");
           const bf16x8_t av = tA.op2(16 * n + lr, 32 * m + 4 * q);
 #pragma unroll
-          for (int e = 0; e < kTerms; ++e) accY[n] = la_mfma(__builtin_bit_cast(bf16x8_t, t[e]), av, accY[n]);
+          for (int e = 0; e < kLaTerms; ++e) accY[n] = la_mfma(__builtin_bit_cast(bf16x8_t, t[e]), av, accY[n]);
         }
       }
 #pragma unroll
@@ -596,22 +603,22 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
     if constexpr (kOut) {
       const bf16x8_t xo = __builtin_bit_cast(bf16x8_t, xw);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < kLaTerms; ++e)
 #pragma unroll
         for (int n = 0; n < NB; ++n) accY[n] = la_mfma(xo, LaRows<64>{s.W[e]}.op(16 * n + lr, q), accY[n]);
     }
-    bf16x8_t xs[3];
+    bf16x8_t xs[kLaTerms];
     {
-      u32x4_t t[3];
+      u32x4_t t[kLaTerms];
       float v[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[2 * e] = __uint_as_float(xw[e] << 16) * (e < 2 ? f0[2 * e] : f1[2 * e - 4]);
         v[2 * e + 1] = __uint_as_float(xw[e] & 0xffff0000u) * (e < 2 ? f0[2 * e + 1] : f1[2 * e - 3]);
       }
-      la_split8<3>(v, t);
+      la_split8<kLaTerms>(v, t);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) xs[k] = __builtin_bit_cast(bf16x8_t, t[k]);
+      for (int k = 0; k < kLaTerms; ++k) xs[k] = __builtin_bit_cast(bf16x8_t, t[k]);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -619,7 +626,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& a, LaTile<C, KIND>& s, int
       for (int r = 0; r < 4; ++r) accS[t][r] *= e_end;
       const bf16x8_t bt = la_col8(tB, 8 * q, 16 * t, l);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) accS[t] = la_mfma(bt, xs[k], accS[t]);
+      for (int k = 0; k < kLaTerms; ++k) accS[t] = la_mfma(bt, xs[k], accS[t]);
     }
     if (poison) {
       if (REV ? bad_at >= 0 : bad_at < kLaQ) {
