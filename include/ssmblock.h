@@ -181,7 +181,9 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
  *   dv            : [batch, seqlen, nheads, dv] in grad_dtype
  *   dlog_decay    : fp32, of log_decay's shape
  *   dinitial_state: [batch, nheads, dv, dk] fp32, or NULL (not computed)
- * The forward's outputs are not needed.  Sequences are cut into time chunks of at
+ * The forward's outputs are not needed.  Values that are not finite reach what depends on
+ * them; a decay also dk and dv of the steps behind it in its 32, and any value dlog_decay of
+ * its head throughout the time chunk.  Sequences are cut into time chunks of at
  * most 2048 steps.  Workspace, on `stream`:
  * batch * seqlen * nheads * ceil(dk / 64) * 8 bytes, with more than one time chunk
  * 8 * batch * n_chunks * nheads * (dk * dv + 1), with dlast_state and
