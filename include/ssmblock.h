@@ -34,8 +34,11 @@ extern "C" {
  * ssm_workspace_bytes() bytes, 16-byte aligned, that nothing but the call's stream uses
  * until the call's kernels have run; the call takes from the pool what does not
  * fit.  The offer ends with that call, also if it is refused; NULL withdraws it.
- * ssm_workspace_bytes: what the thread's last such call wanted (0: nothing); it
- * depends on the call's sizes, types, flags and absent tensors alone.
+ * ssm_workspace_bytes: what the thread's last such call wanted (0: nothing, as where it
+ * was refused); it depends on the call's sizes, types, flags, plan and absent tensors,
+ * on whether a state is updated in place, and on the device's number of CUs, alone.  The
+ * sizes in the calls' comments are for orientation (the parts of a workspace are each
+ * rounded up to 16 bytes): this is the one to allocate by.
  */
 ssm_status ssm_workspace(void* memory, int64_t bytes);
 int64_t ssm_workspace_bytes(void);
@@ -188,9 +191,9 @@ ssm_status ssm_linattn_fwd(const void* q, int64_t q_row, const void* k, int64_t 
  * batch * seqlen * nheads * ceil(dk / 64) * 8 bytes, with more than one time chunk
  * 8 * batch * n_chunks * nheads * (dk * dv + 1), with dlast_state and
  * with initial_state batch * nheads * dk * dv * 4 each, with nheads > ngroups
- * batch * seqlen * nheads * dk * 8 more, with a fixed decay 8 * dk * dv (each
- * rounded up to 64 or 128) for every 128 steps of a head.  Alignment and rows as above, gradients
- * and dout 16-byte aligned.
+ * batch * seqlen * nheads * dk * 8 more, with a fixed decay 8 for every time chunk and
+ * 8 * dk * dv (each rounded up to 64 or 128) for every 128 steps in it but the last, of a
+ * head.  Alignment and rows as above, gradients and dout 16-byte aligned.
  */
 ssm_status ssm_linattn_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
                            const float* log_decay, int flags, float scale, const float* initial_state,
