@@ -142,6 +142,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(v).  The instruction takes values below the smallest normal number as zero,
+// and a row's mean square may lie there where eps does (below 1.2e-38).
+__device__ __forceinline__ float norm_rsqrt(float v) {
+  const bool small = v < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v);
+  return small ? r * 0x1p32f : r;
+}
+
 constexpr int kNormWaves = 4;    // wavefronts per workgroup of the wavefront layout
 
 // Where a lane works.  T > 0: the wavefront layout; T == 0: the workgroup
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(T > 0 ? 64 * kNormWaves : 1024) norm_fwd_kerne
       sq[0] += at.on[v] ? t : 0.0f;
     }
     total(sq);
-    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sq[0], inv_w, a.eps));
+    const float rstd = norm_rsqrt(__builtin_fmaf(sq[0], inv_w, a.eps));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t at0 = row * wide + gbase + at.e0[v];
@@ -474,8 +482,8 @@ __global__ void __launch_bounds__(T > 0 ? 64 * kNormWaves : 1024) norm_bwd_kerne
       s[1] += at.on[v] ? t1 : 0.0f;
     }
     total(s);
-    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], inv_w, a.eps));
-    const float c = rstd * rstd * s[1] * inv_w;
+    const float rstd = norm_rsqrt(__builtin_fmaf(s[0], inv_w, a.eps));
+    const float c = rstd * (rstd * s[1] * inv_w);     // (the square alone could overflow)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float d[8], y[8];   // dr; the normed row
