@@ -64,7 +64,8 @@ int64_t ssm_workspace_bytes(void);
  *
  * with m_i the row's mean under SSM_NORM_CENTER and 0 without it, and v_i the
  * mean of (r[i,.] - m_i)^2.  Statistics and r are fp32; out is formed from the
- * fp32 r, not from the rounded residual_out.
+ * fp32 r, not from the rounded residual_out.  A row's sum of squares has to stay within
+ * fp32 (magnitudes below 2e17 always do): past it the row's statistics are infinite.
  *   x            : [rows, width] in x_dtype, rows x_stride elements apart
  *                  (x_stride >= width)
  *   residual     : [rows, width] in res_dtype, or NULL (r = scale x)
@@ -234,7 +235,7 @@ ssm_status ssm_linattn_state_update(const float* state, float* state_out, const 
  * m at most 327675.  The kernel is made for up to about 64 rows, past which the codes are read again for every 64 (fp32
  * x: 21).  Above 16 rows (5) x is laid out in a workspace of about 2 m k bytes (6) on
  * `stream`.  Sums are fp32; x enters the matrix cores exactly (fp32 as three bf16
- * terms).  A value of x that is not finite makes its row's outputs NaN.  With
+ * terms, in magnitude up to 3.38e38, bf16's largest).  A value of x that is not finite makes its row's outputs NaN.  With
  * k = 0, out is the bias (or 0).
  */
 ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, const void* scales, const uint8_t* zeros,
@@ -246,7 +247,8 @@ ssm_status ssm_q4_matvec(const void* x, int64_t x_row, const uint8_t* codes, con
  * scale = (max(w, 0) - min(w, 0)) / 15 rounded to scale_dtype, zero = the nearest
  * code to -min / scale, code = the nearest to w / scale + zero, within 0..15.
  * |w - (code - zero) scale| is at most scale (half a step, and the rounding of
- * the zero point) up to scale_dtype's rounding.  Finite weights only.
+ * the zero point) up to scale_dtype's rounding.  Finite weights only, whose largest less
+ * smallest in a group is finite too.
  */
 ssm_status ssm_q4_quantize(const void* w, uint8_t* codes, void* scales, uint8_t* zeros, int64_t n, int64_t k,
                            int64_t group, ssm_dtype w_dtype, ssm_dtype scale_dtype, void* stream);

@@ -247,11 +247,11 @@ ssm_status la_rows(const char* name, int64_t rows, int64_t width, int64_t row, i
 // least 256 steps; past that two per CU, of at least 128 steps, since a time chunk
 // costs a fixed part and the carry runs over all of them (microseconds, dk = dv =
 // 128 where not said):
-//   1 x 65537, 16 heads of 64 x 128: 16 chunks 344, 24 297, 32 291, 48 300
-//   1 x 16384, 32 heads: 8 chunks 241, 12 236, 16 252    4 x 2048, 32 heads: 1 chunk 126, 2 130, 3 119, 4 135
-//   1 x 8192, 8 heads: 16 chunks 61, 32 50, 48 56         1 x 2048, 8 heads: 4 chunks 59, 16 34, 32 34
-//   1 x 131072, 2 heads of 128 x 64: 256 chunks 98, 384 108
-// More workgroups than CUs are not cut: 4 x 2048, 40 heads: 1 chunk 148, 2 165.
+//   1 x 65537, 16 heads of 64 x 128: 16 chunks 362, 24 322, 32 339, 48 330
+//   1 x 16384, 32 heads: 8 chunks 263, 12 253, 16 270    4 x 2048, 32 heads: 1 chunk 142, 2 145, 3 136, 4 146
+//   1 x 8192, 8 heads: 16 chunks 61, 32 49, 48 53         1 x 2048, 8 heads: 4 chunks 58, 16 30, 32 31
+//   1 x 131072, 2 heads of 128 x 64: 256 chunks 99, 384 107
+// More workgroups than CUs are not cut: 4 x 2048, 40 heads: 1 chunk 173, 2 175.
 void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, int simds, ssm_plan* p) {
   const int64_t wgs = std::max<int64_t>(1, batch * nheads * ((dv + 63) / 64));
   const int64_t cus = std::max(1, simds / 4);
@@ -270,8 +270,8 @@ void choose_la_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t dv, i
 // Time chunks of a backward: at most kLaBwdChunk steps each, and more where its
 // three walks leave CUs idle.  The walks differ in length, so six workgroups per CU
 // (two fit) even them out better than two, down to 256 steps (microseconds, dk = dv
-// = 128, 2 and 6 per CU): 1 x 4096, 40 heads 379, 317; 1 x 8192, 8 heads 177, 170;
-// with at least 512 steps in place of 256: 1 x 2048, 8 heads 108, 80.
+// = 128, 2 and 6 per CU): 1 x 4096, 40 heads 356, 301; 1 x 8192, 8 heads 162, 152;
+// with at least 512 steps in place of 256: 166, and 1 x 2048, 8 heads 100 in place of 75.
 void choose_la_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t slots, int simds, ssm_plan* p) {
   const int64_t wgs = std::max<int64_t>(1, batch * nheads * slots);
   const int64_t cus = std::max(1, simds / 4);

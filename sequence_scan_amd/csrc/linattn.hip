@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) la_carry_kernel(LaWalk a) {
 // One token: each state row (dk values of one dv channel) is read and written
 // once, 16 bytes per lane, LPR lanes per row; its product with q is summed
 // over those lanes.  A thread takes two rows of one head, all loads first.  Memory
-// bounds it: 64 sequences of 80 heads of 128 x 64 (337 MB) take 55 us, 6.1 TB/s; one
+// bounds it: 64 sequences of 80 heads of 128 x 64 (337 MB) take 57 us, 5.9 TB/s; one
 // sequence 3.9 us.
 template <typename Tin, typename Tout, int LPR>
 __global__ void __launch_bounds__(256) la_step_kernel(LaStep a) {

@@ -20,7 +20,7 @@
 // every eight chunks and by 7e-7 with every four; 4 x 2048, 40 heads took 427, 464
 // and 514 us then.
 //
-// Measured: 4 x 2048, 40 heads of 128 x 128, 433 us (a fixed decay: 522), of which the
+// Measured: 4 x 2048, 40 heads of 128 x 128, 434 us (a fixed decay: 523), of which the
 // decay's kernel is 14 us; the bytes that have to move would take 114 us at a copy's
 // rate.  The walks' registers leave two workgroups per CU, so that the chunks' chains bound
 // it as in the forward.

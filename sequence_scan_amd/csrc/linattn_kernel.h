@@ -31,13 +31,13 @@
 // readout and its scaling, two fifths of a wavefront's vector instructions here), but
 // hold twice the LDS, so two workgroups per CU in place of three.
 //
-// What bounds it: prompts of 8 x 2048, 40 heads of 128 x 128, take 231 us, 3.0 TB/s of
+// What bounds it: prompts of 8 x 2048, 40 heads of 128 x 128, take 232 us, 3.0 TB/s of
 // the bytes that they have to move (135 us at a copy's rate).  Of 226 us, before W and the
 // readout's state had their third term, they took 174 without loads and 197 without
 // stores: a chunk's chain of products, roundings and
 // two barriers is what its three wavefronts per SIMD wait for, and memory overlaps it
 // only in part.  The third terms, 10 of a chunk's 58 products and an eighth of its vector
-// instructions, cost 205 -> 231 us here and 420 -> 433 us in the gradients; without them
+// instructions, cost 205 -> 232 us here and 420 -> 434 us in the gradients; without them
 // fp32 outputs were off by 2.0e-6 to 2.5e-6 of their norm, with them by 1.3e-7.
 #ifndef SSMSCAN_LINATTN_KERNEL_H
 #define SSMSCAN_LINATTN_KERNEL_H

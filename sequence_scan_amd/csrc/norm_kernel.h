@@ -9,10 +9,11 @@
 //             S2 = sum u (r - m) gives both 1 / std and mean(u n):
 //             dr = (u - [mean u] - (r - m) S2 / (W std^2)) / std
 // Memory is what bounds it: a few operations per element against 4 to 20 bytes.
-// Measured (a copy of 1 GiB runs at 5.2 TB/s): add norm of 16384 x 2560, bf16 into an
-// fp32 residual, 95 us, 5.3 TB/s, its backward with all three column sums 144 + 5 us,
-// 5.2 TB/s; gated norm of 16384 x 5120 102 us, 4.9 TB/s; the backward over 80 heads of
-// 64 164 + 4 us, 5.1 TB/s.  One row of 2560 takes 2.2 us, a launch's own time.
+// Measured (PyTorch's copy of 1 GiB runs at 5.2 TB/s, the library's streaming probe at
+// 6.5): add norm of 16384 x 2560, bf16 into an fp32 residual, 96 us, 5.3 TB/s, its
+// backward with all three column sums 142 + 5 us, 5.2 TB/s; gated norm of 16384 x 5120
+// 103 us, 4.9 TB/s; the backward over 80 heads of 64 162 + 4 us, 5.1 TB/s.  One row of 2560
+// takes 2.2 us, a launch's own time.
 //
 // Two layouts.  Up to 512 channels, T lanes of a wavefront (8, 16, 32 or 64)
 // hold one norm, and the sums stay within the wavefront (DPP and the row

@@ -27,11 +27,11 @@
 // all slabs, and the workgroups load them straight to LDS, a slab ahead, and the
 // codes two slabs ahead (q4_wide_kernel).
 //
-// Measured: one row x 10576 x 2560 (13.5 MB of codes) 8.1 us, of which the launch and
-// the wait for the first bytes are about half; 2 rows x 16384 x 16384 (134 MB) 37 us,
-// 3.6 TB/s; 48 rows x 16384 x 8192 (67 MB) 31 us and 3 us for x.  There no one thing
-// bounds it: without its loads, its matrix products or its reads of x it takes 23,
-// 31 and 31 us, since the 16 wavefronts that a CU holds meet at a barrier every slab.
+// Measured, back to back: one row x 10576 x 2560 (13.5 MB of codes) 7.4 us, of which the
+// launch and the wait for the first bytes are about half; 2 rows x 16384 x 16384 (134 MB)
+// 37 us, 3.6 TB/s; 48 rows x 16384 x 8192 (67 MB) 30 us, 3 of them to lay out x.  There no one
+// thing bounds it: of 34 us then, it took 23, 31 and 31 without its loads, its matrix
+// products and its reads of x, since the 16 wavefronts that a CU holds meet at a barrier every slab.
 #include <algorithm>
 
 #include "block.h"
@@ -709,9 +709,9 @@ int q4_slab_cols(const Q4Args& a) { return (int64_t)a.n < 64ll * a.cus ? 32 : 64
 // All of x in LDS, 16 columns per workgroup: for up to four rows (terms counted;
 // each workgroup stages them all), where the workgroups of the form in slabs would
 // leave a quarter of their last round of CUs idle or more.  Measured, all of x against
-// slabs, one row (microseconds): 2560 x 5120 6.1, 7.6; 10576 x 2560 8.1, 9.1; 20480 x
-// 5120 17.6, 21.2; but 8192 x 8192 14.6, 13.5; 16384 x 8192 25.2, 23.3; 65536 x 2560
-// 31.1, 25.8.  10576 x 2560 by rows: 2 8.3, 9.2; 4 9.3, 9.7; 8 11.4, 10.3.
+// slabs, one row (microseconds): 2560 x 5120 6.4, 7.3; 10576 x 2560 7.4, 8.4; 20480 x
+// 5120 14.5, 17.6; but 8192 x 8192 13.4, 11.4; 16384 x 8192 20.5, 17.0; 65536 x 2560
+// 24.5, 19.5.  10576 x 2560 by rows: 2 7.7, 8.4; 4 8.4, 8.8; 8 10.3, 9.2.
 bool q4_fits(const Q4Shape& h, const Q4Args& a) {
   const int cols = q4_slab_cols(a);
   const int64_t wgs = ((int64_t)a.n + cols - 1) / cols, places = (wgs + a.cus - 1) / a.cus * a.cus;
