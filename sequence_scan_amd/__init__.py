@@ -550,3 +550,5 @@ from .block import (SSM_LINATTN_FIXED_DECAY, SSM_NORM_CENTER, SSM_NORM_GATE_LAST
                     ssm_add_norm_bwd, ssm_add_norm_fwd, ssm_gated_norm_bwd, ssm_gated_norm_fwd, ssm_linattn_bwd,
                     ssm_linattn_fwd, ssm_linattn_plan_query, ssm_linattn_state_update, ssm_q4_matvec,
                     ssm_q4_quantize, ssm_workspace, ssm_workspace_bytes)
+from .model import (SSM_GSCAN_LERP, SSM_GSCAN_SEGMENT, ssm_distill_bwd, ssm_distill_fwd,  # noqa: E402,F401
+                    ssm_gscan_bwd, ssm_gscan_fwd, ssm_gscan_update, ssm_xent_bwd, ssm_xent_fwd)

@@ -46,7 +46,9 @@ DEVICE_UNITS = _scan_units() + [(os.path.join(CSRC, f), [], f.split(".")[0]) for
 _NO_DOT2C = ["-Xclang", "-target-feature", "-Xclang", "-dot13-insts"]
 BLOCK_UNITS = [(os.path.join(CSRC, f), _NO_DOT2C if f.startswith("linattn") else [], f.split(".")[0])
                for f in ("norm_add.hip", "norm_gate.hip", "linattn.hip", "linattn_bwd.hip", "q4.hip")]
-HOST_UNITS = [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("api.cpp", "api_block.cpp")]
+# ... and the model operators' (include/ssmmodel.h).
+BLOCK_UNITS += [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("gscan.hip", "vocab.hip")]
+HOST_UNITS = [(os.path.join(CSRC, f), [], f.split(".")[0]) for f in ("api.cpp", "api_block.cpp", "api_model.cpp")]
 SOURCES = sorted({u[0] for u in DEVICE_UNITS + BLOCK_UNITS + HOST_UNITS})
 HEADERS = [os.path.join(CSRC, f) for f in ("internal.h", "device.h", "scan_kernel.h")] + [
     os.path.join(os.path.dirname(HERE), "include", "ssmscan.h")]
