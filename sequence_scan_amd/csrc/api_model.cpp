@@ -42,6 +42,10 @@ ssm_status gs_check(int64_t batch, int64_t seqlen, int64_t width, int flags, std
   if (sz->state > INT32_MAX - 1023)
     return fail(SSM_ERR_UNSUPPORTED, "batch * width = %lld exceeds 2^31 - 1024", (long long)sz->state);
   sz->states = sz->state * ceil_div(seqlen, SSM_GSCAN_SEGMENT);
+  // a workgroup of 512 threads for every 64 channels of a row and 128 steps, or of 256 for 64 steps
+  if (ceil_div(seqlen, ssm::kGsBwdTile) * batch * ceil_div(width, 64) > kMaxThreads / 256)
+    return fail(SSM_ERR_UNSUPPORTED, "batch=%lld by seqlen=%lld by width=%lld exceeds the grid", (long long)batch, (long long)seqlen,
+                (long long)width);
   return SSM_OK;
 }
 
@@ -198,7 +202,16 @@ ssm_status ssm_gscan_fwd(const void* x, int64_t x_row, const void* r, int64_t r_
   a.seqlen = seqlen;
   a.width = width;
   a.out_bf16 = out_dtype == SSM_BF16;
-  return launched(ssm::launch_gscan_fwd(a, to_dt(in_dtype), s));
+  void* ws = nullptr;
+  hipError_t e = hipSuccess;
+  const int64_t bytes = ssm::gscan_chain_bytes(batch, seqlen, width, false);
+  if (bytes > 0) {
+    e = work.get(&ws, bytes, s);
+    if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)bytes, e);
+    a.work = static_cast<char*>(ws);
+  }
+  e = ssm::launch_gscan_fwd(a, to_dt(in_dtype), s);
+  return launched(work.done(e, s));
 }
 
 ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_row, const void* i, int64_t i_row,
@@ -261,14 +274,16 @@ ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_
   a.seqlen = seqlen;
   a.width = width;
   a.out_bf16 = out_dtype == SSM_BF16;
-  if (drate != nullptr) {
+  const int64_t chain = ssm::gscan_chain_bytes(batch, seqlen, width, true);
+  const int64_t bytes = chain + (drate != nullptr ? sz.state * ceil_div(seqlen, ssm::kGsBwdTile) * 4 : 0);
+  if (bytes > 0) {
     void* ws = nullptr;
-    e = work.get(&ws, sz.state * 4, s);
-    if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)(sz.state * 4), e);
-    a.part = static_cast<float*>(ws);
+    e = work.get(&ws, bytes, s);
+    if (e != hipSuccess || ws == nullptr) return fail_hip("workspace allocation", (long long)bytes, e);
+    a.work = static_cast<char*>(ws);
+    if (drate != nullptr) a.part = reinterpret_cast<float*>(a.work + chain);
   }
   e = ssm::launch_gscan_bwd(a, to_dt(in_dtype), s);
-  if (e == hipSuccess && drate != nullptr) e = ssm::launch_gscan_sum(a.part, drate, batch, width, s);
   return launched(work.done(e, s));
 }
 

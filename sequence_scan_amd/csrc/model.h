@@ -10,6 +10,9 @@ namespace ssm {
 // ------------------------------------------------------ gated linear recurrence
 
 constexpr int kGsSegment = 32;    // steps between two stored states
+constexpr int kGsFwdTile = 128;   // steps that a workgroup holds at a time
+constexpr int kGsBwdTile = 64;
+constexpr int kGsGroup = 8;       // tiles whose parts are composed from one published state
 
 struct GscanArgs {
   const void* x;            // token (b, t)'s channels at (b * seqlen + t) * x_row
@@ -29,7 +32,8 @@ struct GscanArgs {
   void* di;
   float* drate;             // nullable
   float* dinitial;          // nullable
-  float* part;              // backward with drate: [batch, width] sums over steps
+  float* part;              // backward with drate: [batch, tiles, width] sums over a tile's steps
+  char* work;               // gscan_chain_bytes bytes, where a sequence has more than one tile
   int64_t batch, seqlen, width;
   int32_t lerp;
   int32_t out_bf16;         // type of out and dout
@@ -38,8 +42,8 @@ struct GscanArgs {
 hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s);
 hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t s);
 hipError_t launch_gscan_step(const GscanArgs& a, DT in, hipStream_t s);
-// out[d] = sum over n rows of part[n, d], in order.
-hipError_t launch_gscan_sum(const float* part, float* out, int64_t n, int64_t width, hipStream_t s);
+// Bytes of GscanArgs::work (0: none), a multiple of 16.
+int64_t gscan_chain_bytes(int64_t batch, int64_t seqlen, int64_t width, bool backward);
 
 // -------------------------------------------------- losses over a vocabulary
 

@@ -54,8 +54,7 @@ def ssm_gscan_fwd(x, r, i=None, rate=None, lerp: bool = False, initial_state=Non
     if out is None:
         out = _new(shape, out_dtype or x.dtype, x)
     st, f32 = (B, D), block._F32
-    in_place = initial_state is not None and initial_state is last_state
-    _with_workspace(call, ("gscan", B, L, D, in_place, dev), x, stream, (
+    _with_workspace(call, ("gscan", B, L, D, dev), x, stream, (
         *args, SSM_GSCAN_LERP if lerp else 0, _want(initial_state, "initial_state", st, f32, dev),
         _want(out, "out", shape, None, dev), _want(last_state, "last_state", st, f32, dev),
         _want(states, "states", (B, -(-L // SSM_GSCAN_SEGMENT), D), f32, dev), B, L, D, block._code[x.dtype],
