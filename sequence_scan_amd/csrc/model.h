@@ -73,9 +73,7 @@ struct VocabArgs {
   int32_t cus;
 };
 
-// Columns of the vocabulary in a piece of the backward, a multiple of kVocabTile.
-int64_t vocab_piece(const VocabArgs& a);
-// Bytes of a.work, or -1 past an int64.
+// Bytes of a.work.
 int64_t vocab_fwd_bytes(const VocabArgs& a);
 int64_t vocab_bwd_bytes(const VocabArgs& a);
 hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s);

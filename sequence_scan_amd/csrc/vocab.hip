@@ -17,11 +17,14 @@ typedef float acc4_t __attribute__((ext_vector_type(4)));
 constexpr int kK = 64;            // contracted elements in a stage: rows of 128 bytes
 constexpr int kTile = kVocabTile;   // rows and columns of a workgroup's tile of C
 
-// A bf16 matrix whose rows run along the contracted dimension.
+// One side of a product, a bf16 matrix in either order:
+//   along  (ACROSS false): [n][k], rows run along the contracted dimension;
+//   across (ACROSS true):  [k][n], rows run across it.
 struct Side {
   const uint16_t* p;
   int64_t ld;       // elements between rows
-  int32_t rows;
+  int32_t n;        // rows or columns of C that it gives (across: a multiple of 8)
+  int32_t k;        // contracted elements that it has (along: a multiple of 8); past them it counts as 0
 };
 
 // A wavefront's load of 64 x 16 bytes straight to LDS through a buffer descriptor:
@@ -41,11 +44,10 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)static_cast<const char*>(p);
 }
 
-// The descriptor of `rows` rows from row r0 on: reads past the last row's end give 0.
-__device__ __forceinline__ i32x4_t buffer_of(const Side& m, int64_t r0, int rows, int k) {
-  const uint64_t base = (uint64_t)(uintptr_t)(m.p + r0 * m.ld);
-  const int64_t left = m.rows - r0 < rows ? m.rows - r0 : rows;
-  const uint32_t bytes = left > 0 ? (uint32_t)(((left - 1) * m.ld + k) * 2) : 0;
+// The descriptor of `rows` rows of `length` elements: reads past the last row's end give 0.
+__device__ __forceinline__ i32x4_t buffer_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t length) {
+  const uint64_t base = (uint64_t)(uintptr_t)p;
+  const uint32_t bytes = rows > 0 && length > 0 ? (uint32_t)(((rows - 1) * ld + length) * 2) : 0;
   i32x4_t d;
   d.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
   d.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xffff);
@@ -55,65 +57,135 @@ __device__ __forceinline__ i32x4_t buffer_of(const Side& m, int64_t r0, int rows
 }
 
 // A workgroup of 2 x 4 wavefronts computes a 256 x 256 tile of C, a wavefront 128 x 64
-// of it.  A stage holds 64 contracted elements of the tile's 256 + 256 rows (64 KB), of
-// which there are two: one is multiplied while the other arrives.
+// of it.  A stage holds 64 contracted elements of the tile's 256 + 256 rows and columns
+// (64 KB), of which there are two: one is multiplied while the other arrives.
 //
-// In LDS a row's eight 16-byte pieces are permuted: piece c of row r is at place
-// c ^ ((r >> 1) & 7).  A matrix operand takes one piece of each of 16 rows, which then
-// meet all 64 banks once.
+// In LDS a stage's side lies as in memory, in pieces that are permuted so that an
+// operand's reads meet all 64 banks once:
+//   along: 256 rows of 128 bytes; the 16-byte piece c of row r is at place
+//     c ^ ((r >> 1) & 7).  An operand takes one piece of each of 16 rows.
+//   across: 64 rows of 512 bytes; the 32-byte piece c of row r is at place
+//     c ^ ((r & 3) | (r >> 1 & 4)).  An operand takes one piece of each of 16 rows,
+//     turned over on the way (ds_read_tr: 16 lanes read four rows of 16 elements, and
+//     receive one column of four each).
 struct Stages {
   alignas(1024) char a[2][kTile * kK * 2];
   alignas(1024) char b[2][kTile * kK * 2];
 };
+constexpr uint32_t kStage = kTile * kK * 2;
 
 // acc[mi][ni][i]: C[wm * 128 + mi * 16 + (lane & 15)][wn * 64 + ni * 16 + 4 * (lane >> 4) + i].
 typedef acc4_t Acc[8][4];
 
-__device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m0, int64_t n0, int k, Stages& s, Acc acc) {
+// A side's loads: a wavefront brings four times 1 KB of a stage.
+template <bool ACROSS>
+struct Loader {
+  const uint16_t* p;
+  int64_t ld;
+  uint32_t off[4];
+  int32_t length, k, c;
+  __device__ __forceinline__ Loader(const Side& s, int64_t n0, int k0, int k1, int wave, int lane) {
+    ld = s.ld;
+    k = (s.k < k1 ? s.k : k1) - k0;
+    length = (int32_t)(s.n - n0 < kTile ? s.n - n0 : kTile);
+    if constexpr (ACROSS) {
+      // rows wave * 8 .. + 7 of the stage, two at a time
+      p = s.p + k0 * s.ld + n0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = wave * 8 + j * 2 + (lane >> 5);
+        const int piece = ((lane >> 1) & 15) ^ ((r & 3) | (r >> 1 & 4));
+        off[j] = (uint32_t)(r * s.ld * 2) + piece * 32 + (lane & 1) * 16;
+      }
+      c = 0;
+    } else {
+      // rows wave * 32 .. + 31 of the tile, eight at a time
+      p = s.p + n0 * s.ld + k0;
+      c = (lane & 7) ^ ((lane >> 4) & 3);       // of rows 0..7 of 16; rows 8..15 differ in bit 2
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        off[j] = (uint32_t)((wave * 32 + j * 8 + (lane >> 3)) * s.ld * 2) + (uint32_t)(c ^ ((j & 1) << 2)) * 16;
+    }
+  }
+  // The stage at contracted element `at` (from k0).
+  __device__ __forceinline__ void operator()(int at, uint32_t to) const {
+    if constexpr (ACROSS) {
+      const int rows = k - at < kK ? k - at : kK;
+      const i32x4_t buffer = buffer_of(p + at * ld, ld, rows, length);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_lds16(buffer, off[j], to + j * 1024);
+    } else {
+      const i32x4_t buffer = buffer_of(p, ld, length, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t past = at + (c ^ ((j & 1) << 2)) * 8 < k ? 0 : 0x80000000u;     // (descriptors end below 2^31)
+        load_lds16(buffer, (off[j] + at * 2) | past, to + j * 1024);
+      }
+    }
+  }
+};
+
+// An operand's reads: 16 rows or columns of C, 32 contracted elements (half kk of a stage).
+template <bool ACROSS>
+struct Reader {
+  uint32_t at;
+  __device__ __forceinline__ Reader(int first, int lane) {
+    if constexpr (ACROSS) {
+      const int r = (lane >> 4) * 8 + ((lane >> 2) & 3);
+      at = r * 512 + (((first >> 4) ^ ((r & 3) | (r >> 1 & 4))) * 32) + (lane & 3) * 8;
+    } else {
+      at = (first + (lane & 15)) * 128 + (((lane >> 4) ^ ((lane & 15) >> 1)) & 7) * 16;
+    }
+  }
+  // Operand `i` counted in 16s from `first`, a multiple of 4 of them.
+  __device__ __forceinline__ bf16x8_t operator()(const char* side, int i, int kk) const {
+    if constexpr (ACROSS) {
+      // (the place of piece first / 16 + i, i below 4 or 8 and first / 16 a multiple of it)
+      const char* q = side + (at ^ (i * 32)) + kk * 32 * 512;
+      typedef short s4_t __attribute__((ext_vector_type(4)));
+      typedef short s8_t __attribute__((ext_vector_type(8)));
+      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t*)(q));
+      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t*)(q + 4 * 512));
+      return __builtin_bit_cast(bf16x8_t, (s8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const bf16x8_t*>(side + i * 2048 + (at ^ (kk * 64)));
+    }
+  }
+};
+
+// acc = the tile at (m0, n0) of A B over the contracted elements k0 to k1 (k0 a multiple of 8).
+template <bool A_ACROSS, bool B_ACROSS>
+__device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m0, int64_t n0, int k0, int k1, Stages& s, Acc acc) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const i32x4_t ba = buffer_of(A, m0, kTile, k), bb = buffer_of(B, n0, kTile, k);
-  // a wavefront loads rows wave * 32 .. + 31 of either side, eight at a time
-  const int row = wave * 32 + (lane >> 3);
-  const int c = (lane & 7) ^ ((lane >> 4) & 3);         // of rows 0..7 of 16; rows 8..15 differ in bit 2
-  uint32_t oa[4], ob[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t piece = (uint32_t)(c ^ ((j & 1) << 2)) * 16;
-    oa[j] = (uint32_t)((row + j * 8) * A.ld * 2) + piece;
-    ob[j] = (uint32_t)((row + j * 8) * B.ld * 2) + piece;
-  }
+  const Loader<A_ACROSS> load_a(A, m0, k0, k1, wave, lane);
+  const Loader<B_ACROSS> load_b(B, n0, k0, k1, wave, lane);
+  const Reader<A_ACROSS> read_a(wm * 128, lane);
+  const Reader<B_ACROSS> read_b(wn * 64, lane);
   const uint32_t la = lds_address(s.a[0]) + wave * 4096, lb = lds_address(s.b[0]) + wave * 4096;
-  constexpr uint32_t kStage = kTile * kK * 2;
-  auto load = [&](int k0, int stage) SSM_INLINE {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int piece = k0 + (c ^ ((j & 1) << 2)) * 8;
-      const uint32_t past = piece < k ? 0 : 0x80000000u;      // (descriptors end below 2^31)
-      load_lds16(ba, (oa[j] + k0 * 2) | past, la + stage * kStage + j * 1024);
-      load_lds16(bb, (ob[j] + k0 * 2) | past, lb + stage * kStage + j * 1024);
-    }
-  };
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = acc4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int at = (lane & 15) * 128 + (((lane >> 4) ^ ((lane & 15) >> 1)) & 7) * 16;
-  load(0, 0);
-  const int stages = (k + kK - 1) / kK;
+  load_a(0, la);
+  load_b(0, lb);
+  const int stages = (k1 - k0 + kK - 1) / kK;
   for (int t = 0; t < stages; ++t) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     block_sync();
-    if (t + 1 < stages) load((t + 1) * kK, (t + 1) & 1);
-    const char* pa = s.a[t & 1] + wm * 128 * 128;
-    const char* pb = s.b[t & 1] + wn * 64 * 128;
+    if (t + 1 < stages) {
+      load_a((t + 1) * kK, la + ((t + 1) & 1) * kStage);
+      load_b((t + 1) * kK, lb + ((t + 1) & 1) * kStage);
+    }
+    const char* pa = s.a[t & 1];
+    const char* pb = s.b[t & 1];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       bf16x8_t fa[8], fb[4];
 #pragma unroll
-      for (int ni = 0; ni < 4; ++ni) fb[ni] = *reinterpret_cast<const bf16x8_t*>(pb + ni * 2048 + (at ^ (kk * 64)));
+      for (int ni = 0; ni < 4; ++ni) fb[ni] = read_b(pb, ni, kk);
 #pragma unroll
-      for (int mi = 0; mi < 8; ++mi) fa[mi] = *reinterpret_cast<const bf16x8_t*>(pa + mi * 2048 + (at ^ (kk * 64)));
+      for (int mi = 0; mi < 8; ++mi) fa[mi] = read_a(pa, mi, kk);
 #pragma unroll
       for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
@@ -126,8 +198,8 @@ __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m
 // The tile of C that a workgroup computes.  Workgroups go round the eight XCDs, whose
 // L2s are their own: each XCD gets a run of tiles, in groups of eight rows of tiles that
 // go through the columns together, so that the 32 tiles under way read 8 + 4 panels.
-__device__ __forceinline__ void tile_place(int tiles_m, int tiles_n, int* m, int* n) {
-  const int total = tiles_m * tiles_n, id = blockIdx.x;
+__device__ __forceinline__ void tile_place(int id, int tiles_m, int tiles_n, int* m, int* n) {
+  const int total = tiles_m * tiles_n;
   const int each = total >> 3, rest = total & 7, xcd = id & 7;
   const int t = xcd * each + (xcd < rest ? xcd : rest) + (id >> 3);
   const int group = t / (8 * tiles_n), first = group * 8;
@@ -145,16 +217,15 @@ template <bool ONE>
 __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2* __restrict__ stats, float* __restrict__ picked,
                                                              int tiles_m, int tiles_n) {
   __shared__ Stages s;
+  __shared__ float2 part[4 * 256];
   int tm, tn;
-  tile_place(tiles_m, tiles_n, &tm, &tn);
+  tile_place(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
   Acc acc;
-  multiply(Side{a.x, a.x_row, a.rows}, Side{a.w, a.w_row, a.vocab}, m0, n0, a.width, s, acc);
+  multiply<false, false>(Side{a.x, a.x_row, a.rows, a.width}, Side{a.w, a.w_row, a.vocab, a.width}, m0, n0, 0, a.width, s, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
   const int n = wn * 64 + 4 * (lane >> 4);          // + ni * 16 + i
   const int columns = (int)(a.vocab - n0 < kTile ? a.vocab - n0 : kTile);
-  block_sync();
-  float2* part = reinterpret_cast<float2*>(s.a[0]);      // [4][256]
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi) {
     const int m = wm * 128 + mi * 16 + (lane & 15);
@@ -207,30 +278,35 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
     }
     stats[(int64_t)tn * a.rows + m0 + m] = r;
   }
-}
-
-// The logits at a row's indices, one wavefront for each.
-__global__ void __launch_bounds__(256) vocab_pick_kernel(VocabArgs a) {
-  const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (e >= (int64_t)a.rows * a.top) return;
-  const int64_t v = a.index[e];
-  float z = 0.0f;
-  if (v >= 0 && v < a.vocab) {
-    const uint16_t* x = a.x + e / a.top * a.x_row;
-    const uint16_t* w = a.w + v * a.w_row;
-    for (int k = lane * 8; k < a.width; k += 512) {
-      float xv[8], wv[8];
-      Vec16<uint16_t>::unpack(*reinterpret_cast<const uint4*>(x + k), xv);
-      Vec16<uint16_t>::unpack(*reinterpret_cast<const uint4*>(w + k), wv);
+  if constexpr (!ONE) {
+    // The logits at the rows' indices, by way of LDS, 128 rows at a time: 16-byte piece c
+    // of row r is at place c ^ (r & 15).
+    float* z = reinterpret_cast<float*>(s.a[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z = __builtin_fmaf(xv[i], wv[i], z);
+    for (int half = 0; half < 2; ++half) {
+      block_sync();
+      if (wm == half) {
+#pragma unroll
+        for (int mi = 0; mi < 8; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < 4; ++ni) {
+            const int piece = (n >> 2) + ni * 4;
+            *reinterpret_cast<acc4_t*>(z + (mi * 16 + (lane & 15)) * 256 + (piece ^ (lane & 15)) * 4) = acc[mi][ni];
+          }
+      }
+      block_sync();
+      const int64_t first = m0 + half * 128, left = a.rows - first;
+      const uint32_t entries = (uint32_t)(left < 0 ? 0 : left > 128 ? 128 : left) * (uint32_t)a.top;
+#pragma unroll 4
+      for (uint32_t e = threadIdx.x; e < entries; e += 512) {
+        const int64_t v = a.index[first * a.top + e] - n0;
+        if (v >= 0 && v < columns) {
+          const uint32_t r = e / (uint32_t)a.top, col = (uint32_t)v;
+          a.logits[first * a.top + e] = z[r * 256 + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)];
+        }
+      }
     }
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) z += __shfl_xor(z, o);
-    z *= a.scale;
   }
-  if (lane == 0) a.logits[e] = z;
 }
 
 // What one row's indices and teacher logits say, over a wavefront: whether the row
@@ -304,6 +380,10 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(VocabArgs a, const floa
     else if (v >= 0) loss = (lse - picked[row]) + a.z_loss * lse * lse;
   } else {
     const Teacher t = teacher_of(a, row, lane);
+    for (int k = lane; k < a.top; k += 64) {
+      const int64_t v = a.index[row * a.top + k];
+      if (v < 0 || v >= a.vocab) a.logits[row * a.top + k] = 0.0f;
+    }
     if (t.past) loss = __builtin_nanf("");
     else if (t.counts) {
       const float t2 = kLog2e / a.temperature;
@@ -357,39 +437,27 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* _
   if (lane == 0) rows[row] = g;
 }
 
-// dst[c][r] = src[r][c] for r below `rows` and c below `cols`, 0 for r from there to
-// dst_rows (its padded length), and for the rows that take no part.
-__global__ void __launch_bounds__(256) vocab_transpose_kernel(const uint16_t* __restrict__ src, int64_t src_ld, int rows, int cols,
-                                                              uint16_t* __restrict__ dst, int64_t dst_ld,
-                                                              const RowGrad* __restrict__ takes) {
-  __shared__ uint16_t t[64][66];
-  const int r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
-  const int i = threadIdx.x & 63, j = threadIdx.x >> 6;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int r = r0 + j + k * 4, c = c0 + i;
-    const bool in = r < rows && c < cols && (!takes || takes[r].target != -2);
-    t[j + k * 4][i] = in ? src[(int64_t)r * src_ld + c] : 0;
-  }
-  block_sync();
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int c = c0 + j + k * 4, r = r0 + i;
-    if (c < cols && r < dst_ld) dst[(int64_t)c * dst_ld + r] = t[i][j + k * 4];
+// x with zeros in the rows that take no part (whose x may hold anything).
+__global__ void __launch_bounds__(256) vocab_rows_of_x_kernel(VocabArgs a, const RowGrad* __restrict__ rows, uint4* __restrict__ out) {
+  const int each = a.width / 8;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const bool takes = rows[row].target != -2;
+    const uint4* from = reinterpret_cast<const uint4*>(a.x + row * a.x_row);
+    for (int e = threadIdx.x; e < each; e += 256) out[row * each + e] = takes ? from[e] : make_uint4(0, 0, 0, 0);
   }
 }
 
-// dz of a piece of the vocabulary from the logits, computed once more, as [rows, ldz]
-// and as [columns, ldt] (each padded with zeros).
+// dz of a piece of the vocabulary, [rows, ldz] and padded with zeros, from the logits,
+// computed once more.
 __global__ void __launch_bounds__(512, 2) vocab_dz_kernel(VocabArgs a, const RowGrad* __restrict__ rows, int64_t v0, int columns,
-                                                          uint16_t* __restrict__ dz, int64_t ldz, uint16_t* __restrict__ dzt,
-                                                          int64_t ldt, int tiles_m, int tiles_n) {
+                                                          uint16_t* __restrict__ dz, int64_t ldz, int tiles_m, int tiles_n) {
   __shared__ Stages s;
   int tm, tn;
-  tile_place(tiles_m, tiles_n, &tm, &tn);
+  tile_place(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
   Acc acc;
-  multiply(Side{a.x, a.x_row, a.rows}, Side{a.w + v0 * a.w_row, a.w_row, columns}, m0, n0, a.width, s, acc);
+  multiply<false, false>(Side{a.x, a.x_row, a.rows, a.width}, Side{a.w + v0 * a.w_row, a.w_row, columns, a.width}, m0, n0, 0,
+                         a.width, s, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
   const float s2 = a.scale * kLog2e;
 #pragma unroll
@@ -407,13 +475,8 @@ __global__ void __launch_bounds__(512, 2) vocab_dz_kernel(VocabArgs a, const Row
         const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[mi][ni][i], s2, -g.lse2));
         d[i] = g.target == -2 || n + i >= columns ? 0.0f : p - (n + i == target ? g.hard : 0.0f);
       }
-      const uint32_t lo = pack_bf16x2(d[0], d[1]), hi = pack_bf16x2(d[2], d[3]);
-      if (m < a.rows && n < ldz) *reinterpret_cast<uint2*>(dz + m * ldz + n) = make_uint2(lo, hi);
-      if (m < ldt) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < columns) dzt[(n + i) * ldt + m] = (uint16_t)((i < 2 ? lo : hi) >> ((i & 1) * 16));
-      }
+      if (m < a.rows && n < ldz)
+        *reinterpret_cast<uint2*>(dz + m * ldz + n) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
     }
   }
 }
@@ -421,7 +484,7 @@ __global__ void __launch_bounds__(512, 2) vocab_dz_kernel(VocabArgs a, const Row
 // Distillation: dz at the teacher's indices, formed from the stored logits in place of
 // the rounded softmax.
 __global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGrad* __restrict__ rows, int64_t v0, int columns,
-                                                        uint16_t* __restrict__ dz, int64_t ldz, uint16_t* __restrict__ dzt, int64_t ldt) {
+                                                        uint16_t* __restrict__ dz, int64_t ldz) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (row >= a.rows) return;
@@ -437,43 +500,133 @@ __global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGr
     for (int j = 0; j < a.top; ++j)
       if (a.index[at + j] == a.index[at + k]) q += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[at + j], t2, -t.top2));
     const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(a.logits_in[at + k], kLog2e, -g.lse2));
-    const uint16_t d = f32_to_bf16_rne(p - g.hard * q * by);
-    dz[row * ldz + n] = d;
-    dzt[n * ldt + row] = d;
+    dz[row * ldz + n] = f32_to_bf16_rne(p - g.hard * q * by);
   }
 }
 
-// out (or sum) = [sum +] A B^T: a piece's part of dx, and dweight.
-__global__ void __launch_bounds__(512, 2) vocab_product_kernel(Side A, Side B, int k, float* __restrict__ sum, bool first, bool last,
-                                                               uint16_t* __restrict__ out, int64_t ld, int tiles_m, int tiles_n) {
-  __shared__ Stages s;
-  int tm, tn;
-  tile_place(tiles_m, tiles_n, &tm, &tn);
-  const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-  Acc acc;
-  multiply(A, B, m0, n0, k, s, acc);
+// What a tile of C becomes: bf16, or fp32 for sums over several parts.
+__device__ __forceinline__ void store_tile(const Acc acc, int64_t m0, int64_t n0, int rows, int columns, float* sum, uint16_t* out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi) {
     const int64_t m = m0 + wm * 128 + mi * 16 + (lane & 15);
-    if (m >= A.rows) continue;
+    if (m >= rows) continue;
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni) {
       const int64_t n = n0 + wn * 64 + ni * 16 + 4 * (lane >> 4);
-      if (n >= B.rows) continue;
-      float4 v = make_float4(acc[mi][ni][0], acc[mi][ni][1], acc[mi][ni][2], acc[mi][ni][3]);
-      if (!first) {
-        const float4 o = *reinterpret_cast<const float4*>(sum + m * ld + n);
-        v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-      }
-      if (last) *reinterpret_cast<uint2*>(out + m * ld + n) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-      else *reinterpret_cast<float4*>(sum + m * ld + n) = v;
+      if (n >= columns) continue;
+      const acc4_t v = acc[mi][ni];
+      if (sum) *reinterpret_cast<acc4_t*>(sum + m * columns + n) = v;
+      else *reinterpret_cast<uint2*>(out + m * columns + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
+  }
+}
+
+// A piece's two products, side by side so that neither leaves CUs idle alone:
+//   dweight[v0 ..] = dz^T x and its part of dx = dz weight, in `slices` of the piece's columns.
+struct Products {
+  const uint16_t* dz;       // [rows, ldz], zeros from `columns` on
+  int64_t ldz;
+  const uint16_t* x;        // [rows, width]
+  const uint16_t* w;        // the piece's rows of weight
+  int64_t w_row;
+  float* sums;              // [slices][rows, width], or NULL: dx itself
+  uint16_t* dx;
+  uint16_t* dw;             // the piece's rows
+  int32_t rows, width, columns;
+  int32_t slices, slice;    // contracted columns of a slice, a multiple of kK
+  int32_t tiles_m, tiles_n, tiles_d;
+  int32_t dx_items, dw_items;
+  int32_t dx_first;
+};
+
+__global__ void __launch_bounds__(512, 2) vocab_products_kernel(Products a) {
+  __shared__ Stages s;
+  const int first = a.dx_first ? a.dx_items : a.dw_items;
+  const bool dx = ((int)blockIdx.x < first) == (a.dx_first != 0);
+  int id = (int)blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
+  int tm, tn;
+  Acc acc;
+  if (dx) {
+    const int each = a.tiles_m * a.tiles_d, slice = id / each;
+    tile_place(id % each, a.tiles_m, a.tiles_d, &tm, &tn);
+    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+    const int k0 = slice * a.slice, k1 = k0 + a.slice < a.columns ? k0 + a.slice : (a.columns + 7) & ~7;
+    multiply<false, true>(Side{a.dz, a.ldz, a.rows, (a.columns + 7) & ~7}, Side{a.w, a.w_row, a.width, a.columns}, m0, n0, k0, k1, s,
+                          acc);
+    store_tile(acc, m0, n0, a.rows, a.width, a.sums ? a.sums + (int64_t)slice * a.rows * a.width : nullptr, a.dx);
+  } else {
+    tile_place(id, a.tiles_n, a.tiles_d, &tm, &tn);
+    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+    multiply<true, true>(Side{a.dz, a.ldz, (int32_t)a.ldz, a.rows}, Side{a.x, a.width, a.width, a.rows}, m0, n0, 0, a.rows, s, acc);
+    store_tile(acc, m0, n0, a.columns, a.width, nullptr, a.dw);
+  }
+}
+
+// dx from the sums of its parts, in order; four elements a thread.
+__global__ void __launch_bounds__(256) vocab_sum_kernel(const float4* __restrict__ sums, int parts, int64_t each, uint2* __restrict__ dx) {
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < each; e += (int64_t)gridDim.x * 256) {
+    float4 v = sums[e];
+    for (int p = 1; p < parts; ++p) {
+      const float4 o = sums[p * each + e];
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    dx[e] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
 }
 
 int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
 int64_t padded(int64_t n) { return (n + kK - 1) / kK * kK; }
+
+// The backward's cut of the vocabulary: tiles of columns in a piece, and slices of a
+// piece for dx.
+struct Cut {
+  int64_t piece;      // columns
+  int pieces, slices;
+};
+
+// Rounds of `cus` workgroups that n1 items of length k1 and then n2 of length k2 take, in units of length.
+int64_t makespan(int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t cus) {
+  const int64_t full = n1 / cus, rest = n1 % cus;
+  const int64_t early = full * k1, late = early + (rest ? k1 : 0);       // when CUs turn to the second kind
+  if (n2 == 0) return late;
+  int64_t end = early + k2;
+  for (;; end += k2) {      // ends of items of the CUs that turned early
+    const int64_t done = (cus - rest) * ((end - early) / k2) + (end > late ? rest * ((end - late) / k2) : 0);
+    if (done >= n2) return end > late ? end : late;
+  }
+}
+
+// Of the pieces whose dz fits kVocabPieceBytes, and the slices of dx's contracted columns,
+// those for which the products' tiles fill the CUs best.  An item's length is counted in
+// stages, with 8 more for its start and end; a slice more costs dx's fp32 sums once
+// written and read (about 1 stage-equivalent of all CUs for every 2^19 elements).
+Cut choose_cut(const VocabArgs& a) {
+  const int64_t cus = std::max(1, a.cus), tm = tiles(a.rows), td = tiles(a.width), tv = tiles(a.vocab);
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kTile);
+  const int64_t fewest = (tv + most - 1) / most;
+  const int64_t kw = padded(a.rows) / kK + 8, kz = padded(a.width) / kK + 8;
+  Cut best{};
+  int64_t least = INT64_MAX;
+  for (int64_t cut = fewest; cut < fewest + 4 && cut <= tv; ++cut) {
+    const int64_t tn = (tv + cut - 1) / cut, pieces = (tv + tn - 1) / tn;
+    for (int64_t slices = 1; slices <= 16; slices *= 2) {
+      if (slices > 1 && (!a.dx || tn * kTile / slices < 512)) break;
+      const int64_t kx = (tn * kTile / kK + slices - 1) / slices + 8;
+      const int64_t nx = a.dx ? tm * td * slices : 0, nw = a.dw ? tn * td : 0;
+      const int64_t products = kx >= kw ? makespan(nx, kx, nw, kw, cus) : makespan(nw, kw, nx, kx, cus);
+      const int64_t z = (tm * tn + cus - 1) / cus * kz;
+      const int64_t parts = pieces * slices;
+      const int64_t cost = pieces * (products + z) + (parts > 1 ? parts * a.rows * a.width >> 19 : 0);
+      if (cost < least) {
+        least = cost;
+        best = Cut{tn * kTile, (int)pieces, (int)slices};
+      }
+    }
+  }
+  best.piece = std::min<int64_t>(best.piece, a.vocab);
+  return best;
+}
 
 // Consecutive parts of the workspace.
 struct Parts {
@@ -494,30 +647,23 @@ struct FwdParts : Parts {
 };
 
 struct BwdParts : Parts {
-  int64_t rows, xt, wt, dz, dzt, sum;
-  int64_t piece, ldz, ldt;
-  explicit BwdParts(const VocabArgs& a) {
-    piece = std::min(vocab_piece(a), (int64_t)a.vocab);
-    ldz = padded(piece);
-    ldt = padded(a.rows);
+  Cut cut;
+  int64_t rows, x, dz, sums;
+  int64_t ldz;
+  int parts;
+  explicit BwdParts(const VocabArgs& a) : cut(choose_cut(a)) {
+    ldz = padded(cut.piece);
+    parts = cut.pieces * cut.slices;
     rows = add((int64_t)a.rows * (int64_t)sizeof(RowGrad));
-    xt = add(a.dw ? a.width * ldt * 2 : 0);
-    wt = add(a.dx ? a.width * ldz * 2 : 0);
+    x = add(a.dw ? (int64_t)a.rows * a.width * 2 : 0);
     dz = add(a.rows * ldz * 2);
-    dzt = add(piece * ldt * 2);
-    sum = add(a.dx && piece < a.vocab ? (int64_t)a.rows * a.width * 4 : 0);
+    sums = add(a.dx && parts > 1 ? parts * (int64_t)a.rows * a.width * 4 : 0);
   }
 };
 
 unsigned fours(int64_t n) { return (unsigned)((n + 3) / 4); }
 
 }  // namespace
-
-int64_t vocab_piece(const VocabArgs& a) {
-  // (past kVocabMaxLd columns a tile of the transposed weights would not fit a descriptor)
-  const int64_t each = std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows));
-  return std::max<int64_t>(kTile, each / kTile * kTile);
-}
 
 int64_t vocab_fwd_bytes(const VocabArgs& a) { return FwdParts(a).bytes; }
 int64_t vocab_bwd_bytes(const VocabArgs& a) { return BwdParts(a).bytes; }
@@ -530,8 +676,6 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
   const bool one = a.teacher == nullptr;
   auto k = one ? vocab_stats_kernel<true> : vocab_stats_kernel<false>;
   hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, stats, picked, tm, tn);
-  if (!one)
-    hipLaunchKernelGGL(vocab_pick_kernel, dim3(fours((int64_t)a.rows * a.top)), dim3(256), 0, s, a);
   auto l = one ? vocab_loss_kernel<true> : vocab_loss_kernel<false>;
   hipLaunchKernelGGL(l, dim3(fours(a.rows)), dim3(256), 0, s, a, stats, picked, tn);
   return hipGetLastError();
@@ -540,35 +684,53 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
 hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
   const BwdParts at(a);
   RowGrad* rows = reinterpret_cast<RowGrad*>(a.work + at.rows);
-  uint16_t* xt = reinterpret_cast<uint16_t*>(a.work + at.xt);
-  uint16_t* wt = reinterpret_cast<uint16_t*>(a.work + at.wt);
+  uint16_t* x = reinterpret_cast<uint16_t*>(a.work + at.x);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.work + at.dz);
-  uint16_t* dzt = reinterpret_cast<uint16_t*>(a.work + at.dzt);
-  float* sum = reinterpret_cast<float*>(a.work + at.sum);
+  float* sums = reinterpret_cast<float*>(a.work + at.sums);
   const bool one = a.teacher == nullptr;
   auto rk = one ? vocab_rows_kernel<true> : vocab_rows_kernel<false>;
   hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows);
-  const unsigned wide = (unsigned)((a.width + 63) / 64);
   if (a.dw)
-    hipLaunchKernelGGL(vocab_transpose_kernel, dim3((unsigned)(at.ldt / 64), wide), dim3(256), 0, s, a.x, a.x_row, a.rows, a.width,
-                       xt, at.ldt, rows);
+    hipLaunchKernelGGL(vocab_rows_of_x_kernel, dim3((unsigned)std::min(a.rows, 16384)), dim3(256), 0, s, a, rows,
+                       reinterpret_cast<uint4*>(x));
   const int tm = (int)tiles(a.rows), td = (int)tiles(a.width);
-  for (int64_t v0 = 0; v0 < a.vocab; v0 += at.piece) {
-    const int columns = (int)std::min<int64_t>(at.piece, a.vocab - v0);
-    const int64_t ldz = padded(columns);
+  int part = 0;
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += at.cut.piece) {
+    const int columns = (int)std::min<int64_t>(at.cut.piece, a.vocab - v0);
     const int tn = (int)tiles(columns);
-    hipLaunchKernelGGL(vocab_dz_kernel, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, rows, v0, columns, dz, ldz, dzt, at.ldt,
-                       tm, tn);
-    if (!one) hipLaunchKernelGGL(vocab_fix_kernel, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, v0, columns, dz, ldz, dzt, at.ldt);
+    hipLaunchKernelGGL(vocab_dz_kernel, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, rows, v0, columns, dz, at.ldz, tm, tn);
+    if (!one) hipLaunchKernelGGL(vocab_fix_kernel, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, v0, columns, dz, at.ldz);
+    Products p{};
+    p.dz = dz;
+    p.ldz = at.ldz;
+    p.x = x;
+    p.w = a.w + v0 * a.w_row;
+    p.w_row = a.w_row;
+    p.rows = a.rows;
+    p.width = a.width;
+    p.columns = columns;
+    p.tiles_m = tm;
+    p.tiles_n = tn;
+    p.tiles_d = td;
     if (a.dx) {
-      hipLaunchKernelGGL(vocab_transpose_kernel, dim3((unsigned)(ldz / 64), wide), dim3(256), 0, s, a.w + v0 * a.w_row, a.w_row,
-                         columns, a.width, wt, ldz, (const RowGrad*)nullptr);
-      hipLaunchKernelGGL(vocab_product_kernel, dim3((unsigned)(tm * td)), dim3(512), 0, s, Side{dz, ldz, a.rows},
-                         Side{wt, ldz, a.width}, (int)ldz, sum, v0 == 0, v0 + columns == a.vocab, a.dx, (int64_t)a.width, tm, td);
+      p.slice = (int32_t)padded((columns + at.cut.slices - 1) / at.cut.slices);
+      p.slices = (columns + p.slice - 1) / p.slice;
+      p.sums = at.parts > 1 ? sums + (int64_t)part * a.rows * a.width : nullptr;
+      p.dx = a.dx;
+      p.dx_items = tm * td * p.slices;
+      part += p.slices;
     }
-    if (a.dw)
-      hipLaunchKernelGGL(vocab_product_kernel, dim3((unsigned)(tn * td)), dim3(512), 0, s, Side{dzt, at.ldt, columns},
-                         Side{xt, at.ldt, a.width}, (int)at.ldt, sum, true, true, a.dw + v0 * a.width, (int64_t)a.width, tn, td);
+    if (a.dw) {
+      p.dw = a.dw + v0 * a.width;
+      p.dw_items = tn * td;
+    }
+    p.dx_first = p.slice >= a.rows;      // the longer ones first
+    hipLaunchKernelGGL(vocab_products_kernel, dim3((unsigned)(p.dx_items + p.dw_items)), dim3(512), 0, s, p);
+  }
+  if (a.dx && at.parts > 1) {
+    const int64_t each = (int64_t)a.rows * a.width / 4;
+    hipLaunchKernelGGL(vocab_sum_kernel, dim3((unsigned)std::min<int64_t>((each + 255) / 256, 1 << 20)), dim3(256), 0, s,
+                       reinterpret_cast<const float4*>(sums), part, each, reinterpret_cast<uint2*>(a.dx));
   }
   return hipGetLastError();
 }
