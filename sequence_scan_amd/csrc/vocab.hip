@@ -167,31 +167,55 @@ __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m
   for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = acc4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  load_a(0, la);
-  load_b(0, lb);
   const int stages = (k1 - k0 + kK - 1) / kK;
+  auto load = [&](int t) SSM_INLINE {
+    load_a(t * kK, la + (t & 1) * kStage);
+    load_b(t * kK, lb + (t & 1) * kStage);
+  };
+  bf16x8_t fa[2][8], fb[2][4];
+  auto read = [&](int t, int kk) SSM_INLINE {
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) fb[kk][ni] = read_b(s.b[t & 1], ni, kk);
+#pragma unroll
+    for (int mi = 0; mi < 8; ++mi) fa[kk][mi] = read_a(s.a[t & 1], mi, kk);
+  };
+  // 12 operands read (24 accesses where they are turned over) among 32 products
+  constexpr int kReads = (A_ACROSS ? 16 : 8) + (B_ACROSS ? 8 : 4);
+  auto products = [&](int kk) SSM_INLINE {
+#pragma unroll
+    for (int mi = 0; mi < 8; ++mi)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int ni = mi & 1 ? 3 - j : j;      // (neighbours share an operand)
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][ni], fa[kk][mi], acc[mi][ni], 0, 0, 0);
+      }
+#pragma unroll
+    for (int i = 0; i < 12; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, kReads / 12, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    }
+    if constexpr (kReads % 12 != 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads % 12, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // A stage's first half is multiplied while its second half is read, the second half
+  // while the next stage's first is: no product waits for LDS.  Between the halves every
+  // wavefront has read all of the stage, so its place is free for the stage after the
+  // next, which then has a whole stage's time to arrive.
+  load(0);
+  if (stages > 1) load(1);
+  if (stages > 1) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  block_sync();
+  read(0, 0);
   for (int t = 0; t < stages; ++t) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    read(t, 1);
+    products(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     block_sync();
-    if (t + 1 < stages) {
-      load_a((t + 1) * kK, la + ((t + 1) & 1) * kStage);
-      load_b((t + 1) * kK, lb + ((t + 1) & 1) * kStage);
-    }
-    const char* pa = s.a[t & 1];
-    const char* pb = s.b[t & 1];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8_t fa[8], fb[4];
-#pragma unroll
-      for (int ni = 0; ni < 4; ++ni) fb[ni] = read_b(pb, ni, kk);
-#pragma unroll
-      for (int mi = 0; mi < 8; ++mi) fa[mi] = read_a(pa, mi, kk);
-#pragma unroll
-      for (int mi = 0; mi < 8; ++mi)
-#pragma unroll
-        for (int ni = 0; ni < 4; ++ni)
-          acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[ni], fa[mi], acc[mi][ni], 0, 0, 0);
-    }
+    if (t + 2 < stages) load(t + 2);
+    read(t + 1 < stages ? t + 1 : t, 0);
+    products(1);
   }
 }
 
@@ -598,26 +622,30 @@ int64_t makespan(int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t cus) {
 }
 
 // Of the pieces whose dz fits kVocabPieceBytes, and the slices of dx's contracted columns,
-// those for which the products' tiles fill the CUs best.  An item's length is counted in
-// stages, with 8 more for its start and end; a slice more costs dx's fp32 sums once
-// written and read (about 1 stage-equivalent of all CUs for every 2^19 elements).
+// those for which the tiles of dz and of the products fill the CUs best.  A tile's time is
+// counted in stages, with 8 more for its start and end; a slice more costs dx's fp32 sums
+// once written and read, about 1 stage of all CUs for every 2^20 elements.  (8192 x 2560 x
+// 50280: pieces of 64 tiles and a rest of 5, whose tiles go round the CUs without a gap.)
 Cut choose_cut(const VocabArgs& a) {
   const int64_t cus = std::max(1, a.cus), tm = tiles(a.rows), td = tiles(a.width), tv = tiles(a.vocab);
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kTile);
-  const int64_t fewest = (tv + most - 1) / most;
+  const int64_t most = std::min(
+      tv, std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kTile));
   const int64_t kw = padded(a.rows) / kK + 8, kz = padded(a.width) / kK + 8;
+  auto piece_cost = [&](int64_t tn, int64_t slices) {
+    const int64_t kx = (tn * kTile / kK + slices - 1) / slices + 8;
+    const int64_t nx = a.dx ? tm * td * slices : 0, nw = a.dw ? tn * td : 0;
+    return (kx >= kw ? makespan(nx, kx, nw, kw, cus) : makespan(nw, kw, nx, kx, cus)) + (tm * tn + cus - 1) / cus * kz;
+  };
   Cut best{};
   int64_t least = INT64_MAX;
-  for (int64_t cut = fewest; cut < fewest + 4 && cut <= tv; ++cut) {
-    const int64_t tn = (tv + cut - 1) / cut, pieces = (tv + tn - 1) / tn;
-    for (int64_t slices = 1; slices <= 16; slices *= 2) {
+  const int64_t step = std::max<int64_t>(1, most / 16);
+  for (int64_t tn = most; tn > most / 2; tn -= step) {
+    const int64_t whole = tv / tn, rest = tv % tn, pieces = whole + (rest != 0);
+    for (int64_t slices = 1; slices <= 8; slices *= 2) {
       if (slices > 1 && (!a.dx || tn * kTile / slices < 512)) break;
-      const int64_t kx = (tn * kTile / kK + slices - 1) / slices + 8;
-      const int64_t nx = a.dx ? tm * td * slices : 0, nw = a.dw ? tn * td : 0;
-      const int64_t products = kx >= kw ? makespan(nx, kx, nw, kw, cus) : makespan(nw, kw, nx, kx, cus);
-      const int64_t z = (tm * tn + cus - 1) / cus * kz;
       const int64_t parts = pieces * slices;
-      const int64_t cost = pieces * (products + z) + (parts > 1 ? parts * a.rows * a.width >> 19 : 0);
+      const int64_t cost = whole * piece_cost(tn, slices) + (rest ? piece_cost(rest, slices) : 0) +
+                           (parts > 1 ? parts * a.rows * a.width >> 20 : 0);
       if (cost < least) {
         least = cost;
         best = Cut{tn * kTile, (int)pieces, (int)slices};
