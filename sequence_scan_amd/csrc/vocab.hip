@@ -12,10 +12,12 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef float acc4_t __attribute__((ext_vector_type(4)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kK = 64;            // contracted elements in a stage: rows of 128 bytes
 constexpr int kTile = kVocabTile;   // rows and columns of a workgroup's tile of C
+constexpr int kFewRows = 16;        // rows that are one matrix operand
+constexpr int kFewWidth = 4096;     // ... whose x fits LDS
 
 // One side of a product, a bf16 matrix in either order:
 //   along  (ACROSS false): [n][k], rows run along the contracted dimension;
@@ -75,7 +77,7 @@ struct Stages {
 constexpr uint32_t kStage = kTile * kK * 2;
 
 // acc[mi][ni][i]: C[wm * 128 + mi * 16 + (lane & 15)][wn * 64 + ni * 16 + 4 * (lane >> 4) + i].
-typedef acc4_t Acc[8][4];
+typedef f4_t Acc[8][4];
 
 // A side's loads: a wavefront brings four times 1 KB of a stage.
 template <bool ACROSS>
@@ -166,7 +168,7 @@ __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = acc4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int stages = (k1 - k0 + kK - 1) / kK;
   auto load = [&](int t) SSM_INLINE {
     load_a(t * kK, la + (t & 1) * kStage);
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
 #pragma unroll
           for (int ni = 0; ni < 4; ++ni) {
             const int piece = (n >> 2) + ni * 4;
-            *reinterpret_cast<acc4_t*>(z + (mi * 16 + (lane & 15)) * 256 + (piece ^ (lane & 15)) * 4) = acc[mi][ni];
+            *reinterpret_cast<f4_t*>(z + (mi * 16 + (lane & 15)) * 256 + (piece ^ (lane & 15)) * 4) = acc[mi][ni];
           }
       }
       block_sync();
@@ -331,6 +333,121 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
       }
     }
   }
+}
+
+// The same for up to 16 rows, where the weights' way from memory is all that counts.  x
+// lies in LDS, in the order in which the matrix cores take it; every wavefront reads an
+// equal share of the vocabulary's rows, 16 at a time, straight to registers, with eight
+// lines of 16 x 64 elements under way and no barrier between them.
+template <int KMAX, bool ONE>
+__global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, float2* __restrict__ stats, float* __restrict__ picked, int share) {
+  constexpr int kAhead = 8;
+  __shared__ alignas(1024) char xs[KMAX / 32 * 1024];       // [32 contracted elements][lane][8 elements]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quarter = lane >> 4;          // of 32 contracted elements
+  const int lines = (a.width + 63) / 64, pieces = (a.width + 7) / 8;
+  for (int e = threadIdx.x; e < lines * 8 * 16; e += 512) {
+    const int c = e >> 4, m = e & 15;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < pieces) v = *reinterpret_cast<const uint4*>(a.x + (int64_t)(m < a.rows ? m : a.rows - 1) * a.x_row + c * 8);
+    *reinterpret_cast<uint4*>(xs + (c >> 2) * 1024 + ((c & 3) * 16 + m) * 16) = v;
+  }
+  const int id = blockIdx.x * 8 + wave;
+  const int64_t first = (int64_t)id * share;
+  const int columns = (int)(first >= a.vocab ? 0 : a.vocab - first < share ? a.vocab - first : share);
+  const int steps = (columns + 15) / 16 * lines;
+  const int64_t target = ONE && (lane & 15) < a.rows ? a.index[lane & 15] - first : -1;
+  bf16x8_t w[kAhead][2];
+  int load_group = 0, load_line = 0;      // what is loaded next
+  const uint16_t* row = a.w;
+  auto begin_row = [&]() SSM_INLINE {
+    // (columns past the share repeat its last)
+    const int c = load_group * 16 + (lane & 15);
+    row = a.w + (first + (c < columns ? c : columns - 1)) * a.w_row;
+  };
+  auto load = [&](bf16x8_t (&f)[2]) SSM_INLINE {
+    const int k = load_line * 64 + quarter * 8;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      // (past the row's end its start, against zeros of x)
+      const int at = k + kk * 32;
+      f[kk] = *reinterpret_cast<const bf16x8_t*>(row + (at < a.width ? at : 0));
+    }
+    if (++load_line == lines) {
+      load_line = 0;
+      ++load_group;
+      begin_row();
+    }
+  };
+  if (steps > 0) begin_row();
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (u < steps) load(w[u]);
+  block_sync();
+  f4_t acc = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  float top2 = -__builtin_inff(), sum = 0.0f;      // of row lane & 15, over this lane's columns
+  int line = 0, n = 4 * quarter;                   // columns n .. + 3 of the share
+  auto step = [&](const bf16x8_t (&f)[2]) SSM_INLINE {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[kk], *reinterpret_cast<const bf16x8_t*>(xs + (line * 2 + kk) * 1024 + lane * 16),
+                                                    acc, 0, 0, 0);
+    if (++line < lines) return;
+    line = 0;
+    float top = top2;
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = acc[i] * a.scale;
+      z[i] = n + i < columns ? v * kLog2e : -__builtin_inff();
+      top = __builtin_fmaxf(top, z[i]);
+      if (ONE && target == n + i && n + i < columns) picked[lane & 15] = v;
+    }
+    const float from = top == -__builtin_inff() ? 0.0f : top;
+    sum *= __builtin_amdgcn_exp2f(top2 - from);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(z[i] - from);
+    top2 = top;
+    acc = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    n += 16;
+  };
+  for (int at = 0; at < steps; at += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (at + u < steps) {
+        step(w[u]);
+        if (at + u + kAhead < steps) load(w[u]);
+      }
+  }
+#pragma unroll
+  for (int o = 16; o < 64; o *= 2) {
+    const float t = __shfl_xor(top2, o), v = __shfl_xor(sum, o), top = __builtin_fmaxf(top2, t);
+    if (top != -__builtin_inff()) sum = sum * __builtin_amdgcn_exp2f(top2 - top) + v * __builtin_amdgcn_exp2f(t - top);
+    top2 = top;
+  }
+  if (lane < a.rows && lane < 16) stats[(int64_t)id * a.rows + lane] = make_float2(top2, sum);
+}
+
+// The logits at the indices of few rows, one wavefront for each.
+__global__ void __launch_bounds__(256) vocab_pick_kernel(VocabArgs a) {
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (e >= a.rows * a.top) return;
+  const int64_t v = a.index[e];
+  if (v < 0 || v >= a.vocab) return;
+  const uint16_t* x = a.x + e / a.top * a.x_row;
+  const uint16_t* w = a.w + v * a.w_row;
+  float z = 0.0f;
+  for (int k = lane * 8; k < a.width; k += 512) {
+    float xv[8], wv[8];
+    Vec16<uint16_t>::unpack(*reinterpret_cast<const uint4*>(x + k), xv);
+    Vec16<uint16_t>::unpack(*reinterpret_cast<const uint4*>(w + k), wv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z = __builtin_fmaf(xv[i], wv[i], z);
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) z += __shfl_xor(z, o);
+  if (lane == 0) a.logits[e] = z * a.scale;
 }
 
 // What one row's indices and teacher logits say, over a wavefront: whether the row
@@ -376,34 +493,64 @@ __device__ __forceinline__ Teacher teacher_of(const VocabArgs& a, int64_t row, i
   return t;
 }
 
-// A row's log sum of exponentials from its pieces', and its loss: a wavefront a row.
+// A row's log sum of exponentials from its pieces', and its loss.  A workgroup of 1024
+// threads takes `each` rows (a power of two up to 16), 1024 / each threads a row for the
+// pieces and a wavefront a row for the loss.
 template <bool ONE>
-__global__ void __launch_bounds__(256) vocab_loss_kernel(VocabArgs a, const float2* __restrict__ stats,
-                                                         const float* __restrict__ picked, int tiles_n) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= a.rows) return;
-  float top = -__builtin_inff();
-  for (int n = lane; n < tiles_n; n += 64) {
-    const float v = stats[(int64_t)n * a.rows + row].x;
-    top = top != top ? top : (v != v ? v : __builtin_fmaxf(top, v));
+__global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const float2* __restrict__ stats,
+                                                          const float* __restrict__ picked, int pieces, int each) {
+  __shared__ float2 part[1024];
+  __shared__ float logs[16];
+  const int64_t row0 = (int64_t)blockIdx.x * each;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  {
+    const int64_t row = row0 + (threadIdx.x & (each - 1));
+    const int per = 1024 / each;
+    float2 r = make_float2(-__builtin_inff(), 0.0f);
+    if (row < a.rows) {
+#pragma unroll 4
+      for (int n = threadIdx.x / each; n < pieces; n += per) {
+        const float2 v = stats[(int64_t)n * a.rows + row];
+        const float top = __builtin_fmaxf(r.x, v.x);
+        // (a maximum is finite or plus infinity; nothing yet: 2^-inf = 0)
+        r.y = r.y * __builtin_amdgcn_exp2f(r.x - top) + v.y * __builtin_amdgcn_exp2f(v.x - top);
+        r.x = top;
+      }
+    }
+    part[threadIdx.x] = r;
   }
-  top = wave_max(top);
-  float sum = 0.0f;
-  for (int n = lane; n < tiles_n; n += 64) {
-    const float2 v = stats[(int64_t)n * a.rows + row];
-    sum = __builtin_fmaf(v.y, __builtin_amdgcn_exp2f(v.x - top), sum);
+  for (int half = 512; half >= each; half /= 2) {
+    block_sync();
+    if (threadIdx.x < half) {
+      const float2 r = part[threadIdx.x], v = part[threadIdx.x + half];
+      if (v.x != -__builtin_inff()) {
+        const float top = __builtin_fmaxf(r.x, v.x);
+        part[threadIdx.x] = make_float2(top, r.y * __builtin_amdgcn_exp2f(r.x - top) + v.y * __builtin_amdgcn_exp2f(v.x - top));
+      }
+    }
   }
-  sum = wave_sum(sum);
-  // top is the largest logit in base 2, of which ln 2 gives back its value to an ulp
-  const float lse = __builtin_fmaf(top, kLn2, __builtin_amdgcn_logf(sum) * kLn2);
-  float loss = 0.0f;
-  if constexpr (ONE) {
-    const int64_t v = a.index[row];
-    if (v >= a.vocab) loss = __builtin_nanf("");
-    else if (v >= 0) loss = (lse - picked[row]) + a.z_loss * lse * lse;
-  } else {
+  block_sync();
+  if (threadIdx.x < each && row0 + threadIdx.x < a.rows) {
+    const float2 r = part[threadIdx.x];
+    // r.x is the largest logit in base 2, of which ln 2 gives back its value to an ulp
+    const float lse = __builtin_fmaf(r.x, kLn2, __builtin_amdgcn_logf(r.y) * kLn2);
+    a.lse[row0 + threadIdx.x] = lse;
+    logs[threadIdx.x] = lse;
+    if constexpr (ONE) {
+      const int64_t v = a.index[row0 + threadIdx.x];
+      float loss = 0.0f;
+      if (v >= a.vocab) loss = __builtin_nanf("");
+      else if (v >= 0) loss = (lse - picked[row0 + threadIdx.x]) + a.z_loss * lse * lse;
+      a.loss[row0 + threadIdx.x] = loss;
+    }
+  }
+  if constexpr (!ONE) {
+    block_sync();
+    const int64_t row = row0 + wave;
+    if (wave >= each || row >= a.rows) return;
+    const float lse = logs[wave];
     const Teacher t = teacher_of(a, row, lane);
+    float loss = 0.0f;
     for (int k = lane; k < a.top; k += 64) {
       const int64_t v = a.index[row * a.top + k];
       if (v < 0 || v >= a.vocab) a.logits[row * a.top + k] = 0.0f;
@@ -420,10 +567,7 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(VocabArgs a, const floa
       }
       loss = wave_sum(loss) * a.temperature * a.temperature;
     }
-  }
-  if (lane == 0) {
-    a.lse[row] = lse;
-    a.loss[row] = loss;
+    if (lane == 0) a.loss[row] = loss;
   }
 }
 
@@ -539,8 +683,8 @@ __device__ __forceinline__ void store_tile(const Acc acc, int64_t m0, int64_t n0
     for (int ni = 0; ni < 4; ++ni) {
       const int64_t n = n0 + wn * 64 + ni * 16 + 4 * (lane >> 4);
       if (n >= columns) continue;
-      const acc4_t v = acc[mi][ni];
-      if (sum) *reinterpret_cast<acc4_t*>(sum + m * columns + n) = v;
+      const f4_t v = acc[mi][ni];
+      if (sum) *reinterpret_cast<f4_t*>(sum + m * columns + n) = v;
       else *reinterpret_cast<uint2*>(out + m * columns + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
   }
@@ -666,10 +810,17 @@ struct Parts {
   }
 };
 
+// Few rows' weights are streamed: (us, width 2560, vocabulary 50280, rows at a time .. and in tiles)
 struct FwdParts : Parts {
-  int64_t stats, picked;
+  bool few;
+  int64_t share, groups, pieces, stats, picked;
   explicit FwdParts(const VocabArgs& a) {
-    stats = add(tiles(a.vocab) * a.rows * 8);
+    few = a.rows <= kFewRows && a.width <= kFewWidth;
+    const int64_t waves = (int64_t)std::max(1, a.cus) * 8 * (a.width <= kFewWidth / 2 ? 2 : 1);      // that x in LDS leaves room for
+    share = (a.vocab + waves - 1) / waves;
+    groups = (a.vocab + share * 8 - 1) / (share * 8);
+    pieces = few ? groups * 8 : tiles(a.vocab);
+    stats = add(pieces * a.rows * 8);
     picked = add(a.teacher ? 0 : (int64_t)a.rows * 4);
   }
 };
@@ -700,12 +851,21 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
   const FwdParts at(a);
   float2* stats = reinterpret_cast<float2*>(a.work + at.stats);
   float* picked = reinterpret_cast<float*>(a.work + at.picked);
-  const int tm = (int)tiles(a.rows), tn = (int)tiles(a.vocab);
   const bool one = a.teacher == nullptr;
-  auto k = one ? vocab_stats_kernel<true> : vocab_stats_kernel<false>;
-  hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, stats, picked, tm, tn);
+  if (at.few) {
+    auto k = a.width <= kFewWidth / 2 ? (one ? vocab_few_kernel<kFewWidth / 2, true> : vocab_few_kernel<kFewWidth / 2, false>)
+                                      : (one ? vocab_few_kernel<kFewWidth, true> : vocab_few_kernel<kFewWidth, false>);
+    hipLaunchKernelGGL(k, dim3((unsigned)at.groups), dim3(512), 0, s, a, stats, picked, (int)at.share);
+    if (!one) hipLaunchKernelGGL(vocab_pick_kernel, dim3(fours(a.rows * a.top)), dim3(256), 0, s, a);
+  } else {
+    const int tm = (int)tiles(a.rows), tn = (int)tiles(a.vocab);
+    auto k = one ? vocab_stats_kernel<true> : vocab_stats_kernel<false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, stats, picked, tm, tn);
+  }
+  int each = 1;
+  while (each < 16 && each < a.rows) each *= 2;
   auto l = one ? vocab_loss_kernel<true> : vocab_loss_kernel<false>;
-  hipLaunchKernelGGL(l, dim3(fours(a.rows)), dim3(256), 0, s, a, stats, picked, tn);
+  hipLaunchKernelGGL(l, dim3((unsigned)((a.rows + each - 1) / each)), dim3(1024), 0, s, a, stats, picked, (int)at.pieces, each);
   return hipGetLastError();
 }
 
