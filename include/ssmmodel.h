@@ -31,7 +31,8 @@ extern "C" {
  *
  *   x, r, i      : [batch, seqlen, width] in in_dtype; token (b, t)'s values start
  *                  (b * seqlen + t) * x_row (r_row, i_row) elements after the first
- *                  token's (slices of a packed projection; rows may not overlap)
+ *                  token's (slices of a packed projection; rows may not overlap, and are
+ *                  at most 2^24 elements apart)
  *   rate         : [width] fp32 or NULL; meant to be >= 0 (below, a > 1 and without
  *                  SSM_GSCAN_LERP m is NaN)
  *   initial_state, last_state: [batch, width] fp32, each NULL for zero or not stored;

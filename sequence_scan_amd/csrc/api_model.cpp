@@ -20,6 +20,8 @@ static_assert(ssm::kGsSegment == SSM_GSCAN_SEGMENT && ssm::kVocabPieceBytes == S
 
 // ------------------------------------------------------ gated linear recurrence
 
+constexpr int64_t kGsMostRow = int64_t{1} << 24;      // elements between rows, and channels
+
 struct GsSizes {
   int64_t tokens;    // batch * seqlen
   int64_t elems;     // ... * width
@@ -39,8 +41,8 @@ ssm_status gs_check(int64_t batch, int64_t seqlen, int64_t width, int flags, std
   if (!mul_ok(batch, seqlen, &sz->tokens) || !mul_ok(sz->tokens, width, &sz->elems) || !mul_ok(sz->elems, 16, &t) ||
       !mul_ok(batch, width, &sz->state) || !mul_ok(sz->state, 16, &t))
     return fail(SSM_ERR_BAD_SHAPE, "element count overflows int64");
-  if (sz->state > INT32_MAX - 1023)
-    return fail(SSM_ERR_UNSUPPORTED, "batch * width = %lld exceeds 2^31 - 1024", (long long)sz->state);
+  if (sz->state > INT32_MAX - 1023 || width > kGsMostRow)
+    return fail(SSM_ERR_UNSUPPORTED, "batch * width = %lld exceeds 2^31 - 1024 or width = %lld 2^24", (long long)sz->state, (long long)width);
   sz->states = sz->state * ceil_div(seqlen, SSM_GSCAN_SEGMENT);
   // a workgroup of 512 threads for every 64 channels of a row and 128 steps, or of 256 for 64 steps
   if (ceil_div(seqlen, ssm::kGsBwdTile) * batch * ceil_div(width, 64) > kMaxThreads / 256)
@@ -56,6 +58,8 @@ ssm_status gs_rows(const char* name, const void* p, int64_t tokens, int64_t widt
   if (row < width)
     return fail(SSM_ERR_UNSUPPORTED, "%s rows are %lld elements apart, less than width=%lld", name, (long long)row,
                 (long long)width);
+  if (row > kGsMostRow)
+    return fail(SSM_ERR_UNSUPPORTED, "%s rows are %lld elements apart: more than 2^24", name, (long long)row);
   int64_t n;
   if (!mul_ok(tokens, row, &n) || !mul_ok(n, 8, &n)) return fail(SSM_ERR_BAD_SHAPE, "%s extent overflows int64", name);
   *bytes = ((tokens - 1) * row + width) * esz;

@@ -8,12 +8,13 @@
 namespace ssm {
 namespace {
 
-constexpr int kSteps = 16;         // steps of a wavefront: what its registers hold
-constexpr int kFwdWaves = 8;       // tiles of 128 steps forward
-constexpr int kBwdWaves = 4;       // ... and 64 back, which keeps twice as much of each
+// Steps of a wavefront, what its registers hold, and wavefronts of a tile.
+constexpr int kFwdSteps = 16, kFwdWaves = 8;
+constexpr int kBwdSteps = 8, kBwdWaves = 8;       // (back, a step keeps three times as much)
+constexpr int kFwdApart = kGsSegment / kFwdSteps, kBwdApart = kGsSegment / kBwdSteps;      // wavefronts between stored states
 
-static_assert(kGsFwdTile == kSteps * kFwdWaves && kGsBwdTile == kSteps * kBwdWaves, "model.h agrees");
-static_assert(kGsSegment == 2 * kSteps, "stored states enter every other wavefront");
+static_assert(kGsFwdTile == kFwdSteps * kFwdWaves && kGsBwdTile == kBwdSteps * kBwdWaves, "model.h agrees");
+static_assert(kGsFwdTile % kGsSegment == 0 && kGsBwdTile % kGsSegment == 0, "tiles begin with a stored state");
 
 // The tile that a workgroup takes: its place in the chain and its strip.
 __device__ __forceinline__ void take_tile(const Chain& c, int* tile, int* strip) {
@@ -28,6 +29,28 @@ __device__ __forceinline__ void take_tile(const Chain& c, int* tile, int* strip)
   *strip = n % c.strips;
 }
 
+// Where a wavefront's steps lie.
+template <int CH, int kSteps>
+struct Place {
+  int64_t b, t0, left, tok;      // batch row; first step; steps of the sequence from there; token
+  int64_t d;                     // the lane's first channel
+  int n;                         // steps of this wavefront's kSteps that there are
+  bool in;                       // whether the channel is
+  __device__ __forceinline__ Place(const GscanArgs& a, int tile, int strip, int steps, int wave, int lane) {
+    const int per_row = (int)((a.width + 64 * CH - 1) / (64 * CH));
+    b = strip / per_row;
+    d = (int64_t)(strip % per_row) * (64 * CH) + lane * CH;
+    in = d < a.width;
+    t0 = (int64_t)tile * steps + wave * kSteps;
+    left = a.seqlen - t0;
+    n = left < 0 ? 0 : left > kSteps ? kSteps : (int)left;
+    tok = b * a.seqlen + t0;
+  }
+  // Byte offset of the lane's channels in a row of values of `size` bytes, in the
+  // wavefront's step j (not needed where all steps are there).
+  __device__ __forceinline__ uint32_t off(int size, int j = 0) const { return in && j < n ? (uint32_t)d * size : kNowhere; }
+};
+
 template <typename T, bool RATE, bool LERP, bool GATE, int CH>
 __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs a, Chain c) {
   __shared__ float2 parts[kFwdWaves][CH][64];
@@ -35,52 +58,42 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
   int tile, strip;
   take_tile(c, &tile, &strip);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per_row = (int)((a.width + 64 * CH - 1) / (64 * CH));
-  const int64_t b = strip / per_row;
-  const int d0 = strip % per_row * (64 * CH) + lane * CH;
-  const bool in = d0 < a.width;
-  const uint32_t d = in ? d0 : 0;             // (lanes past the width repeat the first channels)
-  const int64_t t0 = (int64_t)tile * kGsFwdTile + wave * kSteps;
-  const int64_t left = a.seqlen - t0;
-  const int n = left < 0 ? 0 : left > kSteps ? kSteps : (int)left;
-  const int64_t tok = b * a.seqlen + t0;
-  float rate[CH];
+  constexpr int kSteps = kFwdSteps;
+  const Place<CH, kSteps> at(a, tile, strip, kGsFwdTile, wave, lane);
+  const uint32_t off = at.off(sizeof(T));
+  float rate2[CH], P[kSteps][CH], H[kSteps][CH];
 #pragma unroll
-  for (int k = 0; k < CH; ++k) rate[k] = RATE ? a.rate[d + k] : 0.0f;
-
-  // all loads first: a wavefront has 16 steps of three tensors under way
-  uint32_t x[kSteps], r[kSteps], i[kSteps];
+  for (int k = 0; k < CH; ++k) rate2[k] = RATE && at.in ? a.rate[at.d + k] * kLog2e : 0.0f;
+  auto steps = [&](auto whole) SSM_INLINE {
+    constexpr bool kWhole = decltype(whole)::value;      // all kSteps are there
+    // all loads first: a wavefront has 16 steps of three tensors under way
+    const Rows rx(a.x, at.tok, a.x_row, sizeof(T)), rr(a.r, at.tok, a.r_row, sizeof(T)), ri(a.i, at.tok, a.i_row, sizeof(T));
+    uint32_t x[kSteps], r[kSteps], i[kSteps];
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j)
-    if (j < n) {
-      x[j] = load_raw<T, CH>(a.x, tok + j, a.x_row, d);
-      r[j] = load_raw<T, CH>(a.r, tok + j, a.r_row, d);
-      if constexpr (GATE) i[j] = load_raw<T, CH>(a.i, tok + j, a.i_row, d);
+    for (int j = 0; j < kSteps; ++j) {
+      const uint32_t o = kWhole ? off : at.off(sizeof(T), j);
+      r[j] = load_raw<T, CH>(rr, j, o);
+      if constexpr (GATE) i[j] = load_raw<T, CH>(ri, j, o);
+      x[j] = load_raw<T, CH>(rx, j, o);
     }
-  float P[kSteps][CH], H[kSteps][CH], p[CH], h[CH];
 #pragma unroll
-  for (int k = 0; k < CH; ++k) p[k] = 1.0f, h[k] = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
-    if (j < n) {
+    for (int j = 0; j < kSteps; ++j)
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const Decay e = decay<RATE, LERP>(raw_value<T>(r[j], k), rate[k]);
+        float ea, em;
+        decay<RATE, LERP>(gate_exp<!RATE>(raw_value<T>(r[j], k)), rate2[k], &ea, &em);
         float u = raw_value<T>(x[j], k);
-        if constexpr (GATE) {
-          float pos, neg;
-          sigmoids(raw_value<T>(i[j], k), &pos, &neg);
-          u *= pos;
-        }
-        p[k] *= e.a;
-        h[k] = __builtin_fmaf(e.a, h[k], e.m * u);
+        if constexpr (GATE) u *= gate_open(gate_exp<false>(raw_value<T>(i[j], k)));
+        u *= em;
+        if (!kWhole && j >= at.n) ea = 1.0f, u = 0.0f;
+        P[j][k] = j ? P[j - 1][k] * ea : ea;
+        H[j][k] = j ? __builtin_fmaf(ea, H[j - 1][k], u) : u;
       }
-    }
+  };
+  if (at.n == kSteps) steps(std::true_type{});
+  else steps(std::false_type{});
 #pragma unroll
-    for (int k = 0; k < CH; ++k) P[j][k] = p[k], H[j][k] = h[k];
-  }
-#pragma unroll
-  for (int k = 0; k < CH; ++k) parts[wave][k][lane] = make_float2(p[k], h[k]);
+  for (int k = 0; k < CH; ++k) parts[wave][k][lane] = make_float2(P[kSteps - 1][k], H[kSteps - 1][k]);
   block_sync();
   if (wave == 0) {
     float hin[CH];
@@ -88,7 +101,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
       float tp[CH], th[CH];
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        tp[k] = p[k], th[k] = h[k];
+        tp[k] = P[kSteps - 1][k], th[k] = H[kSteps - 1][k];
 #pragma unroll
         for (int w = 1; w < kFwdWaves; ++w) {
           const float2 v = parts[w][k][lane];
@@ -99,12 +112,13 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
       chain_enter<CH>(c, strip, tile, tp, th, hin);
     } else {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) hin[k] = a.initial ? a.initial[b * a.width + d + k] : 0.0f;
+      for (int k = 0; k < CH; ++k) hin[k] = a.initial && at.in ? a.initial[at.b * a.width + at.d + k] : 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) enter[k][lane] = hin[k];
   }
   block_sync();
+  float h[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     h[k] = enter[k][lane];
@@ -113,121 +127,116 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
       h[k] = __builtin_fmaf(v.x, h[k], v.y);
     }
   }
-  if (!in || n == 0) return;
-  if (a.states && wave % 2 == 0) {
-    float* s = a.states + (b * ((a.seqlen + kGsSegment - 1) / kGsSegment) + t0 / kGsSegment) * a.width + d;
+  if (at.n == 0) return;
+  if (a.states && wave % kFwdApart == 0 && at.in) {
+    float* s = a.states + (at.b * ((a.seqlen + kGsSegment - 1) / kGsSegment) + at.t0 / kGsSegment) * a.width + at.d;
 #pragma unroll
     for (int k = 0; k < CH; ++k) s[k] = h[k];
   }
   float v[CH];
+  auto stores = [&](auto whole, auto type) SSM_INLINE {
+    using Tout = decltype(type);
+    const Rows ro(a.out, at.tok, a.width, sizeof(Tout));
+    const uint32_t off = at.off(sizeof(Tout));
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j)
-    if (j < n) {
+    for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) v[k] = __builtin_fmaf(P[j][k], h[k], H[j][k]);
-      if (a.out_bf16) store_raw<uint16_t, CH>(a.out, tok + j, a.width, d, v);
-      else store_raw<float, CH>(a.out, tok + j, a.width, d, v);
+      for (int k = 0; k < CH; ++k) v[k] = __builtin_fmaf(P[j][k], h[k], H[j][k]);      // (past the last step the last one's)
+      store_raw<Tout, CH>(ro, j, decltype(whole)::value ? off : at.off(sizeof(Tout), j), v);
     }
-  if (a.last && n == left) {
+  };
+  if (at.n == kSteps) {
+    if (a.out_bf16) stores(std::true_type{}, uint16_t{});
+    else stores(std::true_type{}, float{});
+  } else {
+    if (a.out_bf16) stores(std::false_type{}, uint16_t{});
+    else stores(std::false_type{}, float{});
+  }
+  if (a.last && at.n == at.left && at.in) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) a.last[b * a.width + d + k] = v[k];
+    for (int k = 0; k < CH; ++k) a.last[at.b * a.width + at.d + k] = v[k];
   }
 }
 
-// Of a gate's two sigmoids the smaller one, with the argument's sign: the larger is one
-// less it, to an ulp.
-__device__ __forceinline__ float small_sigmoid(float pos, float neg) { return pos < neg ? -pos : neg; }
-__device__ __forceinline__ void both_sigmoids(float s, float* pos, float* neg) {
-  const float m = __builtin_fabsf(s), o = 1.0f - m;
-  const bool shut = __float_as_int(s) < 0;
-  *pos = shut ? m : o;
-  *neg = shut ? o : m;
-}
-
 template <typename T, bool RATE, bool LERP, bool GATE, int CH>
-__global__ void __launch_bounds__(64 * kBwdWaves, 2) gscan_bwd_kernel(GscanArgs a, Chain c) {
+__global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs a, Chain c) {
+  __shared__ uint32_t kept[kBwdWaves][3][kBwdSteps][64];      // x, r and i as they lie in memory, for the second pass
   __shared__ float2 parts[kBwdWaves][CH][64];
-  __shared__ float half[kBwdWaves][CH][64];
+  __shared__ float ahead[kBwdWaves][CH][64];      // forward: what leaves a wavefront for a zero state entering
   __shared__ float enter[CH][64];
   int back, strip;
   take_tile(c, &back, &strip);
   const int tile = c.tiles - 1 - back;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per_row = (int)((a.width + 64 * CH - 1) / (64 * CH));
-  const int64_t b = strip / per_row;
-  const int d0 = strip % per_row * (64 * CH) + lane * CH;
-  const bool in = d0 < a.width;
-  const uint32_t d = in ? d0 : 0;
-  const int64_t t0 = (int64_t)tile * kGsBwdTile + wave * kSteps;
-  const int64_t left = a.seqlen - t0;
-  const int n = left < 0 ? 0 : left > kSteps ? kSteps : (int)left;
-  const int64_t tok = b * a.seqlen + t0;
+  constexpr int kSteps = kBwdSteps;
+  const Place<CH, kSteps> at(a, tile, strip, kGsBwdTile, wave, lane);
+  const uint32_t off = at.off(sizeof(T));
+  // the state stored last before the wavefront's steps
   float rate[CH], h[CH];
 #pragma unroll
-  for (int k = 0; k < CH; ++k) rate[k] = RATE ? a.rate[d + k] : 0.0f, h[k] = 0.0f;
-  if (wave % 2 == 0 && n > 0) {
-    const float* s = a.states_in + (b * ((a.seqlen + kGsSegment - 1) / kGsSegment) + t0 / kGsSegment) * a.width + d;
+  for (int k = 0; k < CH; ++k) rate[k] = RATE && at.in ? a.rate[at.d + k] : 0.0f, h[k] = 0.0f;
+  if (at.n > 0 && at.in) {
+    const float* s = a.states_in + (at.b * ((a.seqlen + kGsSegment - 1) / kGsSegment) + at.t0 / kGsSegment) * a.width + at.d;
 #pragma unroll
     for (int k = 0; k < CH; ++k) h[k] = s[k];
   }
-  uint32_t x[kSteps], r[kSteps], i[kSteps];
-  float g[kSteps][CH];
+  // what a step keeps in registers: its decay, the input's coefficient and the gradient
+  float A[kSteps][CH], M[kSteps][CH], g[kSteps][CH], p[CH], q[CH], f[CH];
+  auto steps = [&](auto whole, auto type) SSM_INLINE {
+    constexpr bool kWhole = decltype(whole)::value;
+    using Tout = decltype(type);
+    const Rows rx(a.x, at.tok, a.x_row, sizeof(T)), rr(a.r, at.tok, a.r_row, sizeof(T)), ri(a.i, at.tok, a.i_row, sizeof(T));
+    const Rows rg(a.dout, at.tok, a.width, sizeof(Tout));
+    const uint32_t off_g = at.off(sizeof(Tout));
+    uint32_t x[kSteps], r[kSteps], i[kSteps];
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j)
-    if (j < n) {
-      x[j] = load_raw<T, CH>(a.x, tok + j, a.x_row, d);
-      r[j] = load_raw<T, CH>(a.r, tok + j, a.r_row, d);
-      if constexpr (GATE) i[j] = load_raw<T, CH>(a.i, tok + j, a.i_row, d);
-      if (a.out_bf16) {
-        const uint32_t w = load_raw<uint16_t, CH>(a.dout, tok + j, a.width, d);
-#pragma unroll
-        for (int k = 0; k < CH; ++k) g[j][k] = raw_value<uint16_t>(w, k);
-      } else {
-#pragma unroll
-        for (int k = 0; k < CH; ++k) g[j][k] = static_cast<const float*>(a.dout)[(tok + j) * a.width + d + k];
-      }
+    for (int j = 0; j < kSteps; ++j) {
+      const uint32_t o = kWhole ? off : at.off(sizeof(T), j);
+      r[j] = load_raw<T, CH>(rr, j, o);
+      if constexpr (GATE) i[j] = load_raw<T, CH>(ri, j, o);
+      x[j] = load_raw<T, CH>(rx, j, o);
+      load_values<Tout, CH>(rg, j, kWhole ? off_g : at.off(sizeof(Tout), j), g[j]);
     }
-  // per step and channel: the decay, the input's coefficient and the gates' sigmoids
-  float A[kSteps][CH], M[kSteps][CH], sr[kSteps][CH], si[kSteps][CH];
-  float enters[CH];
 #pragma unroll
-  for (int k = 0; k < CH; ++k) enters[k] = h[k];
+    for (int k = 0; k < CH; ++k) f[k] = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j)
-    if (j < n) {
+    for (int j = 0; j < kSteps; ++j)
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const Decay e = decay<RATE, LERP>(raw_value<T>(r[j], k), rate[k]);
-        A[j][k] = e.a;
-        M[j][k] = e.m;
-        sr[j][k] = small_sigmoid(e.pos, e.neg);
+        decay<RATE, LERP>(gate_exp<!RATE>(raw_value<T>(r[j], k)), rate[k] * kLog2e, &A[j][k], &M[j][k]);
         float u = raw_value<T>(x[j], k);
-        if constexpr (GATE) {
-          float pos, neg;
-          sigmoids(raw_value<T>(i[j], k), &pos, &neg);
-          si[j][k] = small_sigmoid(pos, neg);
-          u *= pos;
-        }
-        h[k] = __builtin_fmaf(e.a, h[k], e.m * u);
+        if constexpr (GATE) u *= gate_open(gate_exp<false>(raw_value<T>(i[j], k)));
+        if (!kWhole && j >= at.n) A[j][k] = 1.0f, M[j][k] = 0.0f;
+        f[k] = __builtin_fmaf(A[j][k], f[k], M[j][k] * u);
       }
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      kept[wave][0][j][lane] = x[j];
+      kept[wave][1][j][lane] = r[j];
+      if constexpr (GATE) kept[wave][2][j][lane] = i[j];
     }
-  // back through the wavefront's steps: what leaves it for a zero gradient entering
-  float p[CH], q[CH];
+    // back through the wavefront's steps: what leaves it for a zero gradient entering
 #pragma unroll
-  for (int k = 0; k < CH; ++k) p[k] = 1.0f, q[k] = 0.0f;
+    for (int k = 0; k < CH; ++k) {
+      p[k] = A[kSteps - 1][k], q[k] = A[kSteps - 1][k] * g[kSteps - 1][k];
 #pragma unroll
-  for (int j = kSteps - 1; j >= 0; --j)
-    if (j < n) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
+      for (int j = kSteps - 2; j >= 0; --j) {
         p[k] *= A[j][k];
         q[k] = A[j][k] * (q[k] + g[j][k]);
       }
     }
+  };
+  if (at.n == kSteps) {
+    if (a.out_bf16) steps(std::true_type{}, uint16_t{});
+    else steps(std::true_type{}, float{});
+  } else {
+    if (a.out_bf16) steps(std::false_type{}, uint16_t{});
+    else steps(std::false_type{}, float{});
+  }
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     parts[wave][k][lane] = make_float2(p[k], q[k]);
-    half[wave][k][lane] = h[k];
+    ahead[wave][k][lane] = f[k];
   }
   block_sync();
   if (wave == kBwdWaves - 1) {
@@ -247,7 +256,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 2) gscan_bwd_kernel(GscanArgs 
       chain_enter<CH>(c, strip, back, tp, tq, gin);
     } else {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) gin[k] = a.dlast ? a.dlast[b * a.width + d + k] : 0.0f;
+      for (int k = 0; k < CH; ++k) gin[k] = a.dlast && at.in ? a.dlast[at.b * a.width + at.d + k] : 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) enter[k][lane] = gin[k];
@@ -262,67 +271,67 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 2) gscan_bwd_kernel(GscanArgs 
       const float2 v = parts[w][k][lane];
       carry[k] = __builtin_fmaf(v.x, carry[k], v.y);
     }
-    h[k] = wave % 2 == 0 ? enters[k] : half[wave - 1][k][lane];
+    for (int w = wave / kBwdApart * kBwdApart; w < wave; ++w) h[k] = __builtin_fmaf(parts[w][k][lane].x, h[k], ahead[w][k][lane]);
     sum[k] = 0.0f;
-  }
 #pragma unroll
-  for (int j = kSteps - 1; j >= 0; --j)
-    if (j < n) {
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        g[j][k] += carry[k];
-        carry[k] = A[j][k] * g[j][k];
-      }
+    for (int j = kSteps - 1; j >= 0; --j) {
+      g[j][k] += carry[k];
+      carry[k] = A[j][k] * g[j][k];
     }
-  if (a.dinitial && t0 == 0 && in) {
+  }
+  if (a.dinitial && at.t0 == 0 && at.in) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) a.dinitial[b * a.width + d + k] = carry[k];
+    for (int k = 0; k < CH; ++k) a.dinitial[at.b * a.width + at.d + k] = carry[k];
   }
   // forward again, with the states on the way
+  auto gradients = [&](auto whole) SSM_INLINE {
+    const Rows rx(a.dx, at.tok, a.width, sizeof(T)), rr(a.dr, at.tok, a.width, sizeof(T)), ri(a.di, at.tok, a.width, sizeof(T));
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j)
-    if (j < n) {
-      float dx[CH], dr[CH], di[CH];
+    for (int j = 0; j < kSteps; ++j) {
+        const uint32_t o = decltype(whole)::value ? off : at.off(sizeof(T), j);
+        float dx[CH], dr[CH], di[CH];
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const float xv = raw_value<T>(x[j], k);
-        float pos = 1.0f, neg = 0.0f, rpos, rneg;
-        if constexpr (GATE) both_sigmoids(si[j][k], &pos, &neg);
-        both_sigmoids(sr[j][k], &rpos, &rneg);
-        const float u = xv * pos, gm = g[j][k] * M[j][k];
-        Decay e;
-        e.a = A[j][k];
-        e.m = M[j][k];
-        const float by = g[j][k] * __builtin_fmaf(e.a, h[k], u * decay_slope<LERP>(e));
-        dx[k] = gm * pos;
-        di[k] = gm * u * neg;
-        if constexpr (RATE) {
+        for (int k = 0; k < CH; ++k) {
+          float u = raw_value<T>(kept[wave][0][j][lane], k);
+          const float er = gate_exp<true>(raw_value<T>(kept[wave][1][j][lane], k));
+          const float rpos = gate_open(er), gm = g[j][k] * M[j][k];
+          dx[k] = gm;
+          if constexpr (GATE) {
+            const float ei = gate_exp<true>(raw_value<T>(kept[wave][2][j][lane], k));
+            const float pos = gate_open(ei);
+            u *= pos;
+            dx[k] *= pos;
+            di[k] = gm * u * (ei * pos);
+          }
+          const float by = g[j][k] * __builtin_fmaf(A[j][k], h[k], u * decay_slope<LERP>(A[j][k], M[j][k]));
           const float bp = by * rpos;
-          sum[k] -= bp;
-          dr[k] = -bp * rate[k] * rneg;
-        } else {
-          dr[k] = by * rneg;
+          if constexpr (RATE) {
+            sum[k] -= decltype(whole)::value || j < at.n ? bp : 0.0f;
+            dr[k] = -bp * rate[k] * (er * rpos);
+          } else {
+            dr[k] = bp * er;
+          }
+          h[k] = __builtin_fmaf(A[j][k], h[k], M[j][k] * u);
         }
-        h[k] = __builtin_fmaf(e.a, h[k], e.m * u);
+        store_raw<T, CH>(rx, j, o, dx);
+        store_raw<T, CH>(rr, j, o, dr);
+        if constexpr (GATE) store_raw<T, CH>(ri, j, o, di);
       }
-      if (in) {
-        store_raw<T, CH>(a.dx, tok + j, a.width, d, dx);
-        store_raw<T, CH>(a.dr, tok + j, a.width, d, dr);
-        if constexpr (GATE) store_raw<T, CH>(a.di, tok + j, a.width, d, di);
-      }
-    }
+  };
+  if (at.n == kSteps) gradients(std::true_type{});
+  else gradients(std::false_type{});
   if (RATE && a.part) {
     block_sync();
 #pragma unroll
-    for (int k = 0; k < CH; ++k) half[wave][k][lane] = sum[k];
+    for (int k = 0; k < CH; ++k) ahead[wave][k][lane] = sum[k];
     block_sync();
-    if (wave == 0 && in) {
+    if (wave == 0 && at.in) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        float s = half[0][k][lane];
+        float s = ahead[0][k][lane];
 #pragma unroll
-        for (int w = 1; w < kBwdWaves; ++w) s += half[w][k][lane];
-        a.part[(b * c.tiles + tile) * a.width + d + k] = s;
+        for (int w = 1; w < kBwdWaves; ++w) s += ahead[w][k][lane];
+        a.part[(at.b * c.tiles + tile) * a.width + at.d + k] = s;
       }
     }
   }
@@ -352,18 +361,14 @@ __global__ void __launch_bounds__(256) gscan_step_kernel(GscanArgs a) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= a.batch * a.width) return;
   const int64_t b = e / a.width, d = e % a.width;
-  auto get = [&](const void* p, int64_t row) SSM_INLINE { return raw_value<T>(load_raw<T, 1>(p, b, row, (uint32_t)d), 0); };
-  const Decay c = decay<RATE, LERP>(get(a.r, a.r_row), RATE ? a.rate[d] : 0.0f);
-  float u = get(a.x, a.x_row);
-  if constexpr (GATE) {
-    float pos, neg;
-    sigmoids(get(a.i, a.i_row), &pos, &neg);
-    u *= pos;
-  }
-  const float h[1] = {__builtin_fmaf(c.a, a.initial[e], c.m * u)};
-  a.last[e] = h[0];
-  if (a.out_bf16) store_raw<uint16_t, 1>(a.out, b, a.width, (uint32_t)d, h);
-  else store_raw<float, 1>(a.out, b, a.width, (uint32_t)d, h);
+  float ea, em;
+  decay<RATE, LERP>(gate_exp<!RATE>(Io<T>::cvt(Io<T>::load(a.r, b * a.r_row + d))), RATE ? a.rate[d] * kLog2e : 0.0f, &ea, &em);
+  float u = Io<T>::cvt(Io<T>::load(a.x, b * a.x_row + d));
+  if constexpr (GATE) u *= gate_open(gate_exp<false>(Io<T>::cvt(Io<T>::load(a.i, b * a.i_row + d))));
+  const float h = __builtin_fmaf(ea, a.initial[e], em * u);
+  a.last[e] = h;
+  if (a.out_bf16) Io<uint16_t>::store(a.out, e, h);
+  else Io<float>::store(a.out, e, h);
 }
 
 // out[d] = sum over n rows of part[n][d], in a fixed order: 16 wavefronts take every

@@ -10,56 +10,49 @@
 namespace ssm {
 namespace {
 
-// sigmoid(v) and sigmoid(-v), each to a few ulp: with e = exp(-v) they are 1 / (1 + e)
-// and e / (1 + e).  Where e is infinite the second is 1; a NaN stays one.
-__device__ __forceinline__ void sigmoids(float v, float* pos, float* neg) {
+// exp(-v), from which sigmoid(v) = 1 / (1 + e) and sigmoid(-v) = e / (1 + e), each to a few
+// ulp.  Where the second is needed, e is held at 8e37 past fp32's range, whose reciprocal is
+// still a normal number: the sigmoids are then 1.25e-38 and 1.  A NaN stays one.
+template <bool BOTH>
+__device__ __forceinline__ float gate_exp(float v) {
   const float e = __builtin_amdgcn_exp2f(-v * kLog2e);
-  const float p = __builtin_amdgcn_rcpf(1.0f + e);
-  *pos = p;
-  *neg = e > 8.0e37f ? 1.0f : e * p;
+  return BOTH && e > 8.0e37f ? 8.0e37f : e;
 }
+__device__ __forceinline__ float gate_open(float e) { return __builtin_amdgcn_rcpf(1.0f + e); }
 
-// 1 - exp(-w) for w >= 0 (and, by the same formulas, w < 0), given exp(-w) to an ulp.
-// Below 1/2 the difference would lose what w is small by: there the series
-// w (1 - w/2 (1 - w/3 (..))) up to w^8, whose next term is w^8 / 9! < 1.1e-8 of it.
+// 1 - exp(-w) for w >= 0, given exp(-w) to an ulp.  Below 3/4 the difference would lose
+// what w is small by: there w times a polynomial of degree 5 in w, fitted to
+// (1 - exp(-w)) / w over [0, 3/4] (off by at most 2.1e-8 of it, exact at 0).
 __device__ __forceinline__ float one_minus_exp(float w, float e) {
-  float s = __builtin_fmaf(w, -1.0f / 8.0f, 1.0f);
-  s = __builtin_fmaf(w * s, -1.0f / 7.0f, 1.0f);
-  s = __builtin_fmaf(w * s, -1.0f / 6.0f, 1.0f);
-  s = __builtin_fmaf(w * s, -1.0f / 5.0f, 1.0f);
-  s = __builtin_fmaf(w * s, -1.0f / 4.0f, 1.0f);
-  s = __builtin_fmaf(w * s, -1.0f / 3.0f, 1.0f);
-  s = __builtin_fmaf(w * s, -1.0f / 2.0f, 1.0f);
-  return __builtin_fabsf(w) < 0.5f ? w * s : 1.0f - e;
+  float s = __builtin_fmaf(w, -0.00101896108f, 0.00804723334f);
+  s = __builtin_fmaf(s, w, -0.0415632911f);
+  s = __builtin_fmaf(s, w, 0.166650176f);
+  s = __builtin_fmaf(s, w, -0.499999136f);
+  s = w * __builtin_fmaf(s, w, 1.0f);
+  asm volatile("" : "+v"(s));       // (computed, not branched around: a branch would part the steps)
+  return w < 0.75f ? s : 1.0f - e;
 }
 
-struct Decay {
-  float a;      // the decay
-  float m;      // the input's coefficient
-  float pos;    // sigmoid(r)
-  float neg;    // sigmoid(-r)
-};
-
+// A step's decay and its input's coefficient, from e = exp(-r); rate2 = rate log2 e.
 template <bool RATE, bool LERP>
-__device__ __forceinline__ Decay decay(float r, float rate) {
-  Decay d;
-  sigmoids(r, &d.pos, &d.neg);
+__device__ __forceinline__ void decay(float e, float rate2, float* a, float* m) {
+  const float pos = gate_open(e);
   if constexpr (RATE) {
-    const float y = rate * d.pos;
-    d.a = __builtin_amdgcn_exp2f(-y * kLog2e);
-    d.m = LERP ? one_minus_exp(y, d.a) : __builtin_amdgcn_sqrtf(one_minus_exp(2.0f * y, d.a * d.a));
+    const float y = rate2 * pos;
+    *a = __builtin_amdgcn_exp2f(-y);
+    *m = LERP ? one_minus_exp(y * kLn2, *a) : __builtin_amdgcn_sqrtf(one_minus_exp(y * (2.0f * kLn2), *a * *a));
   } else {
-    d.a = d.pos;
-    d.m = LERP ? d.neg : __builtin_amdgcn_sqrtf(d.neg * (1.0f + d.pos));
+    *a = pos;
+    const float neg = e * pos;
+    *m = LERP ? neg : __builtin_amdgcn_sqrtf(neg * (1.0f + pos));
   }
-  return d;
 }
 
 // dm/dlog a: of 1 - a, or of sqrt(1 - a^2), where a zero m has no derivative (0).
 template <bool LERP>
-__device__ __forceinline__ float decay_slope(const Decay& d) {
-  if constexpr (LERP) return -d.a;
-  return d.m == 0.0f ? 0.0f : -d.a * d.a * __builtin_amdgcn_rcpf(d.m);
+__device__ __forceinline__ float decay_slope(float a, float m) {
+  if constexpr (LERP) return -a;
+  return m == 0.0f ? 0.0f : -a * a * __builtin_amdgcn_rcpf(m);
 }
 
 // ------------------------------------------------------------ the chain of tiles
@@ -158,29 +151,58 @@ __device__ __forceinline__ void chain_enter(const Chain& c, int strip, int tile,
 
 // ------------------------------------------------------------------------ a tile
 
+// A tensor's rows from some token on, through a buffer descriptor: the row is a scalar
+// offset and the lane's channels a vector one, so that an access costs no arithmetic, and
+// what a lane whose offset is kNowhere reads is 0 and what it writes is dropped.  (Rows are
+// at most 2^24 elements apart: 15 of them stay within the descriptor.)
+constexpr uint32_t kNowhere = 0x80000000u;
+struct Rows {
+  __amdgpu_buffer_rsrc_t at;
+  uint32_t row;       // bytes
+  __device__ __forceinline__ Rows(const void* p, int64_t token, int64_t row_elems, int size) : row((uint32_t)row_elems * size) {
+    // (the same for all lanes)
+    char* first = const_cast<char*>(static_cast<const char*>(p)) + token * row_elems * size;
+    const uint64_t bits = (uint64_t)(uintptr_t)first;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)bits), hi = __builtin_amdgcn_readfirstlane((uint32_t)(bits >> 32));
+    at = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), 0, 0x7fffffff, 0x00020000);
+  }
+};
+
 // A lane's CH neighbouring channels of a token as they lie in memory: one fp32 or bf16
 // value, or two bf16 values in a word.
 template <typename T, int CH>
-__device__ __forceinline__ uint32_t load_raw(const void* p, int64_t token, int64_t row, uint32_t d) {
-  const char* at = static_cast<const char*>(p) + token * row * (int64_t)sizeof(T);     // the same for all lanes
-  const uint32_t off = d * (uint32_t)sizeof(T);
-  if constexpr (sizeof(T) * CH == 4) return *reinterpret_cast<const uint32_t*>(at + off);
-  else return *reinterpret_cast<const uint16_t*>(at + off);
+__device__ __forceinline__ uint32_t load_raw(const Rows& r, int j, uint32_t d) {
+  if constexpr (sizeof(T) * CH == 4) return __builtin_amdgcn_raw_buffer_load_b32(r.at, d, j * r.row, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b16(r.at, d, j * r.row, 0);
 }
 template <typename T>
 __device__ __forceinline__ float raw_value(uint32_t w, int k) {
   if constexpr (sizeof(T) == 4) return __uint_as_float(w);
   else return __uint_as_float(k ? w & 0xffff0000u : w << 16);
 }
+// ... and CH values.
 template <typename T, int CH>
-__device__ __forceinline__ void store_raw(void* p, int64_t token, int64_t row, uint32_t d, const float (&v)[CH]) {
-  char* at = static_cast<char*>(p) + token * row * (int64_t)sizeof(T) + d * (uint32_t)sizeof(T);
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (CH == 2) *reinterpret_cast<float2*>(at) = make_float2(v[0], v[1]);
-    else *reinterpret_cast<float*>(at) = v[0];
+__device__ __forceinline__ void load_values(const Rows& r, int j, uint32_t d, float (&v)[CH]) {
+  if constexpr (sizeof(T) * CH == 8) {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(r.at, d, j * r.row, 0);
+    v[0] = __uint_as_float(w[0]);
+    v[1] = __uint_as_float(w[1]);
   } else {
-    if constexpr (CH == 2) *reinterpret_cast<uint32_t*>(at) = pack_bf16x2(v[0], v[1]);
-    else *reinterpret_cast<uint16_t*>(at) = f32_to_bf16_rne(v[0]);
+    const uint32_t w = load_raw<T, CH>(r, j, d);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) v[k] = raw_value<T>(w, k);
+  }
+}
+template <typename T, int CH>
+__device__ __forceinline__ void store_raw(const Rows& r, int j, uint32_t d, const float (&v)[CH]) {
+  if constexpr (sizeof(T) == 4) {
+    typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+    if constexpr (CH == 2)
+      __builtin_amdgcn_raw_buffer_store_b64(u2_t{__float_as_uint(v[0]), __float_as_uint(v[1])}, r.at, d, j * r.row, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r.at, d, j * r.row, 0);
+  } else {
+    if constexpr (CH == 2) __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), r.at, d, j * r.row, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(v[0]), r.at, d, j * r.row, 0);
   }
 }
 
