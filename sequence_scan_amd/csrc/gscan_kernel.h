@@ -57,14 +57,13 @@ __device__ __forceinline__ float decay_slope(float a, float m) {
 
 // ------------------------------------------------------------ the chain of tiles
 //
-// A workgroup holds a tile in registers: kSteps steps of each of its wavefronts, 64 CH
+// A workgroup holds a tile in registers: some steps of each of its wavefronts, 64 CH
 // channels.  Within it a step is h -> a h + b, so a tile is h -> P h + H with P and H
 // its own, known once it is loaded.  What enters a tile is then joined without reading
-// anything twice: tiles come in groups of kGsGroup; a tile publishes (P, H), waits for
-// the state that enters its group and for the (P, H) of the group's tiles before it,
-// and composes them in order; the group's last tile publishes the state that enters the
-// next group.  Sums are composed in a fixed order, so the results do not depend on which
-// workgroup runs when.
+// anything twice: tiles come in groups; a tile publishes (P, H), composes the (P, H) of
+// the group's tiles before it in order, and waits for the state that enters its group;
+// the group's last tile publishes the state that enters the next group.  Everything is
+// composed in a fixed order, so the results do not depend on which workgroup runs when.
 //
 // Every wait ends: tiles are handed out by a counter, in the order of the chain, so what
 // a tile waits for belongs to workgroups that are running already; publishing (P, H)
@@ -74,12 +73,14 @@ __device__ __forceinline__ float decay_slope(float a, float m) {
 
 constexpr uint32_t kUnwritten = 0xffffffffu;    // a NaN that no arithmetic returns
 constexpr int kMostPolls = 1 << 22;
+constexpr int kPartsAtOnce = 4;
 
 struct Chain {
   uint64_t* parts;       // [strips][tiles][channels] (P, H)
   uint32_t* states;      // [strips][groups][channels]: the state that enters a group
   uint32_t* next;        // tiles handed out
   int32_t tiles, groups, strips;
+  int32_t group;         // tiles of a group
 };
 
 // (P, H) as one word; a NaN as the usual one.
@@ -98,51 +99,59 @@ template <int CH>
 __device__ __forceinline__ void chain_enter(const Chain& c, int strip, int tile, const float (&P)[CH], const float (&H)[CH],
                                             float (&h)[CH]) {
   const int lane = threadIdx.x & 63;
-  const int group = tile / kGsGroup, in = tile % kGsGroup;
+  const int group = tile / c.group, in = tile % c.group;
   uint64_t* mine = c.parts + ((int64_t)strip * c.tiles + tile) * (64 * CH) + lane;
   uint32_t* state = c.states + ((int64_t)strip * c.groups + group) * (64 * CH) + lane;
-  const bool last = in == kGsGroup - 1 || tile == c.tiles - 1;
+  const bool last = in == c.group - 1 || tile == c.tiles - 1;
   if (!last) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) publish(mine + 64 * k, P[k], H[k]);
   }
+  float gp[CH], gh[CH];      // of the group's tiles before this one
+#pragma unroll
+  for (int k = 0; k < CH; ++k) gp[k] = 1.0f, gh[k] = 0.0f;
+  for (int j0 = 0; j0 < in; j0 += kPartsAtOnce) {
+    uint64_t w[kPartsAtOnce][CH];
+    for (int poll = 0; poll < kMostPolls; ++poll) {
+      bool missing = false;
+#pragma unroll
+      for (int j = 0; j < kPartsAtOnce; ++j)
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          // (in the last round, the group's last one before this again)
+          const int from = j0 + j < in ? j0 + j : in - 1;
+          w[j][k] = __hip_atomic_load(mine + (from - in) * (64 * CH) + 64 * k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+      for (int j = 0; j < kPartsAtOnce; ++j)
+#pragma unroll
+        for (int k = 0; k < CH; ++k) missing |= (uint32_t)w[j][k] == kUnwritten;
+      if (!__any(missing)) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int j = 0; j < kPartsAtOnce; ++j)
+      if (j0 + j < in) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const float p = __uint_as_float((uint32_t)w[j][k]);
+          gp[k] *= p;
+          gh[k] = __builtin_fmaf(p, gh[k], __uint_as_float((uint32_t)(w[j][k] >> 32)));
+        }
+      }
+  }
   uint32_t s[CH];
-  uint64_t w[kGsGroup - 1][CH];
-#pragma unroll
-  for (int k = 0; k < CH; ++k) s[k] = kUnwritten;
-#pragma unroll
-  for (int j = 0; j < kGsGroup - 1; ++j)
-#pragma unroll
-    for (int k = 0; k < CH; ++k) w[j][k] = ~0ull;
   for (int poll = 0; poll < kMostPolls; ++poll) {
     bool missing = false;
 #pragma unroll
     for (int k = 0; k < CH; ++k) s[k] = __hip_atomic_load(state + 64 * k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-    for (int j = 0; j < kGsGroup - 1; ++j)
-      if (j < in) {
-#pragma unroll
-        for (int k = 0; k < CH; ++k)
-          w[j][k] = __hip_atomic_load(mine + (j - in) * (64 * CH) + 64 * k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-#pragma unroll
     for (int k = 0; k < CH; ++k) missing |= s[k] == kUnwritten;
-#pragma unroll
-    for (int j = 0; j < kGsGroup - 1; ++j)
-      if (j < in) {
-#pragma unroll
-        for (int k = 0; k < CH; ++k) missing |= (uint32_t)w[j][k] == kUnwritten;
-      }
     if (!__any(missing)) break;
     __builtin_amdgcn_s_sleep(1);
   }
 #pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    h[k] = __uint_as_float(s[k]);
-#pragma unroll
-    for (int j = 0; j < kGsGroup - 1; ++j)
-      if (j < in) h[k] = __builtin_fmaf(__uint_as_float((uint32_t)w[j][k]), h[k], __uint_as_float((uint32_t)(w[j][k] >> 32)));
-  }
+  for (int k = 0; k < CH; ++k) h[k] = __builtin_fmaf(gp[k], __uint_as_float(s[k]), gh[k]);
   if (last && tile + 1 < c.tiles) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) publish(state + 64 * CH + 64 * k, __builtin_fmaf(P[k], h[k], H[k]));

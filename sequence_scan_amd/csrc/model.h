@@ -12,7 +12,6 @@ namespace ssm {
 constexpr int kGsSegment = 32;    // steps between two stored states
 constexpr int kGsFwdTile = 128;   // steps that a workgroup holds at a time
 constexpr int kGsBwdTile = 64;
-constexpr int kGsGroup = 8;       // tiles whose parts are composed from one published state
 
 struct GscanArgs {
   const void* x;            // token (b, t)'s channels at (b * seqlen + t) * x_row
