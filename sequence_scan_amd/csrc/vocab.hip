@@ -221,6 +221,17 @@ __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m
   }
 }
 
+// Two neighbouring operands' columns of a row of C, rounded to bf16, as eight in a row:
+// quarter q = lane >> 4 of the wavefront has columns 4 q .. + 3 of either; exchanged
+// between neighbouring quarters, the even one of a pair has eight of the first, the odd
+// one eight of the second.  first_of_eight: where they begin, of the two's 32 columns.
+__device__ __forceinline__ uint4 eight_bf16(const float (&a)[4], const float (&b)[4]) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[0], a[1]), pack_bf16x2(b[0], b[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[2], a[3]), pack_bf16x2(b[2], b[3]), false, false);
+  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
+}
+__device__ __forceinline__ int first_of_eight(int lane) { return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8; }
+
 // The tile of C that a workgroup computes.  Workgroups go round the eight XCDs, whose
 // L2s are their own: each XCD gets a run of tiles, in groups of eight rows of tiles that
 // go through the columns together, so that the 32 tiles under way read 8 + 4 panels.
@@ -635,16 +646,20 @@ __global__ void __launch_bounds__(512, 2) vocab_dz_kernel(VocabArgs a, const Row
     if (m < a.rows) g = rows[m];
     const int64_t target = g.target < 0 ? -1 : g.target - v0;
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) {
-      const int64_t n = n0 + wn * 64 + ni * 16 + 4 * (lane >> 4);
-      float d[4];
+    for (int ni = 0; ni < 4; ni += 2) {
+      float d[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[mi][ni][i], s2, -g.lse2));
-        d[i] = g.target == -2 || n + i >= columns ? 0.0f : p - (n + i == target ? g.hard : 0.0f);
+      for (int h = 0; h < 2; ++h) {
+        const int64_t n = n0 + wn * 64 + (ni + h) * 16 + 4 * (lane >> 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[mi][ni + h][i], s2, -g.lse2));
+          d[h][i] = g.target == -2 || n + i >= columns ? 0.0f : p - (n + i == target ? g.hard : 0.0f);
+        }
       }
-      if (m < a.rows && n < ldz)
-        *reinterpret_cast<uint2*>(dz + m * ldz + n) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+      const uint4 v = eight_bf16(d[0], d[1]);
+      const int64_t n = n0 + wn * 64 + ni * 16 + first_of_eight(lane);
+      if (m < a.rows && n < ldz) *reinterpret_cast<uint4*>(dz + m * ldz + n) = v;
     }
   }
 }
@@ -678,14 +693,24 @@ __device__ __forceinline__ void store_tile(const Acc acc, int64_t m0, int64_t n0
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi) {
     const int64_t m = m0 + wm * 128 + mi * 16 + (lane & 15);
-    if (m >= rows) continue;
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) {
-      const int64_t n = n0 + wn * 64 + ni * 16 + 4 * (lane >> 4);
-      if (n >= columns) continue;
-      const f4_t v = acc[mi][ni];
-      if (sum) *reinterpret_cast<f4_t*>(sum + m * columns + n) = v;
-      else *reinterpret_cast<uint2*>(out + m * columns + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    for (int ni = 0; ni < 4; ni += 2) {
+      if (sum) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t n = n0 + wn * 64 + (ni + h) * 16 + 4 * (lane >> 4);
+          if (m < rows && n < columns) *reinterpret_cast<f4_t*>(sum + m * columns + n) = acc[mi][ni + h];
+        }
+      } else {
+        float v[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[h][i] = acc[mi][ni + h][i];
+        const uint4 w = eight_bf16(v[0], v[1]);
+        const int64_t n = n0 + wn * 64 + ni * 16 + first_of_eight(lane);
+        if (m < rows && n < columns) *reinterpret_cast<uint4*>(out + m * columns + n) = w;
+      }
     }
   }
 }
