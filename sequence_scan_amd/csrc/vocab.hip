@@ -263,6 +263,21 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
   const int n = wn * 64 + 4 * (lane >> 4);          // + ni * 16 + i
   const int columns = (int)(a.vocab - n0 < kTile ? a.vocab - n0 : kTile);
+  // Many indices: those of 128 rows at a time, of which a thread holds the first kHeld
+  // while the tile is dealt with.
+  constexpr int kHeld = ONE ? 1 : 16;
+  int64_t held[kHeld];
+  auto entries_of = [&](int half) SSM_INLINE {
+    const int64_t left = a.rows - (m0 + half * 128);
+    return (uint32_t)(left < 0 ? 0 : left > 128 ? 128 : left) * (uint32_t)a.top;
+  };
+  auto hold = [&](int half) SSM_INLINE {
+    const uint32_t entries = entries_of(half);
+    const int64_t* at = a.index + (m0 + half * 128) * a.top;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) held[j] = threadIdx.x + j * 512 < entries ? at[threadIdx.x + j * 512] : -1;
+  };
+  if constexpr (!ONE) hold(0);
 #pragma unroll
   for (int mi = 0; mi < 8; ++mi) {
     const int m = wm * 128 + mi * 16 + (lane & 15);
@@ -332,16 +347,20 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
           }
       }
       block_sync();
-      const int64_t first = m0 + half * 128, left = a.rows - first;
-      const uint32_t entries = (uint32_t)(left < 0 ? 0 : left > 128 ? 128 : left) * (uint32_t)a.top;
-#pragma unroll 4
-      for (uint32_t e = threadIdx.x; e < entries; e += 512) {
-        const int64_t v = a.index[first * a.top + e] - n0;
+      const uint32_t entries = entries_of(half);
+      const int64_t first = (m0 + half * 128) * a.top;
+      auto pick = [&](uint32_t e, int64_t index) SSM_INLINE {
+        const int64_t v = index - n0;
         if (v >= 0 && v < columns) {
           const uint32_t r = e / (uint32_t)a.top, col = (uint32_t)v;
-          a.logits[first * a.top + e] = z[r * 256 + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)];
+          a.logits[first + e] = z[r * 256 + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)];
         }
-      }
+      };
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) pick(threadIdx.x + j * 512, held[j]);
+#pragma unroll 4
+      for (uint32_t e = threadIdx.x + kHeld * 512; e < entries; e += 512) pick(e, a.index[first + e]);
+      if (half == 0) hold(1);
     }
   }
 }
