@@ -610,12 +610,14 @@ struct RowGrad {
   int32_t target;       // cross entropy: its column, or -1
 };
 
+// A wavefront a row.  Distillation: also hard q for each of the row's indices, where the
+// same index twice has the sum of both.
 template <bool ONE>
-__global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows) {
+__global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows, float* __restrict__ hard) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (row >= a.rows) return;
-  RowGrad g{0.0f, 0.0f, 0.0f, -1};
+  RowGrad g{0.0f, 0.0f, 0.0f, -2};
   const float lse = a.lse_in[row];
   if constexpr (ONE) {
     const int64_t v = a.index[row];
@@ -624,13 +626,22 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* _
       g = RowGrad{lse * kLog2e, d * __builtin_fmaf(2.0f * a.z_loss, lse, 1.0f), d, (int32_t)v};
     }
   } else {
-    // (a.scale is over the temperature: its square leaves one of them)
-    const float d = a.dloss[row] * a.temperature * a.temperature * a.scale;
-    if (teacher_of(a, row, lane).counts) g = RowGrad{lse * kLog2e, d, d, -1};
-    else g.target = -2;
-  }
-  if constexpr (ONE) {
-    if (g.target < 0) g.target = -2;
+    const Teacher t = teacher_of(a, row, lane);
+    if (t.counts) {
+      // (a.scale is over the temperature: its square leaves one of them)
+      const float d = a.dloss[row] * a.temperature * a.temperature * a.scale;
+      g = RowGrad{lse * kLog2e, d, d, -1};
+      const float t2 = kLog2e / a.temperature, by = d / t.sum;
+      const int64_t at = row * a.top;
+      for (int k = lane; k < a.top; k += 64) {
+        const int64_t v = a.index[at + k];
+        float q = 0.0f;
+#pragma unroll 4
+        for (int j = 0; j < a.top; ++j)
+          if (a.index[at + j] == v) q += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[at + j], t2, -t.top2));
+        hard[at + k] = q * by;
+      }
+    }
   }
   if (lane == 0) rows[row] = g;
 }
@@ -685,24 +696,17 @@ __global__ void __launch_bounds__(512, 2) vocab_dz_kernel(VocabArgs a, const Row
 
 // Distillation: dz at the teacher's indices, formed from the stored logits in place of
 // the rounded softmax.
-__global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGrad* __restrict__ rows, int64_t v0, int columns,
-                                                        uint16_t* __restrict__ dz, int64_t ldz) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= a.rows) return;
-  const RowGrad g = rows[row];
-  if (g.target == -2) return;
-  const Teacher t = teacher_of(a, row, lane);
-  const float t2 = kLog2e / a.temperature, by = 1.0f / t.sum;
-  const int64_t at = row * a.top;
-  for (int k = lane; k < a.top; k += 64) {
-    const int64_t n = a.index[at + k] - v0;
+__global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGrad* __restrict__ rows, const float* __restrict__ hard,
+                                                        int64_t v0, int columns, uint16_t* __restrict__ dz, int64_t ldz) {
+  const int64_t entries = (int64_t)a.rows * a.top;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < entries; e += (int64_t)gridDim.x * 256) {
+    const int64_t n = a.index[e] - v0;
     if (n < 0 || n >= columns) continue;
-    float q = 0.0f;
-    for (int j = 0; j < a.top; ++j)
-      if (a.index[at + j] == a.index[at + k]) q += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[at + j], t2, -t.top2));
-    const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(a.logits_in[at + k], kLog2e, -g.lse2));
-    dz[row * ldz + n] = f32_to_bf16_rne(p - g.hard * q * by);
+    const int64_t row = e / a.top;
+    const RowGrad g = rows[row];
+    if (g.target == -2) continue;
+    const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(a.logits_in[e], kLog2e, -g.lse2));
+    dz[row * ldz + n] = f32_to_bf16_rne(p - hard[e]);
   }
 }
 
@@ -871,13 +875,14 @@ struct FwdParts : Parts {
 
 struct BwdParts : Parts {
   Cut cut;
-  int64_t rows, x, dz, sums;
+  int64_t rows, hard, x, dz, sums;
   int64_t ldz;
   int parts;
   explicit BwdParts(const VocabArgs& a) : cut(choose_cut(a)) {
     ldz = padded(cut.piece);
     parts = cut.pieces * cut.slices;
     rows = add((int64_t)a.rows * (int64_t)sizeof(RowGrad));
+    hard = add(a.teacher ? (int64_t)a.rows * a.top * 4 : 0);
     x = add(a.dw ? (int64_t)a.rows * a.width * 2 : 0);
     dz = add(a.rows * ldz * 2);
     sums = add(a.dx && parts > 1 ? parts * (int64_t)a.rows * a.width * 4 : 0);
@@ -916,12 +921,13 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
 hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
   const BwdParts at(a);
   RowGrad* rows = reinterpret_cast<RowGrad*>(a.work + at.rows);
+  float* hard = reinterpret_cast<float*>(a.work + at.hard);
   uint16_t* x = reinterpret_cast<uint16_t*>(a.work + at.x);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.work + at.dz);
   float* sums = reinterpret_cast<float*>(a.work + at.sums);
   const bool one = a.teacher == nullptr;
   auto rk = one ? vocab_rows_kernel<true> : vocab_rows_kernel<false>;
-  hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows);
+  hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard);
   if (a.dw)
     hipLaunchKernelGGL(vocab_rows_of_x_kernel, dim3((unsigned)std::min(a.rows, 16384)), dim3(256), 0, s, a, rows,
                        reinterpret_cast<uint4*>(x));
@@ -931,7 +937,9 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
     const int columns = (int)std::min<int64_t>(at.cut.piece, a.vocab - v0);
     const int tn = (int)tiles(columns);
     hipLaunchKernelGGL(vocab_dz_kernel, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, rows, v0, columns, dz, at.ldz, tm, tn);
-    if (!one) hipLaunchKernelGGL(vocab_fix_kernel, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, v0, columns, dz, at.ldz);
+    if (!one)
+      hipLaunchKernelGGL(vocab_fix_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)a.rows * a.top + 255) / 256, 1 << 16)), dim3(256), 0,
+                         s, a, rows, hard, v0, columns, dz, at.ldz);
     Products p{};
     p.dz = dz;
     p.ldz = at.ldz;
