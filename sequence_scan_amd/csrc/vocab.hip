@@ -15,7 +15,6 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kK = 64;            // contracted elements in a stage: rows of 128 bytes
-constexpr int kTile = kVocabTile;   // rows and columns of a workgroup's tile of C
 constexpr int kFewRows = 16;        // rows that are one matrix operand
 constexpr int kFewWidth = 4096;     // ... whose x fits LDS
 
@@ -58,30 +57,50 @@ __device__ __forceinline__ i32x4_t buffer_of(const uint16_t* p, int64_t ld, int6
   return d;
 }
 
-// A workgroup of 2 x 4 wavefronts computes a 256 x 256 tile of C, a wavefront 128 x 64
-// of it.  A stage holds 64 contracted elements of the tile's 256 + 256 rows and columns
-// (64 KB), of which there are two: one is multiplied while the other arrives.
+// A workgroup computes a tile of C, a wavefront kMi x kNi blocks of 16 x 16 of it.  A stage
+// holds kK contracted elements of the tile's rows and columns; kStages of them are in LDS,
+// one being multiplied while the others arrive.
+//
+//   Large: 256 x 256 by 2 x 4 wavefronts, 64 KB a stage, two stages.  Its products take
+//     most of a stage's time, so one stage ahead is enough.
+//   Small: 128 x 128 by 2 x 2 wavefronts, 32 KB a stage, four stages: where tiles are few,
+//     a stage's time is the time that its data take to arrive, and three are under way.
 //
 // In LDS a stage's side lies as in memory, in pieces that are permuted so that an
 // operand's reads meet all 64 banks once:
-//   along: 256 rows of 128 bytes; the 16-byte piece c of row r is at place
+//   along: a row is 128 bytes; the 16-byte piece c of row r is at place
 //     c ^ ((r >> 1) & 7).  An operand takes one piece of each of 16 rows.
-//   across: 64 rows of 512 bytes; the 32-byte piece c of row r is at place
+//   across: 64 rows; the 32-byte piece c of row r is at place
 //     c ^ ((r & 3) | (r >> 1 & 4)).  An operand takes one piece of each of 16 rows,
 //     turned over on the way (ds_read_tr: 16 lanes read four rows of 16 elements, and
 //     receive one column of four each).
-struct Stages {
-  alignas(1024) char a[2][kTile * kK * 2];
-  alignas(1024) char b[2][kTile * kK * 2];
+struct Large {
+  static constexpr int kTile = 256, kWm = 2, kWn = 4, kStages = 2;
+  static constexpr int kWaves = kWm * kWn, kThreads = 64 * kWaves, kMi = kTile / kWm / 16, kNi = kTile / kWn / 16;
+  static constexpr int kPerSimd = 2;
 };
-constexpr uint32_t kStage = kTile * kK * 2;
+struct Small {
+  static constexpr int kTile = 128, kWm = 2, kWn = 2, kStages = 4;
+  static constexpr int kWaves = kWm * kWn, kThreads = 64 * kWaves, kMi = kTile / kWm / 16, kNi = kTile / kWn / 16;
+  static constexpr int kPerSimd = 1;
+};
+static_assert(Large::kNi == 4 && Small::kNi == 4, "a wavefront has 64 columns of C");
 
-// acc[mi][ni][i]: C[wm * 128 + mi * 16 + (lane & 15)][wn * 64 + ni * 16 + 4 * (lane >> 4) + i].
-typedef f4_t Acc[8][4];
+template <typename Shape>
+struct Stages {
+  alignas(1024) char a[Shape::kStages][Shape::kTile * kK * 2];
+  alignas(1024) char b[Shape::kStages][Shape::kTile * kK * 2];
+};
+
+// acc[mi][ni][i]: C[wm * 16 kMi + mi * 16 + (lane & 15)][wn * 64 + ni * 16 + 4 * (lane >> 4) + i].
+template <typename Shape>
+using Acc = f4_t[Shape::kMi][4];
 
 // A side's loads: a wavefront brings four times 1 KB of a stage.
-template <bool ACROSS>
+template <typename Shape, bool ACROSS>
 struct Loader {
+  static constexpr int kTile = Shape::kTile;
+  static_assert(kTile * kK * 2 == Shape::kWaves * 4096, "four loads");
   const uint16_t* p;
   int64_t ld;
   uint32_t off[4];
@@ -91,13 +110,13 @@ struct Loader {
     k = (s.k < k1 ? s.k : k1) - k0;
     length = (int32_t)(s.n - n0 < kTile ? s.n - n0 : kTile);
     if constexpr (ACROSS) {
-      // rows wave * 8 .. + 7 of the stage, two at a time
+      // kK / kWaves rows of the stage, as many at a time as make 1 KB
+      constexpr int kPieces = kTile / 8, kRows = 64 / kPieces;
       p = s.p + k0 * s.ld + n0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = wave * 8 + j * 2 + (lane >> 5);
-        const int piece = ((lane >> 1) & 15) ^ ((r & 3) | (r >> 1 & 4));
-        off[j] = (uint32_t)(r * s.ld * 2) + piece * 32 + (lane & 1) * 16;
+        const int r = wave * (kK / Shape::kWaves) + j * kRows + lane / kPieces, half = lane % kPieces;
+        off[j] = (uint32_t)(r * s.ld * 2) + ((half >> 1) ^ ((r & 3) | (r >> 1 & 4))) * 32 + (half & 1) * 16;
       }
       c = 0;
     } else {
@@ -109,11 +128,12 @@ struct Loader {
         off[j] = (uint32_t)((wave * 32 + j * 8 + (lane >> 3)) * s.ld * 2) + (uint32_t)(c ^ ((j & 1) << 2)) * 16;
     }
   }
-  // The stage at contracted element `at` (from k0).
+  // The stage at contracted element `at` (from k0; past the last, zeros).
   __device__ __forceinline__ void operator()(int at, uint32_t to) const {
     if constexpr (ACROSS) {
-      const int rows = k - at < kK ? k - at : kK;
-      const i32x4_t buffer = buffer_of(p + at * ld, ld, rows, length);
+      // (a column past the matrix is one of C that is not stored: what is read there, the
+      // next row's, does not matter; past the last row there are zeros)
+      const i32x4_t buffer = buffer_of(p + (int64_t)at * ld, ld, k - at < kK ? k - at : kK, length);
 #pragma unroll
       for (int j = 0; j < 4; ++j) load_lds16(buffer, off[j], to + j * 1024);
     } else {
@@ -128,26 +148,27 @@ struct Loader {
 };
 
 // An operand's reads: 16 rows or columns of C, 32 contracted elements (half kk of a stage).
-template <bool ACROSS>
+template <typename Shape, bool ACROSS>
 struct Reader {
+  static constexpr int kRow = Shape::kTile * 2;      // bytes of a row that runs across
   uint32_t at;
   __device__ __forceinline__ Reader(int first, int lane) {
     if constexpr (ACROSS) {
       const int r = (lane >> 4) * 8 + ((lane >> 2) & 3);
-      at = r * 512 + (((first >> 4) ^ ((r & 3) | (r >> 1 & 4))) * 32) + (lane & 3) * 8;
+      at = r * kRow + (((first >> 4) ^ ((r & 3) | (r >> 1 & 4))) * 32) + (lane & 3) * 8;
     } else {
       at = (first + (lane & 15)) * 128 + (((lane >> 4) ^ ((lane & 15) >> 1)) & 7) * 16;
     }
   }
-  // Operand `i` counted in 16s from `first`, a multiple of 4 of them.
+  // Operand i, counted in 16s from `first`.
   __device__ __forceinline__ bf16x8_t operator()(const char* side, int i, int kk) const {
     if constexpr (ACROSS) {
-      // (the place of piece first / 16 + i, i below 4 or 8 and first / 16 a multiple of it)
-      const char* q = side + (at ^ (i * 32)) + kk * 32 * 512;
+      // (piece first / 16 + i: first / 16 is a multiple of 4 or 8, and i below that)
+      const char* q = side + (at ^ (i * 32)) + kk * 32 * kRow;
       typedef short s4_t __attribute__((ext_vector_type(4)));
       typedef short s8_t __attribute__((ext_vector_type(8)));
       const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t*)(q));
-      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t*)(q + 4 * 512));
+      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t*)(q + 4 * kRow));
       return __builtin_bit_cast(bf16x8_t, (s8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       return *reinterpret_cast<const bf16x8_t*>(side + i * 2048 + (at ^ (kk * 64)));
@@ -156,69 +177,75 @@ struct Reader {
 };
 
 // acc = the tile at (m0, n0) of A B over the contracted elements k0 to k1 (k0 a multiple of 8).
-template <bool A_ACROSS, bool B_ACROSS>
-__device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m0, int64_t n0, int k0, int k1, Stages& s, Acc acc) {
+//
+// A stage's first half is multiplied while its second half is read, the second half
+// while the next stage's first is: no product waits for LDS.  Between the halves every
+// wavefront has read all of the stage, so its place is free for the stage kStages on,
+// and the next stage has to be there.
+template <typename Shape, bool A_ACROSS, bool B_ACROSS>
+__device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m0, int64_t n0, int k0, int k1, Stages<Shape>& s,
+                                         Acc<Shape>& acc) {
+  constexpr int kMi = Shape::kMi, kS = Shape::kStages;
+  constexpr uint32_t kStage = Shape::kTile * kK * 2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
-  const Loader<A_ACROSS> load_a(A, m0, k0, k1, wave, lane);
-  const Loader<B_ACROSS> load_b(B, n0, k0, k1, wave, lane);
-  const Reader<A_ACROSS> read_a(wm * 128, lane);
-  const Reader<B_ACROSS> read_b(wn * 64, lane);
+  const int wm = wave / Shape::kWn, wn = wave % Shape::kWn;
+  const Loader<Shape, A_ACROSS> load_a(A, m0, k0, k1, wave, lane);
+  const Loader<Shape, B_ACROSS> load_b(B, n0, k0, k1, wave, lane);
+  const Reader<Shape, A_ACROSS> read_a(wm * kMi * 16, lane);
+  const Reader<Shape, B_ACROSS> read_b(wn * 64, lane);
   const uint32_t la = lds_address(s.a[0]) + wave * 4096, lb = lds_address(s.b[0]) + wave * 4096;
 #pragma unroll
-  for (int mi = 0; mi < 8; ++mi)
+  for (int mi = 0; mi < kMi; ++mi)
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int stages = (k1 - k0 + kK - 1) / kK;
   auto load = [&](int t) SSM_INLINE {
-    load_a(t * kK, la + (t & 1) * kStage);
-    load_b(t * kK, lb + (t & 1) * kStage);
+    load_a(t * kK, la + (t & (kS - 1)) * kStage);
+    load_b(t * kK, lb + (t & (kS - 1)) * kStage);
   };
-  bf16x8_t fa[2][8], fb[2][4];
+  bf16x8_t fa[2][kMi], fb[2][4];
   auto read = [&](int t, int kk) SSM_INLINE {
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) fb[kk][ni] = read_b(s.b[t & 1], ni, kk);
+    for (int ni = 0; ni < 4; ++ni) fb[kk][ni] = read_b(s.b[t & (kS - 1)], ni, kk);
 #pragma unroll
-    for (int mi = 0; mi < 8; ++mi) fa[kk][mi] = read_a(s.a[t & 1], mi, kk);
+    for (int mi = 0; mi < kMi; ++mi) fa[kk][mi] = read_a(s.a[t & (kS - 1)], mi, kk);
   };
-  // 12 operands read (24 accesses where they are turned over) among 32 products
-  constexpr int kReads = (A_ACROSS ? 16 : 8) + (B_ACROSS ? 8 : 4);
+  // kMi + 4 operands read (twice as many accesses where they are turned over) among 4 kMi products
+  constexpr int kOperands = kMi + 4, kReads = kMi * (A_ACROSS ? 2 : 1) + 4 * (B_ACROSS ? 2 : 1);
+  constexpr int kEach = kReads / kOperands, kBeside = kMi == 8 ? 2 : 1;
   auto products = [&](int kk) SSM_INLINE {
 #pragma unroll
-    for (int mi = 0; mi < 8; ++mi)
+    for (int mi = 0; mi < kMi; ++mi)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int ni = mi & 1 ? 3 - j : j;      // (neighbours share an operand)
         acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[kk][ni], fa[kk][mi], acc[mi][ni], 0, 0, 0);
       }
 #pragma unroll
-    for (int i = 0; i < 12; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, kReads / 12, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    for (int i = 0; i < kOperands; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kBeside, 0);
     }
-    if constexpr (kReads % 12 != 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads % 12, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+    if constexpr (kReads % kOperands != 0) __builtin_amdgcn_sched_group_barrier(0x100, kReads % kOperands, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 4 * kMi - kOperands * kBeside, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // A stage's first half is multiplied while its second half is read, the second half
-  // while the next stage's first is: no product waits for LDS.  Between the halves every
-  // wavefront has read all of the stage, so its place is free for the stage after the
-  // next, which then has a whole stage's time to arrive.
-  load(0);
-  if (stages > 1) load(1);
-  if (stages > 1) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int t = 0; t < kS; ++t) load(t);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(8 * (kS - 1)) : "memory");      // (eight loads a stage)
   block_sync();
   read(0, 0);
   for (int t = 0; t < stages; ++t) {
     read(t, 1);
     products(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(8 * (kS - 2)) : "memory");
     block_sync();
-    if (t + 2 < stages) load(t + 2);
-    read(t + 1 < stages ? t + 1 : t, 0);
+    load(t + kS);      // (past the last stage zeros, so that the counts hold)
+    read(t + 1, 0);
     products(1);
   }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  block_sync();
 }
 
 // Two neighbouring operands' columns of a row of C, rounded to bf16, as eight in a row:
@@ -248,39 +275,50 @@ __device__ __forceinline__ void tile_place(int id, int tiles_m, int tiles_n, int
 
 // ----------------------------------------------------------------- the forward
 
-// For every 256 columns a row's maximum and sum of exponentials (base 2), and the
+// What a row's dz is formed from: dz = soft exp2(z log2 e - lse2) less hard q at its
+// indices.  soft = hard = 0 for a row that takes no part.
+struct RowGrad {
+  float lse2, soft, hard;
+  int32_t target;       // cross entropy: its column, or -1
+};
+
+// For every tile's columns a row's maximum and sum of exponentials (base 2), and the
 // target's logit where it lies in them.
-template <bool ONE>
-__global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2* __restrict__ stats, float* __restrict__ picked,
-                                                             int tiles_m, int tiles_n) {
-  __shared__ Stages s;
-  __shared__ float2 part[4 * 256];
+template <typename Shape, bool ONE>
+__global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_kernel(VocabArgs a, float2* __restrict__ stats,
+                                                                                       float* __restrict__ picked, int tiles_m, int tiles_n) {
+  constexpr int kTile = Shape::kTile, kMi = Shape::kMi, kWn = Shape::kWn, kHalf = kMi * 16;
+  __shared__ Stages<Shape> s;
+  __shared__ float2 part[kWn * kTile];
   int tm, tn;
   tile_place(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-  Acc acc;
-  multiply<false, false>(Side{a.x, a.x_row, a.rows, a.width}, Side{a.w, a.w_row, a.vocab, a.width}, m0, n0, 0, a.width, s, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
+  Acc<Shape> acc;
+  multiply<Shape, false, false>(Side{a.x, a.x_row, a.rows, a.width}, Side{a.w, a.w_row, a.vocab, a.width}, m0, n0, 0, a.width, s, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / kWn, wn = wave % kWn;
   const int n = wn * 64 + 4 * (lane >> 4);          // + ni * 16 + i
   const int columns = (int)(a.vocab - n0 < kTile ? a.vocab - n0 : kTile);
-  // Many indices: those of 128 rows at a time, of which a thread holds the first kHeld
-  // while the tile is dealt with.
+  // Many indices: those of half the tile's rows at a time, of which a thread holds the
+  // first kHeld while the tile is dealt with.
   constexpr int kHeld = ONE ? 1 : 16;
   int64_t held[kHeld];
   auto entries_of = [&](int half) SSM_INLINE {
-    const int64_t left = a.rows - (m0 + half * 128);
-    return (uint32_t)(left < 0 ? 0 : left > 128 ? 128 : left) * (uint32_t)a.top;
+    const int64_t left = a.rows - (m0 + half * kHalf);
+    return (uint32_t)(left < 0 ? 0 : left > kHalf ? kHalf : left) * (uint32_t)a.top;
   };
   auto hold = [&](int half) SSM_INLINE {
     const uint32_t entries = entries_of(half);
-    const int64_t* at = a.index + (m0 + half * 128) * a.top;
+    const int64_t* at = a.index + (m0 + half * kHalf) * a.top;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) held[j] = threadIdx.x + j * 512 < entries ? at[threadIdx.x + j * 512] : -1;
+    for (int j = 0; j < kHeld; ++j) {
+      const uint32_t e = threadIdx.x + j * Shape::kThreads;
+      held[j] = e < entries ? at[e] : -1;
+    }
   };
   if constexpr (!ONE) hold(0);
 #pragma unroll
-  for (int mi = 0; mi < 8; ++mi) {
-    const int m = wm * 128 + mi * 16 + (lane & 15);
+  for (int mi = 0; mi < kMi; ++mi) {
+    const int m = wm * kHalf + mi * 16 + (lane & 15);
     float top = -__builtin_inff();
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni)
@@ -292,14 +330,14 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
       }
     if constexpr (ONE) {
       if (m0 + m < a.rows) {
-        const int64_t d = a.index[m0 + m] - n0 - n;
-        if (d >= 0 && d < 64 && (d & 12) == 0) {
+        const int64_t v = a.index[m0 + m], d = v - n0 - n;
+        if (v >= 0 && d >= 0 && d < 64 && (d & 12) == 0 && n + d < columns) {
           float z = 0.0f;
 #pragma unroll
           for (int ni = 0; ni < 4; ++ni)
 #pragma unroll
             for (int i = 0; i < 4; ++i) z = d == ni * 16 + i ? acc[mi][ni][i] : z;
-          if (n0 + n + d < a.vocab) picked[m0 + m] = z;
+          picked[m0 + m] = z;
         }
       }
     }
@@ -313,15 +351,15 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
       for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[mi][ni][i], kLog2e, -top2));
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    if (lane < 16) part[wn * 256 + m] = make_float2(top2, sum);
+    if (lane < 16) part[wn * kTile + m] = make_float2(top2, sum);
   }
   block_sync();
   const int m = threadIdx.x;
   if (m < kTile && m0 + m < a.rows) {
     float2 r = part[m];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      const float2 o = part[w * 256 + m];
+    for (int w = 1; w < kWn; ++w) {
+      const float2 o = part[w * kTile + m];
       if (w * 64 < columns) {
         const float top = __builtin_fmaxf(r.x, o.x);
         r.y = r.y * __builtin_amdgcn_exp2f(r.x - top) + o.y * __builtin_amdgcn_exp2f(o.x - top);
@@ -331,35 +369,36 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
     stats[(int64_t)tn * a.rows + m0 + m] = r;
   }
   if constexpr (!ONE) {
-    // The logits at the rows' indices, by way of LDS, 128 rows at a time: 16-byte piece c
-    // of row r is at place c ^ (r & 15).
+    // The logits at the rows' indices, by way of LDS, half the rows at a time: 16-byte
+    // piece c of row r is at place c ^ (r & 15).
     float* z = reinterpret_cast<float*>(s.a[0]);
+    static_assert(sizeof(Stages<Shape>) >= kHalf * kTile * 4, "half the tile in fp32 fits");
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       block_sync();
       if (wm == half) {
 #pragma unroll
-        for (int mi = 0; mi < 8; ++mi)
+        for (int mi = 0; mi < kMi; ++mi)
 #pragma unroll
           for (int ni = 0; ni < 4; ++ni) {
             const int piece = (n >> 2) + ni * 4;
-            *reinterpret_cast<f4_t*>(z + (mi * 16 + (lane & 15)) * 256 + (piece ^ (lane & 15)) * 4) = acc[mi][ni];
+            *reinterpret_cast<f4_t*>(z + (mi * 16 + (lane & 15)) * kTile + (piece ^ (lane & 15)) * 4) = acc[mi][ni];
           }
       }
       block_sync();
       const uint32_t entries = entries_of(half);
-      const int64_t first = (m0 + half * 128) * a.top;
-      auto pick = [&](uint32_t e, int64_t index) SSM_INLINE {
-        const int64_t v = index - n0;
-        if (v >= 0 && v < columns) {
-          const uint32_t r = e / (uint32_t)a.top, col = (uint32_t)v;
-          a.logits[first + e] = z[r * 256 + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)];
+      const int64_t first = (m0 + half * kHalf) * a.top;
+      auto pick = [&](uint32_t e, int64_t v) SSM_INLINE {
+        const int64_t d = v - n0;
+        if (v >= 0 && d >= 0 && d < columns) {
+          const uint32_t r = e / (uint32_t)a.top, col = (uint32_t)d;
+          a.logits[first + e] = z[r * kTile + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)];
         }
       };
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j) pick(threadIdx.x + j * 512, held[j]);
+      for (int j = 0; j < kHeld; ++j) pick(threadIdx.x + j * Shape::kThreads, held[j]);
 #pragma unroll 4
-      for (uint32_t e = threadIdx.x + kHeld * 512; e < entries; e += 512) pick(e, a.index[first + e]);
+      for (uint32_t e = threadIdx.x + kHeld * Shape::kThreads; e < entries; e += Shape::kThreads) pick(e, a.index[first + e]);
       if (half == 0) hold(1);
     }
   }
@@ -369,8 +408,18 @@ __global__ void __launch_bounds__(512, 2) vocab_stats_kernel(VocabArgs a, float2
 // lies in LDS, in the order in which the matrix cores take it; every wavefront reads an
 // equal share of the vocabulary's rows, 16 at a time, straight to registers, with eight
 // lines of 16 x 64 elements under way and no barrier between them.
-template <int KMAX, bool ONE>
-__global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, float2* __restrict__ stats, float* __restrict__ picked, int share) {
+// What becomes of the logits: statistics and the target's logit, statistics, or dz of a
+// piece of the vocabulary (a.w and a.vocab are then the piece's).
+enum FewKind { kFewTarget, kFewStats, kFewDz };
+struct FewOut {
+  float2* stats;
+  float* picked;
+  const RowGrad* rows;      // dz [rows, ldz], padded with zeros
+  uint16_t* dz;
+  int64_t ldz, v0;
+};
+template <int KMAX, FewKind KIND>
+__global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, FewOut out, int share) {
   constexpr int kAhead = 8;
   __shared__ alignas(1024) char xs[KMAX / 32 * 1024];       // [32 contracted elements][lane][8 elements]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -386,7 +435,17 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, float2* 
   const int64_t first = (int64_t)id * share;
   const int columns = (int)(first >= a.vocab ? 0 : a.vocab - first < share ? a.vocab - first : share);
   const int steps = (columns + 15) / 16 * lines;
-  const int64_t target = ONE && (lane & 15) < a.rows ? a.index[lane & 15] - first : -1;
+  const bool has_row = (lane & 15) < a.rows;
+  int64_t target = -1;              // of row lane & 15, counted from the share's first column
+  RowGrad g{0.0f, 0.0f, 0.0f, -2};
+  if (KIND == kFewTarget && has_row) {
+    const int64_t v = a.index[lane & 15];
+    target = v < 0 ? -1 : v - first;
+  }
+  if (KIND == kFewDz && has_row) {
+    g = out.rows[lane & 15];
+    target = g.target < 0 ? -1 : g.target - out.v0 - first;
+  }
   bf16x8_t w[kAhead][2];
   int load_group = 0, load_line = 0;      // what is loaded next
   const uint16_t* row = a.w;
@@ -424,20 +483,29 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, float2* 
                                                     acc, 0, 0, 0);
     if (++line < lines) return;
     line = 0;
-    float top = top2;
-    float z[4];
+    if constexpr (KIND == kFewDz) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float v = acc[i] * a.scale;
-      z[i] = n + i < columns ? v * kLog2e : -__builtin_inff();
-      top = __builtin_fmaxf(top, z[i]);
-      if (ONE && target == n + i && n + i < columns) picked[lane & 15] = v;
+      for (int i = 0; i < 4; ++i) {
+        const float p = g.soft * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i], a.scale * kLog2e, -g.lse2));
+        const float d = g.target == -2 ? 0.0f : p - (n + i == target ? g.hard : 0.0f);
+        if (has_row && n + i < columns) out.dz[(lane & 15) * out.ldz + first + n + i] = f32_to_bf16_rne(d);
+      }
+    } else {
+      float top = top2;
+      float z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = acc[i] * a.scale;
+        z[i] = n + i < columns ? v * kLog2e : -__builtin_inff();
+        top = __builtin_fmaxf(top, z[i]);
+        if (KIND == kFewTarget && target == n + i && n + i < columns) out.picked[lane & 15] = v;
+      }
+      const float from = top == -__builtin_inff() ? 0.0f : top;
+      sum *= __builtin_amdgcn_exp2f(top2 - from);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(z[i] - from);
+      top2 = top;
     }
-    const float from = top == -__builtin_inff() ? 0.0f : top;
-    sum *= __builtin_amdgcn_exp2f(top2 - from);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(z[i] - from);
-    top2 = top;
     acc = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     n += 16;
   };
@@ -449,13 +517,19 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, float2* 
         if (at + u + kAhead < steps) load(w[u]);
       }
   }
+  if constexpr (KIND == kFewDz) {
+    // the padding, by the wavefront of the last column
+    if (columns > 0 && first + columns == a.vocab && has_row)
+      for (int64_t c = a.vocab + quarter; c < out.ldz; c += 4) out.dz[(lane & 15) * out.ldz + c] = 0;
+  } else {
 #pragma unroll
-  for (int o = 16; o < 64; o *= 2) {
-    const float t = __shfl_xor(top2, o), v = __shfl_xor(sum, o), top = __builtin_fmaxf(top2, t);
-    if (top != -__builtin_inff()) sum = sum * __builtin_amdgcn_exp2f(top2 - top) + v * __builtin_amdgcn_exp2f(t - top);
-    top2 = top;
+    for (int o = 16; o < 64; o *= 2) {
+      const float t = __shfl_xor(top2, o), v = __shfl_xor(sum, o), top = __builtin_fmaxf(top2, t);
+      if (top != -__builtin_inff()) sum = sum * __builtin_amdgcn_exp2f(top2 - top) + v * __builtin_amdgcn_exp2f(t - top);
+      top2 = top;
+    }
+    if (lane < 16 && has_row) out.stats[(int64_t)id * a.rows + lane] = make_float2(top2, sum);
   }
-  if (lane < a.rows && lane < 16) stats[(int64_t)id * a.rows + lane] = make_float2(top2, sum);
 }
 
 // The logits at the indices of few rows, one wavefront for each.
@@ -603,17 +677,12 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
 
 // ---------------------------------------------------------------- the gradients
 
-// What a row's dz is formed from: dz = soft exp2(z log2 e - lse2) less hard q at its
-// indices.  soft = hard = 0 for a row that takes no part.
-struct RowGrad {
-  float lse2, soft, hard;
-  int32_t target;       // cross entropy: its column, or -1
-};
-
-// A wavefront a row.  Distillation: also hard q for each of the row's indices, where the
-// same index twice has the sum of both.
+// A wavefront a row: what its dz is formed from, and (for dweight) its x, zeros where the
+// row takes no part, whatever x holds there.  Distillation: also hard q for each of the
+// row's indices, where the same index twice has the sum of both.
 template <bool ONE>
-__global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows, float* __restrict__ hard) {
+__global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows, float* __restrict__ hard,
+                                                         uint16_t* __restrict__ x) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (row >= a.rows) return;
@@ -644,34 +713,32 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* _
     }
   }
   if (lane == 0) rows[row] = g;
-}
-
-// x with zeros in the rows that take no part (whose x may hold anything).
-__global__ void __launch_bounds__(256) vocab_rows_of_x_kernel(VocabArgs a, const RowGrad* __restrict__ rows, uint4* __restrict__ out) {
-  const int each = a.width / 8;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const bool takes = rows[row].target != -2;
+  if (x != nullptr) {
     const uint4* from = reinterpret_cast<const uint4*>(a.x + row * a.x_row);
-    for (int e = threadIdx.x; e < each; e += 256) out[row * each + e] = takes ? from[e] : make_uint4(0, 0, 0, 0);
+    uint4* to = reinterpret_cast<uint4*>(x + row * a.width);
+#pragma unroll 4
+    for (int e = lane; e < a.width / 8; e += 64) to[e] = g.target == -2 ? make_uint4(0, 0, 0, 0) : from[e];
   }
 }
 
 // dz of a piece of the vocabulary, [rows, ldz] and padded with zeros, from the logits,
 // computed once more.
-__global__ void __launch_bounds__(512, 2) vocab_dz_kernel(VocabArgs a, const RowGrad* __restrict__ rows, int64_t v0, int columns,
+template <typename Shape>
+__global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_dz_kernel(VocabArgs a, const RowGrad* __restrict__ rows, int64_t v0, int columns,
                                                           uint16_t* __restrict__ dz, int64_t ldz, int tiles_m, int tiles_n) {
-  __shared__ Stages s;
+  constexpr int kTile = Shape::kTile, kMi = Shape::kMi;
+  __shared__ Stages<Shape> s;
   int tm, tn;
   tile_place(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-  Acc acc;
-  multiply<false, false>(Side{a.x, a.x_row, a.rows, a.width}, Side{a.w + v0 * a.w_row, a.w_row, columns, a.width}, m0, n0, 0,
-                         a.width, s, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
+  Acc<Shape> acc;
+  multiply<Shape, false, false>(Side{a.x, a.x_row, a.rows, a.width}, Side{a.w + v0 * a.w_row, a.w_row, columns, a.width}, m0, n0, 0,
+                                a.width, s, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / Shape::kWn, wn = wave % Shape::kWn;
   const float s2 = a.scale * kLog2e;
 #pragma unroll
-  for (int mi = 0; mi < 8; ++mi) {
-    const int64_t m = m0 + wm * 128 + mi * 16 + (lane & 15);
+  for (int mi = 0; mi < kMi; ++mi) {
+    const int64_t m = m0 + wm * kMi * 16 + mi * 16 + (lane & 15);
     RowGrad g{0.0f, 0.0f, 0.0f, -2};
     if (m < a.rows) g = rows[m];
     const int64_t target = g.target < 0 ? -1 : g.target - v0;
@@ -711,11 +778,12 @@ __global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGr
 }
 
 // What a tile of C becomes: bf16, or fp32 for sums over several parts.
-__device__ __forceinline__ void store_tile(const Acc acc, int64_t m0, int64_t n0, int rows, int columns, float* sum, uint16_t* out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
+template <typename Shape>
+__device__ __forceinline__ void store_tile(const Acc<Shape>& acc, int64_t m0, int64_t n0, int rows, int columns, float* sum, uint16_t* out) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / Shape::kWn, wn = wave % Shape::kWn;
 #pragma unroll
-  for (int mi = 0; mi < 8; ++mi) {
-    const int64_t m = m0 + wm * 128 + mi * 16 + (lane & 15);
+  for (int mi = 0; mi < Shape::kMi; ++mi) {
+    const int64_t m = m0 + wm * Shape::kMi * 16 + mi * 16 + (lane & 15);
 #pragma unroll
     for (int ni = 0; ni < 4; ni += 2) {
       if (sum) {
@@ -739,112 +807,142 @@ __device__ __forceinline__ void store_tile(const Acc acc, int64_t m0, int64_t n0
 }
 
 // A piece's two products, side by side so that neither leaves CUs idle alone:
-//   dweight[v0 ..] = dz^T x and its part of dx = dz weight, in `slices` of the piece's columns.
+//   dweight[v0 ..] = dz^T x, the rows in slices, and its part of dx = dz weight, the piece's
+//   columns in slices.
 struct Products {
   const uint16_t* dz;       // [rows, ldz], zeros from `columns` on
   int64_t ldz;
   const uint16_t* x;        // [rows, width]
   const uint16_t* w;        // the piece's rows of weight
   int64_t w_row;
-  float* sums;              // [slices][rows, width], or NULL: dx itself
+  float* x_sums;            // [slices][rows, width], or NULL: dx itself
+  float* w_sums;            // [slices][columns, width], or NULL: dweight itself
   uint16_t* dx;
   uint16_t* dw;             // the piece's rows
   int32_t rows, width, columns;
-  int32_t slices, slice;    // contracted columns of a slice, a multiple of kK
+  int32_t x_slice, w_slice;       // contracted elements of a slice, multiples of kK
   int32_t tiles_m, tiles_n, tiles_d;
-  int32_t dx_items, dw_items;
-  int32_t dx_first;
+  int32_t x_items, w_items;
+  int32_t x_first;
 };
 
-__global__ void __launch_bounds__(512, 2) vocab_products_kernel(Products a) {
-  __shared__ Stages s;
-  const int first = a.dx_first ? a.dx_items : a.dw_items;
-  const bool dx = ((int)blockIdx.x < first) == (a.dx_first != 0);
-  int id = (int)blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
+template <typename Shape>
+__global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_products_kernel(Products a) {
+  __shared__ Stages<Shape> s;
+  const int first = a.x_first ? a.x_items : a.w_items;
+  const bool dx = ((int)blockIdx.x < first) == (a.x_first != 0);
+  const int id = (int)blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
+  const int tiles = dx ? a.tiles_m : a.tiles_n, each = tiles * a.tiles_d, slice = id / each;
   int tm, tn;
-  Acc acc;
+  tile_place(id % each, tiles, a.tiles_d, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * Shape::kTile, n0 = (int64_t)tn * Shape::kTile;
+  Acc<Shape> acc;
   if (dx) {
-    const int each = a.tiles_m * a.tiles_d, slice = id / each;
-    tile_place(id % each, a.tiles_m, a.tiles_d, &tm, &tn);
-    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-    const int k0 = slice * a.slice, k1 = k0 + a.slice < a.columns ? k0 + a.slice : (a.columns + 7) & ~7;
-    multiply<false, true>(Side{a.dz, a.ldz, a.rows, (a.columns + 7) & ~7}, Side{a.w, a.w_row, a.width, a.columns}, m0, n0, k0, k1, s,
-                          acc);
-    store_tile(acc, m0, n0, a.rows, a.width, a.sums ? a.sums + (int64_t)slice * a.rows * a.width : nullptr, a.dx);
+    const int k0 = slice * a.x_slice, end = (a.columns + 7) & ~7, k1 = k0 + a.x_slice < end ? k0 + a.x_slice : end;
+    multiply<Shape, false, true>(Side{a.dz, a.ldz, a.rows, end}, Side{a.w, a.w_row, a.width, a.columns}, m0, n0, k0, k1, s, acc);
+    store_tile<Shape>(acc, m0, n0, a.rows, a.width, a.x_sums ? a.x_sums + (int64_t)slice * a.rows * a.width : nullptr, a.dx);
   } else {
-    tile_place(id, a.tiles_n, a.tiles_d, &tm, &tn);
-    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-    multiply<true, true>(Side{a.dz, a.ldz, (int32_t)a.ldz, a.rows}, Side{a.x, a.width, a.width, a.rows}, m0, n0, 0, a.rows, s, acc);
-    store_tile(acc, m0, n0, a.columns, a.width, nullptr, a.dw);
+    const int k0 = slice * a.w_slice, k1 = k0 + a.w_slice < a.rows ? k0 + a.w_slice : a.rows;
+    multiply<Shape, true, true>(Side{a.dz, a.ldz, (int32_t)a.ldz, a.rows}, Side{a.x, a.width, a.width, a.rows}, m0, n0, k0, k1, s, acc);
+    store_tile<Shape>(acc, m0, n0, a.columns, a.width, a.w_sums ? a.w_sums + (int64_t)slice * a.columns * a.width : nullptr, a.dw);
   }
 }
 
-// dx from the sums of its parts, in order; four elements a thread.
-__global__ void __launch_bounds__(256) vocab_sum_kernel(const float4* __restrict__ sums, int parts, int64_t each, uint2* __restrict__ dx) {
+// bf16 from the sums of its parts, in order; four elements a thread.
+__global__ void __launch_bounds__(256) vocab_sum_kernel(const float4* __restrict__ sums, int parts, int64_t each, uint2* __restrict__ out) {
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < each; e += (int64_t)gridDim.x * 256) {
     float4 v = sums[e];
+#pragma unroll 4
     for (int p = 1; p < parts; ++p) {
       const float4 o = sums[p * each + e];
       v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
     }
-    dx[e] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    out[e] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   }
 }
 
-int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
+int64_t tiles(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 int64_t padded(int64_t n) { return (n + kK - 1) / kK * kK; }
 
-// The backward's cut of the vocabulary: tiles of columns in a piece, and slices of a
-// piece for dx.
-struct Cut {
-  int64_t piece;      // columns
-  int pieces, slices;
+// What a product's tiles take, in units of about 10 ns: rounds of `cus` workgroups, of
+// `start` and `stage` for each kK contracted elements.  With these the shapes are chosen
+// (us, forward, Large / Small tiles): 249 x 2384 x 550 55.5 / 28.3, 600 x 1168 x 5059 35.7 /
+// 21.1, 64 x 2560 x 50280 69.8 / 59.6, 333 x 768 x 32003 32.6 / 41.6, 1747 x 2824 x 20240 239 /
+// 304, 2039 x 1536 x 50280 309 / 468.
+struct Times {
+  int64_t stage, start;
 };
+constexpr Times kLargeTimes{140, 500}, kSmallTimes{65, 250};
+int64_t item(const Times& t, int64_t k) { return t.start + t.stage * (padded(k) / kK); }
 
-// Rounds of `cus` workgroups that n1 items of length k1 and then n2 of length k2 take, in units of length.
+bool large_tiles(int64_t rows, int64_t columns, int64_t k, int64_t cus) {
+  const int64_t l = tiles(tiles(rows, Large::kTile) * tiles(columns, Large::kTile), cus) * item(kLargeTimes, k);
+  const int64_t s = tiles(tiles(rows, Small::kTile) * tiles(columns, Small::kTile), cus) * item(kSmallTimes, k);
+  return l <= s;
+}
+
+// Time that n1 items of k1 and then n2 of k2 take, on `cus` CUs that take the next when free.
 int64_t makespan(int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t cus) {
   const int64_t full = n1 / cus, rest = n1 % cus;
   const int64_t early = full * k1, late = early + (rest ? k1 : 0);       // when CUs turn to the second kind
   if (n2 == 0) return late;
-  int64_t end = early + k2;
-  for (;; end += k2) {      // ends of items of the CUs that turned early
+  int64_t end = early + std::max<int64_t>(1, n2 / cus) * k2;      // (no earlier: ends of items of the CUs that turned early)
+  for (;; end += k2) {
     const int64_t done = (cus - rest) * ((end - early) / k2) + (end > late ? rest * ((end - late) / k2) : 0);
     if (done >= n2) return end > late ? end : late;
   }
 }
 
-// Of the pieces whose dz fits kVocabPieceBytes, and the slices of dx's contracted columns,
-// those for which the tiles of dz and of the products fill the CUs best.  A tile's time is
-// counted in stages, with 8 more for its start and end; a slice more costs dx's fp32 sums
-// once written and read, about 1 stage of all CUs for every 2^20 elements.  (8192 x 2560 x
-// 50280: pieces of 64 tiles and a rest of 5, whose tiles go round the CUs without a gap.)
+// The backward's cut: columns of a piece of the vocabulary, slices of the contracted
+// dimensions of dx (the piece's columns) and dweight (the rows), and the tiles.
+struct Cut {
+  int64_t piece;
+  int pieces, x_slices, w_slices;
+  bool large;
+};
+
+// Of the pieces whose dz fits kVocabPieceBytes, and the slices, those for which the tiles
+// of dz and of the products take least.  A slice more costs its fp32 sums once written and
+// read, about 8 bytes an element at 5 TB/s.  (8192 x 2560 x 50280: pieces of 64 tiles
+// and a rest of 5, whose tiles go round the CUs without a gap, 7300 us in place of 7360 in
+// four equal ones.  Rows in slices: the gradients of 6135 x 304 x 1341 157 -> 67 us; columns
+// in up to 64: 20 x 1272 x 55589 196 -> 112.)
 Cut choose_cut(const VocabArgs& a) {
-  const int64_t cus = std::max(1, a.cus), tm = tiles(a.rows), td = tiles(a.width), tv = tiles(a.vocab);
+  const int64_t cus = std::max(1, a.cus), tv = tiles(a.vocab, kVocabTile);
   const int64_t most = std::min(
-      tv, std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kTile));
-  const int64_t kw = padded(a.rows) / kK + 8, kz = padded(a.width) / kK + 8;
-  auto piece_cost = [&](int64_t tn, int64_t slices) {
-    const int64_t kx = (tn * kTile / kK + slices - 1) / slices + 8;
-    const int64_t nx = a.dx ? tm * td * slices : 0, nw = a.dw ? tn * td : 0;
-    return (kx >= kw ? makespan(nx, kx, nw, kw, cus) : makespan(nw, kw, nx, kx, cus)) + (tm * tn + cus - 1) / cus * kz;
-  };
+      tv, std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kVocabTile));
+  const bool one = most == tv;
   Cut best{};
   int64_t least = INT64_MAX;
   const int64_t step = std::max<int64_t>(1, most / 16);
-  for (int64_t tn = most; tn > most / 2; tn -= step) {
-    const int64_t whole = tv / tn, rest = tv % tn, pieces = whole + (rest != 0);
-    for (int64_t slices = 1; slices <= 8; slices *= 2) {
-      if (slices > 1 && (!a.dx || tn * kTile / slices < 512)) break;
-      const int64_t parts = pieces * slices;
-      const int64_t cost = whole * piece_cost(tn, slices) + (rest ? piece_cost(rest, slices) : 0) +
-                           (parts > 1 ? parts * a.rows * a.width >> 20 : 0);
-      if (cost < least) {
-        least = cost;
-        best = Cut{tn * kTile, (int)pieces, (int)slices};
+  for (int64_t tn = most; tn == most || (!one && tn > most / 2); tn -= step) {
+    const int64_t columns = std::min<int64_t>(tn * kVocabTile, a.vocab), whole = a.vocab / columns, rest = a.vocab % columns;
+    for (int large = 1; large >= (one ? 0 : 1); --large) {
+      const int64_t tile = large ? Large::kTile : Small::kTile;
+      const Times& t = large ? kLargeTimes : kSmallTimes;
+      const int64_t tm = tiles(a.rows, tile), td = tiles(a.width, tile);
+      for (int64_t xs = 1; xs <= (one ? 64 : 8); xs *= 2) {
+        if (xs > 1 && (!a.dx || columns / xs < 512)) break;
+        for (int64_t ws = 1; ws <= (one ? 16 : 1); ws *= 2) {
+          if (ws > 1 && (!a.dw || a.rows / ws < 256)) break;
+          auto cost_of = [&](int64_t c) {
+            const int64_t nx = a.dx ? tm * td * xs : 0, nw = a.dw ? tiles(c, tile) * td * ws : 0;
+            const int64_t kx = item(t, (c + xs - 1) / xs), kw = item(t, (a.rows + ws - 1) / ws);
+            const int64_t z = tiles(tiles(a.rows, Large::kTile) * tiles(c, Large::kTile), cus) * item(kLargeTimes, a.width);
+            return (kx >= kw ? makespan(nx, kx, nw, kw, cus) : makespan(nw, kw, nx, kx, cus)) + (one ? 0 : z);
+          };
+          const int64_t parts = (whole + (rest != 0)) * xs;
+          const int64_t cost = whole * cost_of(columns) + (rest ? cost_of(rest) : 0) +
+                               (parts > 1 ? 400 + parts * a.rows * a.width / 6250 : 0) +
+                               (ws > 1 ? 400 + ws * (int64_t)a.vocab * a.width / 6250 : 0);
+          if (cost < least) {
+            least = cost;
+            best = Cut{columns, (int)(whole + (rest != 0)), (int)xs, (int)ws, large != 0};
+          }
+        }
       }
     }
   }
-  best.piece = std::min<int64_t>(best.piece, a.vocab);
   return best;
 }
 
@@ -858,16 +956,31 @@ struct Parts {
   }
 };
 
-// Few rows' weights are streamed: (us, width 2560, vocabulary 50280, rows at a time .. and in tiles)
-struct FwdParts : Parts {
+// Few rows' weights are streamed, each wavefront of the device an equal share of them (as
+// many as x in LDS leaves room for).
+struct Few {
   bool few;
-  int64_t share, groups, pieces, stats, picked;
-  explicit FwdParts(const VocabArgs& a) {
+  int64_t share, groups;
+  Few(const VocabArgs& a, int64_t columns) {
     few = a.rows <= kFewRows && a.width <= kFewWidth;
-    const int64_t waves = (int64_t)std::max(1, a.cus) * 8 * (a.width <= kFewWidth / 2 ? 2 : 1);      // that x in LDS leaves room for
-    share = (a.vocab + waves - 1) / waves;
-    groups = (a.vocab + share * 8 - 1) / (share * 8);
-    pieces = few ? groups * 8 : tiles(a.vocab);
+    const int64_t waves = (int64_t)std::max(1, a.cus) * 8 * (a.width <= kFewWidth / 2 ? 2 : 1);
+    share = (columns + waves - 1) / waves;
+    groups = (columns + share * 8 - 1) / (share * 8);
+  }
+  template <FewKind KIND>
+  void launch(const VocabArgs& a, const FewOut& out, hipStream_t s) const {
+    auto k = a.width <= kFewWidth / 2 ? vocab_few_kernel<kFewWidth / 2, KIND> : vocab_few_kernel<kFewWidth, KIND>;
+    hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(512), 0, s, a, out, (int)share);
+  }
+};
+
+struct FwdParts : Parts {
+  Few few;
+  bool large;
+  int64_t pieces, stats, picked;
+  explicit FwdParts(const VocabArgs& a) : few(a, a.vocab) {
+    large = large_tiles(a.rows, a.vocab, a.width, std::max(1, a.cus));
+    pieces = few.few ? few.groups * 8 : tiles(a.vocab, large ? Large::kTile : Small::kTile);
     stats = add(pieces * a.rows * 8);
     picked = add(a.teacher ? 0 : (int64_t)a.rows * 4);
   }
@@ -875,21 +988,53 @@ struct FwdParts : Parts {
 
 struct BwdParts : Parts {
   Cut cut;
-  int64_t rows, hard, x, dz, sums;
+  int64_t rows, hard, x, dz, x_sums, w_sums;
   int64_t ldz;
   int parts;
   explicit BwdParts(const VocabArgs& a) : cut(choose_cut(a)) {
     ldz = padded(cut.piece);
-    parts = cut.pieces * cut.slices;
+    parts = cut.pieces * cut.x_slices;
     rows = add((int64_t)a.rows * (int64_t)sizeof(RowGrad));
     hard = add(a.teacher ? (int64_t)a.rows * a.top * 4 : 0);
     x = add(a.dw ? (int64_t)a.rows * a.width * 2 : 0);
     dz = add(a.rows * ldz * 2);
-    sums = add(a.dx && parts > 1 ? parts * (int64_t)a.rows * a.width * 4 : 0);
+    x_sums = add(a.dx && parts > 1 ? parts * (int64_t)a.rows * a.width * 4 : 0);
+    w_sums = add(a.dw && cut.w_slices > 1 ? cut.w_slices * cut.piece * a.width * 4 : 0);
   }
 };
 
 unsigned fours(int64_t n) { return (unsigned)((n + 3) / 4); }
+
+void launch_sum(const float* sums, int parts, int64_t elems, uint16_t* out, hipStream_t s) {
+  const int64_t each = elems / 4;
+  hipLaunchKernelGGL(vocab_sum_kernel, dim3((unsigned)std::min<int64_t>((each + 255) / 256, 1 << 20)), dim3(256), 0, s,
+                     reinterpret_cast<const float4*>(sums), parts, each, reinterpret_cast<uint2*>(out));
+}
+
+template <typename Shape>
+void launch_stats(const VocabArgs& a, float2* stats, float* picked, hipStream_t s) {
+  const int tm = (int)tiles(a.rows, Shape::kTile), tn = (int)tiles(a.vocab, Shape::kTile);
+  auto k = a.teacher ? vocab_stats_kernel<Shape, false> : vocab_stats_kernel<Shape, true>;
+  hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(Shape::kThreads), 0, s, a, stats, picked, tm, tn);
+}
+
+template <typename Shape>
+void launch_dz(const VocabArgs& a, const RowGrad* rows, int64_t v0, int columns, uint16_t* dz, int64_t ldz, hipStream_t s) {
+  const int tm = (int)tiles(a.rows, Shape::kTile), tn = (int)tiles(columns, Shape::kTile);
+  hipLaunchKernelGGL(vocab_dz_kernel<Shape>, dim3((unsigned)(tm * tn)), dim3(Shape::kThreads), 0, s, a, rows, v0, columns, dz, ldz, tm,
+                     tn);
+}
+
+template <typename Shape>
+void launch_products(Products& p, int x_slices, int w_slices, hipStream_t s) {
+  p.tiles_m = (int32_t)tiles(p.rows, Shape::kTile);
+  p.tiles_n = (int32_t)tiles(p.columns, Shape::kTile);
+  p.tiles_d = (int32_t)tiles(p.width, Shape::kTile);
+  p.x_items = p.dx ? p.tiles_m * p.tiles_d * x_slices : 0;
+  p.w_items = p.dw ? p.tiles_n * p.tiles_d * w_slices : 0;
+  p.x_first = p.x_slice >= p.w_slice;      // the longer ones first
+  hipLaunchKernelGGL(vocab_products_kernel<Shape>, dim3((unsigned)(p.x_items + p.w_items)), dim3(Shape::kThreads), 0, s, p);
+}
 
 }  // namespace
 
@@ -901,15 +1046,17 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
   float2* stats = reinterpret_cast<float2*>(a.work + at.stats);
   float* picked = reinterpret_cast<float*>(a.work + at.picked);
   const bool one = a.teacher == nullptr;
-  if (at.few) {
-    auto k = a.width <= kFewWidth / 2 ? (one ? vocab_few_kernel<kFewWidth / 2, true> : vocab_few_kernel<kFewWidth / 2, false>)
-                                      : (one ? vocab_few_kernel<kFewWidth, true> : vocab_few_kernel<kFewWidth, false>);
-    hipLaunchKernelGGL(k, dim3((unsigned)at.groups), dim3(512), 0, s, a, stats, picked, (int)at.share);
+  if (at.few.few) {
+    FewOut out{};
+    out.stats = stats;
+    out.picked = picked;
+    if (one) at.few.launch<kFewTarget>(a, out, s);
+    else at.few.launch<kFewStats>(a, out, s);
     if (!one) hipLaunchKernelGGL(vocab_pick_kernel, dim3(fours(a.rows * a.top)), dim3(256), 0, s, a);
+  } else if (at.large) {
+    launch_stats<Large>(a, stats, picked, s);
   } else {
-    const int tm = (int)tiles(a.rows), tn = (int)tiles(a.vocab);
-    auto k = one ? vocab_stats_kernel<true> : vocab_stats_kernel<false>;
-    hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, stats, picked, tm, tn);
+    launch_stats<Small>(a, stats, picked, s);
   }
   int each = 1;
   while (each < 16 && each < a.rows) each *= 2;
@@ -920,23 +1067,35 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
 
 hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
   const BwdParts at(a);
+  const Cut& cut = at.cut;
   RowGrad* rows = reinterpret_cast<RowGrad*>(a.work + at.rows);
   float* hard = reinterpret_cast<float*>(a.work + at.hard);
   uint16_t* x = reinterpret_cast<uint16_t*>(a.work + at.x);
   uint16_t* dz = reinterpret_cast<uint16_t*>(a.work + at.dz);
-  float* sums = reinterpret_cast<float*>(a.work + at.sums);
+  float* x_sums = reinterpret_cast<float*>(a.work + at.x_sums);
+  float* w_sums = reinterpret_cast<float*>(a.work + at.w_sums);
   const bool one = a.teacher == nullptr;
   auto rk = one ? vocab_rows_kernel<true> : vocab_rows_kernel<false>;
-  hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard);
-  if (a.dw)
-    hipLaunchKernelGGL(vocab_rows_of_x_kernel, dim3((unsigned)std::min(a.rows, 16384)), dim3(256), 0, s, a, rows,
-                       reinterpret_cast<uint4*>(x));
-  const int tm = (int)tiles(a.rows), td = (int)tiles(a.width);
+  hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard, a.dw ? x : nullptr);
   int part = 0;
-  for (int64_t v0 = 0; v0 < a.vocab; v0 += at.cut.piece) {
-    const int columns = (int)std::min<int64_t>(at.cut.piece, a.vocab - v0);
-    const int tn = (int)tiles(columns);
-    hipLaunchKernelGGL(vocab_dz_kernel, dim3((unsigned)(tm * tn)), dim3(512), 0, s, a, rows, v0, columns, dz, at.ldz, tm, tn);
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += cut.piece) {
+    const int columns = (int)std::min<int64_t>(cut.piece, a.vocab - v0);
+    const Few few(a, columns);
+    if (few.few) {
+      VocabArgs piece = a;
+      piece.w = a.w + v0 * a.w_row;
+      piece.vocab = columns;
+      FewOut out{};
+      out.rows = rows;
+      out.dz = dz;
+      out.ldz = at.ldz;
+      out.v0 = v0;
+      few.launch<kFewDz>(piece, out, s);
+    } else if (large_tiles(a.rows, columns, a.width, std::max(1, a.cus))) {
+      launch_dz<Large>(a, rows, v0, columns, dz, at.ldz, s);
+    } else {
+      launch_dz<Small>(a, rows, v0, columns, dz, at.ldz, s);
+    }
     if (!one)
       hipLaunchKernelGGL(vocab_fix_kernel, dim3((unsigned)std::min<int64_t>(((int64_t)a.rows * a.top + 255) / 256, 1 << 16)), dim3(256), 0,
                          s, a, rows, hard, v0, columns, dz, at.ldz);
@@ -949,29 +1108,23 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
     p.rows = a.rows;
     p.width = a.width;
     p.columns = columns;
-    p.tiles_m = tm;
-    p.tiles_n = tn;
-    p.tiles_d = td;
+    p.x_slice = (int32_t)padded((columns + cut.x_slices - 1) / cut.x_slices);
+    p.w_slice = (int32_t)padded((a.rows + cut.w_slices - 1) / cut.w_slices);
+    const int xs = (columns + p.x_slice - 1) / p.x_slice, ws = (a.rows + p.w_slice - 1) / p.w_slice;
     if (a.dx) {
-      p.slice = (int32_t)padded((columns + at.cut.slices - 1) / at.cut.slices);
-      p.slices = (columns + p.slice - 1) / p.slice;
-      p.sums = at.parts > 1 ? sums + (int64_t)part * a.rows * a.width : nullptr;
+      p.x_sums = at.parts > 1 ? x_sums + (int64_t)part * a.rows * a.width : nullptr;
       p.dx = a.dx;
-      p.dx_items = tm * td * p.slices;
-      part += p.slices;
+      part += xs;
     }
     if (a.dw) {
+      p.w_sums = cut.w_slices > 1 ? w_sums : nullptr;
       p.dw = a.dw + v0 * a.width;
-      p.dw_items = tn * td;
     }
-    p.dx_first = p.slice >= a.rows;      // the longer ones first
-    hipLaunchKernelGGL(vocab_products_kernel, dim3((unsigned)(p.dx_items + p.dw_items)), dim3(512), 0, s, p);
+    if (cut.large) launch_products<Large>(p, xs, ws, s);
+    else launch_products<Small>(p, xs, ws, s);
+    if (p.w_sums) launch_sum(w_sums, ws, (int64_t)columns * a.width, p.dw, s);
   }
-  if (a.dx && at.parts > 1) {
-    const int64_t each = (int64_t)a.rows * a.width / 4;
-    hipLaunchKernelGGL(vocab_sum_kernel, dim3((unsigned)std::min<int64_t>((each + 255) / 256, 1 << 20)), dim3(256), 0, s,
-                       reinterpret_cast<const float4*>(sums), part, each, reinterpret_cast<uint2*>(a.dx));
-  }
+  if (a.dx && at.parts > 1) launch_sum(x_sums, part, (int64_t)a.rows * a.width, a.dx, s);
   return hipGetLastError();
 }
 
