@@ -100,8 +100,8 @@ ssm_status ssm_gscan_update(const float* state, float* state_out, const void* x,
  *            or more makes the loss NaN and takes no part in the gradients.
  *   loss, lse: [rows] fp32 (lse of every row, with a target or without)
  * width a multiple of 8 up to SSM_VOCAB_MAX_WIDTH; x and weight 16-byte aligned, their rows a
- * multiple of 8 elements apart, at most 2^22; rows at most 2^22, vocab from 1 to 2^30, and
- * at most 2^23 tiles of 256 rows by 256 columns.
+ * multiple of 8 elements apart, at most 2^22; rows at most 2^22, vocab from 1 to 2^30, x and
+ * weight of at most 2^37 elements, and at most 2^23 tiles of 256 rows by 256 columns.
  * Logits and sums are fp32.  Workspace: 8 bytes for every row and 256 columns, and 4
  * for every row.
  */

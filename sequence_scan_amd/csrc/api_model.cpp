@@ -8,8 +8,10 @@
 #include <initializer_list>
 
 #include "../../include/ssmmodel.h"
+#include "gscan_plan.h"
 #include "host_block.h"
 #include "model.h"
+#include "vocab_plan.h"
 
 namespace {
 
@@ -72,7 +74,8 @@ ssm_status launched(hipError_t e) {
 
 // -------------------------------------------------- losses over a vocabulary
 
-constexpr int64_t kVocabMost = int64_t{1} << 30, kVocabRows = int64_t{1} << 22, kVocabTiles = int64_t{1} << 23;
+constexpr int64_t kVocabMost = int64_t{1} << 30, kVocabRows = int64_t{1} << 22, kVocabTiles = int64_t{1} << 23,
+                  kVocabElems = int64_t{1} << 37;
 
 struct VocabSizes {
   int64_t xb, wb;     // bytes that x and weight span
@@ -90,6 +93,9 @@ ssm_status vocab_check(const void* x, int64_t x_row, const void* w, int64_t w_ro
     return fail(SSM_ERR_UNSUPPORTED, "width=%lld must be a positive multiple of 8, at most %d", (long long)width, SSM_VOCAB_MAX_WIDTH);
   if (vocab < 1 || vocab > kVocabMost || rows > kVocabRows)
     return fail(SSM_ERR_UNSUPPORTED, "vocab=%lld must be from 1 to 2^30 and rows=%lld at most 2^22", (long long)vocab, (long long)rows);
+  if (rows * width > kVocabElems || vocab * width > kVocabElems)
+    return fail(SSM_ERR_UNSUPPORTED, "rows=%lld or vocab=%lld by width=%lld exceeds 2^37 elements", (long long)rows, (long long)vocab,
+                (long long)width);
   if (ceil_div(rows, ssm::kVocabTile) * ceil_div(vocab, ssm::kVocabTile) > kVocabTiles)
     return fail(SSM_ERR_UNSUPPORTED, "rows=%lld by vocab=%lld exceeds 2^23 tiles of 256 by 256", (long long)rows, (long long)vocab);
   if (top < 1 || top > SSM_DISTILL_MAX_TOP)

@@ -419,36 +419,6 @@ int channels(const GscanArgs& a, DT in) {
              : 1;
 }
 
-// Tiles of a group: few leave less to read of the tiles before, many make fewer hops along
-// the chain.  Where workgroups are many, the hops hide behind them (us):
-//   8 x 2048 x 5120 (16 tiles): groups of 2 147.8, 4 147.2, 8 149.4
-//   1 x 65537 x 2560 (513 tiles, 10260 workgroups): 8 200.9, 12 204.4, 16 208.9
-//   1 x 60000 x 256, forward and back (469 and 938 tiles, 938 and 1876 workgroups): 8 155.7, 12 133.4, 16 126.8, 32 128.5
-int group_of(int tiles, int strips) { return tiles <= 32 ? 4 : (int64_t)tiles * strips > 2048 ? 8 : 16; }
-
-struct Layout {
-  Chain c;
-  int ch;
-  int64_t bytes;     // of the chain's workspace
-};
-Layout layout(int64_t batch, int64_t seqlen, int64_t width, int64_t steps, int ch, char* work) {
-  Layout l{};
-  l.ch = ch;
-  const int64_t each = 64 * ch;
-  l.c.strips = (int32_t)(batch * ((width + each - 1) / each));
-  l.c.tiles = (int32_t)((seqlen + steps - 1) / steps);
-  l.c.group = group_of(l.c.tiles, l.c.strips);
-  l.c.groups = (l.c.tiles + l.c.group - 1) / l.c.group;
-  if (l.c.tiles > 1) {
-    const int64_t parts = (int64_t)l.c.strips * l.c.tiles * each * 8, states = (int64_t)l.c.strips * l.c.groups * each * 4;
-    l.c.parts = reinterpret_cast<uint64_t*>(work);
-    l.c.states = reinterpret_cast<uint32_t*>(work + parts);
-    l.c.next = reinterpret_cast<uint32_t*>(work + parts + states);
-    l.bytes = parts + states + 16;
-  }
-  return l;
-}
-
 void begin(const Layout& l, const float* first, int64_t width, hipStream_t s) {
   if (l.c.tiles <= 1) return;
   const int64_t n = (int64_t)l.c.strips * l.c.tiles * 64 * l.ch;
@@ -458,14 +428,8 @@ void begin(const Layout& l, const float* first, int64_t width, hipStream_t s) {
 
 }  // namespace
 
-int64_t gscan_chain_bytes(int64_t batch, int64_t seqlen, int64_t width, bool backward) {
-  // (strips of single channels are as many or more bytes than those of two)
-  const int64_t steps = backward ? kGsBwdTile : kGsFwdTile;
-  return std::max(layout(batch, seqlen, width, steps, 1, nullptr).bytes, layout(batch, seqlen, width, steps, 2, nullptr).bytes);
-}
-
 hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s) {
-  const Layout l = layout(a.batch, a.seqlen, a.width, kGsFwdTile, channels(a, in), a.work);
+  const Layout l = gscan_layout(a.batch, a.seqlen, a.width, kGsFwdTile, channels(a, in), a.work);
   begin(l, a.initial, a.width, s);
   auto k = in == DT::F32 ? SSM_GSCAN_PICK(fwd_kernel, float, 1)
            : l.ch == 2   ? SSM_GSCAN_PICK(fwd_kernel, uint16_t, 2)
@@ -475,7 +439,7 @@ hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s) {
 }
 
 hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t s) {
-  const Layout l = layout(a.batch, a.seqlen, a.width, kGsBwdTile, channels(a, in), a.work);
+  const Layout l = gscan_layout(a.batch, a.seqlen, a.width, kGsBwdTile, channels(a, in), a.work);
   begin(l, a.dlast, a.width, s);
   auto k = in == DT::F32 ? SSM_GSCAN_PICK(bwd_kernel, float, 1)
            : l.ch == 2   ? SSM_GSCAN_PICK(bwd_kernel, uint16_t, 2)

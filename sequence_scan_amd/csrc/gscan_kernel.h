@@ -5,6 +5,7 @@
 #define SSMSCAN_GSCAN_KERNEL_H
 
 #include "device.h"
+#include "gscan_plan.h"
 #include "model.h"
 
 namespace ssm {
@@ -74,14 +75,6 @@ __device__ __forceinline__ float decay_slope(float a, float m) {
 constexpr uint32_t kUnwritten = 0xffffffffu;    // a NaN that no arithmetic returns
 constexpr int kMostPolls = 1 << 22;
 constexpr int kPartsAtOnce = 4;
-
-struct Chain {
-  uint64_t* parts;       // [strips][tiles][channels] (P, H)
-  uint32_t* states;      // [strips][groups][channels]: the state that enters a group
-  uint32_t* next;        // tiles handed out
-  int32_t tiles, groups, strips;
-  int32_t group;         // tiles of a group
-};
 
 // (P, H) as one word; a NaN as the usual one.
 __device__ __forceinline__ uint32_t word_of(float v) { return v == v ? __float_as_uint(v) : 0x7fc00000u; }

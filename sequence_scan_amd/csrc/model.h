@@ -32,7 +32,7 @@ struct GscanArgs {
   float* drate;             // nullable
   float* dinitial;          // nullable
   float* part;              // backward with drate: [batch, tiles, width] sums over a tile's steps
-  char* work;               // gscan_chain_bytes bytes, where a sequence has more than one tile
+  char* work;               // gscan_chain_bytes bytes (gscan_plan.h), where a sequence has more than one tile
   int64_t batch, seqlen, width;
   int32_t lerp;
   int32_t out_bf16;         // type of out and dout
@@ -41,8 +41,6 @@ struct GscanArgs {
 hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s);
 hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t s);
 hipError_t launch_gscan_step(const GscanArgs& a, DT in, hipStream_t s);
-// Bytes of GscanArgs::work (0: none), a multiple of 16.
-int64_t gscan_chain_bytes(int64_t batch, int64_t seqlen, int64_t width, bool backward);
 
 // -------------------------------------------------- losses over a vocabulary
 
@@ -64,7 +62,7 @@ struct VocabArgs {
   float* logits;            // forward: [rows, top] (cross entropy: workspace)
   uint16_t* dx;             // backward, each nullable
   uint16_t* dw;
-  char* work;
+  char* work;               // vocab_fwd_bytes or vocab_bwd_bytes bytes (vocab_plan.h)
   int32_t rows, width, vocab, top;
   float scale;              // z = scale x w^T (over the temperature)
   float z_loss;
@@ -72,9 +70,6 @@ struct VocabArgs {
   int32_t cus;
 };
 
-// Bytes of a.work.
-int64_t vocab_fwd_bytes(const VocabArgs& a);
-int64_t vocab_bwd_bytes(const VocabArgs& a);
 hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s);
 

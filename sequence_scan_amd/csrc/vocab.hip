@@ -6,17 +6,16 @@
 
 #include "device.h"
 #include "model.h"
+#include "vocab_plan.h"
 
 namespace ssm {
 namespace {
 
+using namespace vocab;
+
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kK = 64;            // contracted elements in a stage: rows of 128 bytes
-constexpr int kFewRows = 16;        // rows that are one matrix operand
-constexpr int kFewWidth = 4096;     // ... whose x fits LDS
 
 // One side of a product, a bf16 matrix in either order:
 //   along  (ACROSS false): [n][k], rows run along the contracted dimension;
@@ -75,12 +74,12 @@ __device__ __forceinline__ i32x4_t buffer_of(const uint16_t* p, int64_t ld, int6
 //     turned over on the way (ds_read_tr: 16 lanes read four rows of 16 elements, and
 //     receive one column of four each).
 struct Large {
-  static constexpr int kTile = 256, kWm = 2, kWn = 4, kStages = 2;
+  static constexpr int kTile = kLargeTile, kWm = 2, kWn = 4, kStages = 2;
   static constexpr int kWaves = kWm * kWn, kThreads = 64 * kWaves, kMi = kTile / kWm / 16, kNi = kTile / kWn / 16;
   static constexpr int kPerSimd = 2;
 };
 struct Small {
-  static constexpr int kTile = 128, kWm = 2, kWn = 2, kStages = 4;
+  static constexpr int kTile = kSmallTile, kWm = 2, kWn = 2, kStages = 4;
   static constexpr int kWaves = kWm * kWn, kThreads = 64 * kWaves, kMi = kTile / kWm / 16, kNi = kTile / kWn / 16;
   static constexpr int kPerSimd = 1;
 };
@@ -279,8 +278,9 @@ __device__ __forceinline__ void tile_place(int id, int tiles_m, int tiles_n, int
 // indices.  soft = hard = 0 for a row that takes no part.
 struct RowGrad {
   float lse2, soft, hard;
-  int32_t target;       // cross entropy: its column, or -1
+  int32_t target;       // cross entropy: its column; -1 for none, -2 for a row that takes no part
 };
+static_assert(sizeof(RowGrad) == kRowGradBytes, "vocab_plan.h agrees");
 
 // For every tile's columns a row's maximum and sum of exponentials (base 2), and the
 // target's logit where it lies in them.
@@ -861,147 +861,11 @@ __global__ void __launch_bounds__(256) vocab_sum_kernel(const float4* __restrict
   }
 }
 
-int64_t tiles(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
-int64_t padded(int64_t n) { return (n + kK - 1) / kK * kK; }
-
-// What a product's tiles take, in units of about 10 ns: rounds of `cus` workgroups, of
-// `start` and `stage` for each kK contracted elements.  With these the shapes are chosen
-// (us, forward, Large / Small tiles): 249 x 2384 x 550 55.5 / 28.3, 600 x 1168 x 5059 35.7 /
-// 21.1, 64 x 2560 x 50280 69.8 / 59.6, 333 x 768 x 32003 32.6 / 41.6, 1747 x 2824 x 20240 239 /
-// 304, 2039 x 1536 x 50280 309 / 468.
-struct Times {
-  int64_t stage, start;
-};
-constexpr Times kLargeTimes{140, 500}, kSmallTimes{65, 250};
-int64_t item(const Times& t, int64_t k) { return t.start + t.stage * (padded(k) / kK); }
-
-bool large_tiles(int64_t rows, int64_t columns, int64_t k, int64_t cus) {
-  const int64_t l = tiles(tiles(rows, Large::kTile) * tiles(columns, Large::kTile), cus) * item(kLargeTimes, k);
-  const int64_t s = tiles(tiles(rows, Small::kTile) * tiles(columns, Small::kTile), cus) * item(kSmallTimes, k);
-  return l <= s;
+template <FewKind KIND>
+void launch_few(const Few& few, const VocabArgs& a, const FewOut& out, hipStream_t s) {
+  auto k = a.width <= kFewWidth / 2 ? vocab_few_kernel<kFewWidth / 2, KIND> : vocab_few_kernel<kFewWidth, KIND>;
+  hipLaunchKernelGGL(k, dim3((unsigned)few.groups), dim3(512), 0, s, a, out, (int)few.share);
 }
-
-// Time that n1 items of k1 and then n2 of k2 take, on `cus` CUs that take the next when free.
-int64_t makespan(int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t cus) {
-  const int64_t full = n1 / cus, rest = n1 % cus;
-  const int64_t early = full * k1, late = early + (rest ? k1 : 0);       // when CUs turn to the second kind
-  if (n2 == 0) return late;
-  int64_t end = early + std::max<int64_t>(1, n2 / cus) * k2;      // (no earlier: ends of items of the CUs that turned early)
-  for (;; end += k2) {
-    const int64_t done = (cus - rest) * ((end - early) / k2) + (end > late ? rest * ((end - late) / k2) : 0);
-    if (done >= n2) return end > late ? end : late;
-  }
-}
-
-// The backward's cut: columns of a piece of the vocabulary, slices of the contracted
-// dimensions of dx (the piece's columns) and dweight (the rows), and the tiles.
-struct Cut {
-  int64_t piece;
-  int pieces, x_slices, w_slices;
-  bool large;
-};
-
-// Of the pieces whose dz fits kVocabPieceBytes, and the slices, those for which the tiles
-// of dz and of the products take least.  A slice more costs its fp32 sums once written and
-// read, about 8 bytes an element at 5 TB/s.  (8192 x 2560 x 50280: pieces of 64 tiles
-// and a rest of 5, whose tiles go round the CUs without a gap, 7300 us in place of 7360 in
-// four equal ones.  Rows in slices: the gradients of 6135 x 304 x 1341 157 -> 67 us; columns
-// in up to 64: 20 x 1272 x 55589 196 -> 112.)
-Cut choose_cut(const VocabArgs& a) {
-  const int64_t cus = std::max(1, a.cus), tv = tiles(a.vocab, kVocabTile);
-  const int64_t most = std::min(
-      tv, std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kVocabTile));
-  const bool one = most == tv;
-  Cut best{};
-  int64_t least = INT64_MAX;
-  const int64_t step = std::max<int64_t>(1, most / 16);
-  for (int64_t tn = most; tn == most || (!one && tn > most / 2); tn -= step) {
-    const int64_t columns = std::min<int64_t>(tn * kVocabTile, a.vocab), whole = a.vocab / columns, rest = a.vocab % columns;
-    for (int large = 1; large >= (one ? 0 : 1); --large) {
-      const int64_t tile = large ? Large::kTile : Small::kTile;
-      const Times& t = large ? kLargeTimes : kSmallTimes;
-      const int64_t tm = tiles(a.rows, tile), td = tiles(a.width, tile);
-      for (int64_t xs = 1; xs <= (one ? 64 : 8); xs *= 2) {
-        if (xs > 1 && (!a.dx || columns / xs < 512)) break;
-        for (int64_t ws = 1; ws <= (one ? 16 : 1); ws *= 2) {
-          if (ws > 1 && (!a.dw || a.rows / ws < 256)) break;
-          auto cost_of = [&](int64_t c) {
-            const int64_t nx = a.dx ? tm * td * xs : 0, nw = a.dw ? tiles(c, tile) * td * ws : 0;
-            const int64_t kx = item(t, (c + xs - 1) / xs), kw = item(t, (a.rows + ws - 1) / ws);
-            const int64_t z = tiles(tiles(a.rows, Large::kTile) * tiles(c, Large::kTile), cus) * item(kLargeTimes, a.width);
-            return (kx >= kw ? makespan(nx, kx, nw, kw, cus) : makespan(nw, kw, nx, kx, cus)) + (one ? 0 : z);
-          };
-          const int64_t parts = (whole + (rest != 0)) * xs;
-          const int64_t cost = whole * cost_of(columns) + (rest ? cost_of(rest) : 0) +
-                               (parts > 1 ? 400 + parts * a.rows * a.width / 6250 : 0) +
-                               (ws > 1 ? 400 + ws * (int64_t)a.vocab * a.width / 6250 : 0);
-          if (cost < least) {
-            least = cost;
-            best = Cut{columns, (int)(whole + (rest != 0)), (int)xs, (int)ws, large != 0};
-          }
-        }
-      }
-    }
-  }
-  return best;
-}
-
-// Consecutive parts of the workspace.
-struct Parts {
-  int64_t bytes = 0;
-  int64_t add(int64_t n) {
-    const int64_t at = bytes;
-    bytes += (n + 255) / 256 * 256;
-    return at;
-  }
-};
-
-// Few rows' weights are streamed, each wavefront of the device an equal share of them (as
-// many as x in LDS leaves room for).
-struct Few {
-  bool few;
-  int64_t share, groups;
-  Few(const VocabArgs& a, int64_t columns) {
-    few = a.rows <= kFewRows && a.width <= kFewWidth;
-    const int64_t waves = (int64_t)std::max(1, a.cus) * 8 * (a.width <= kFewWidth / 2 ? 2 : 1);
-    share = (columns + waves - 1) / waves;
-    groups = (columns + share * 8 - 1) / (share * 8);
-  }
-  template <FewKind KIND>
-  void launch(const VocabArgs& a, const FewOut& out, hipStream_t s) const {
-    auto k = a.width <= kFewWidth / 2 ? vocab_few_kernel<kFewWidth / 2, KIND> : vocab_few_kernel<kFewWidth, KIND>;
-    hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(512), 0, s, a, out, (int)share);
-  }
-};
-
-struct FwdParts : Parts {
-  Few few;
-  bool large;
-  int64_t pieces, stats, picked;
-  explicit FwdParts(const VocabArgs& a) : few(a, a.vocab) {
-    large = large_tiles(a.rows, a.vocab, a.width, std::max(1, a.cus));
-    pieces = few.few ? few.groups * 8 : tiles(a.vocab, large ? Large::kTile : Small::kTile);
-    stats = add(pieces * a.rows * 8);
-    picked = add(a.teacher ? 0 : (int64_t)a.rows * 4);
-  }
-};
-
-struct BwdParts : Parts {
-  Cut cut;
-  int64_t rows, hard, x, dz, x_sums, w_sums;
-  int64_t ldz;
-  int parts;
-  explicit BwdParts(const VocabArgs& a) : cut(choose_cut(a)) {
-    ldz = padded(cut.piece);
-    parts = cut.pieces * cut.x_slices;
-    rows = add((int64_t)a.rows * (int64_t)sizeof(RowGrad));
-    hard = add(a.teacher ? (int64_t)a.rows * a.top * 4 : 0);
-    x = add(a.dw ? (int64_t)a.rows * a.width * 2 : 0);
-    dz = add(a.rows * ldz * 2);
-    x_sums = add(a.dx && parts > 1 ? parts * (int64_t)a.rows * a.width * 4 : 0);
-    w_sums = add(a.dw && cut.w_slices > 1 ? cut.w_slices * cut.piece * a.width * 4 : 0);
-  }
-};
 
 unsigned fours(int64_t n) { return (unsigned)((n + 3) / 4); }
 
@@ -1038,9 +902,6 @@ void launch_products(Products& p, int x_slices, int w_slices, hipStream_t s) {
 
 }  // namespace
 
-int64_t vocab_fwd_bytes(const VocabArgs& a) { return FwdParts(a).bytes; }
-int64_t vocab_bwd_bytes(const VocabArgs& a) { return BwdParts(a).bytes; }
-
 hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
   const FwdParts at(a);
   float2* stats = reinterpret_cast<float2*>(a.work + at.stats);
@@ -1050,8 +911,8 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
     FewOut out{};
     out.stats = stats;
     out.picked = picked;
-    if (one) at.few.launch<kFewTarget>(a, out, s);
-    else at.few.launch<kFewStats>(a, out, s);
+    if (one) launch_few<kFewTarget>(at.few, a, out, s);
+    else launch_few<kFewStats>(at.few, a, out, s);
     if (!one) hipLaunchKernelGGL(vocab_pick_kernel, dim3(fours(a.rows * a.top)), dim3(256), 0, s, a);
   } else if (at.large) {
     launch_stats<Large>(a, stats, picked, s);
@@ -1079,18 +940,19 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard, a.dw ? x : nullptr);
   int part = 0;
   for (int64_t v0 = 0; v0 < a.vocab; v0 += cut.piece) {
-    const int columns = (int)std::min<int64_t>(cut.piece, a.vocab - v0);
+    const Piece piece(a, cut, v0);
+    const int columns = piece.columns;
     const Few few(a, columns);
     if (few.few) {
-      VocabArgs piece = a;
-      piece.w = a.w + v0 * a.w_row;
-      piece.vocab = columns;
+      VocabArgs part_of = a;
+      part_of.w = a.w + v0 * a.w_row;
+      part_of.vocab = columns;
       FewOut out{};
       out.rows = rows;
       out.dz = dz;
       out.ldz = at.ldz;
       out.v0 = v0;
-      few.launch<kFewDz>(piece, out, s);
+      launch_few<kFewDz>(few, part_of, out, s);
     } else if (large_tiles(a.rows, columns, a.width, std::max(1, a.cus))) {
       launch_dz<Large>(a, rows, v0, columns, dz, at.ldz, s);
     } else {
@@ -1108,21 +970,20 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
     p.rows = a.rows;
     p.width = a.width;
     p.columns = columns;
-    p.x_slice = (int32_t)padded((columns + cut.x_slices - 1) / cut.x_slices);
-    p.w_slice = (int32_t)padded((a.rows + cut.w_slices - 1) / cut.w_slices);
-    const int xs = (columns + p.x_slice - 1) / p.x_slice, ws = (a.rows + p.w_slice - 1) / p.w_slice;
+    p.x_slice = piece.x_slice;
+    p.w_slice = piece.w_slice;
     if (a.dx) {
       p.x_sums = at.parts > 1 ? x_sums + (int64_t)part * a.rows * a.width : nullptr;
       p.dx = a.dx;
-      part += xs;
+      part += piece.x_slices;
     }
     if (a.dw) {
       p.w_sums = cut.w_slices > 1 ? w_sums : nullptr;
       p.dw = a.dw + v0 * a.width;
     }
-    if (cut.large) launch_products<Large>(p, xs, ws, s);
-    else launch_products<Small>(p, xs, ws, s);
-    if (p.w_sums) launch_sum(w_sums, ws, (int64_t)columns * a.width, p.dw, s);
+    if (cut.large) launch_products<Large>(p, piece.x_slices, piece.w_slices, s);
+    else launch_products<Small>(p, piece.x_slices, piece.w_slices, s);
+    if (p.w_sums) launch_sum(w_sums, piece.w_slices, (int64_t)columns * a.width, p.dw, s);
   }
   if (a.dx && at.parts > 1) launch_sum(x_sums, part, (int64_t)a.rows * a.width, a.dx, s);
   return hipGetLastError();
