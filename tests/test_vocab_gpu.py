@@ -279,3 +279,95 @@ def test_pieces_of_the_vocabulary():
     bar = (2.0 ** -8 + 2.0 ** -17 + 2 * T * 2.0 ** -24) * size + 2.0 ** -8 * want.abs() + \
         2.0 ** -17 * (dloss.double().abs()[:, None] * p).t() @ x.double().abs()
     assert ((got["dweight"][cols].double() - want).abs() <= bar).all()
+
+
+# ------------------------------------------- sizes of many tiles, in 64 bits on the GPU
+
+
+def check_many_tiles(T, D, V, K=None, place=lambda t: t, seed=0):
+    """As check_xent and check_distill (K indices), with the reference and its bars on the GPU."""
+    say(f"many tiles {T} x {D} x {V}, {K}")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = place(torch.randn(T, D, device="cuda", generator=g).bfloat16())
+    w = place((torch.randn(V, D, device="cuda", generator=g) * 2 / D ** 0.5).bfloat16())
+    dloss = torch.randn(T, device="cuda", generator=g)
+    xd, wd, dd, U = x.double(), w.double(), dloss.double()[:, None], ref.U
+    z = xd @ wd.t()
+    z_off = 2 * (D + 4) * U * (xd.abs() @ wd.abs().t())
+    lse = torch.logsumexp(z, -1)
+    lse_off = z_off.amax(-1) + U * (300 + 8 * z.amax(-1).abs() + 8 * lse.abs())
+    if K is None:
+        target = torch.randint(0, V, (T,), device="cuda", generator=g)
+        target[torch.rand(T, device="cuda", generator=g) < 0.2] = -1
+        takes = target >= 0
+        at = target.clamp(min=0)[:, None]
+        loss, got_lse = ssm.ssm_xent_fwd(x, w, target)
+        want = torch.where(takes, lse - z.gather(1, at)[:, 0], 0.0)
+        off = lse_off + z_off.gather(1, at)[:, 0] + 4 * U * (lse.abs() + z.gather(1, at)[:, 0].abs())
+        hard = torch.zeros_like(z).scatter_(1, at, 1.0)
+        got = ssm.ssm_xent_bwd(dloss, x, w, target, got_lse)
+    else:
+        index = torch.rand(T, V, device="cuda", generator=g).topk(K, -1).indices
+        teacher = torch.randn(T, K, device="cuda", generator=g) * 3
+        takes = torch.ones(T, dtype=torch.bool, device="cuda")
+        loss, got_lse, logits = ssm.ssm_distill_fwd(x, w, index, teacher)
+        logq = torch.log_softmax(teacher.double(), -1)
+        mine = z.gather(1, index)
+        assert ((logits.double() - mine).abs() <= z_off.gather(1, index) * 1.01).all()
+        want = (logq.exp() * (logq - mine + lse[:, None])).sum(-1)
+        size = (logq.exp() * (logq.abs() + mine.abs() + lse[:, None].abs())).sum(-1)
+        off = (logq.exp() * z_off.gather(1, index)).sum(-1) + lse_off + U * (size * (200 + K) + 100)
+        hard = torch.zeros_like(z).scatter_(1, index, logq.exp())
+        got = ssm.ssm_distill_bwd(dloss, x, w, index, teacher, got_lse, logits)
+    assert ((got_lse.double() - lse).abs() <= lse_off * 1.01).all()
+    assert ((loss.double() - want).abs() <= off * 1.01).all()
+    p = torch.exp(z - lse[:, None])
+    f = torch.where(takes[:, None], dd, 0.0)
+    dz = f * (p - hard)
+    dz_off = f.abs() * (p * (z_off + lse_off[:, None] + 8 * U * (z.abs() + lse.abs()[:, None] + 4)) + 60 * U * (p + hard)) * 1.01
+    dz_off = dz_off + 2.0 ** -8 * (dz.abs() + dz_off)
+    for name, a, a_off, b in (("dx", dz, dz_off, wd), ("dweight", dz.t(), dz_off.t(), xd)):
+        v = a @ b
+        bar = a_off @ b.abs() + 2 * (a.shape[1] + 8) * U * (a.abs() @ b.abs()) + 2.0 ** -8 * v.abs() * 1.01
+        worst = ((got[name].double() - v).abs() / (bar * 1.01 + 1e-37)).max().item()
+        assert worst <= 1, (name, worst)
+    assert not got["dx"][~takes].any()
+
+
+# (large tiles in one piece, in several, with a ragged end of each dimension; rows in slices; columns in slices)
+@pytest.mark.parametrize("T,D,V", [(1100, 1160, 21003), (2100, 72, 9000), (6100, 304, 1341), (40, 1032, 30001), (700, 2056, 4099)])
+@pytest.mark.parametrize("K", [None, 12])
+def test_many_tiles(T, D, V, K):
+    check_many_tiles(T, D, V, K)
+
+
+@pytest.mark.parametrize("T,D,V", [(13000, 264, 12100)])
+def test_many_tiles_in_pieces(T, D, V):
+    check_many_tiles(T, D, V)
+
+
+def test_many_tiles_of_slices():
+    check_many_tiles(1100, 520, 21003, place=far)
+
+
+@pytest.mark.parametrize("T", [1, 3, 16])
+@pytest.mark.parametrize("D", [8, 72, 2048, 2056, 4096, 4104])
+def test_few_rows(T, D):
+    """Weights streamed, x in LDS for either of its sizes, and the width past it."""
+    check_many_tiles(T, D, 2600)
+    check_many_tiles(T, D, 33, 5)
+
+
+def test_bits_repeat():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, w = torch.randn(700, 264, device="cuda", generator=g).bfloat16(), torch.randn(9000, 264, device="cuda", generator=g).bfloat16() / 8
+    index, teacher = torch.randint(0, 9000, (700, 20), device="cuda", generator=g), torch.randn(700, 20, device="cuda", generator=g)
+    d, first = torch.randn(700, device="cuda", generator=g), None
+    for _ in range(4):
+        loss, lse, z = ssm.ssm_distill_fwd(x, w, index, teacher, 2.0)
+        now = [loss, lse, z, *ssm.ssm_distill_bwd(d, x, w, index, teacher, lse, z, 2.0).values()]
+        loss, lse = ssm.ssm_xent_fwd(x, w, index[:, 0].contiguous())
+        now += [loss, lse, *ssm.ssm_xent_bwd(d, x, w, index[:, 0].contiguous(), lse).values()]
+        first = first or now
+        for a, b in zip(now, first):
+            assert torch.equal(a, b)
