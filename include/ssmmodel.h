@@ -44,7 +44,9 @@ extern "C" {
  * States, gates and sums are fp32.  1 - a and 1 - a^2 are formed without cancellation.
  * A value that is not finite reaches its channel's later steps only.
  * Workspace, where a sequence is longer than one tile of SSM_GSCAN_TILE steps: about
- * 10 bytes for every tile and channel of a batch row.  batch * width at most 2^31 - 1024.
+ * 9 bytes for every tile and channel of a batch row, channels counted in 128s.  width at
+ * most 2^24, batch * width at most 2^31 - 1024, and
+ * batch * ceil(width / 64) * ceil(seqlen / 64) at most 2^23 - 2.
  */
 #define SSM_GSCAN_LERP 1
 #define SSM_GSCAN_SEGMENT 32
@@ -66,8 +68,8 @@ ssm_status ssm_gscan_fwd(const void* x, int64_t x_row, const void* r, int64_t r_
  *   dx, dr, di : [batch, seqlen, width] in in_dtype, contiguous; di iff i is given
  *   drate      : [width] fp32, or NULL (not computed; iff rate is NULL it has to be)
  *   dinitial_state: [batch, width] fp32, or NULL
- * Workspace: as for the forward, and 4 bytes for every tile and channel of a batch row
- * where drate is computed.
+ * Workspace: as for the forward with tiles half as long, and 4 bytes for every such tile
+ * and channel of a batch row where drate is computed.
  */
 ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_row, const void* i, int64_t i_row,
                          const float* rate, int flags, const float* states, const void* dout,
@@ -90,7 +92,7 @@ ssm_status ssm_gscan_update(const float* state, float* state_out, const void* x,
  *   lse[t]  = log sum_v exp(z[t,v])
  *   loss[t] = lse[t] - z[t, target[t]] + z_loss lse[t]^2
  *
- * The logits are not stored: the forward keeps a maximum and a sum for every 256
+ * The logits are not stored: the forward keeps a maximum and a sum for every tile of
  * columns of a row, and the gradients compute the logits again, a piece of the
  * vocabulary at a time.
  *   x      : [rows, width] bf16, rows x_row elements apart
@@ -101,9 +103,10 @@ ssm_status ssm_gscan_update(const float* state, float* state_out, const void* x,
  *   loss, lse: [rows] fp32 (lse of every row, with a target or without)
  * width a multiple of 8 up to SSM_VOCAB_MAX_WIDTH; x and weight 16-byte aligned, their rows a
  * multiple of 8 elements apart, at most 2^22; rows at most 2^22, vocab from 1 to 2^30, x and
- * weight of at most 2^37 elements, and at most 2^23 tiles of 256 rows by 256 columns.
- * Logits and sums are fp32.  Workspace: 8 bytes for every row and 256 columns, and 4
- * for every row.
+ * weight of at most 2^37 elements, and at most 2^22 tiles of 256 rows by 256 columns.
+ * Logits and sums are fp32.  Workspace: 8 bytes for every row and 256 columns, or 128
+ * where tiles are few, and 4 for every row; up to 16 rows: 8 bytes for every row and
+ * wavefront of the device.
  */
 #define SSM_VOCAB_MAX_WIDTH 65536
 ssm_status ssm_xent_fwd(const void* x, int64_t x_row, const void* weight, int64_t w_row, const int64_t* target,
@@ -117,9 +120,11 @@ ssm_status ssm_xent_fwd(const void* x, int64_t x_row, const void* weight, int64_
  *   if not wanted, contiguous, 16-byte aligned)
  * dz is rounded to bf16 for its two products, whose sums are fp32: off by at most 2^-8 of
  * each of their terms, and 2^-8 of the result for the result's own rounding.
- * Workspace: dz and what the products read of x and weight, transposed, for a piece of
- * the vocabulary: with v columns of it, about 4 rows v + 2 width (v + rows) + 4 rows width
- * bytes; v is chosen so that dz of a piece takes at most SSM_VOCAB_PIECE_BYTES.
+ * Workspace: dz of a piece of the vocabulary, 2 rows v bytes with v columns of it, where
+ * v is chosen so that this is at most SSM_VOCAB_PIECE_BYTES or v at most 4096; 16 bytes a
+ * row; where dweight is wanted a copy of x, 2 rows width; where dx is the sum of several
+ * pieces its fp32 sums, 4 rows width; and where tiles are few such sums of up to 64 slices
+ * of dx and 16 of dweight.
  */
 #define SSM_VOCAB_PIECE_BYTES 268435456
 ssm_status ssm_xent_bwd(const float* dloss, const void* x, int64_t x_row, const void* weight, int64_t w_row,
@@ -142,7 +147,8 @@ ssm_status ssm_xent_bwd(const float* dloss, const void* x, int64_t x_row, const 
  *            z / temperature at the indices (0 where there is none): the gradients need
  *            both.  All fp32.
  * A row without any index has loss 0 and no part in the gradients, whatever x
- * holds there.  top from 1 to SSM_DISTILL_MAX_TOP; the rest as for ssm_xent_fwd.
+ * holds there.  top from 1 to SSM_DISTILL_MAX_TOP, temperature positive
+ * with a normal square; the rest as for ssm_xent_fwd.
  */
 #define SSM_DISTILL_MAX_TOP 1024
 ssm_status ssm_distill_fwd(const void* x, int64_t x_row, const void* weight, int64_t w_row, const int64_t* index,
@@ -153,7 +159,7 @@ ssm_status ssm_distill_fwd(const void* x, int64_t x_row, const void* weight, int
 /*
  * Its gradients with respect to x and weight (the teacher gets none):
  *   dz[t,v] = dloss[t] temperature scale (p[t,v] - sum_{k: index[t,k] = v} q[t,k])
- * The rest as for ssm_xent_bwd.
+ * The rest as for ssm_xent_bwd; workspace also 4 rows top bytes.
  */
 ssm_status ssm_distill_bwd(const float* dloss, const void* x, int64_t x_row, const void* weight, int64_t w_row,
                            const int64_t* index, const float* teacher, float scale, float temperature,

@@ -46,8 +46,8 @@ ssm_status gs_check(int64_t batch, int64_t seqlen, int64_t width, int flags, std
   if (sz->state > INT32_MAX - 1023 || width > kGsMostRow)
     return fail(SSM_ERR_UNSUPPORTED, "batch * width = %lld exceeds 2^31 - 1024 or width = %lld 2^24", (long long)sz->state, (long long)width);
   sz->states = sz->state * ceil_div(seqlen, SSM_GSCAN_SEGMENT);
-  // a workgroup of 512 threads for every 64 channels of a row and 128 steps, or of 256 for 64 steps
-  if (ceil_div(seqlen, ssm::kGsBwdTile) * batch * ceil_div(width, 64) > kMaxThreads / 256)
+  // a workgroup of 512 threads for every 64 channels of a row and 128 steps, back 64
+  if (ceil_div(seqlen, ssm::kGsBwdTile) * batch * ceil_div(width, 64) > kMaxThreads / 512)
     return fail(SSM_ERR_UNSUPPORTED, "batch=%lld by seqlen=%lld by width=%lld exceeds the grid", (long long)batch, (long long)seqlen,
                 (long long)width);
   return SSM_OK;
@@ -74,7 +74,7 @@ ssm_status launched(hipError_t e) {
 
 // -------------------------------------------------- losses over a vocabulary
 
-constexpr int64_t kVocabMost = int64_t{1} << 30, kVocabRows = int64_t{1} << 22, kVocabTiles = int64_t{1} << 23,
+constexpr int64_t kVocabMost = int64_t{1} << 30, kVocabRows = int64_t{1} << 22, kVocabTiles = int64_t{1} << 22,
                   kVocabElems = int64_t{1} << 37;
 
 struct VocabSizes {
@@ -97,7 +97,7 @@ ssm_status vocab_check(const void* x, int64_t x_row, const void* w, int64_t w_ro
     return fail(SSM_ERR_UNSUPPORTED, "rows=%lld or vocab=%lld by width=%lld exceeds 2^37 elements", (long long)rows, (long long)vocab,
                 (long long)width);
   if (ceil_div(rows, ssm::kVocabTile) * ceil_div(vocab, ssm::kVocabTile) > kVocabTiles)
-    return fail(SSM_ERR_UNSUPPORTED, "rows=%lld by vocab=%lld exceeds 2^23 tiles of 256 by 256", (long long)rows, (long long)vocab);
+    return fail(SSM_ERR_UNSUPPORTED, "rows=%lld by vocab=%lld exceeds 2^22 tiles of 256 by 256", (long long)rows, (long long)vocab);
   if (top < 1 || top > SSM_DISTILL_MAX_TOP)
     return fail(SSM_ERR_UNSUPPORTED, "top=%lld must be from 1 to %d", (long long)top, SSM_DISTILL_MAX_TOP);
   if (!std::isfinite(scale)) return fail(SSM_ERR_UNSUPPORTED, "scale must be finite");
@@ -139,8 +139,8 @@ ssm::VocabArgs vocab_args(const void* x, int64_t x_row, const void* w, int64_t w
 
 ssm_status check_temperature(float scale, float temperature) {
   if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(scale / temperature) ||
-      !std::isfinite(temperature * temperature))
-    return fail(SSM_ERR_UNSUPPORTED, "temperature must be positive and finite, as must scale / temperature and its square");
+      !std::isnormal(temperature * temperature))
+    return fail(SSM_ERR_UNSUPPORTED, "temperature must be positive and finite, its square a normal number and scale / temperature finite");
   return SSM_OK;
 }
 

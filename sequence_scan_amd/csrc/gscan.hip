@@ -288,35 +288,35 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
     const Rows rx(a.dx, at.tok, a.width, sizeof(T)), rr(a.dr, at.tok, a.width, sizeof(T)), ri(a.di, at.tok, a.width, sizeof(T));
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
-        const uint32_t o = decltype(whole)::value ? off : at.off(sizeof(T), j);
-        float dx[CH], dr[CH], di[CH];
+      const uint32_t o = decltype(whole)::value ? off : at.off(sizeof(T), j);
+      float dx[CH], dr[CH], di[CH];
 #pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          float u = raw_value<T>(kept[wave][0][j][lane], k);
-          const float er = gate_exp<true>(raw_value<T>(kept[wave][1][j][lane], k));
-          const float rpos = gate_open(er), gm = g[j][k] * M[j][k];
-          dx[k] = gm;
-          if constexpr (GATE) {
-            const float ei = gate_exp<true>(raw_value<T>(kept[wave][2][j][lane], k));
-            const float pos = gate_open(ei);
-            u *= pos;
-            dx[k] *= pos;
-            di[k] = gm * u * (ei * pos);
-          }
-          const float by = g[j][k] * __builtin_fmaf(A[j][k], h[k], u * decay_slope<LERP>(A[j][k], M[j][k]));
-          const float bp = by * rpos;
-          if constexpr (RATE) {
-            sum[k] -= decltype(whole)::value || j < at.n ? bp : 0.0f;
-            dr[k] = -bp * rate[k] * (er * rpos);
-          } else {
-            dr[k] = bp * er;
-          }
-          h[k] = __builtin_fmaf(A[j][k], h[k], M[j][k] * u);
+      for (int k = 0; k < CH; ++k) {
+        float u = raw_value<T>(kept[wave][0][j][lane], k);
+        const float er = gate_exp<true>(raw_value<T>(kept[wave][1][j][lane], k));
+        const float rpos = gate_open(er), gm = g[j][k] * M[j][k];
+        dx[k] = gm;
+        if constexpr (GATE) {
+          const float ei = gate_exp<true>(raw_value<T>(kept[wave][2][j][lane], k));
+          const float pos = gate_open(ei);
+          u *= pos;
+          dx[k] *= pos;
+          di[k] = gm * u * (ei * pos);
         }
-        store_raw<T, CH>(rx, j, o, dx);
-        store_raw<T, CH>(rr, j, o, dr);
-        if constexpr (GATE) store_raw<T, CH>(ri, j, o, di);
+        const float by = g[j][k] * __builtin_fmaf(A[j][k], h[k], u * decay_slope<LERP>(A[j][k], M[j][k]));
+        const float bp = by * rpos;
+        if constexpr (RATE) {
+          sum[k] -= decltype(whole)::value || j < at.n ? bp : 0.0f;
+          dr[k] = -bp * rate[k] * (er * rpos);
+        } else {
+          dr[k] = bp * er;
+        }
+        h[k] = __builtin_fmaf(A[j][k], h[k], M[j][k] * u);
       }
+      store_raw<T, CH>(rx, j, o, dx);
+      store_raw<T, CH>(rr, j, o, dr);
+      if constexpr (GATE) store_raw<T, CH>(ri, j, o, di);
+    }
   };
   if (at.n == kSteps) gradients(std::true_type{});
   else gradients(std::false_type{});

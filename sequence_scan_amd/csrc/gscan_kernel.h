@@ -21,17 +21,21 @@ __device__ __forceinline__ float gate_exp(float v) {
 }
 __device__ __forceinline__ float gate_open(float e) { return __builtin_amdgcn_rcpf(1.0f + e); }
 
-// 1 - exp(-w) for w >= 0, given exp(-w) to an ulp.  Below 3/4 the difference would lose
-// what w is small by: there w times a polynomial of degree 5 in w, fitted to
-// (1 - exp(-w)) / w over [0, 3/4] (off by at most 2.1e-8 of it, exact at 0).
+// 1 - exp(-w), given exp(-w) to an ulp, for w >= 0 or (SIGNED) of either sign.  Below 3/4
+// the difference would lose what w is small by: there w times a polynomial of degree 5 in
+// w, fitted to (1 - exp(-w)) / w over [0, 3/4] (off by at most 2.1e-8 of it, exact at 0);
+// of the other sign it is -exp(-w) (1 - exp(w)).
+template <bool SIGNED>
 __device__ __forceinline__ float one_minus_exp(float w, float e) {
-  float s = __builtin_fmaf(w, -0.00101896108f, 0.00804723334f);
-  s = __builtin_fmaf(s, w, -0.0415632911f);
-  s = __builtin_fmaf(s, w, 0.166650176f);
-  s = __builtin_fmaf(s, w, -0.499999136f);
-  s = w * __builtin_fmaf(s, w, 1.0f);
+  const float v = SIGNED ? __builtin_fabsf(w) : w;
+  float s = __builtin_fmaf(v, -0.00101896108f, 0.00804723334f);
+  s = __builtin_fmaf(s, v, -0.0415632911f);
+  s = __builtin_fmaf(s, v, 0.166650176f);
+  s = __builtin_fmaf(s, v, -0.499999136f);
+  s = w * __builtin_fmaf(s, v, 1.0f);
+  if (SIGNED) s *= w < 0.0f ? e : 1.0f;
   asm volatile("" : "+v"(s));       // (computed, not branched around: a branch would part the steps)
-  return w < 0.75f ? s : 1.0f - e;
+  return v < 0.75f ? s : 1.0f - e;
 }
 
 // A step's decay and its input's coefficient, from e = exp(-r); rate2 = rate log2 e.
@@ -41,7 +45,7 @@ __device__ __forceinline__ void decay(float e, float rate2, float* a, float* m) 
   if constexpr (RATE) {
     const float y = rate2 * pos;
     *a = __builtin_amdgcn_exp2f(-y);
-    *m = LERP ? one_minus_exp(y * kLn2, *a) : __builtin_amdgcn_sqrtf(one_minus_exp(y * (2.0f * kLn2), *a * *a));
+    *m = LERP ? one_minus_exp<true>(y * kLn2, *a) : __builtin_amdgcn_sqrtf(one_minus_exp<false>(y * (2.0f * kLn2), *a * *a));
   } else {
     *a = pos;
     const float neg = e * pos;

@@ -282,6 +282,10 @@ struct RowGrad {
 };
 static_assert(sizeof(RowGrad) == kRowGradBytes, "vocab_plan.h agrees");
 
+// A row's statistics are a maximum and the sum of 2^(value - maximum).  The maximum of no
+// values, or of values that are all minus infinity, is this: differences of maxima stay numbers.
+constexpr float kLowest = -3.0e38f;
+
 // For every tile's columns a row's maximum and sum of exponentials (base 2), and the
 // target's logit where it lies in them.
 template <typename Shape, bool ONE>
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
     }
     top = __builtin_fmaxf(top, __shfl_xor(top, 16));
     top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-    const float top2 = top == -__builtin_inff() ? 0.0f : top * kLog2e;
+    const float top2 = __builtin_fmaxf(top * kLog2e, kLowest);
     float sum = 0.0f;
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni)
@@ -360,11 +364,9 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
 #pragma unroll
     for (int w = 1; w < kWn; ++w) {
       const float2 o = part[w * kTile + m];
-      if (w * 64 < columns) {
-        const float top = __builtin_fmaxf(r.x, o.x);
-        r.y = r.y * __builtin_amdgcn_exp2f(r.x - top) + o.y * __builtin_amdgcn_exp2f(o.x - top);
-        r.x = top;
-      }
+      const float top = __builtin_fmaxf(r.x, o.x);
+      r.y = r.y * __builtin_amdgcn_exp2f(r.x - top) + o.y * __builtin_amdgcn_exp2f(o.x - top);
+      r.x = top;
     }
     stats[(int64_t)tn * a.rows + m0 + m] = r;
   }
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, FewOut o
     if (u < steps) load(w[u]);
   block_sync();
   f4_t acc = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  float top2 = -__builtin_inff(), sum = 0.0f;      // of row lane & 15, over this lane's columns
+  float top2 = kLowest, sum = 0.0f;                // of row lane & 15, over this lane's columns
   int line = 0, n = 4 * quarter;                   // columns n .. + 3 of the share
   auto step = [&](const bf16x8_t (&f)[2]) SSM_INLINE {
 #pragma unroll
@@ -500,10 +502,9 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, FewOut o
         top = __builtin_fmaxf(top, z[i]);
         if (KIND == kFewTarget && target == n + i && n + i < columns) out.picked[lane & 15] = v;
       }
-      const float from = top == -__builtin_inff() ? 0.0f : top;
-      sum *= __builtin_amdgcn_exp2f(top2 - from);
+      sum *= __builtin_amdgcn_exp2f(top2 - top);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(z[i] - from);
+      for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(z[i] - top);
       top2 = top;
     }
     acc = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, FewOut o
 #pragma unroll
     for (int o = 16; o < 64; o *= 2) {
       const float t = __shfl_xor(top2, o), v = __shfl_xor(sum, o), top = __builtin_fmaxf(top2, t);
-      if (top != -__builtin_inff()) sum = sum * __builtin_amdgcn_exp2f(top2 - top) + v * __builtin_amdgcn_exp2f(t - top);
+      sum = sum * __builtin_amdgcn_exp2f(top2 - top) + v * __builtin_amdgcn_exp2f(t - top);
       top2 = top;
     }
     if (lane < 16 && has_row) out.stats[(int64_t)id * a.rows + lane] = make_float2(top2, sum);
@@ -610,13 +611,12 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
   {
     const int64_t row = row0 + (threadIdx.x & (each - 1));
     const int per = 1024 / each;
-    float2 r = make_float2(-__builtin_inff(), 0.0f);
+    float2 r = make_float2(kLowest, 0.0f);
     if (row < a.rows) {
 #pragma unroll 4
       for (int n = threadIdx.x / each; n < pieces; n += per) {
         const float2 v = stats[(int64_t)n * a.rows + row];
         const float top = __builtin_fmaxf(r.x, v.x);
-        // (a maximum is finite or plus infinity; nothing yet: 2^-inf = 0)
         r.y = r.y * __builtin_amdgcn_exp2f(r.x - top) + v.y * __builtin_amdgcn_exp2f(v.x - top);
         r.x = top;
       }
@@ -627,10 +627,8 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
     block_sync();
     if (threadIdx.x < half) {
       const float2 r = part[threadIdx.x], v = part[threadIdx.x + half];
-      if (v.x != -__builtin_inff()) {
-        const float top = __builtin_fmaxf(r.x, v.x);
-        part[threadIdx.x] = make_float2(top, r.y * __builtin_amdgcn_exp2f(r.x - top) + v.y * __builtin_amdgcn_exp2f(v.x - top));
-      }
+      const float top = __builtin_fmaxf(r.x, v.x);
+      part[threadIdx.x] = make_float2(top, r.y * __builtin_amdgcn_exp2f(r.x - top) + v.y * __builtin_amdgcn_exp2f(v.x - top));
     }
   }
   block_sync();
@@ -767,8 +765,8 @@ __global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGr
                                                         int64_t v0, int columns, uint16_t* __restrict__ dz, int64_t ldz) {
   const int64_t entries = (int64_t)a.rows * a.top;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < entries; e += (int64_t)gridDim.x * 256) {
-    const int64_t n = a.index[e] - v0;
-    if (n < 0 || n >= columns) continue;
+    const int64_t v = a.index[e], n = v - v0;
+    if (v < v0 || n >= columns) continue;
     const int64_t row = e / a.top;
     const RowGrad g = rows[row];
     if (g.target == -2) continue;
@@ -777,22 +775,27 @@ __global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGr
   }
 }
 
-// What a tile of C becomes: bf16, or fp32 for sums over several parts.
+// What becomes of a tile of C: added to fp32 sums (`add`: of those there are; no other
+// workgroup has the tile), which are stored, or, with out, rounded to bf16.
 template <typename Shape>
-__device__ __forceinline__ void store_tile(const Acc<Shape>& acc, int64_t m0, int64_t n0, int rows, int columns, float* sum, uint16_t* out) {
+__device__ __forceinline__ void store_tile(Acc<Shape>& acc, int64_t m0, int64_t n0, int rows, int columns, float* sum, bool add,
+                                           uint16_t* out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / Shape::kWn, wn = wave % Shape::kWn;
 #pragma unroll
   for (int mi = 0; mi < Shape::kMi; ++mi) {
     const int64_t m = m0 + wm * Shape::kMi * 16 + mi * 16 + (lane & 15);
 #pragma unroll
     for (int ni = 0; ni < 4; ni += 2) {
-      if (sum) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t n = n0 + wn * 64 + (ni + h) * 16 + 4 * (lane >> 4);
-          if (m < rows && n < columns) *reinterpret_cast<f4_t*>(sum + m * columns + n) = acc[mi][ni + h];
+      for (int h = 0; h < 2; ++h) {
+        const int64_t n = n0 + wn * 64 + (ni + h) * 16 + 4 * (lane >> 4);
+        f4_t* at = reinterpret_cast<f4_t*>(sum + m * columns + n);
+        if (m < rows && n < columns) {
+          if (add) acc[mi][ni + h] += *at;
+          if (!out) *at = acc[mi][ni + h];
         }
-      } else {
+      }
+      if (out) {
         float v[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -815,10 +818,11 @@ struct Products {
   const uint16_t* x;        // [rows, width]
   const uint16_t* w;        // the piece's rows of weight
   int64_t w_row;
-  float* x_sums;            // [slices][rows, width], or NULL: dx itself
-  float* w_sums;            // [slices][columns, width], or NULL: dweight itself
-  uint16_t* dx;
-  uint16_t* dw;             // the piece's rows
+  float* x_sums;            // [slices][rows, width]
+  float* w_sums;            // [slices][columns, width]
+  uint16_t* dx;             // NULL: the sums
+  uint16_t* dw;             // the piece's rows; NULL: the sums
+  int32_t x_add;            // x_sums hold those of the pieces before
   int32_t rows, width, columns;
   int32_t x_slice, w_slice;       // contracted elements of a slice, multiples of kK
   int32_t tiles_m, tiles_n, tiles_d;
@@ -840,11 +844,11 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_produc
   if (dx) {
     const int k0 = slice * a.x_slice, end = (a.columns + 7) & ~7, k1 = k0 + a.x_slice < end ? k0 + a.x_slice : end;
     multiply<Shape, false, true>(Side{a.dz, a.ldz, a.rows, end}, Side{a.w, a.w_row, a.width, a.columns}, m0, n0, k0, k1, s, acc);
-    store_tile<Shape>(acc, m0, n0, a.rows, a.width, a.x_sums ? a.x_sums + (int64_t)slice * a.rows * a.width : nullptr, a.dx);
+    store_tile<Shape>(acc, m0, n0, a.rows, a.width, a.x_sums + (int64_t)slice * a.rows * a.width, a.x_add != 0, a.dx);
   } else {
     const int k0 = slice * a.w_slice, k1 = k0 + a.w_slice < a.rows ? k0 + a.w_slice : a.rows;
     multiply<Shape, true, true>(Side{a.dz, a.ldz, (int32_t)a.ldz, a.rows}, Side{a.x, a.width, a.width, a.rows}, m0, n0, k0, k1, s, acc);
-    store_tile<Shape>(acc, m0, n0, a.columns, a.width, a.w_sums ? a.w_sums + (int64_t)slice * a.columns * a.width : nullptr, a.dw);
+    store_tile<Shape>(acc, m0, n0, a.columns, a.width, a.w_sums + (int64_t)slice * a.columns * a.width, false, a.dw);
   }
 }
 
@@ -890,12 +894,12 @@ void launch_dz(const VocabArgs& a, const RowGrad* rows, int64_t v0, int columns,
 }
 
 template <typename Shape>
-void launch_products(Products& p, int x_slices, int w_slices, hipStream_t s) {
+void launch_products(Products& p, int x_slices, int w_slices, hipStream_t s) {      // (0 slices: not wanted)
   p.tiles_m = (int32_t)tiles(p.rows, Shape::kTile);
   p.tiles_n = (int32_t)tiles(p.columns, Shape::kTile);
   p.tiles_d = (int32_t)tiles(p.width, Shape::kTile);
-  p.x_items = p.dx ? p.tiles_m * p.tiles_d * x_slices : 0;
-  p.w_items = p.dw ? p.tiles_n * p.tiles_d * w_slices : 0;
+  p.x_items = p.tiles_m * p.tiles_d * x_slices;
+  p.w_items = p.tiles_n * p.tiles_d * w_slices;
   p.x_first = p.x_slice >= p.w_slice;      // the longer ones first
   hipLaunchKernelGGL(vocab_products_kernel<Shape>, dim3((unsigned)(p.x_items + p.w_items)), dim3(Shape::kThreads), 0, s, p);
 }
@@ -938,7 +942,7 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
   const bool one = a.teacher == nullptr;
   auto rk = one ? vocab_rows_kernel<true> : vocab_rows_kernel<false>;
   hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard, a.dw ? x : nullptr);
-  int part = 0;
+  int x_slices = 0;
   for (int64_t v0 = 0; v0 < a.vocab; v0 += cut.piece) {
     const Piece piece(a, cut, v0);
     const int columns = piece.columns;
@@ -972,20 +976,20 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
     p.columns = columns;
     p.x_slice = piece.x_slice;
     p.w_slice = piece.w_slice;
-    if (a.dx) {
-      p.x_sums = at.parts > 1 ? x_sums + (int64_t)part * a.rows * a.width : nullptr;
-      p.dx = a.dx;
-      part += piece.x_slices;
-    }
-    if (a.dw) {
-      p.w_sums = cut.w_slices > 1 ? w_sums : nullptr;
-      p.dw = a.dw + v0 * a.width;
-    }
-    if (cut.large) launch_products<Large>(p, piece.x_slices, piece.w_slices, s);
-    else launch_products<Small>(p, piece.x_slices, piece.w_slices, s);
-    if (p.w_sums) launch_sum(w_sums, piece.w_slices, (int64_t)columns * a.width, p.dw, s);
+    // dx is rounded once, behind the last piece: by its products, or over the slices
+    const bool last = v0 + columns == a.vocab;
+    p.x_sums = x_sums;
+    p.x_add = v0 > 0;
+    p.dx = last && cut.x_slices == 1 ? a.dx : nullptr;
+    p.w_sums = w_sums;
+    uint16_t* dw = a.dw ? a.dw + v0 * a.width : nullptr;
+    p.dw = cut.w_slices == 1 ? dw : nullptr;
+    if (cut.large) launch_products<Large>(p, a.dx ? piece.x_slices : 0, a.dw ? piece.w_slices : 0, s);
+    else launch_products<Small>(p, a.dx ? piece.x_slices : 0, a.dw ? piece.w_slices : 0, s);
+    if (dw && !p.dw) launch_sum(w_sums, piece.w_slices, (int64_t)columns * a.width, dw, s);
+    x_slices = std::max(x_slices, piece.x_slices);      // (the last piece may have fewer)
   }
-  if (a.dx && at.parts > 1) launch_sum(x_sums, part, (int64_t)a.rows * a.width, a.dx, s);
+  if (a.dx && cut.x_slices > 1) launch_sum(x_sums, x_slices, (int64_t)a.rows * a.width, a.dx, s);
   return hipGetLastError();
 }
 

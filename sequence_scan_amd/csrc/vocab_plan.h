@@ -49,6 +49,9 @@ inline int64_t makespan(int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t 
   }
 }
 
+// (The least piece: each piece reads and writes dx's fp32 sums once.  Gradients of 65536 x
+// 1024 x 30000, 1024 columns at a time 25.4 ms, 4096 16.1; 131072 x 512 x 20000, 1024 59.6,
+// 4096 18.7.)
 // The backward's cut: columns of a piece of the vocabulary, slices of the contracted
 // dimensions of dx (the piece's columns) and dweight (the rows), and the tiles.
 struct Cut {
@@ -58,15 +61,15 @@ struct Cut {
 };
 
 // Of the pieces whose dz fits kVocabPieceBytes, and the slices, those for which the tiles
-// of dz and of the products take least.  A slice more costs its fp32 sums once written and
-// read, about 8 bytes an element at 5 TB/s.  (8192 x 2560 x 50280: pieces of 64 tiles
+// of dz and of the products take least.  A piece or a slice more costs its fp32 sums once
+// written and read, about 8 bytes an element at 5 TB/s.  (8192 x 2560 x 50280: pieces of 64 tiles
 // and a rest of 5, whose tiles go round the CUs without a gap, 7300 us in place of 7360 in
 // four equal ones.  Rows in slices: the gradients of 6135 x 304 x 1341 157 -> 67 us; columns
 // in up to 64: 20 x 1272 x 55589 196 -> 112.)
 inline Cut choose_cut(const VocabArgs& a) {
   const int64_t cus = std::max(1, a.cus), tv = tiles(a.vocab, kVocabTile);
   const int64_t most = std::min(
-      tv, std::max<int64_t>(1, std::min<int64_t>(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows)) / kVocabTile));
+      tv, std::max(kVocabPieceLeast, std::min(kVocabMaxLd, kVocabPieceBytes / 2 / std::max(1, a.rows))) / kVocabTile);
   const bool one = most == tv;
   Cut best{};
   int64_t least = INT64_MAX;
@@ -141,15 +144,13 @@ struct BwdParts : Parts {
   Cut cut;
   int64_t rows, hard, x, dz, x_sums, w_sums;
   int64_t ldz;
-  int parts;
   explicit BwdParts(const VocabArgs& a) : cut(choose_cut(a)) {
     ldz = padded(cut.piece);
-    parts = cut.pieces * cut.x_slices;
     rows = add((int64_t)a.rows * kRowGradBytes);
     hard = add(a.teacher ? (int64_t)a.rows * a.top * 4 : 0);
     x = add(a.dw ? (int64_t)a.rows * a.width * 2 : 0);
     dz = add(a.rows * ldz * 2);
-    x_sums = add(a.dx && parts > 1 ? parts * (int64_t)a.rows * a.width * 4 : 0);
+    x_sums = add(a.dx && (cut.pieces > 1 || cut.x_slices > 1) ? cut.x_slices * (int64_t)a.rows * a.width * 4 : 0);
     w_sums = add(a.dw && cut.w_slices > 1 ? cut.w_slices * cut.piece * a.width * 4 : 0);
   }
 };

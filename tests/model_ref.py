@@ -78,11 +78,11 @@ class Gscan:
         e = g * inner
         e_off = g_off * np.abs(inner) + np.abs(g) * inner_off + g_off * inner_off + 4 * U * np.abs(e)
         by = self.neg * (1 if self.rate is None else -self.rate * self.pos)
-        gm_off = (g_off + 2 * c * np.abs(g)) * m
-        out = {"dx": (g * m * self.ipos, (gm_off + c * np.abs(g) * m) * self.ipos),
+        gm_off = (g_off + 2 * c * np.abs(g)) * np.abs(m)
+        out = {"dx": (g * m * self.ipos, (gm_off + c * np.abs(g * m)) * self.ipos),
                "dr": (e * by, (e_off + 2 * c * np.abs(e)) * np.abs(by))}
         if self.has_i:
-            out["di"] = (g * m * u * self.ineg, (gm_off + 2 * c * np.abs(g) * m) * np.abs(u) * self.ineg)
+            out["di"] = (g * m * u * self.ineg, (gm_off + 2 * c * np.abs(g * m)) * np.abs(u) * self.ineg)
         if self.rate is not None:
             # a sum over B L terms, added in any order: n roundings of what has been added
             n = B * L

@@ -152,23 +152,24 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t) {
   if (at.ldz % kK || at.ldz < at.cut.piece || at.ldz > kVocabMaxLd || at.cut.piece < 1 ||
       (at.cut.piece < a.vocab && at.cut.piece % kVocabTile))
     fail("piece");
-  if (a.rows * at.ldz * 2 > kVocabPieceBytes && at.cut.piece > kVocabTile) fail("piece bytes");
-  int parts = 0, pieces = 0;
+  if (a.rows * at.ldz * 2 > kVocabPieceBytes && at.cut.piece > kVocabPieceLeast) fail("piece bytes");
+  int first = 0, slices = 0, pieces = 0;
   for (int64_t v0 = 0; v0 < a.vocab; v0 += at.cut.piece, ++pieces) {
     const Piece p(a, at.cut, v0);
     if (p.x_slice % kK || p.w_slice % kK || (int64_t)p.x_slices * p.x_slice < p.columns || (int64_t)(p.x_slices - 1) * p.x_slice >= p.columns ||
         (int64_t)p.w_slices * p.w_slice < a.rows || (int64_t)(p.w_slices - 1) * p.w_slice >= a.rows || p.w_slices > at.cut.w_slices)
       fail("slices");
     if (p.w_slices > 1 && at.cut.pieces > 1) fail("slices of rows in pieces");
-    parts += p.x_slices;
+    if (v0 == 0) first = p.x_slices;
+    slices = std::max(slices, p.x_slices);
   }
-  if (pieces != at.cut.pieces || parts > at.parts || (at.parts == 1 && parts != 1)) fail("parts");
+  if (pieces != at.cut.pieces || slices > at.cut.x_slices || first < slices) fail("slices");
   regions(a.work, vocab_bwd_bytes(a),
           {{at.rows, a.rows * (int64_t)kRowGradBytes},
            {at.hard, a.teacher ? (int64_t)a.rows * a.top * 4 : 0},
            {at.x, a.dw ? rw * 2 : 0},
            {at.dz, a.rows * at.ldz * 2},
-           {at.x_sums, a.dx && at.parts > 1 ? parts * rw * 4 : 0},
+           {at.x_sums, a.dx && (pieces > 1 || at.cut.x_slices > 1) ? slices * rw * 4 : 0},
            {at.w_sums, a.dw && at.cut.w_slices > 1 ? at.cut.w_slices * at.cut.piece * a.width * 4 : 0}});
   return hipSuccess;
 }

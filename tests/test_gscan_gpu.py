@@ -266,3 +266,21 @@ def test_bits_repeat():
         first = first or now
         for a, b in zip(now, first):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [1, 40, 150])
+def test_growing_decays(L, dtype):
+    """Rates below zero, with 1 - a as the input's coefficient: a > 1."""
+    d = draw(2, L, 66, dtype, True, True)
+    rate, r64 = pair(np.random.default_rng(0).uniform(-1.2, 0.3, 66) * np.linspace(0.01, 1, 66), F32)
+    states = states_for(2, L, 66)
+    out = ssm.ssm_gscan_fwd(d["x"][0], d["r"][0], d["i"][0], rate, True, states=states)
+    want = ref.Gscan(d["x"][1], d["r"][1], d["i"][1], r64, True)
+    near(out, want.h, want.h_off, HALF[dtype], "out")
+    g = ssm.ssm_gscan_bwd(d["x"][0], d["r"][0], d["i"][0], rate, d["dout"][0], states, True)
+    for n, v in g.items():
+        near(v, *want.grad(d["dout"][1])[n], HALF[dtype] if n != "drate" else 0, n)
+    S = torch.zeros(2, 66, device="cuda")
+    step = ssm.ssm_gscan_update(S, *(d[n][0][:, 0].contiguous() for n in "xri"), rate, True)
+    near(step, want.h[:, 0], want.h_off[:, 0], HALF[dtype], "step")

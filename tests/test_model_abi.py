@@ -75,6 +75,7 @@ BAD = [
     (fwd, dict(batch=1 << 40, seqlen=1 << 40), SHAPE, "overflow"), (fwd, dict(batch=1 << 26), UNSUPPORTED, "2^31"),
     (fwd, dict(batch=1, width=1 << 25, x_row=1 << 25, r_row=1 << 25, i_row=1 << 25), UNSUPPORTED, "2^24"),
     (fwd, dict(batch=1, seqlen=1 << 32), UNSUPPORTED, "grid"),
+    (fwd, dict(batch=1 << 23, seqlen=1, width=1), UNSUPPORTED, "grid"), (fwd, dict(batch=1 << 22, seqlen=65, width=1), UNSUPPORTED, "grid"),
     (bwd, dict(dx=ptr(0)), UNSUPPORTED, "overlaps"), (bwd, dict(di=ptr(8)), UNSUPPORTED, "overlaps"),
     (bwd, dict(dinitial_state=ptr(6)), UNSUPPORTED, "overlaps"), (bwd, dict(rate=None), UNSUPPORTED, "drate"),
     (bwd, dict(i=None), UNSUPPORTED, "di"), (bwd, dict(seqlen=-1), SHAPE, "seqlen"), (bwd, dict(dr=ptr(8) + 1), UNSUPPORTED, "dr"),
@@ -85,6 +86,7 @@ BAD = [
     (xent, dict(width=65544, x_row=65544, w_row=65544), UNSUPPORTED, "65536"), (xent, dict(vocab=0), UNSUPPORTED, "vocab"),
     (xent, dict(vocab=(1 << 30) + 1), UNSUPPORTED, "vocab"), (xent, dict(rows=(1 << 22) + 1), UNSUPPORTED, "rows"),
     (xent, dict(rows=1 << 22, vocab=1 << 20), UNSUPPORTED, "tiles"), (xent, dict(in_dtype=F32), UNSUPPORTED, "bf16"),
+    (xent, dict(rows=1 << 22, vocab=65537), UNSUPPORTED, "tiles"),
     (xent, dict(vocab=1 << 24, width=65536, x_row=65536, w_row=65536), UNSUPPORTED, "2^37"),
     (xent, dict(x_row=56), UNSUPPORTED, "x rows"), (xent, dict(x_row=68), UNSUPPORTED, "x rows"), (xent, dict(w_row=(1 << 22) + 8), UNSUPPORTED, "weight rows"),
     (xent, dict(x=ptr(0) + 8), UNSUPPORTED, "x"), (xent, dict(weight=ptr(1) + 2), UNSUPPORTED, "weight"), (xent, dict(target=ptr(2) + 4), UNSUPPORTED, "target"),
@@ -96,6 +98,7 @@ BAD = [
     (distill, dict(top=0), UNSUPPORTED, "top"), (distill, dict(top=1025), UNSUPPORTED, "1024"), (distill, dict(top=-1), SHAPE, "top"),
     (distill, dict(temperature=0.0), UNSUPPORTED, "temperature"), (distill, dict(temperature=float("nan")), UNSUPPORTED, "temperature"),
     (distill, dict(temperature=1e-39), UNSUPPORTED, "temperature"), (distill, dict(temperature=1e30), UNSUPPORTED, "temperature"),
+    (distill, dict(temperature=1e-20), UNSUPPORTED, "temperature"),
     (distill, dict(logits=ptr(3)), UNSUPPORTED, "overlaps"), (distill, dict(index=ptr(2) + 4), UNSUPPORTED, "index"),
     (distill_bwd, dict(dx=ptr(6)), UNSUPPORTED, "overlaps"), (distill_bwd, dict(dweight=ptr(2) + 16), UNSUPPORTED, "overlaps"),
     (distill_bwd, dict(temperature=-1.0), UNSUPPORTED, "temperature"), (distill_bwd, dict(w_row=8), UNSUPPORTED, "weight rows"),

@@ -371,3 +371,23 @@ def test_bits_repeat():
         first = first or now
         for a, b in zip(now, first):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,V", [(5, 3000), (200, 3000), (2100, 9000)])
+def test_logits_of_minus_infinity(T, V):
+    """Whole tiles of them beside logits far below zero; rows of nothing else have lse minus infinity."""
+    D = 64
+    x = torch.ones(T, D, device="cuda", dtype=torch.bfloat16)
+    w = torch.full((V, D), -60.0, device="cuda", dtype=torch.bfloat16)
+    w[:2000], w[2500:] = float("-inf"), float("-inf")
+    target = torch.full((T,), 2100, device="cuda")
+    loss, lse = ssm.ssm_xent_fwd(x, w, target)
+    want = -60.0 * D + np.log(500.0)
+    # 64 sums of 60, a conversion of base there and back, and a logarithm
+    bar = 400 * ref.U * 60 * D
+    assert ((lse.double() - want).abs() <= bar).all() and ((loss.double() - np.log(500.0)).abs() <= 2 * bar).all()
+    index = target[:, None].expand(T, 3).contiguous()
+    loss, lse, z = ssm.ssm_distill_fwd(x, w, index, torch.zeros(T, 3, device="cuda"))
+    assert ((lse.double() - want).abs() <= bar).all() and (z == -60.0 * D).all()
+    w[:] = float("-inf")
+    assert torch.isneginf(ssm.ssm_xent_fwd(x, w, target)[1]).all()
