@@ -180,7 +180,8 @@ struct Reader {
 // A stage's first half is multiplied while its second half is read, the second half
 // while the next stage's first is: no product waits for LDS.  Between the halves every
 // wavefront has read all of the stage, so its place is free for the stage kStages on,
-// and the next stage has to be there.
+// and the next stage has to be there.  (At the end nothing is on its way to the stages; a
+// barrier is due before they hold anything else.)
 template <typename Shape, bool A_ACROSS, bool B_ACROSS>
 __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m0, int64_t n0, int k0, int k1, Stages<Shape>& s,
                                          Acc<Shape>& acc) {
@@ -244,7 +245,6 @@ __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m
     products(1);
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  block_sync();
 }
 
 // Two neighbouring operands' columns of a row of C, rounded to bf16, as eight in a row:
