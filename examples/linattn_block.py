@@ -7,7 +7,9 @@
 
 * ``prompt`` runs a whole prompt (dense products) and leaves the state;
 * ``token`` runs one token from it, with the projections in 4 bits (ssm_q4_matvec);
-* ``gradients`` is the block's backward pass (ssm_*_bwd), recomputing what it needs.
+* ``gradients`` is the block's backward pass (ssm_*_bwd), recomputing what it needs;
+* ``train`` is a training step of a model that ends with the block: a norm behind it, the
+  cross entropy of a vocabulary (ssm_xent_*), and the gradients of it all.
 
 Run:  python examples/linattn_block.py   (an MI355X; prints what it checked and timed)
 """
@@ -47,6 +49,7 @@ class LinAttnBlock:
         self.norm_weight = (1 + 0.1 * torch.randn(width, generator=r)).to(device)
         self.head_weight = (1 + 0.1 * torch.randn(heads * dim, generator=r)).to(device)
         self.decay_bias = torch.linspace(-5, -1, heads).to(device)
+        self.last_weight = (1 + 0.1 * torch.randn(width, generator=r)).to(device)
 
     def _split(self, p):
         q, k, v, z, a = p[..., :sum(self.sizes)].split(self.sizes, -1)
@@ -94,6 +97,18 @@ class LinAttnBlock:
         an = ssm.ssm_add_norm_bwd((dp @ self.w_in).view(B, L, D), r, self.norm_weight, dresidual_out=dresidual, x=x)
         return {"x": an["dx"], "residual": an["dresidual"], "norm_weight": an["dweight"], "head_weight": gn["dweight"],
                 "decay_bias": da.sum((0, 1)), "w_in": dp.t() @ u2, "w_out": d2.t() @ o.view(B * L, -1)}
+
+    def train(self, x, residual, head, target):
+        """The losses [batch, seqlen] of the targets under softmax(head norm(residual stream)), head
+        [vocab, width] (a negative target does not count), and the gradients of their mean."""
+        out, r, _ = self.prompt(x, residual)
+        y, last = ssm.ssm_add_norm_fwd(out, r, self.last_weight)
+        loss, lse = ssm.ssm_xent_fwd(y, head, target)
+        counts = target >= 0
+        dy = ssm.ssm_xent_bwd(counts / counts.sum(), y, head, target, lse)
+        dn = ssm.ssm_add_norm_bwd(dy["dx"], last, self.last_weight, x=out)
+        g = self.gradients(x, residual, dn["dx"], dn["dresidual"])
+        return loss, {**g, "head": dy["dweight"], "last_weight": dn["dweight"]}
 
 
 def reference(block, x, residual, weights):
@@ -144,9 +159,31 @@ def check(block, L=96, steps=8, batch=2, device="cuda"):
     return errors
 
 
+def check_training(block, L=96, batch=2, vocab=1000, device="cuda"):
+    """Errors (of each result's largest value) of a training step, against plain float32."""
+    D = block.norm_weight.numel()
+    r = torch.Generator(device="cpu").manual_seed(2)
+    x = torch.randn(batch, L, D, generator=r).to(device, BF16)
+    res = torch.randn(batch, L, D, generator=r).to(device)
+    head = (torch.randn(vocab, D, generator=r) * D ** -0.5).to(device, BF16)
+    target = torch.randint(-1, vocab, (batch, L), generator=r).to(device)
+    leaves = {"norm_weight": block.norm_weight, "w_in": block.w_in, "head_weight": block.head_weight, "w_out": block.w_out,
+              "decay_bias": block.decay_bias, "last_weight": block.last_weight, "head": head, "x": x, "residual": res}
+    leaves = {n: t.float().clone().requires_grad_() for n, t in leaves.items()}
+    out, new = reference(block, leaves["x"], leaves["residual"], list(leaves.values())[:5])
+    new = new + out
+    y = new * torch.rsqrt(new.square().mean(-1, keepdim=True) + 1e-5) * leaves["last_weight"]
+    z, at = y @ leaves["head"].t(), target.clamp(min=0)[..., None]
+    want = (torch.logsumexp(z, -1) - z.gather(-1, at)[..., 0]) * (target >= 0)
+    (want.sum() / (target >= 0).sum()).backward()
+    loss, g = block.train(x, res, head, target)
+    pairs = {"loss": (loss, want.detach()), **{"d " + n: (g[n], t.grad) for n, t in leaves.items()}}
+    return {n: ((a.float() - b).abs().max() / b.abs().max()).item() for n, (a, b) in pairs.items()}
+
+
 def main():
     small = LinAttnBlock()
-    for name, e in check(small).items():
+    for name, e in (*check(small).items(), *check_training(small).items()):
         print(f"{name:14s} {e:.1e} of its largest value from plain float32")
     block = LinAttnBlock(width=2560, heads=40, groups=40, dim=64, group=128)
     x = torch.randn(1, 4096, 2560, device="cuda").to(BF16)
@@ -166,6 +203,9 @@ def main():
     one, r1 = x[:, 0].contiguous(), res[:, 0].contiguous()
     timed("one token, one block", lambda: block.token(one, r1, state), 50)
     timed("forward and backward over 4096 tokens, one block", lambda: block.gradients(x, res, x, res), 5)
+    head = (torch.randn(50280, 2560, device="cuda") * 2560 ** -0.5).to(BF16)
+    target = torch.randint(0, 50280, (1, 4096), device="cuda")
+    timed("a training step over 4096 tokens, one block and 50280 words", lambda: block.train(x, res, head, target), 5)
 
 
 if __name__ == "__main__":

@@ -1,5 +1,8 @@
 """The model operators (include/ssmmodel.h) as a program uses them: together, captured in
 HIP graphs, on other streams, refused calls, tensors past 2^31 elements."""
+import os
+import sys
+
 import numpy as np
 import pytest
 
@@ -13,6 +16,7 @@ torch = pytest.importorskip("torch")
 ssm = pytest.importorskip("sequence_scan_amd")
 
 F32, BF16 = torch.float32, torch.bfloat16
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -266,6 +270,22 @@ def test_a_training_step(kind):
         e = ((got[name].double() - leaf.grad).abs().max() / leaf.grad.abs().max()).item()
         say(f"{name} {e:.2e}")
         assert e <= 12 * 4 * 2.0 ** -8, (name, e)
+
+
+def test_example_training_step():
+    """The example's block with a vocabulary behind it, against plain float32.  About eight roundings to bf16
+    (2^-8) lie between the input and a loss and as many back to a gradient, each of values up to about four times
+    those they are summed with: 8 * 4 * 2^-8 = 0.125 of the largest, and twice that."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import linattn_block
+    finally:
+        sys.path.pop(0)
+    errors = linattn_block.check_training(linattn_block.LinAttnBlock(width=512, heads=6, groups=3, dim=64, group=64))
+    say(str(errors))
+    assert len(errors) == 10
+    for name, e in errors.items():
+        assert e <= (0.25 if name.startswith("d ") else 0.125), (name, e)
 
 
 def test_tokens_continue_a_prompt():
