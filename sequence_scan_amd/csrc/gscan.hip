@@ -51,7 +51,7 @@ struct Place {
   __device__ __forceinline__ uint32_t off(int size, int j = 0) const { return in && j < n ? (uint32_t)d * size : kNowhere; }
 };
 
-template <typename T, bool RATE, bool LERP, bool GATE, int CH>
+template <typename T, bool RATE, bool LERP, bool GATE, int CH, bool STREAM>
 __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs a, Chain c) {
   __shared__ float2 parts[kFwdWaves][CH][64];
   __shared__ float enter[CH][64];
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
     for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) v[k] = __builtin_fmaf(P[j][k], h[k], H[j][k]);      // (past the last step the last one's)
-      store_raw<Tout, CH>(ro, j, decltype(whole)::value ? off : at.off(sizeof(Tout), j), v);
+      store_raw<STREAM, Tout, CH>(ro, j, decltype(whole)::value ? off : at.off(sizeof(Tout), j), v);
     }
   };
   if (at.n == kSteps) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
   }
 }
 
-template <typename T, bool RATE, bool LERP, bool GATE, int CH>
+template <typename T, bool RATE, bool LERP, bool GATE, int CH, bool STREAM>
 __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs a, Chain c) {
   __shared__ uint32_t kept[kBwdWaves][3][kBwdSteps][64];      // x, r and i as they lie in memory, for the second pass
   __shared__ float2 parts[kBwdWaves][CH][64];
@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
         }
         h[k] = __builtin_fmaf(A[j][k], h[k], M[j][k] * u);
       }
-      store_raw<T, CH>(rx, j, o, dx);
-      store_raw<T, CH>(rr, j, o, dr);
-      if constexpr (GATE) store_raw<T, CH>(ri, j, o, di);
+      store_raw<STREAM, T, CH>(rx, j, o, dx);
+      store_raw<STREAM, T, CH>(rr, j, o, dr);
+      if constexpr (GATE) store_raw<STREAM, T, CH>(ri, j, o, di);
     }
   };
   if (at.n == kSteps) gradients(std::true_type{});
@@ -399,10 +399,10 @@ __global__ void __launch_bounds__(1024) gscan_sum_kernel(const float* __restrict
                     : (a.i ? kernel<true, false, true, __VA_ARGS__> : kernel<true, false, false, __VA_ARGS__>))    \
           : (a.lerp ? (a.i ? kernel<false, true, true, __VA_ARGS__> : kernel<false, true, false, __VA_ARGS__>)     \
                     : (a.i ? kernel<false, false, true, __VA_ARGS__> : kernel<false, false, false, __VA_ARGS__>)))
-template <bool RATE, bool LERP, bool GATE, typename T, int CH>
-constexpr auto fwd_kernel = &gscan_fwd_kernel<T, RATE, LERP, GATE, CH>;
-template <bool RATE, bool LERP, bool GATE, typename T, int CH>
-constexpr auto bwd_kernel = &gscan_bwd_kernel<T, RATE, LERP, GATE, CH>;
+template <bool RATE, bool LERP, bool GATE, typename T, int CH, bool STREAM>
+constexpr auto fwd_kernel = &gscan_fwd_kernel<T, RATE, LERP, GATE, CH, STREAM>;
+template <bool RATE, bool LERP, bool GATE, typename T, int CH, bool STREAM>
+constexpr auto bwd_kernel = &gscan_bwd_kernel<T, RATE, LERP, GATE, CH, STREAM>;
 template <bool RATE, bool LERP, bool GATE, typename T>
 constexpr auto step_kernel = &gscan_step_kernel<T, RATE, LERP, GATE>;
 
@@ -419,6 +419,13 @@ int channels(const GscanArgs& a, DT in) {
              : 1;
 }
 
+// Outputs go past the caches where their rows are whole lines of 128 bytes (us, with and
+// without: forward of 8 x 2048 x 5120 bf16 143 / 147, 2 x 2048 x 5120 43.6 / 48.2, 1 x 65537 x
+// 2560 196 / 201; forward and back 4 x 2048 x 5120 224 / 232, fp32 2 x 1024 x 5120 107 / 118).
+// A line written in parts does not take it: 3 x 1021 x 1537 fp32, forward and back, 71 / 67.
+// (Loads past the caches: 8 x 2048 x 5120 141, but 1 x 2048 x 5120 34.6 in place of 32.3.)
+bool streams(int64_t width, int size) { return width * size % 128 == 0; }
+
 void begin(const Layout& l, const float* first, int64_t width, hipStream_t s) {
   if (l.c.tiles <= 1) return;
   const int64_t n = (int64_t)l.c.strips * l.c.tiles * 64 * l.ch;
@@ -431,9 +438,10 @@ void begin(const Layout& l, const float* first, int64_t width, hipStream_t s) {
 hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s) {
   const Layout l = gscan_layout(a.batch, a.seqlen, a.width, kGsFwdTile, channels(a, in), a.work);
   begin(l, a.initial, a.width, s);
-  auto k = in == DT::F32 ? SSM_GSCAN_PICK(fwd_kernel, float, 1)
-           : l.ch == 2   ? SSM_GSCAN_PICK(fwd_kernel, uint16_t, 2)
-                         : SSM_GSCAN_PICK(fwd_kernel, uint16_t, 1);
+  const bool stream = streams(a.width, a.out_bf16 ? 2 : 4);
+  auto k = in == DT::F32 ? (stream ? SSM_GSCAN_PICK(fwd_kernel, float, 1, true) : SSM_GSCAN_PICK(fwd_kernel, float, 1, false))
+           : l.ch == 2   ? (stream ? SSM_GSCAN_PICK(fwd_kernel, uint16_t, 2, true) : SSM_GSCAN_PICK(fwd_kernel, uint16_t, 2, false))
+                         : SSM_GSCAN_PICK(fwd_kernel, uint16_t, 1, false);
   hipLaunchKernelGGL(k, dim3((unsigned)(l.c.strips * l.c.tiles)), dim3(64 * kFwdWaves), 0, s, a, l.c);
   return hipGetLastError();
 }
@@ -441,9 +449,10 @@ hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s) {
 hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t s) {
   const Layout l = gscan_layout(a.batch, a.seqlen, a.width, kGsBwdTile, channels(a, in), a.work);
   begin(l, a.dlast, a.width, s);
-  auto k = in == DT::F32 ? SSM_GSCAN_PICK(bwd_kernel, float, 1)
-           : l.ch == 2   ? SSM_GSCAN_PICK(bwd_kernel, uint16_t, 2)
-                         : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1);
+  const bool stream = streams(a.width, in == DT::F32 ? 4 : 2);
+  auto k = in == DT::F32 ? (stream ? SSM_GSCAN_PICK(bwd_kernel, float, 1, true) : SSM_GSCAN_PICK(bwd_kernel, float, 1, false))
+           : l.ch == 2   ? (stream ? SSM_GSCAN_PICK(bwd_kernel, uint16_t, 2, true) : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 2, false))
+                         : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1, false);
   hipLaunchKernelGGL(k, dim3((unsigned)(l.c.strips * l.c.tiles)), dim3(64 * kBwdWaves), 0, s, a, l.c);
   if (a.drate)
     hipLaunchKernelGGL(gscan_sum_kernel, dim3((unsigned)((a.width + 63) / 64)), dim3(1024), 0, s, a.part, a.drate,

@@ -199,19 +199,20 @@ __device__ __forceinline__ void load_values(const Rows& r, int j, uint32_t d, fl
     for (int k = 0; k < CH; ++k) v[k] = raw_value<T>(w, k);
   }
 }
-template <typename T, int CH>
+// STREAM: past the caches.
+template <bool STREAM, typename T, int CH>
 __device__ __forceinline__ void store_raw(const Rows& r, int j, uint32_t d, const float (&v)[CH]) {
+  constexpr int kAux = STREAM ? 2 : 0;      // non-temporal
   if constexpr (sizeof(T) == 4) {
     typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
     if constexpr (CH == 2)
-      __builtin_amdgcn_raw_buffer_store_b64(u2_t{__float_as_uint(v[0]), __float_as_uint(v[1])}, r.at, d, j * r.row, 0);
-    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r.at, d, j * r.row, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(u2_t{__float_as_uint(v[0]), __float_as_uint(v[1])}, r.at, d, j * r.row, kAux);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r.at, d, j * r.row, kAux);
   } else {
-    if constexpr (CH == 2) __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), r.at, d, j * r.row, 0);
-    else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(v[0]), r.at, d, j * r.row, 0);
+    if constexpr (CH == 2) __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), r.at, d, j * r.row, kAux);
+    else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_rne(v[0]), r.at, d, j * r.row, kAux);
   }
 }
-
 }  // namespace
 }  // namespace ssm
 
