@@ -37,7 +37,7 @@ _ARGS = {
 }
 _fns: dict = {}
 _code: dict = {}            # torch dtype -> the C ABI's code
-_F32 = _U8 = _empty = _raw_stream = _device = None
+_F32 = _U8 = _empty = _empty_like = _raw_stream = _device = None
 
 
 def _fn(name: str):
@@ -54,9 +54,9 @@ def _fn(name: str):
 def _start():
     """What the wrappers use of PyTorch, looked up once: a decode step makes dozens of
     these calls, and each microsecond of a wrapper counts."""
-    global _F32, _U8, _empty, _raw_stream, _device
+    global _F32, _U8, _empty, _empty_like, _raw_stream, _device
     import torch
-    _F32, _U8, _empty = torch.float32, torch.uint8, torch.empty
+    _F32, _U8, _empty, _empty_like = torch.float32, torch.uint8, torch.empty, torch.empty_like
     _code.update({torch.float32: SSM_F32, torch.bfloat16: SSM_BF16})
     # the public form builds a Stream object first, 2.7 us against 0.1 us
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -139,6 +139,9 @@ def _kind(dtype) -> int:
 
 
 def _new(shape, dtype, like):
+    # empty_like takes 0.9 us, empty 1.9
+    if like.shape == shape and like.is_contiguous():
+        return _empty_like(like, dtype=dtype)
     return _empty(shape, dtype=dtype, device=like.device)
 
 

@@ -10,7 +10,7 @@ import ctypes
 from typing import Optional
 
 from . import _check, block
-from .block import _fn, _new, _on, _rows, _want, _with_workspace
+from .block import _fn, _kind, _new, _on, _rows, _want, _with_workspace
 
 SSM_GSCAN_LERP = 1
 SSM_GSCAN_SEGMENT = 32
@@ -99,10 +99,14 @@ def ssm_gscan_update(state, x, r, i=None, rate=None, lerp: bool = False, out=Non
     B, D = shape
     if out is None:
         out = _new(shape, out_dtype or x.dtype, x)
+        code = _kind(out.dtype)
+        op = out.data_ptr()
+    else:
+        op = _want(out, "out", shape, None, dev)
+        code = block._code[out.dtype]
     sp = _want(state, "state", shape, block._F32, dev)
     _check(call(sp, sp if state_out is None else _want(state_out, "state_out", shape, block._F32, dev), *args,
-                SSM_GSCAN_LERP if lerp else 0, _want(out, "out", shape, None, dev), B, D, block._code[x.dtype],
-                block._code[out.dtype], _on(stream, dev)))
+                SSM_GSCAN_LERP if lerp else 0, op, B, D, block._code[x.dtype], code, _on(stream, dev)))
     return out
 
 
@@ -145,7 +149,8 @@ def ssm_xent_fwd(x, weight, target, scale: float = 1.0, z_loss: float = 0.0, str
     call = _fn("ssm_xent_fwd")
     dev, lead, T, D, V, args = _head(x, weight)
     f32 = block._F32
-    loss, lse = _new(lead, f32, x), _new(lead, f32, x)
+    loss = _new(lead, f32, x)
+    lse = _new(lead, f32, loss)
     _with_workspace(call, ("xent", T, D, V, dev), x, stream, (
         *args, _want(target, "target", lead, _int64(), dev), scale, z_loss, loss.data_ptr(), lse.data_ptr(), T, D, V,
         block._code[x.dtype], _on(stream, dev)))
@@ -184,7 +189,8 @@ def ssm_distill_fwd(x, weight, index, teacher, temperature: float = 1.0, scale: 
     dev, lead, T, D, V, args = _head(x, weight)
     K, tops = _tops(index, lead)
     f32 = block._F32
-    loss, lse, logits = _new(lead, f32, x), _new(lead, f32, x), _new(tops, f32, x)
+    loss, logits = _new(lead, f32, x), _new(tops, f32, x)
+    lse = _new(lead, f32, loss)
     _with_workspace(call, ("distill", T, D, V, K, dev), x, stream, (
         *args, _want(index, "index", tops, _int64(), dev), _want(teacher, "teacher", tops, f32, dev), scale, temperature,
         loss.data_ptr(), lse.data_ptr(), logits.data_ptr(), T, D, V, K, block._code[x.dtype], _on(stream, dev)))
