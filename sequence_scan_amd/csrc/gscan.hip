@@ -8,7 +8,10 @@
 namespace ssm {
 namespace {
 
-// Steps of a wavefront, what its registers hold, and wavefronts of a tile.
+// Steps of a wavefront, what its registers hold, and wavefronts of a tile.  More steps need
+// fewer words of the chain and put more loads under way; the registers of two workgroups of
+// 8 wavefronts a CU hold 16 (us, 8 x 2048 x 5120 and 1 x 65537 x 2560, steps x wavefronts: 16 x 8
+// 152 and 197, 8 x 16 143 and 217, 8 x 8 165 and 335, 16 x 4 161 and 282, 16 x 16 164 and 199).
 constexpr int kFwdSteps = 16, kFwdWaves = 8;
 constexpr int kBwdSteps = 8, kBwdWaves = 8;       // (back, a step keeps three times as much)
 constexpr int kFwdApart = kGsSegment / kFwdSteps, kBwdApart = kGsSegment / kBwdSteps;      // wavefronts between stored states
@@ -51,6 +54,11 @@ struct Place {
   __device__ __forceinline__ uint32_t off(int size, int j = 0) const { return in && j < n ? (uint32_t)d * size : kNowhere; }
 };
 
+// The forward.  A wavefront's steps are h -> P_j h + H_j with P and H running products and
+// sums, so what enters it is all that is missing when its loads are through: the wavefronts'
+// last (P, H) meet in LDS, the tile's in the chain.  Bound by HBM: x, r and i are read once,
+// out written once.  8 x 2048 x 5120 bf16 with all three (671 MB) 143 us, 4.7 TB/s; 1 x 65537 x
+// 2560 of two tensors (1007 MB) 196 us, 5.1 TB/s, what a large copy reaches (5.1).
 template <typename T, bool RATE, bool LERP, bool GATE, int CH, bool STREAM>
 __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs a, Chain c) {
   __shared__ float2 parts[kFwdWaves][CH][64];
@@ -158,6 +166,13 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
   }
 }
 
+// The gradients.  g_t = dout_t + a_{t+1} g_{t+1} is the same recurrence back in time: a
+// wavefront knows what leaves it for a zero gradient entering, the chain runs from the last
+// tile to the first.  The states before each step, which e needs, come forward from the one
+// stored every kGsSegment steps, by the same composition over at most 4 wavefronts.  x, r and
+// i stay in LDS as they were loaded between the two passes, a, m and g in registers; the
+// sigmoids are taken twice: registers that held those too would spill.  Bound by HBM: 4 x 2048 x 5120 bf16 reads four
+// tensors and the states and writes three, 608 MB in 145 us, 4.2 TB/s.
 template <typename T, bool RATE, bool LERP, bool GATE, int CH, bool STREAM>
 __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs a, Chain c) {
   __shared__ uint32_t kept[kBwdWaves][3][kBwdSteps][64];      // x, r and i as they lie in memory, for the second pass
@@ -338,6 +353,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
 }
 
 // Before a chain: everything unwritten but the first group's state, and no tile taken.
+// (4 to 6 us beside kernels of 80 to 200, mostly a launch: 1 x 65537 x 2560 writes 11 MB.)
 __global__ void __launch_bounds__(256) gscan_begin_kernel(Chain c, const float* __restrict__ first, int64_t width, int ch) {
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, stride = (int64_t)gridDim.x * 256;
   const int64_t each = 64 * ch, parts = (int64_t)c.strips * c.tiles * each, states = (int64_t)c.strips * c.groups * each;
@@ -356,6 +372,8 @@ __global__ void __launch_bounds__(256) gscan_begin_kernel(Chain c, const float* 
   if (n == 0) *c.next = 0;
 }
 
+// One token: an element a lane.  256 x 8192 bf16 (34 MB with the states, which the caches
+// hold from call to call) 8.5 us, 1 x 2560 2.8, a launch's least.
 template <typename T, bool RATE, bool LERP, bool GATE>
 __global__ void __launch_bounds__(256) gscan_step_kernel(GscanArgs a) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(256) gscan_step_kernel(GscanArgs a) {
 }
 
 // out[d] = sum over n rows of part[n][d], in a fixed order: 16 wavefronts take every
-// sixteenth row of 64 columns.
+// sixteenth row of 64 columns.  (128 rows of 5120: 4 us.)
 __global__ void __launch_bounds__(1024) gscan_sum_kernel(const float* __restrict__ part, float* __restrict__ out, int64_t n,
                                                          int64_t width) {
   __shared__ float t[16][64];

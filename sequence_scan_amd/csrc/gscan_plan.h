@@ -19,7 +19,8 @@ struct Chain {
 };
 
 // Tiles of a group: few leave less to read of the tiles before, many make fewer hops along
-// the chain.  Where workgroups are many, the hops hide behind them (us):
+// the chain.  Where workgroups are many, the hops hide behind them (us, with outputs stored
+// through the caches):
 //   8 x 2048 x 5120 (16 tiles): groups of 2 147.8, 4 147.2, 8 149.4
 //   1 x 65537 x 2560 (513 tiles, 10260 workgroups): 8 200.9, 12 204.4, 16 208.9
 //   1 x 60000 x 256, forward and back (469 and 938 tiles, 938 and 1876 workgroups): 8 155.7, 12 133.4, 16 126.8, 32 128.5

@@ -177,6 +177,15 @@ struct Reader {
 
 // acc = the tile at (m0, n0) of A B over the contracted elements k0 to k1 (k0 a multiple of 8).
 //
+// What bounds it is the matrix cores' power: in long runs of these products the clock falls
+// to about 2.06 GHz.  A training step of 8192 x 2560 x 50280 (8.4 TFLOP) 7000 us; without any
+// load from memory 5730 in place of 7156, from L2 alone 6 % less, with half the operands'
+// reads 2 %, with products alone 5020.  So everything that moves fewer bits through the
+// cores is worth more than anything that waits less: 16 x 16 x 32 products 7380 us, 32 x 32 x 16
+// 7940; neighbours that share an operand 7295, that do not 7345; while loads issued between
+// the products (7030 for 6850), quarter stages fetched four ahead (7382 for 7300) and no wait
+// at all (the same) gave nothing.
+//
 // A stage's first half is multiplied while its second half is read, the second half
 // while the next stage's first is: no product waits for LDS.  Between the halves every
 // wavefront has read all of the stage, so its place is free for the stage kStages on,
@@ -287,7 +296,10 @@ static_assert(sizeof(RowGrad) == kRowGradBytes, "vocab_plan.h agrees");
 constexpr float kLowest = -3.0e38f;
 
 // For every tile's columns a row's maximum and sum of exponentials (base 2), and the
-// target's logit where it lies in them.
+// target's logit where it lies in them.  The logits live in the registers of a tile only:
+// what leaves is 8 bytes for a row of 256 columns.  8192 x 2560 x 50280: 1690 us, 1245 TFLOP/s
+// (a library's product of 8192 x 8192 x 8192 1328, of this form and size 1155 with its logits);
+// 2039 x 1536 x 50280 290 us, 1086 TFLOP/s, with the clock not yet down.
 template <typename Shape, bool ONE>
 __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_kernel(VocabArgs a, float2* __restrict__ stats,
                                                                                        float* __restrict__ picked, int tiles_m, int tiles_n) {
@@ -409,7 +421,10 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
 // The same for up to 16 rows, where the weights' way from memory is all that counts.  x
 // lies in LDS, in the order in which the matrix cores take it; every wavefront reads an
 // equal share of the vocabulary's rows, 16 at a time, straight to registers, with eight
-// lines of 16 x 64 elements under way and no barrier between them.
+// lines of 16 x 64 elements under way and no barrier between them.  Bound by HBM: one row x
+// 2560 x 50280 reads 257 MB in 50 us, 5.1 TB/s.  (A call 54.7 us; with twelve lines 54.5, with
+// non-temporal loads 61.7: part of the weights is still in the last cache from the call
+// before.  16 x 4096 x 50280, 412 MB: 99.8, 97.5 and 96.2.)
 // What becomes of the logits: statistics and the target's logit, statistics, or dz of a
 // piece of the vocabulary (a.w and a.vocab are then the piece's).
 enum FewKind { kFewTarget, kFewStats, kFewDz };
@@ -533,7 +548,8 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, FewOut o
   }
 }
 
-// The logits at the indices of few rows, one wavefront for each.
+// The logits at the indices of few rows, one wavefront for each: at most 16 top reads of a row
+// of weights.
 __global__ void __launch_bounds__(256) vocab_pick_kernel(VocabArgs a) {
   const int e = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
@@ -600,7 +616,8 @@ __device__ __forceinline__ Teacher teacher_of(const VocabArgs& a, int64_t row, i
 
 // A row's log sum of exponentials from its pieces', and its loss.  A workgroup of 1024
 // threads takes `each` rows (a power of two up to 16), 1024 / each threads a row for the
-// pieces and a wavefront a row for the loss.
+// pieces and a wavefront a row for the loss.  Short and by reads: 8192 rows of 197 pieces (13 MB)
+// 6.5 us; with 4096 rows' 64 teacher logits 8.3.
 template <bool ONE>
 __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const float2* __restrict__ stats,
                                                           const float* __restrict__ picked, int pieces, int each) {
@@ -677,7 +694,9 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
 
 // A wavefront a row: what its dz is formed from, and (for dweight) its x, zeros where the
 // row takes no part, whatever x holds there.  Distillation: also hard q for each of the
-// row's indices, where the same index twice has the sum of both.
+// row's indices, where the same index twice has the sum of both (every pair is looked at:
+// top^2 / 64 steps a row, which 16 bytes a step from L1 keep short).  8192 rows of 2560 14 us,
+// 4096 rows of 1536 with 64 indices 20.
 template <bool ONE>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows, float* __restrict__ hard,
                                                          uint16_t* __restrict__ x) {
@@ -720,7 +739,10 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* _
 }
 
 // dz of a piece of the vocabulary, [rows, ldz] and padded with zeros, from the logits,
-// computed once more.
+// computed once more: storing them in the forward would cost 2 rows vocab bytes of memory
+// and gain a quarter of the step.  dz is rounded to bf16 (2^-8 of each element), the matrix
+// cores' type: a piece of fp32 would double its bytes and triple its products.  8192 x 2560 x
+// 16384: 600 us, 1145 TFLOP/s, with 268 MB written.
 template <typename Shape>
 __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_dz_kernel(VocabArgs a, const RowGrad* __restrict__ rows, int64_t v0, int columns,
                                                           uint16_t* __restrict__ dz, int64_t ldz, int tiles_m, int tiles_n) {
@@ -760,7 +782,7 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_dz_ker
 }
 
 // Distillation: dz at the teacher's indices, formed from the stored logits in place of
-// the rounded softmax.
+// the rounded softmax, so that p - q is rounded once.  4096 x 64 indices 7 us a piece.
 __global__ void __launch_bounds__(256) vocab_fix_kernel(VocabArgs a, const RowGrad* __restrict__ rows, const float* __restrict__ hard,
                                                         int64_t v0, int columns, uint16_t* __restrict__ dz, int64_t ldz) {
   const int64_t entries = (int64_t)a.rows * a.top;
@@ -812,6 +834,7 @@ __device__ __forceinline__ void store_tile(Acc<Shape>& acc, int64_t m0, int64_t 
 // A piece's two products, side by side so that neither leaves CUs idle alone:
 //   dweight[v0 ..] = dz^T x, the rows in slices, and its part of dx = dz weight, the piece's
 //   columns in slices.
+// 8192 x 2560 x 16384: 1055 us, 1300 TFLOP/s, as the library's largest products.
 struct Products {
   const uint16_t* dz;       // [rows, ldz], zeros from `columns` on
   int64_t ldz;
@@ -852,7 +875,7 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_produc
   }
 }
 
-// bf16 from the sums of its parts, in order; four elements a thread.
+// bf16 from the sums of its parts, in order; four elements a thread.  (Two of 4096 x 1536: 11 us.)
 __global__ void __launch_bounds__(256) vocab_sum_kernel(const float4* __restrict__ sums, int parts, int64_t each, uint2* __restrict__ out) {
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < each; e += (int64_t)gridDim.x * 256) {
     float4 v = sums[e];
