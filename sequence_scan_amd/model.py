@@ -38,6 +38,16 @@ def _gates(x, r, i, rate, dims: int):
     return dev, shape, (xp, xr, rp, rr, ip, ir, _want(rate, "rate", shape[-1:], block._F32, dev))
 
 
+def _out(out, out_dtype, x, shape, dev):
+    """The output, a new one if none is given, its pointer and the C ABI's code of its dtype."""
+    if out is None:
+        dtype = out_dtype or x.dtype
+        code = _kind(dtype)
+        out = _new(shape, dtype, x)
+        return out, out.data_ptr(), code
+    return out, _want(out, "out", shape, None, dev), block._code[out.dtype]
+
+
 def ssm_gscan_fwd(x, r, i=None, rate=None, lerp: bool = False, initial_state=None, out=None, last_state=None,
                   states=None, out_dtype=None, stream=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t for each channel, with
@@ -51,14 +61,13 @@ def ssm_gscan_fwd(x, r, i=None, rate=None, lerp: bool = False, initial_state=Non
     call = _fn("ssm_gscan_fwd")
     dev, shape, args = _gates(x, r, i, rate, 3)
     B, L, D = shape
-    if out is None:
-        out = _new(shape, out_dtype or x.dtype, x)
+    out, op, code = _out(out, out_dtype, x, shape, dev)
     st, f32 = (B, D), block._F32
     _with_workspace(call, ("gscan", B, L, D, dev), x, stream, (
-        *args, SSM_GSCAN_LERP if lerp else 0, _want(initial_state, "initial_state", st, f32, dev),
-        _want(out, "out", shape, None, dev), _want(last_state, "last_state", st, f32, dev),
-        _want(states, "states", (B, -(-L // SSM_GSCAN_SEGMENT), D), f32, dev), B, L, D, block._code[x.dtype],
-        block._code[out.dtype], _on(stream, dev)))
+        *args, SSM_GSCAN_LERP if lerp else 0, _want(initial_state, "initial_state", st, f32, dev), op,
+        _want(last_state, "last_state", st, f32, dev),
+        _want(states, "states", (B, -(-L // SSM_GSCAN_SEGMENT), D), f32, dev), B, L, D, block._code[x.dtype], code,
+        _on(stream, dev)))
     return out
 
 
@@ -97,13 +106,7 @@ def ssm_gscan_update(state, x, r, i=None, rate=None, lerp: bool = False, out=Non
     call = _fn("ssm_gscan_update")
     dev, shape, args = _gates(x, r, i, rate, 2)
     B, D = shape
-    if out is None:
-        out = _new(shape, out_dtype or x.dtype, x)
-        code = _kind(out.dtype)
-        op = out.data_ptr()
-    else:
-        op = _want(out, "out", shape, None, dev)
-        code = block._code[out.dtype]
+    out, op, code = _out(out, out_dtype, x, shape, dev)
     sp = _want(state, "state", shape, block._F32, dev)
     _check(call(sp, sp if state_out is None else _want(state_out, "state_out", shape, block._F32, dev), *args,
                 SSM_GSCAN_LERP if lerp else 0, op, B, D, block._code[x.dtype], code, _on(stream, dev)))

@@ -87,6 +87,30 @@ def test_graph_replays(name):
             assert torch.equal(a, b), f"replay {r}: output {i} differs from the eager result"
 
 
+@pytest.mark.parametrize("name", NAMES)
+def test_graph_of_a_shape_not_met_before(name):
+    """Captured calls whose workspace is the library's own, part of the graph."""
+    from sequence_scan_amd import block
+    say(f"graph, own workspace: {name}")
+    call = operators()[name]
+    want = [t.clone() for t in call()]
+    got = []
+
+    def run():
+        block._wanted.clear()
+        got[:] = call()
+    g = _capture(run)
+    for r in range(3):
+        for t in got:
+            t.fill_(float("nan"))
+        call()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), f"replay {r}: output {i} differs from the eager result"
+
+
 def test_two_graphs_in_turn():
     """Two captured chains, replayed in turn and on two streams at once, keep apart."""
     say("two graphs")
