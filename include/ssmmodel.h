@@ -121,7 +121,7 @@ ssm_status ssm_xent_fwd(const void* x, int64_t x_row, const void* weight, int64_
  * dz is rounded to bf16 for its two products, whose sums are fp32: off by at most 2^-8 of
  * each of their terms, and 2^-8 of the result for the result's own rounding.
  * Workspace: dz of a piece of the vocabulary, 2 rows v bytes with v columns of it, where
- * v is chosen so that this is at most SSM_VOCAB_PIECE_BYTES or v at most 4096; 16 bytes a
+ * v is chosen so that this is at most SSM_VOCAB_PIECE_BYTES or v at most 8192; 16 bytes a
  * row; where dweight is wanted a copy of x, 2 rows width; where dx is the sum of several
  * pieces its fp32 sums, 4 rows width; and where tiles are few such sums of up to 64 slices
  * of dx and 16 of dweight.

@@ -46,7 +46,7 @@ hipError_t launch_gscan_step(const GscanArgs& a, DT in, hipStream_t s);
 
 constexpr int kVocabTile = 256;   // of rows and columns; pieces of the vocabulary are multiples of it
 constexpr int64_t kVocabPieceBytes = 268435456;   // of dz at a time, or kVocabPieceLeast columns
-constexpr int64_t kVocabPieceLeast = 4096;
+constexpr int64_t kVocabPieceLeast = 8192;
 constexpr int64_t kVocabMaxLd = int64_t{1} << 22;   // elements between rows: 256 rows stay within 2^31 bytes
 
 struct VocabArgs {

@@ -49,9 +49,12 @@ inline int64_t makespan(int64_t n1, int64_t k1, int64_t n2, int64_t k2, int64_t 
   }
 }
 
-// (The least piece: each piece reads and writes dx's fp32 sums once.  Gradients of 65536 x
-// 1024 x 30000, 1024 columns at a time 25.4 ms, 4096 16.1; 131072 x 512 x 20000, 1024 59.6,
-// 4096 18.7.)
+// (The least piece: each piece reads and writes dx's fp32 sums once, and few columns are few
+// tiles.  Loss and gradients, ms, of pieces of 1024 / 4096 / 8192 / 16384 columns: 32768 x 1024 x
+// 50280 - / 15.9 / 13.0 / 12.9, 65536 x 2560 x 20000 - / 22.8 / 22.5 / 22.6; gradients of 65536 x
+// 1024 x 30000 25.4 / 16.1.  Below 32768 rows kVocabPieceBytes decides: half of it 2.26 in
+// place of 2.28 at 4096 x 1536 x 50280, but 7.21 for 7.00 at 8192 x 2560, 7.80 for 6.41 at 16384 x
+// 1024; four times 7.04, 6.40.)
 // The backward's cut: columns of a piece of the vocabulary, slices of the contracted
 // dimensions of dx (the piece's columns) and dweight (the rows), and the tiles.
 struct Cut {
