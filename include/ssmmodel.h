@@ -148,7 +148,8 @@ ssm_status ssm_xent_bwd(const float* dloss, const void* x, int64_t x_row, const 
  *            both.  All fp32.
  * A row without any index has loss 0 and no part in the gradients, whatever x
  * holds there.  top from 1 to SSM_DISTILL_MAX_TOP, temperature positive
- * with a normal square; the rest as for ssm_xent_fwd.
+ * with a normal square; the rest as for ssm_xent_fwd, and where rows,
+ * tiles of columns and top are many 8 rows top bytes more of workspace, and 2 for every row and tile.
  */
 #define SSM_DISTILL_MAX_TOP 1024
 ssm_status ssm_distill_fwd(const void* x, int64_t x_row, const void* weight, int64_t w_row, const int64_t* index,

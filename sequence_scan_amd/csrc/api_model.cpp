@@ -17,8 +17,9 @@ namespace {
 
 using namespace ssmhost;
 
-static_assert(ssm::kGsSegment == SSM_GSCAN_SEGMENT && ssm::kVocabPieceBytes == SSM_VOCAB_PIECE_BYTES,
-              "model.h and ssmmodel.h agree");
+static_assert(ssm::kGsSegment == SSM_GSCAN_SEGMENT && ssm::kVocabPieceBytes == SSM_VOCAB_PIECE_BYTES &&
+                  ssm::vocab::kMostTops == SSM_DISTILL_MAX_TOP,
+              "model.h, vocab_plan.h and ssmmodel.h agree");
 
 // ------------------------------------------------------ gated linear recurrence
 

@@ -84,6 +84,7 @@ struct Small {
   static constexpr int kPerSimd = 1;
 };
 static_assert(Large::kNi == 4 && Small::kNi == 4, "a wavefront has 64 columns of C");
+static_assert(Large::kTile == 256 && Small::kTile == 128, "tiles are powers of two");
 
 template <typename Shape>
 struct Stages {
@@ -295,14 +296,25 @@ static_assert(sizeof(RowGrad) == kRowGradBytes, "vocab_plan.h agrees");
 // values, or of values that are all minus infinity, is this: differences of maxima stay numbers.
 constexpr float kLowest = -3.0e38f;
 
+// What a row's indices are to the forward: the target; top indices, each looked at by every
+// tile; or, of many, those in order, of which a tile takes its own.
+enum StatsKind { kTarget, kTops, kSortedTops };
+struct Sorted {
+  const uint64_t* keys;       // [rows, top]: index << kPlaceBits | place
+  const uint16_t* starts;     // [rows, tiles + 1]: how many lie before a tile's columns
+};
+constexpr int kPlaceBits = 10;
+static_assert(1 << kPlaceBits == kMostTops, "a place fits");
+
 // For every tile's columns a row's maximum and sum of exponentials (base 2), and the
 // target's logit where it lies in them.  The logits live in the registers of a tile only:
 // what leaves is 8 bytes for a row of 256 columns.  8192 x 2560 x 50280: 1690 us, 1245 TFLOP/s
 // (a library's product of 8192 x 8192 x 8192 1328, of this form and size 1155 with its logits);
 // 2039 x 1536 x 50280 290 us, 1086 TFLOP/s, with the clock not yet down.
-template <typename Shape, bool ONE>
+template <typename Shape, StatsKind KIND>
 __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_kernel(VocabArgs a, float2* __restrict__ stats,
-                                                                                       float* __restrict__ picked, int tiles_m, int tiles_n) {
+                                                                                       float* __restrict__ picked, Sorted sorted, int tiles_m,
+                                                                                       int tiles_n) {
   constexpr int kTile = Shape::kTile, kMi = Shape::kMi, kWn = Shape::kWn, kHalf = kMi * 16;
   __shared__ Stages<Shape> s;
   __shared__ float2 part[kWn * kTile];
@@ -314,24 +326,37 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / kWn, wn = wave % kWn;
   const int n = wn * 64 + 4 * (lane >> 4);          // + ni * 16 + i
   const int columns = (int)(a.vocab - n0 < kTile ? a.vocab - n0 : kTile);
-  // Many indices: those of half the tile's rows at a time, of which a thread holds the
-  // first kHeld while the tile is dealt with.
-  constexpr int kHeld = ONE ? 1 : 16;
+  // The indices of half the tile's rows at a time, of which a thread holds the first kHeld
+  // while the tile is dealt with; or where its row's own begin and end, and the first of those.
+  constexpr int kHeld = KIND == kTops ? 16 : 1, kPer = Shape::kThreads / kHalf;
   int64_t held[kHeld];
+  int own = 0, own_end = 0;
+  const int own_row = threadIdx.x / kPer;
   auto entries_of = [&](int half) SSM_INLINE {
     const int64_t left = a.rows - (m0 + half * kHalf);
     return (uint32_t)(left < 0 ? 0 : left > kHalf ? kHalf : left) * (uint32_t)a.top;
   };
   auto hold = [&](int half) SSM_INLINE {
-    const uint32_t entries = entries_of(half);
-    const int64_t* at = a.index + (m0 + half * kHalf) * a.top;
+    if constexpr (KIND == kTops) {
+      const uint32_t entries = entries_of(half);
+      const int64_t* at = a.index + (m0 + half * kHalf) * a.top;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const uint32_t e = threadIdx.x + j * Shape::kThreads;
-      held[j] = e < entries ? at[e] : -1;
+      for (int j = 0; j < kHeld; ++j) {
+        const uint32_t e = threadIdx.x + j * Shape::kThreads;
+        held[j] = e < entries ? at[e] : -1;
+      }
+    } else {
+      const int64_t row = m0 + half * kHalf + own_row;
+      own = own_end = 0;
+      if (row < a.rows) {
+        const uint16_t* at = sorted.starts + row * (tiles_n + 1) + tn;
+        own = at[0] + threadIdx.x % kPer;
+        own_end = at[1];
+      }
+      if (own < own_end) held[0] = sorted.keys[row * a.top + own];
     }
   };
-  if constexpr (!ONE) hold(0);
+  if constexpr (KIND != kTarget) hold(0);
 #pragma unroll
   for (int mi = 0; mi < kMi; ++mi) {
     const int m = wm * kHalf + mi * 16 + (lane & 15);
@@ -344,7 +369,7 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
         acc[mi][ni][i] = z;
         top = __builtin_fmaxf(top, z);
       }
-    if constexpr (ONE) {
+    if constexpr (KIND == kTarget) {
       if (m0 + m < a.rows) {
         const int64_t v = a.index[m0 + m], d = v - n0 - n;
         if (v >= 0 && d >= 0 && d < 64 && (d & 12) == 0 && n + d < columns) {
@@ -382,7 +407,7 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
     }
     stats[(int64_t)tn * a.rows + m0 + m] = r;
   }
-  if constexpr (!ONE) {
+  if constexpr (KIND != kTarget) {
     // The logits at the rows' indices, by way of LDS, half the rows at a time: 16-byte
     // piece c of row r is at place c ^ (r & 15).
     float* z = reinterpret_cast<float*>(s.a[0]);
@@ -400,19 +425,26 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_
           }
       }
       block_sync();
-      const uint32_t entries = entries_of(half);
       const int64_t first = (m0 + half * kHalf) * a.top;
-      auto pick = [&](uint32_t e, int64_t v) SSM_INLINE {
-        const int64_t d = v - n0;
-        if (v >= 0 && d >= 0 && d < columns) {
-          const uint32_t r = e / (uint32_t)a.top, col = (uint32_t)d;
-          a.logits[first + e] = z[r * kTile + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)];
-        }
-      };
+      auto logit = [&](uint32_t r, uint32_t col) SSM_INLINE { return z[r * kTile + ((col >> 2) ^ (r & 15)) * 4 + (col & 3)]; };
+      if constexpr (KIND == kTops) {
+        auto pick = [&](uint32_t e, int64_t v) SSM_INLINE {
+          const int64_t d = v - n0;
+          if (v >= 0 && d >= 0 && d < columns) a.logits[first + e] = logit(e / (uint32_t)a.top, (uint32_t)d);
+        };
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j) pick(threadIdx.x + j * Shape::kThreads, held[j]);
+        for (int j = 0; j < kHeld; ++j) pick(threadIdx.x + j * Shape::kThreads, held[j]);
+        const uint32_t entries = entries_of(half);
 #pragma unroll 4
-      for (uint32_t e = threadIdx.x + kHeld * Shape::kThreads; e < entries; e += Shape::kThreads) pick(e, a.index[first + e]);
+        for (uint32_t e = threadIdx.x + kHeld * Shape::kThreads; e < entries; e += Shape::kThreads) pick(e, a.index[first + e]);
+      } else {
+        while (own < own_end) {
+          const int64_t at = first + (int64_t)own_row * a.top;
+          a.logits[at + (held[0] & (kMostTops - 1))] = logit(own_row, (uint32_t)((held[0] >> kPlaceBits) - n0));
+          own += kPer;
+          if (own < own_end) held[0] = sorted.keys[at + own];
+        }
+      }
       if (half == 0) hold(1);
     }
   }
@@ -614,6 +646,51 @@ __device__ __forceinline__ Teacher teacher_of(const VocabArgs& a, int64_t row, i
   return t;
 }
 
+// A row's indices in the vocabulary as keys in order, all ones for the others, by a wavefront
+// in n (a power of two, at least top) words of LDS; all wavefronts of a workgroup together.
+__device__ __forceinline__ void sort_row(const VocabArgs& a, int64_t row, int n, int lane, uint64_t* keys) {
+  for (int i = lane; i < n; i += 64) {
+    uint64_t key = ~0ull;
+    if (row < a.rows && i < a.top) {
+      const int64_t v = a.index[row * a.top + i];
+      if (v >= 0 && v < a.vocab) key = (uint64_t)v << kPlaceBits | i;
+    }
+    keys[i] = key;
+  }
+  block_sync();
+  for (int k = 2; k <= n; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int i = lane; i < n / 2; i += 64) {
+        const int lo = (i & ~(j - 1)) * 2 + (i & (j - 1)), hi = lo + j;
+        const uint64_t x = keys[lo], y = keys[hi];
+        if ((x > y) == ((lo & k) == 0)) keys[lo] = y, keys[hi] = x;
+      }
+      block_sync();
+    }
+}
+
+// The forward's: rows' keys and where each tile of 2^shift columns begins among them.  4096
+// rows of 64 indices 15 us, of 1024 105: a sort's 21 or 55 rounds through LDS.
+__global__ void __launch_bounds__(256) vocab_sort_kernel(VocabArgs a, uint64_t* __restrict__ out, uint16_t* __restrict__ starts, int shift,
+                                                         int tiles_n, int n) {
+  __shared__ uint64_t sorted[4][kMostTops];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * 4 + wave;
+  uint64_t* keys = sorted[wave];
+  sort_row(a, row, n, lane, keys);
+  if (row >= a.rows) return;
+  for (int i = lane; i < a.top; i += 64) out[row * a.top + i] = keys[i];
+  uint16_t* s = starts + row * (tiles_n + 1);
+  auto tile_of = [&](int i) SSM_INLINE {
+    const uint64_t t = keys[i] >> kPlaceBits >> shift;
+    return t < (uint64_t)tiles_n ? (int)t : tiles_n;
+  };
+  for (int i = lane; i <= a.top; i += 64) {
+    const int to = i < a.top ? tile_of(i) : tiles_n;
+    for (int t = i ? tile_of(i - 1) + 1 : 0; t <= to; ++t) s[t] = (uint16_t)i;
+  }
+}
+
 // A row's log sum of exponentials from its pieces', and its loss.  A workgroup of 1024
 // threads takes `each` rows (a power of two up to 16), 1024 / each threads a row for the
 // pieces and a wavefront a row for the loss.  Short and by reads: 8192 rows of 197 pieces (13 MB)
@@ -694,14 +771,17 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
 
 // A wavefront a row: what its dz is formed from, and (for dweight) its x, zeros where the
 // row takes no part, whatever x holds there.  Distillation: also hard q for each of the
-// row's indices, where the same index twice has the sum of both (every pair is looked at:
-// top^2 / 64 steps a row, which 16 bytes a step from L1 keep short).  8192 rows of 2560 14 us,
-// 4096 rows of 1536 with 64 indices 20.
+// row's indices, where the same index twice has the sum of both: in order, they lie together.
+// 8192 rows of 2560 14 us, 4096 rows of 1536 with 64 indices 15, with 1024 126 (comparing every
+// pair: 20 and 2840).
 template <bool ONE>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows, float* __restrict__ hard,
-                                                         uint16_t* __restrict__ x) {
+                                                         uint16_t* __restrict__ x, int n) {
+  __shared__ uint64_t sorted[ONE ? 1 : 4][ONE ? 1 : kMostTops];
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
+  uint64_t* keys = sorted[ONE ? 0 : threadIdx.x >> 6];
+  if constexpr (!ONE) sort_row(a, row, n, lane, keys);
   if (row >= a.rows) return;
   RowGrad g{0.0f, 0.0f, 0.0f, -2};
   const float lse = a.lse_in[row];
@@ -719,13 +799,15 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* _
       g = RowGrad{lse * kLog2e, d, d, -1};
       const float t2 = kLog2e / a.temperature, by = d / t.sum;
       const int64_t at = row * a.top;
-      for (int k = lane; k < a.top; k += 64) {
-        const int64_t v = a.index[at + k];
+      for (int i = lane; i < a.top; i += 64) {
+        const uint64_t v = keys[i] >> kPlaceBits;
+        if (v >= (uint64_t)a.vocab) break;
+        int e = i;
+        while (e > 0 && keys[e - 1] >> kPlaceBits == v) --e;
         float q = 0.0f;
-#pragma unroll 4
-        for (int j = 0; j < a.top; ++j)
-          if (a.index[at + j] == v) q += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[at + j], t2, -t.top2));
-        hard[at + k] = q * by;
+        for (; e < a.top && keys[e] >> kPlaceBits == v; ++e)
+          q += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[at + (keys[e] & (kMostTops - 1))], t2, -t.top2));
+        hard[at + (keys[i] & (kMostTops - 1))] = q * by;
       }
     }
   }
@@ -902,11 +984,25 @@ void launch_sum(const float* sums, int parts, int64_t elems, uint16_t* out, hipS
                      reinterpret_cast<const float4*>(sums), parts, each, reinterpret_cast<uint2*>(out));
 }
 
+// The words in which a row's indices are put in order.
+int sort_words(const VocabArgs& a) {
+  int n = 64;
+  while (n < a.top) n *= 2;
+  return n;
+}
+
 template <typename Shape>
-void launch_stats(const VocabArgs& a, float2* stats, float* picked, hipStream_t s) {
+void launch_stats(const VocabArgs& a, const FwdParts& at, float2* stats, float* picked, hipStream_t s) {
   const int tm = (int)tiles(a.rows, Shape::kTile), tn = (int)tiles(a.vocab, Shape::kTile);
-  auto k = a.teacher ? vocab_stats_kernel<Shape, false> : vocab_stats_kernel<Shape, true>;
-  hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(Shape::kThreads), 0, s, a, stats, picked, tm, tn);
+  Sorted sorted{};
+  if (at.sorted) {
+    uint64_t* keys = reinterpret_cast<uint64_t*>(a.work + at.keys);
+    uint16_t* starts = reinterpret_cast<uint16_t*>(a.work + at.starts);
+    hipLaunchKernelGGL(vocab_sort_kernel, dim3(fours(a.rows)), dim3(256), 0, s, a, keys, starts, Shape::kTile == 256 ? 8 : 7, tn, sort_words(a));
+    sorted = Sorted{keys, starts};
+  }
+  auto k = !a.teacher ? vocab_stats_kernel<Shape, kTarget> : at.sorted ? vocab_stats_kernel<Shape, kSortedTops> : vocab_stats_kernel<Shape, kTops>;
+  hipLaunchKernelGGL(k, dim3((unsigned)(tm * tn)), dim3(Shape::kThreads), 0, s, a, stats, picked, sorted, tm, tn);
 }
 
 template <typename Shape>
@@ -942,9 +1038,9 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t s) {
     else launch_few<kFewStats>(at.few, a, out, s);
     if (!one) hipLaunchKernelGGL(vocab_pick_kernel, dim3(fours(a.rows * a.top)), dim3(256), 0, s, a);
   } else if (at.large) {
-    launch_stats<Large>(a, stats, picked, s);
+    launch_stats<Large>(a, at, stats, picked, s);
   } else {
-    launch_stats<Small>(a, stats, picked, s);
+    launch_stats<Small>(a, at, stats, picked, s);
   }
   int each = 1;
   while (each < 16 && each < a.rows) each *= 2;
@@ -964,7 +1060,7 @@ hipError_t launch_vocab_bwd(const VocabArgs& a, hipStream_t s) {
   float* w_sums = reinterpret_cast<float*>(a.work + at.w_sums);
   const bool one = a.teacher == nullptr;
   auto rk = one ? vocab_rows_kernel<true> : vocab_rows_kernel<false>;
-  hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard, a.dw ? x : nullptr);
+  hipLaunchKernelGGL(rk, dim3(fours(a.rows)), dim3(256), 0, s, a, rows, hard, a.dw ? x : nullptr, one ? 0 : sort_words(a));
   int x_slices = 0;
   for (int64_t v0 = 0; v0 < a.vocab; v0 += cut.piece) {
     const Piece piece(a, cut, v0);

@@ -16,6 +16,7 @@ constexpr int kLargeTile = 256, kSmallTile = 128;      // rows and columns of a 
 constexpr int kFewRows = 16;        // rows that are one matrix operand
 constexpr int kFewWidth = 4096;     // ... whose x fits LDS
 constexpr int kRowGradBytes = 16;
+constexpr int kMostTops = 1024;     // teacher's logits of a row
 
 inline int64_t tiles(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 inline int64_t padded(int64_t n) { return (n + kK - 1) / kK * kK; }
@@ -133,13 +134,20 @@ struct Few {
 
 struct FwdParts : Parts {
   Few few;
-  bool large;
-  int64_t pieces, stats, picked;
+  bool large, sorted;
+  int64_t pieces, stats, picked, keys, starts;
   explicit FwdParts(const VocabArgs& a) : few(a, a.vocab) {
     large = large_tiles(a.rows, a.vocab, a.width, std::max(1, a.cus));
     pieces = few.few ? few.groups * 8 : tiles(a.vocab, large ? kLargeTile : kSmallTile);
     stats = add(pieces * a.rows * 8);
     picked = add(a.teacher ? 0 : (int64_t)a.rows * 4);
+    // Every tile reads its rows' indices, or they are put in order once and a tile finds its
+    // own (us, forward, read by all / in order): 100 x 512 x 5000 with 1024 logits a row (34 MB of
+    // reads) 96 / 109, 500 x 768 x 32000 with 100 (50 MB) 42 / 49, 4096 x 1536 x 50280 with 65
+    // (420 MB) 586 / 567, with 128 713 / 572, with 1024 2489 / 771.
+    sorted = a.teacher && !few.few && pieces * a.rows * a.top * 8 > (int64_t{1} << 27);
+    keys = add(sorted ? (int64_t)a.rows * a.top * 8 : 0);
+    starts = add(sorted ? a.rows * (pieces + 1) * 2 : 0);
   }
 };
 

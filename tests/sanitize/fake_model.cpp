@@ -135,7 +135,10 @@ hipError_t launch_vocab_fwd(const VocabArgs& a, hipStream_t) {
   const int64_t tile = at.large ? kLargeTile : kSmallTile;
   if (at.few.few ? at.pieces * at.few.share < a.vocab || at.pieces != at.few.groups * 8 : at.pieces * tile < a.vocab) fail("pieces");
   if (at.few.few && (a.rows > kFewRows || a.width > kFewWidth)) fail("few");
-  regions(a.work, vocab_fwd_bytes(a), {{at.stats, at.pieces * a.rows * 8}, {at.picked, a.teacher ? 0 : (int64_t)a.rows * 4}});
+  regions(a.work, vocab_fwd_bytes(a), {{at.stats, at.pieces * a.rows * 8},
+                                       {at.picked, a.teacher ? 0 : (int64_t)a.rows * 4},
+                                       {at.keys, at.sorted ? (int64_t)a.rows * a.top * 8 : 0},
+                                       {at.starts, at.sorted ? a.rows * (at.pieces + 1) * 2 : 0}});
   return hipSuccess;
 }
 

@@ -346,6 +346,41 @@ def test_many_tiles_in_pieces(T, D, V):
     check_many_tiles(T, D, V)
 
 
+@pytest.mark.parametrize("T,D,V,K", [(2100, 72, 19000, 128), (1100, 136, 21003, 300), (700, 64, 4099, 1024), (1500, 64, 2570, 1024),
+                                     (40, 1032, 30001, 100), (400, 72, 30001, 1000), (8, 64, 5000, 1024)])
+def test_many_indices_of_many_tiles(T, D, V, K):
+    check_many_tiles(T, D, V, K)
+
+
+def test_many_indices_in_one_place():
+    """1024 indices of which most are one column, and none elsewhere; others are past the vocabulary or negative."""
+    T, D, V, K = 1500, 64, 3001, 1024
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, w = torch.randn(T, D, device="cuda", generator=g).bfloat16(), torch.randn(V, D, device="cuda", generator=g).bfloat16() / 8
+    index = torch.full((T, K), V - 1, device="cuda")
+    index[:, ::3] = -1
+    index[:, 5] = 255
+    index[7, 9], index[8] = V, -1
+    teacher = torch.zeros(T, K, device="cuda")
+    loss, lse, z = ssm.ssm_distill_fwd(x, w, index, teacher)
+    wide = x.double() @ w.double().t()
+    at = index.clamp(0, V - 1)
+    has = ((index >= 0) & (index < V)).double()
+    assert ((z.double() - wide.gather(1, at) * has).abs() <= 2 * (D + 4) * ref.U * (x.double().abs() @ w.double().abs().t()).gather(1, at) * 1.01).all()
+    q = has / has.sum(-1, keepdim=True)
+    assert torch.isnan(loss[7]) and loss[8] == 0
+    d = torch.ones(T, device="cuda")
+    got = ssm.ssm_distill_bwd(d, x, w, index, teacher, lse, z)
+    assert not got["dx"][7:9].any()
+    takes = torch.ones(T, dtype=torch.bool, device="cuda")
+    takes[7:9] = False
+    p = torch.softmax(wide, -1)
+    dz = torch.where(takes[:, None], p.scatter_add(1, at, -q.nan_to_num()), 0.0)
+    # dz is rounded once and the result once; its own error, some 300 roundings of fp32, is below a sixteenth of that
+    bar = 2.0 ** -8 * 1.07 * (dz.abs().t() @ x.double().abs()) + 2.0 ** -8 * (dz.t() @ x.double()).abs() + 1e-6
+    assert ((got["dweight"].double() - dz.t() @ x.double()).abs() <= bar).all()
+
+
 def test_many_tiles_of_slices():
     check_many_tiles(1100, 520, 21003, place=far)
 
