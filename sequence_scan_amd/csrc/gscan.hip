@@ -16,36 +16,43 @@ constexpr int kFwdSteps = 16, kFwdWaves = 8;
 constexpr int kBwdSteps = 8, kBwdWaves = 8;       // (back, a step keeps three times as much)
 constexpr int kFwdApart = kGsSegment / kFwdSteps, kBwdApart = kGsSegment / kBwdSteps;      // wavefronts between stored states
 
-static_assert(kGsFwdTile == kFwdSteps * kFwdWaves && kGsBwdTile == kBwdSteps * kBwdWaves, "model.h agrees");
+static_assert(kFwdWaves == kGsWaves && kBwdWaves == kGsWaves && kGsFwdTile == kFwdSteps * kFwdWaves && kGsBwdTile == kBwdSteps * kBwdWaves, "model.h agrees");
 static_assert(kGsFwdTile % kGsSegment == 0 && kGsBwdTile % kGsSegment == 0, "tiles begin with a stored state");
 
-// The tile that a workgroup takes: its place in the chain and its strip.
+// Three forms of the kernels: the plain one; one whose outputs go past the caches; and one for
+// short sequences, several strips of which share a workgroup.
+enum Form { kPlain, kStream, kShort };
+
+// The tile that a workgroup takes: its place in the chain and its strip; short sequences have
+// one tile, and strips are told by wavefronts.
+template <Form FORM>
 __device__ __forceinline__ void take_tile(const Chain& c, int* tile, int* strip) {
   int n = blockIdx.x;
-  if (c.tiles > 1) {
+  if (FORM != kShort && c.tiles > 1) {
     __shared__ uint32_t taken;
     if (threadIdx.x == 0) taken = atomicAdd(c.next, 1u);
     block_sync();
     n = (int)__builtin_amdgcn_readfirstlane(taken);
   }
-  *tile = n / c.strips;
-  *strip = n % c.strips;
+  *tile = FORM == kShort ? 0 : n / c.strips;
+  *strip = FORM == kShort ? n : n % c.strips;
 }
 
 // Where a wavefront's steps lie.
-template <int CH, int kSteps>
+template <int CH, int kSteps, Form FORM>
 struct Place {
   int64_t b, t0, left, tok;      // batch row; first step; steps of the sequence from there; token
   int64_t d;                     // the lane's first channel
   int n;                         // steps of this wavefront's kSteps that there are
   bool in;                       // whether the channel is
-  __device__ __forceinline__ Place(const GscanArgs& a, int tile, int strip, int steps, int wave, int lane) {
+  __device__ __forceinline__ Place(const GscanArgs& a, const Chain& c, int tile, int strip, int steps, int wave, int lane) {
     const int per_row = (int)((a.width + 64 * CH - 1) / (64 * CH));
     b = strip / per_row;
     d = (int64_t)(strip % per_row) * (64 * CH) + lane * CH;
-    in = d < a.width;
+    const bool there = FORM != kShort || strip < c.strips;      // (the last workgroup's may not be)
+    in = d < a.width && there;
     t0 = (int64_t)tile * steps + wave * kSteps;
-    left = a.seqlen - t0;
+    left = there ? a.seqlen - t0 : -1;
     n = left < 0 ? 0 : left > kSteps ? kSteps : (int)left;
     tok = b * a.seqlen + t0;
   }
@@ -59,15 +66,17 @@ struct Place {
 // last (P, H) meet in LDS, the tile's in the chain.  Bound by HBM: x, r and i are read once,
 // out written once.  8 x 2048 x 5120 bf16 with all three (671 MB) 143 us, 4.7 TB/s; 1 x 65537 x
 // 2560 of two tensors (1007 MB) 196 us, 5.1 TB/s, what a large copy reaches (5.1).
-template <typename T, bool RATE, bool LERP, bool GATE, int CH, bool STREAM>
+template <typename T, bool RATE, bool LERP, bool GATE, int CH, Form FORM>
 __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs a, Chain c) {
   __shared__ float2 parts[kFwdWaves][CH][64];
-  __shared__ float enter[CH][64];
+  __shared__ float enter[FORM == kShort ? kFwdWaves : 1][CH][64];      // at a strip's first wavefront
   int tile, strip;
-  take_tile(c, &tile, &strip);
+  take_tile<FORM>(c, &tile, &strip);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = FORM == kShort ? wave & -c.waves : 0;      // of the strip's wavefronts
+  if (FORM == kShort) strip = (strip * kFwdWaves + wave) / c.waves;
   constexpr int kSteps = kFwdSteps;
-  const Place<CH, kSteps> at(a, tile, strip, kGsFwdTile, wave, lane);
+  const Place<CH, kSteps, FORM> at(a, c, tile, strip, kGsFwdTile, wave - first, lane);
   const uint32_t off = at.off(sizeof(T));
   float rate2[CH], P[kSteps][CH], H[kSteps][CH];
 #pragma unroll
@@ -103,9 +112,9 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
 #pragma unroll
   for (int k = 0; k < CH; ++k) parts[wave][k][lane] = make_float2(P[kSteps - 1][k], H[kSteps - 1][k]);
   block_sync();
-  if (wave == 0) {
+  if (wave == first) {
     float hin[CH];
-    if (c.tiles > 1) {
+    if (FORM != kShort && c.tiles > 1) {
       float tp[CH], th[CH];
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
@@ -123,20 +132,20 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
       for (int k = 0; k < CH; ++k) hin[k] = a.initial && at.in ? a.initial[at.b * a.width + at.d + k] : 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < CH; ++k) enter[k][lane] = hin[k];
+    for (int k = 0; k < CH; ++k) enter[first][k][lane] = hin[k];
   }
   block_sync();
   float h[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    h[k] = enter[k][lane];
-    for (int w = 0; w < wave; ++w) {
+    h[k] = enter[first][k][lane];
+    for (int w = first; w < wave; ++w) {
       const float2 v = parts[w][k][lane];
       h[k] = __builtin_fmaf(v.x, h[k], v.y);
     }
   }
   if (at.n == 0) return;
-  if (a.states && wave % kFwdApart == 0 && at.in) {
+  if (a.states && (wave - first) % kFwdApart == 0 && at.in) {
     float* s = a.states + (at.b * ((a.seqlen + kGsSegment - 1) / kGsSegment) + at.t0 / kGsSegment) * a.width + at.d;
 #pragma unroll
     for (int k = 0; k < CH; ++k) s[k] = h[k];
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
     for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) v[k] = __builtin_fmaf(P[j][k], h[k], H[j][k]);      // (past the last step the last one's)
-      store_raw<STREAM, Tout, CH>(ro, j, decltype(whole)::value ? off : at.off(sizeof(Tout), j), v);
+      store_raw<FORM == kStream, Tout, CH>(ro, j, decltype(whole)::value ? off : at.off(sizeof(Tout), j), v);
     }
   };
   if (at.n == kSteps) {
@@ -173,18 +182,20 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
 // i stay in LDS as they were loaded between the two passes, a, m and g in registers; the
 // sigmoids are taken twice: registers that held those too would spill.  Bound by HBM: 4 x 2048 x 5120 bf16 reads four
 // tensors and the states and writes three, 608 MB in 145 us, 4.2 TB/s.
-template <typename T, bool RATE, bool LERP, bool GATE, int CH, bool STREAM>
+template <typename T, bool RATE, bool LERP, bool GATE, int CH, Form FORM>
 __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs a, Chain c) {
   __shared__ uint32_t kept[kBwdWaves][3][kBwdSteps][64];      // x, r and i as they lie in memory, for the second pass
   __shared__ float2 parts[kBwdWaves][CH][64];
   __shared__ float ahead[kBwdWaves][CH][64];      // forward: what leaves a wavefront for a zero state entering
-  __shared__ float enter[CH][64];
+  __shared__ float enter[FORM == kShort ? kBwdWaves : 1][CH][64];      // at a strip's first wavefront
   int back, strip;
-  take_tile(c, &back, &strip);
+  take_tile<FORM>(c, &back, &strip);
   const int tile = c.tiles - 1 - back;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = FORM == kShort ? wave & -c.waves : 0, last = FORM == kShort ? first + c.waves - 1 : kBwdWaves - 1;
+  if (FORM == kShort) strip = (strip * kBwdWaves + wave) / c.waves;
   constexpr int kSteps = kBwdSteps;
-  const Place<CH, kSteps> at(a, tile, strip, kGsBwdTile, wave, lane);
+  const Place<CH, kSteps, FORM> at(a, c, tile, strip, kGsBwdTile, wave - first, lane);
   const uint32_t off = at.off(sizeof(T));
   // the state stored last before the wavefront's steps
   float rate[CH], h[CH];
@@ -254,9 +265,9 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
     ahead[wave][k][lane] = f[k];
   }
   block_sync();
-  if (wave == kBwdWaves - 1) {
+  if (wave == last) {
     float gin[CH];
-    if (c.tiles > 1) {
+    if (FORM != kShort && c.tiles > 1) {
       float tp[CH], tq[CH];
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
@@ -274,19 +285,19 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
       for (int k = 0; k < CH; ++k) gin[k] = a.dlast && at.in ? a.dlast[at.b * a.width + at.d + k] : 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < CH; ++k) enter[k][lane] = gin[k];
+    for (int k = 0; k < CH; ++k) enter[first][k][lane] = gin[k];
   }
   block_sync();
   // the gradient entering from behind, and the state entering from before
   float carry[CH], sum[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    carry[k] = enter[k][lane];
-    for (int w = kBwdWaves - 1; w > wave; --w) {
+    carry[k] = enter[first][k][lane];
+    for (int w = last; w > wave; --w) {
       const float2 v = parts[w][k][lane];
       carry[k] = __builtin_fmaf(v.x, carry[k], v.y);
     }
-    for (int w = wave / kBwdApart * kBwdApart; w < wave; ++w) h[k] = __builtin_fmaf(parts[w][k][lane].x, h[k], ahead[w][k][lane]);
+    for (int w = first + (wave - first) / kBwdApart * kBwdApart; w < wave; ++w) h[k] = __builtin_fmaf(parts[w][k][lane].x, h[k], ahead[w][k][lane]);
     sum[k] = 0.0f;
 #pragma unroll
     for (int j = kSteps - 1; j >= 0; --j) {
@@ -328,9 +339,9 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
         }
         h[k] = __builtin_fmaf(A[j][k], h[k], M[j][k] * u);
       }
-      store_raw<STREAM, T, CH>(rx, j, o, dx);
-      store_raw<STREAM, T, CH>(rr, j, o, dr);
-      if constexpr (GATE) store_raw<STREAM, T, CH>(ri, j, o, di);
+      store_raw<FORM == kStream, T, CH>(rx, j, o, dx);
+      store_raw<FORM == kStream, T, CH>(rr, j, o, dr);
+      if constexpr (GATE) store_raw<FORM == kStream, T, CH>(ri, j, o, di);
     }
   };
   if (at.n == kSteps) gradients(std::true_type{});
@@ -340,12 +351,11 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
 #pragma unroll
     for (int k = 0; k < CH; ++k) ahead[wave][k][lane] = sum[k];
     block_sync();
-    if (wave == 0 && at.in) {
+    if (wave == first && at.in) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        float s = ahead[0][k][lane];
-#pragma unroll
-        for (int w = 1; w < kBwdWaves; ++w) s += ahead[w][k][lane];
+        float s = ahead[first][k][lane];
+        for (int w = first + 1; w <= last; ++w) s += ahead[w][k][lane];
         a.part[(at.b * c.tiles + tile) * a.width + at.d + k] = s;
       }
     }
@@ -411,16 +421,21 @@ __global__ void __launch_bounds__(1024) gscan_sum_kernel(const float* __restrict
   }
 }
 
-// The kernel for a type and the three choices.
+// The kernel for a type and the three choices, and the form (a lane's one bf16 value is never a
+// whole line's).
 #define SSM_GSCAN_PICK(kernel, ...)                                                                                  \
   (a.rate ? (a.lerp ? (a.i ? kernel<true, true, true, __VA_ARGS__> : kernel<true, true, false, __VA_ARGS__>)       \
                     : (a.i ? kernel<true, false, true, __VA_ARGS__> : kernel<true, false, false, __VA_ARGS__>))    \
           : (a.lerp ? (a.i ? kernel<false, true, true, __VA_ARGS__> : kernel<false, true, false, __VA_ARGS__>)     \
                     : (a.i ? kernel<false, false, true, __VA_ARGS__> : kernel<false, false, false, __VA_ARGS__>)))
-template <bool RATE, bool LERP, bool GATE, typename T, int CH, bool STREAM>
-constexpr auto fwd_kernel = &gscan_fwd_kernel<T, RATE, LERP, GATE, CH, STREAM>;
-template <bool RATE, bool LERP, bool GATE, typename T, int CH, bool STREAM>
-constexpr auto bwd_kernel = &gscan_bwd_kernel<T, RATE, LERP, GATE, CH, STREAM>;
+#define SSM_GSCAN_FORM(kernel, ...)                                                 \
+  (l.c.waves < kGsWaves ? SSM_GSCAN_PICK(kernel, __VA_ARGS__, kShort)               \
+   : stream             ? SSM_GSCAN_PICK(kernel, __VA_ARGS__, kStream)              \
+                        : SSM_GSCAN_PICK(kernel, __VA_ARGS__, kPlain))
+template <bool RATE, bool LERP, bool GATE, typename T, int CH, Form FORM>
+constexpr auto fwd_kernel = &gscan_fwd_kernel<T, RATE, LERP, GATE, CH, FORM>;
+template <bool RATE, bool LERP, bool GATE, typename T, int CH, Form FORM>
+constexpr auto bwd_kernel = &gscan_bwd_kernel<T, RATE, LERP, GATE, CH, FORM>;
 template <bool RATE, bool LERP, bool GATE, typename T>
 constexpr auto step_kernel = &gscan_step_kernel<T, RATE, LERP, GATE>;
 
@@ -457,10 +472,11 @@ hipError_t launch_gscan_fwd(const GscanArgs& a, DT in, hipStream_t s) {
   const Layout l = gscan_layout(a.batch, a.seqlen, a.width, kGsFwdTile, channels(a, in), a.work);
   begin(l, a.initial, a.width, s);
   const bool stream = streams(a.width, a.out_bf16 ? 2 : 4);
-  auto k = in == DT::F32 ? (stream ? SSM_GSCAN_PICK(fwd_kernel, float, 1, true) : SSM_GSCAN_PICK(fwd_kernel, float, 1, false))
-           : l.ch == 2   ? (stream ? SSM_GSCAN_PICK(fwd_kernel, uint16_t, 2, true) : SSM_GSCAN_PICK(fwd_kernel, uint16_t, 2, false))
-                         : SSM_GSCAN_PICK(fwd_kernel, uint16_t, 1, false);
-  hipLaunchKernelGGL(k, dim3((unsigned)(l.c.strips * l.c.tiles)), dim3(64 * kFwdWaves), 0, s, a, l.c);
+  auto k = in == DT::F32 ? SSM_GSCAN_FORM(fwd_kernel, float, 1)
+           : l.ch == 2   ? SSM_GSCAN_FORM(fwd_kernel, uint16_t, 2)
+           : l.c.waves < kGsWaves ? SSM_GSCAN_PICK(fwd_kernel, uint16_t, 1, kShort)
+                                  : SSM_GSCAN_PICK(fwd_kernel, uint16_t, 1, kPlain);
+  hipLaunchKernelGGL(k, dim3((unsigned)l.blocks), dim3(64 * kFwdWaves), 0, s, a, l.c);
   return hipGetLastError();
 }
 
@@ -468,10 +484,11 @@ hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t s) {
   const Layout l = gscan_layout(a.batch, a.seqlen, a.width, kGsBwdTile, channels(a, in), a.work);
   begin(l, a.dlast, a.width, s);
   const bool stream = streams(a.width, in == DT::F32 ? 4 : 2);
-  auto k = in == DT::F32 ? (stream ? SSM_GSCAN_PICK(bwd_kernel, float, 1, true) : SSM_GSCAN_PICK(bwd_kernel, float, 1, false))
-           : l.ch == 2   ? (stream ? SSM_GSCAN_PICK(bwd_kernel, uint16_t, 2, true) : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 2, false))
-                         : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1, false);
-  hipLaunchKernelGGL(k, dim3((unsigned)(l.c.strips * l.c.tiles)), dim3(64 * kBwdWaves), 0, s, a, l.c);
+  auto k = in == DT::F32 ? SSM_GSCAN_FORM(bwd_kernel, float, 1)
+           : l.ch == 2   ? SSM_GSCAN_FORM(bwd_kernel, uint16_t, 2)
+           : l.c.waves < kGsWaves ? SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1, kShort)
+                                  : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1, kPlain);
+  hipLaunchKernelGGL(k, dim3((unsigned)l.blocks), dim3(64 * kBwdWaves), 0, s, a, l.c);
   if (a.drate)
     hipLaunchKernelGGL(gscan_sum_kernel, dim3((unsigned)((a.width + 63) / 64)), dim3(1024), 0, s, a.part, a.drate,
                        a.batch * l.c.tiles, a.width);

@@ -16,7 +16,10 @@ struct Chain {
   uint32_t* next;        // tiles handed out
   int32_t tiles, groups, strips;
   int32_t group;         // tiles of a group
+  int32_t waves;         // wavefronts of a strip: all of a workgroup, or where one tile is enough and its sequence
+                         // short a power of two of them, and the others of the workgroup the next strips
 };
+constexpr int kGsWaves = 8;       // of a workgroup
 
 // Tiles of a group: few leave less to read of the tiles before, many make fewer hops along
 // the chain.  Where workgroups are many, the hops hide behind them (us, with outputs stored
@@ -29,6 +32,7 @@ inline int group_of(int tiles, int strips) { return tiles <= 32 ? 4 : (int64_t)t
 struct Layout {
   Chain c;
   int ch;
+  int64_t blocks;    // workgroups
   int64_t bytes;     // of the chain's workspace
 };
 inline Layout gscan_layout(int64_t batch, int64_t seqlen, int64_t width, int64_t steps, int ch, char* work) {
@@ -39,6 +43,13 @@ inline Layout gscan_layout(int64_t batch, int64_t seqlen, int64_t width, int64_t
   l.c.tiles = (int32_t)((seqlen + steps - 1) / steps);
   l.c.group = group_of(l.c.tiles, l.c.strips);
   l.c.groups = (l.c.tiles + l.c.group - 1) / l.c.group;
+  // Strips side by side where a sequence leaves wavefronts idle (us, one strip to a workgroup
+  // and several: 4096 x 8 x 512 277 / 42, 2048 x 16 x 1024 287 / 59, 512 x 64 x 1024 83 / 57;
+  // forward and back 607 / 115, 614 / 169, 188 / 163).
+  l.c.waves = kGsWaves;
+  while (l.c.tiles == 1 && l.c.waves > 1 && seqlen <= steps / kGsWaves * (l.c.waves / 2)) l.c.waves /= 2;
+  const int64_t at_once = kGsWaves / l.c.waves;
+  l.blocks = (l.c.strips + at_once - 1) / at_once * l.c.tiles;
   if (l.c.tiles > 1) {
     const int64_t parts = (int64_t)l.c.strips * l.c.tiles * each * 8, states = (int64_t)l.c.strips * l.c.groups * each * 4;
     l.c.parts = reinterpret_cast<uint64_t*>(work);

@@ -284,3 +284,11 @@ def test_growing_decays(L, dtype):
     S = torch.zeros(2, 66, device="cuda")
     step = ssm.ssm_gscan_update(S, *(d[n][0][:, 0].contiguous() for n in "xri"), rate, True)
     near(step, want.h[:, 0], want.h_off[:, 0], HALF[dtype], "step")
+
+
+@pytest.mark.parametrize("L", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 48, 64, 65])
+@pytest.mark.parametrize("D,dtype", [(66, BF16), (130, F32), (65, BF16)])
+def test_short_sequences_of_many_rows(L, D, dtype):
+    """Several rows to a workgroup, the last one's not all there."""
+    check(37, L, D, dtype, True, True, False, True)
+    check(5, L, D, dtype, False, False, True, False)
