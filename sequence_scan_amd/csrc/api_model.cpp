@@ -286,7 +286,8 @@ ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_
   a.width = width;
   a.out_bf16 = out_dtype == SSM_BF16;
   const int64_t chain = ssm::gscan_chain_bytes(batch, seqlen, width, true);
-  const int64_t bytes = chain + (drate != nullptr ? sz.state * ceil_div(seqlen, ssm::kGsBwdTile) * 4 : 0);
+  const int64_t rows = batch * ceil_div(seqlen, ssm::kGsBwdTile);
+  const int64_t bytes = chain + (drate != nullptr ? (rows + ssm::gscan_sum_slices(rows)) * width * 4 : 0);
   if (bytes > 0) {
     void* ws = nullptr;
     e = work.get(&ws, bytes, s);

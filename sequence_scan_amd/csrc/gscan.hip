@@ -399,17 +399,19 @@ __global__ void __launch_bounds__(256) gscan_step_kernel(GscanArgs a) {
   else Io<float>::store(a.out, e, h);
 }
 
-// out[d] = sum over n rows of part[n][d], in a fixed order: 16 wavefronts take every
-// sixteenth row of 64 columns.  (128 rows of 5120: 4 us.)
-__global__ void __launch_bounds__(1024) gscan_sum_kernel(const float* __restrict__ part, float* __restrict__ out, int64_t n,
+// out[y][d] = sum of part[n][d] over slice y of n rows, in a fixed order: 16 wavefronts take
+// every sixteenth row of 64 columns.  (128 rows of 5120: 4 us.  In one slice, and in up to 64 and
+// those then, forward and back: 8192 rows of 1024 329 and 314 us, 4096 of 512 115 and 108, 2048
+// of 1024 179 and 175, 512 of 1024 158 and 159.)
+__global__ void __launch_bounds__(1024) gscan_sum_kernel(const float* __restrict__ part, float* __restrict__ out, int64_t n, int64_t each,
                                                          int64_t width) {
   __shared__ float t[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t d = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t d = (int64_t)blockIdx.x * 64 + lane, from = blockIdx.y * each, to = from + each < n ? from + each : n;
   float s = 0.0f;
   if (d < width) {
 #pragma unroll 8
-    for (int64_t i = wave; i < n; i += 16) s += part[i * width + d];
+    for (int64_t i = from + wave; i < to; i += 16) s += part[i * width + d];
   }
   t[wave][lane] = s;
   block_sync();
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(1024) gscan_sum_kernel(const float* __restrict
     float r = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) r += t[i][lane];
-    out[d] = r;
+    out[blockIdx.y * width + d] = r;
   }
 }
 
@@ -489,9 +491,13 @@ hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t s) {
            : l.c.waves < kGsWaves ? SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1, kShort)
                                   : SSM_GSCAN_PICK(bwd_kernel, uint16_t, 1, kPlain);
   hipLaunchKernelGGL(k, dim3((unsigned)l.blocks), dim3(64 * kBwdWaves), 0, s, a, l.c);
-  if (a.drate)
-    hipLaunchKernelGGL(gscan_sum_kernel, dim3((unsigned)((a.width + 63) / 64)), dim3(1024), 0, s, a.part, a.drate,
-                       a.batch * l.c.tiles, a.width);
+  if (a.drate) {
+    const int64_t rows = a.batch * l.c.tiles, slices = gscan_sum_slices(rows), each = (rows + slices - 1) / slices;
+    const unsigned strips = (unsigned)((a.width + 63) / 64);
+    float* sums = slices > 1 ? a.part + rows * a.width : a.drate;
+    hipLaunchKernelGGL(gscan_sum_kernel, dim3(strips, (unsigned)slices), dim3(1024), 0, s, a.part, sums, rows, each, a.width);
+    if (slices > 1) hipLaunchKernelGGL(gscan_sum_kernel, dim3(strips), dim3(1024), 0, s, sums, a.drate, slices, slices, a.width);
+  }
   return hipGetLastError();
 }
 

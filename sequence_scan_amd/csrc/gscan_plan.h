@@ -67,6 +67,9 @@ inline int64_t gscan_chain_bytes(int64_t batch, int64_t seqlen, int64_t width, b
   return std::max(gscan_layout(batch, seqlen, width, steps, 1, nullptr).bytes, gscan_layout(batch, seqlen, width, steps, 2, nullptr).bytes);
 }
 
+// Slices in which many rows of drate's sums are added first (1: all at once).
+inline int64_t gscan_sum_slices(int64_t rows) { return rows < 2048 ? 1 : std::min<int64_t>(rows / 128, 64); }
+
 }  // namespace ssm
 
 #endif  // SSMSCAN_GSCAN_PLAN_H

@@ -31,7 +31,7 @@ struct GscanArgs {
   void* di;
   float* drate;             // nullable
   float* dinitial;          // nullable
-  float* part;              // backward with drate: [batch, tiles, width] sums over a tile's steps
+  float* part;              // backward with drate: [batch, tiles, width] sums over a tile's steps, and [gscan_sum_slices, width]
   char* work;               // gscan_chain_bytes bytes (gscan_plan.h), where a sequence has more than one tile
   int64_t batch, seqlen, width;
   int32_t lerp;

@@ -111,7 +111,8 @@ hipError_t launch_gscan_bwd(const GscanArgs& a, DT in, hipStream_t) {
   maybe("dinitial", a.dinitial, state, 4);
   if (a.drate) {
     touch("drate", a.drate, a.width, 4);
-    touch("part", a.part, state * ((a.seqlen + kGsBwdTile - 1) / kGsBwdTile), 4);
+    const int64_t rows = a.batch * ((a.seqlen + kGsBwdTile - 1) / kGsBwdTile);
+    touch("part", a.part, (rows + gscan_sum_slices(rows)) * a.width, 4);
   }
   chain(a, kGsBwdTile, true);
   return hipSuccess;

@@ -268,6 +268,11 @@ def test_bits_repeat():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("B,L,D", [(2047, 3, 20), (2048, 3, 20), (3000, 2, 70), (30, 5000, 20)])
+def test_rates_gradient_over_many_tiles(B, L, D):
+    check(B, L, D, BF16, True, True, False, False)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("L", [1, 40, 150])
 def test_growing_decays(L, dtype):
