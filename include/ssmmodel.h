@@ -69,7 +69,7 @@ ssm_status ssm_gscan_fwd(const void* x, int64_t x_row, const void* r, int64_t r_
  *   drate      : [width] fp32, or NULL (not computed; iff rate is NULL it has to be)
  *   dinitial_state: [batch, width] fp32, or NULL
  * Workspace: as for the forward with tiles half as long, and 4 bytes for every such tile
- * and channel of a batch row where drate is computed.
+ * and channel of a batch row (and for up to 64 tiles more) where drate is computed.
  */
 ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_row, const void* i, int64_t i_row,
                          const float* rate, int flags, const float* states, const void* dout,

@@ -670,7 +670,7 @@ __device__ __forceinline__ void sort_row(const VocabArgs& a, int64_t row, int n,
 }
 
 // The forward's: rows' keys and where each tile of 2^shift columns begins among them.  4096
-// rows of 64 indices 15 us, of 1024 105: a sort's 21 or 55 rounds through LDS.
+// rows of 64 indices 13 us, of 1024 105: a sort's 21 or 55 rounds through LDS.
 __global__ void __launch_bounds__(256) vocab_sort_kernel(VocabArgs a, uint64_t* __restrict__ out, uint16_t* __restrict__ starts, int shift,
                                                          int tiles_n, int n) {
   __shared__ uint64_t sorted[4][kMostTops];
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
 // A wavefront a row: what its dz is formed from, and (for dweight) its x, zeros where the
 // row takes no part, whatever x holds there.  Distillation: also hard q for each of the
 // row's indices, where the same index twice has the sum of both: in order, they lie together.
-// 8192 rows of 2560 14 us, 4096 rows of 1536 with 64 indices 15, with 1024 126 (comparing every
+// 8192 rows of 2560 14 us, 4096 rows of 1536 with 64 indices 14, with 1024 126 (comparing every
 // pair: 20 and 2840).
 template <bool ONE>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* __restrict__ rows, float* __restrict__ hard,
