@@ -426,3 +426,45 @@ def test_logits_of_minus_infinity(T, V):
     assert ((lse.double() - want).abs() <= bar).all() and (z == -60.0 * D).all()
     w[:] = float("-inf")
     assert torch.isneginf(ssm.ssm_xent_fwd(x, w, target)[1]).all()
+
+
+@pytest.mark.parametrize("T,K", [(10, 4), (300, 4), (1500, 1024)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.4e38])
+def test_what_stands_beside_no_index(T, K, bad):
+    """Teacher's logits without an index, and x and dloss of rows without any, may be anything: same bits."""
+    D, V = 64, 3001
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, w = torch.randn(T, D, device="cuda", generator=g).bfloat16(), torch.randn(V, D, device="cuda", generator=g).bfloat16() / 8
+    index = torch.randint(0, V, (T, K), device="cuda", generator=g)
+    index[torch.rand(T, K, device="cuda", generator=g) < 0.3] = -1
+    none = torch.rand(T, device="cuda", generator=g) < 0.3
+    none[0], none[1], index[1, 0] = True, False, 5
+    index[none] = -7
+    teacher, d = torch.randn(T, K, device="cuda", generator=g), torch.randn(T, device="cuda", generator=g)
+
+    def run():
+        loss, lse, z = ssm.ssm_distill_fwd(x, w, index, teacher, 2.0)
+        grads = ssm.ssm_distill_bwd(d, x, w, index, teacher, lse, z, 2.0)
+        return [loss, z, grads["dx"], grads["dweight"]]
+    first = run()
+    teacher[index < 0] = bad
+    empty = (index < 0).all(-1)
+    x[empty], d[empty] = bad, bad
+    for a, b in zip(run(), first):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+    assert not first[0][empty].any() and not first[2][empty].any()
+
+
+@pytest.mark.parametrize("T", [10, 300])
+def test_gradients_beside_no_target(T):
+    """dloss of rows without a target may be anything."""
+    x, w = torch.randn(T, 64, device="cuda").bfloat16(), torch.randn(500, 64, device="cuda").bfloat16() / 8
+    target = torch.arange(T, device="cuda") % 400
+    target[::3] = -1
+    _, lse = ssm.ssm_xent_fwd(x, w, target)
+    d = torch.randn(T, device="cuda")
+    first = ssm.ssm_xent_bwd(d, x, w, target, lse)
+    d[::3], lse[::3] = float("nan"), float("inf")
+    again = ssm.ssm_xent_bwd(d, x, w, target, lse)
+    for n in first:
+        assert torch.equal(first[n], again[n]) and torch.isfinite(first[n]).all()
