@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(256) vocab_pick_kernel(VocabArgs a) {
 // lies past the vocabulary, and the softmax of the teacher's.
 struct Teacher {
   bool counts, past;
-  float top2, sum;      // of the teacher's logits over the temperature, in base 2
+  float top, sum;       // the largest of the teacher's logits, and the sum of e^((logit - top) / temperature)
 };
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -632,16 +632,16 @@ __device__ __forceinline__ Teacher teacher_of(const VocabArgs& a, int64_t row, i
     const int64_t v = a.index[row * a.top + k];
     past |= v >= a.vocab;
     if (v >= 0) {
-      const float l = a.teacher[row * a.top + k] * t2;
+      const float l = a.teacher[row * a.top + k];
       top = top != top ? top : (l != l ? l : __builtin_fmaxf(top, l));
     }
   }
-  t.top2 = wave_max(top);
+  t.top = wave_max(top);
   t.past = __any(past);
-  t.counts = !t.past && t.top2 != -__builtin_inff();
+  t.counts = !t.past && t.top != -__builtin_inff();
   float sum = 0.0f;
   for (int k = lane; k < a.top; k += 64)
-    if (a.index[row * a.top + k] >= 0) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[row * a.top + k], t2, -t.top2));
+    if (a.index[row * a.top + k] >= 0) sum += __builtin_amdgcn_exp2f((a.teacher[row * a.top + k] - t.top) * t2);
   t.sum = wave_sum(sum);
   return t;
 }
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(VocabArgs a, const flo
       const float t2 = kLog2e / a.temperature;
       const float logsum = __builtin_amdgcn_logf(t.sum);
       for (int k = lane; k < a.top; k += 64) {
-        const float l2 = __builtin_fmaf(a.teacher[row * a.top + k], t2, -t.top2) - logsum;     // log2 q
+        const float l2 = (a.teacher[row * a.top + k] - t.top) * t2 - logsum;     // log2 q
         const float q = __builtin_amdgcn_exp2f(l2);
         if (a.index[row * a.top + k] >= 0 && q != 0.0f)
           loss = __builtin_fmaf(q, __builtin_fmaf(l2, kLn2, lse - a.logits[row * a.top + k]), loss);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(VocabArgs a, RowGrad* _
         while (e > 0 && keys[e - 1] >> kPlaceBits == v) --e;
         float q = 0.0f;
         for (; e < a.top && keys[e] >> kPlaceBits == v; ++e)
-          q += __builtin_amdgcn_exp2f(__builtin_fmaf(a.teacher[at + (keys[e] & (kMostTops - 1))], t2, -t.top2));
+          q += __builtin_amdgcn_exp2f((a.teacher[at + (keys[e] & (kMostTops - 1))] - t.top) * t2);
         hard[at + (keys[i] & (kMostTops - 1))] = q * by;
       }
     }

@@ -468,3 +468,27 @@ def test_gradients_beside_no_target(T):
     again = ssm.ssm_xent_bwd(d, x, w, target, lse)
     for n in first:
         assert torch.equal(first[n], again[n]) and torch.isfinite(first[n]).all()
+
+
+@pytest.mark.parametrize("temperature", [0.5, 1.0, 3.0])
+def test_teachers_of_the_lowest_value(temperature):
+    """Logits of fp32's lowest value are without weight beside others, and equal ones alone."""
+    T, D, V, K = 40, 64, 500, 6
+    x, w = torch.randn(T, D, device="cuda").bfloat16(), torch.randn(V, D, device="cuda").bfloat16() / 8
+    index = torch.rand(T, V, device="cuda").topk(K, -1).indices
+    teacher = torch.randn(T, K, device="cuda")
+    lowest = torch.finfo(F32).min
+    some = teacher.clone()
+    some[:, 2:4] = lowest
+    some[::2] = lowest
+    plain = some.clone()
+    plain[:, 2:4] = float("-inf")
+    plain[::2] = 1.5
+    d = torch.randn(T, device="cuda")
+    results = []
+    for t in (some, plain):
+        loss, lse, z = ssm.ssm_distill_fwd(x, w, index, t, temperature)
+        assert (loss > 0).all()
+        results.append([loss, *ssm.ssm_distill_bwd(d, x, w, index, t, lse, z, temperature).values()])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
