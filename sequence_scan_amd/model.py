@@ -27,8 +27,15 @@ block._ARGS.update({
 })
 
 
+def _missing(name: str):
+    # (of the tensors that sizes and types are taken from; the C ABI names the others)
+    return ValueError(f"{name} is required")
+
+
 def _gates(x, r, i, rate, dims: int):
     """What the recurrence's calls share: sizes, and the arguments up to rate."""
+    if x is None:
+        raise _missing("x")
     if x.dim() != dims:
         raise ValueError("x must be [batch, seqlen, width]" if dims == 3 else "x must be [batch, width]")
     dev, shape = x.get_device(), x.shape
@@ -79,6 +86,8 @@ def ssm_gscan_bwd(x, r, i, rate, dout, states, lerp: bool = False, dlast_state=N
     false) and, as asked, dinitial_state."""
     call = _fn("ssm_gscan_bwd")
     dev, shape, args = _gates(x, r, i, rate, 3)
+    if dout is None:
+        raise _missing("dout")
     B, L, D = shape
     f32 = block._F32
     if want_rate is None:
@@ -120,6 +129,8 @@ def _int64():
 
 def _head(x, weight):
     """Sizes, and the arguments x to w_row, of a loss over a vocabulary: x [..., width]."""
+    if x is None or weight is None:
+        raise _missing("x" if x is None else "weight")
     if x.dim() < 1 or weight.dim() != 2:
         raise ValueError("x must be [..., width] and weight [vocab, width]")
     V, D = weight.shape
@@ -176,6 +187,8 @@ def ssm_xent_bwd(dloss, x, weight, target, lse, scale: float = 1.0, z_loss: floa
 
 
 def _tops(index, lead):
+    if index is None:
+        raise _missing("index")
     if index.dim() != len(lead) + 1:
         raise ValueError("index must be [..., top], with x's leading dimensions")
     return index.shape[-1], (*lead, index.shape[-1])
