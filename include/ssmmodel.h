@@ -80,7 +80,7 @@ ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_
 /*
  * One token for every (b, d).  state, state_out: [batch, width] fp32, one buffer (in
  * place) or two; x, r, i, out: [batch, width], rows of x, r and i x_row, r_row and i_row
- * elements apart.
+ * elements apart.  width at most 2^24, batch * width at most 2^31 - 1024.
  */
 ssm_status ssm_gscan_update(const float* state, float* state_out, const void* x, int64_t x_row, const void* r,
                             int64_t r_row, const void* i, int64_t i_row, const float* rate, int flags, void* out,

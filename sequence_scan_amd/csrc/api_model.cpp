@@ -32,8 +32,9 @@ struct GsSizes {
   int64_t states;    // elements of the stored states
 };
 
+// tiles: the call runs over tiles of steps (a single token's does not).
 ssm_status gs_check(int64_t batch, int64_t seqlen, int64_t width, int flags, std::initializer_list<ssm_dtype> types,
-                    GsSizes* sz) {
+                    bool tiles, GsSizes* sz) {
   if (batch < 0 || seqlen < 0 || width < 0)
     return fail(SSM_ERR_BAD_SHAPE, "negative size (batch=%lld seqlen=%lld width=%lld)", (long long)batch, (long long)seqlen,
                 (long long)width);
@@ -47,8 +48,9 @@ ssm_status gs_check(int64_t batch, int64_t seqlen, int64_t width, int flags, std
   if (sz->state > INT32_MAX - 1023 || width > kGsMostRow)
     return fail(SSM_ERR_UNSUPPORTED, "batch * width = %lld exceeds 2^31 - 1024 or width = %lld 2^24", (long long)sz->state, (long long)width);
   sz->states = sz->state * ceil_div(seqlen, SSM_GSCAN_SEGMENT);
-  // a workgroup of 512 threads for every 64 channels of a row and 128 steps, back 64
-  if (ceil_div(seqlen, ssm::kGsBwdTile) * batch * ceil_div(width, 64) > kMaxThreads / 512)
+  // a workgroup of 512 threads for every 64 channels of a row and 128 steps, back 64 (one
+  // limit for both: what runs forward can have its gradients)
+  if (tiles && ceil_div(seqlen, ssm::kGsBwdTile) * batch * ceil_div(width, 64) > kMaxThreads / 512)
     return fail(SSM_ERR_UNSUPPORTED, "batch=%lld by seqlen=%lld by width=%lld exceeds the grid", (long long)batch, (long long)seqlen,
                 (long long)width);
   return SSM_OK;
@@ -171,7 +173,7 @@ ssm_status ssm_gscan_fwd(const void* x, int64_t x_row, const void* r, int64_t r_
                          ssm_dtype out_dtype, void* stream) {
   Workspace work;
   GsSizes sz;
-  ssm_status st = gs_check(batch, seqlen, width, flags, {in_dtype, out_dtype}, &sz);
+  ssm_status st = gs_check(batch, seqlen, width, flags, {in_dtype, out_dtype}, true, &sz);
   const int64_t si = esize(in_dtype), so = esize(out_dtype);
   int64_t xb, rb, ib;
   if (st == SSM_OK) st = gs_rows("x", x, sz.tokens, width, x_row, si, &xb);
@@ -232,7 +234,7 @@ ssm_status ssm_gscan_bwd(const void* x, int64_t x_row, const void* r, int64_t r_
                          void* stream) {
   Workspace work;
   GsSizes sz;
-  ssm_status st = gs_check(batch, seqlen, width, flags, {in_dtype, out_dtype}, &sz);
+  ssm_status st = gs_check(batch, seqlen, width, flags, {in_dtype, out_dtype}, true, &sz);
   const int64_t si = esize(in_dtype), so = esize(out_dtype);
   int64_t xb, rb, ib;
   if (st == SSM_OK) st = gs_rows("x", x, sz.tokens, width, x_row, si, &xb);
@@ -303,7 +305,7 @@ ssm_status ssm_gscan_update(const float* state, float* state_out, const void* x,
                             int64_t r_row, const void* i, int64_t i_row, const float* rate, int flags, void* out,
                             int64_t batch, int64_t width, ssm_dtype in_dtype, ssm_dtype out_dtype, void* stream) {
   GsSizes sz;
-  ssm_status st = gs_check(batch, 1, width, flags, {in_dtype, out_dtype}, &sz);
+  ssm_status st = gs_check(batch, 1, width, flags, {in_dtype, out_dtype}, false, &sz);
   const int64_t si = esize(in_dtype), so = esize(out_dtype);
   int64_t xb, rb, ib;
   if (st == SSM_OK) st = gs_rows("x", x, batch, width, x_row, si, &xb);

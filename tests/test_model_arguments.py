@@ -3,6 +3,8 @@ without a GPU (each refusal comes before any HIP call is made)."""
 import pytest
 
 import sequence_scan_amd as ssm
+from test_block_abi import NULL, UNSUPPORTED
+from test_model_abi import step
 
 torch = pytest.importorskip("torch")
 
@@ -31,3 +33,12 @@ def calls():
 def test_a_missing_tensor_is_named(name, missing, kw):
     with pytest.raises(ValueError, match=rf"\b{missing} is required"):
         getattr(ssm, name)(**kw)
+
+
+@pytest.mark.parametrize("batch,width", [((1 << 23) - 1, 1), (1 << 23, 1), ((1 << 31) - 1024, 1), (1 << 24, 64), (1 << 23, 255), (127, 1 << 24)])
+def test_a_token_for_as_many_rows_as_the_header_says(batch, width):
+    """Only batch * width and width are limited (a tensor is left out, so that nothing runs)."""
+    rows = dict(x_row=width, r_row=width, i_row=width)
+    assert step(x=None, batch=batch, width=width, **rows) == NULL, ssm.ssm_last_error()
+    assert step(x=None, batch=batch + (1 << 31) // width, width=width, **rows) == UNSUPPORTED
+    assert "2^31" in ssm.ssm_last_error()
