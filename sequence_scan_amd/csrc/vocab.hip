@@ -497,20 +497,24 @@ __global__ void __launch_bounds__(512, 2) vocab_few_kernel(VocabArgs a, FewOut o
   }
   bf16x8_t w[kAhead][2];
   int load_group = 0, load_line = 0;      // what is loaded next
-  const uint16_t* row = a.w;
+  // A group of 16 rows through a buffer descriptor, so that what lies past a row's end is 0, as in x: an
+  // infinity there, of whatever row it is, would make the sum a NaN.  (16 rows stay within 2^27 bytes.)
+  constexpr uint32_t kPast = 0x80000000u;
+  const uint16_t* group = a.w;
+  uint32_t off = 0;       // of the lane's row and its first element
   auto begin_row = [&]() SSM_INLINE {
     // (columns past the share repeat its last)
-    const int c = load_group * 16 + (lane & 15);
-    row = a.w + (first + (c < columns ? c : columns - 1)) * a.w_row;
+    const int at = load_group * 16, c = at + (lane & 15);
+    group = a.w + (first + at) * a.w_row;
+    off = (uint32_t)(((c < columns ? c : columns - 1) - at) * (int)a.w_row * 2 + quarter * 16);
   };
   auto load = [&](bf16x8_t (&f)[2]) SSM_INLINE {
-    const int k = load_line * 64 + quarter * 8;
+    const auto buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(group), 0, 0x7fffffff, 0x00020000);
+    const int k = load_line * 64;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      // (past the row's end its start, against zeros of x)
-      const int at = k + kk * 32;
-      f[kk] = *reinterpret_cast<const bf16x8_t*>(row + (at < a.width ? at : 0));
-    }
+    for (int kk = 0; kk < 2; ++kk)
+      f[kk] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                               buffer, k + kk * 32 + quarter * 8 < a.width ? off : kPast, (k + kk * 32) * 2, 0));
     if (++load_line == lines) {
       load_line = 0;
       ++load_group;
