@@ -33,8 +33,9 @@ extern "C" {
  *                  (b * seqlen + t) * x_row (r_row, i_row) elements after the first
  *                  token's (slices of a packed projection; rows may not overlap, and are
  *                  at most 2^24 elements apart)
- *   rate         : [width] fp32 or NULL; meant to be >= 0 (below, a > 1 and without
- *                  SSM_GSCAN_LERP m is NaN)
+ *   rate         : [width] fp32 or NULL; meant to be >= 0 (below, a > 1, and without
+ *                  SSM_GSCAN_LERP m is NaN; with it, where the product of the decays of up to
+                  16 tiles leaves fp32's range, a state of 0 stays 0 and others are infinite)
  *   initial_state, last_state: [batch, width] fp32, each NULL for zero or not stored;
  *                  last_state may be initial_state (in place)
  *   out          : [batch, seqlen, width] in out_dtype

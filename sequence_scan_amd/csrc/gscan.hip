@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
   const int first = FORM == kShort ? wave & -c.waves : 0;      // of the strip's wavefronts
   if (FORM == kShort) strip = (strip * kFwdWaves + wave) / c.waves;
   constexpr int kSteps = kFwdSteps;
+  constexpr bool kGrow = RATE && LERP;      // (a rate below 0; without LERP its m is NaN)
   const Place<CH, kSteps, FORM> at(a, c, tile, strip, kGsFwdTile, wave - first, lane);
   const uint32_t off = at.off(sizeof(T));
   float rate2[CH], P[kSteps][CH], H[kSteps][CH];
@@ -123,10 +124,10 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
         for (int w = 1; w < kFwdWaves; ++w) {
           const float2 v = parts[w][k][lane];
           tp[k] *= v.x;
-          th[k] = __builtin_fmaf(v.x, th[k], v.y);
+          th[k] = onward<kGrow>(v.x, th[k], v.y);
         }
       }
-      chain_enter<CH>(c, strip, tile, tp, th, hin);
+      chain_enter<kGrow, CH>(c, strip, tile, tp, th, hin);
     } else {
 #pragma unroll
       for (int k = 0; k < CH; ++k) hin[k] = a.initial && at.in ? a.initial[at.b * a.width + at.d + k] : 0.0f;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
     h[k] = enter[first][k][lane];
     for (int w = first; w < wave; ++w) {
       const float2 v = parts[w][k][lane];
-      h[k] = __builtin_fmaf(v.x, h[k], v.y);
+      h[k] = onward<kGrow>(v.x, h[k], v.y);
     }
   }
   if (at.n == 0) return;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) v[k] = __builtin_fmaf(P[j][k], h[k], H[j][k]);      // (past the last step the last one's)
+      for (int k = 0; k < CH; ++k) v[k] = onward<kGrow>(P[j][k], h[k], H[j][k]);      // (past the last step the last one's)
       store_raw<FORM == kStream, Tout, CH>(ro, j, decltype(whole)::value ? off : at.off(sizeof(Tout), j), v);
     }
   };
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
   const int first = FORM == kShort ? wave & -c.waves : 0, last = FORM == kShort ? first + c.waves - 1 : kBwdWaves - 1;
   if (FORM == kShort) strip = (strip * kBwdWaves + wave) / c.waves;
   constexpr int kSteps = kBwdSteps;
+  constexpr bool kGrow = RATE && LERP;
   const Place<CH, kSteps, FORM> at(a, c, tile, strip, kGsBwdTile, wave - first, lane);
   const uint32_t off = at.off(sizeof(T));
   // the state stored last before the wavefront's steps
@@ -276,10 +278,10 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
         for (int w = kBwdWaves - 2; w >= 0; --w) {
           const float2 v = parts[w][k][lane];
           tp[k] *= v.x;
-          tq[k] = __builtin_fmaf(v.x, tq[k], v.y);
+          tq[k] = onward<kGrow>(v.x, tq[k], v.y);
         }
       }
-      chain_enter<CH>(c, strip, back, tp, tq, gin);
+      chain_enter<kGrow, CH>(c, strip, back, tp, tq, gin);
     } else {
 #pragma unroll
       for (int k = 0; k < CH; ++k) gin[k] = a.dlast && at.in ? a.dlast[at.b * a.width + at.d + k] : 0.0f;
@@ -295,9 +297,9 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
     carry[k] = enter[first][k][lane];
     for (int w = last; w > wave; --w) {
       const float2 v = parts[w][k][lane];
-      carry[k] = __builtin_fmaf(v.x, carry[k], v.y);
+      carry[k] = onward<kGrow>(v.x, carry[k], v.y);
     }
-    for (int w = first + (wave - first) / kBwdApart * kBwdApart; w < wave; ++w) h[k] = __builtin_fmaf(parts[w][k][lane].x, h[k], ahead[w][k][lane]);
+    for (int w = first + (wave - first) / kBwdApart * kBwdApart; w < wave; ++w) h[k] = onward<kGrow>(parts[w][k][lane].x, h[k], ahead[w][k][lane]);
     sum[k] = 0.0f;
 #pragma unroll
     for (int j = kSteps - 1; j >= 0; --j) {

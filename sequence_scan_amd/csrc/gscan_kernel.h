@@ -60,6 +60,14 @@ __device__ __forceinline__ float decay_slope(float a, float m) {
   return m == 0.0f ? 0.0f : -a * a * __builtin_amdgcn_rcpf(m);
 }
 
+// p h + b, over steps whose decays' product is p.  GROW: decays may exceed 1, and p fp32's
+// range, where a state of 0 stays 0 as in the steps themselves.
+template <bool GROW>
+__device__ __forceinline__ float onward(float p, float h, float b) {
+  const float v = __builtin_fmaf(p, h, b);
+  return GROW && h == 0.0f ? b : v;
+}
+
 // ------------------------------------------------------------ the chain of tiles
 //
 // A workgroup holds a tile in registers: some steps of each of its wavefronts, 64 CH
@@ -92,7 +100,7 @@ __device__ __forceinline__ void publish(uint32_t* at, float h) {
 // What enters tile `tile` (counted along the chain) of a strip, for one wavefront's
 // channels lane + 64 c; P and H are the tile's own.  Publishes them, and for the last of a
 // group the next group's state.
-template <int CH>
+template <bool GROW, int CH>
 __device__ __forceinline__ void chain_enter(const Chain& c, int strip, int tile, const float (&P)[CH], const float (&H)[CH],
                                             float (&h)[CH]) {
   const int lane = threadIdx.x & 63;
@@ -133,7 +141,7 @@ __device__ __forceinline__ void chain_enter(const Chain& c, int strip, int tile,
         for (int k = 0; k < CH; ++k) {
           const float p = __uint_as_float((uint32_t)w[j][k]);
           gp[k] *= p;
-          gh[k] = __builtin_fmaf(p, gh[k], __uint_as_float((uint32_t)(w[j][k] >> 32)));
+          gh[k] = onward<GROW>(p, gh[k], __uint_as_float((uint32_t)(w[j][k] >> 32)));
         }
       }
   }
@@ -148,10 +156,10 @@ __device__ __forceinline__ void chain_enter(const Chain& c, int strip, int tile,
     __builtin_amdgcn_s_sleep(1);
   }
 #pragma unroll
-  for (int k = 0; k < CH; ++k) h[k] = __builtin_fmaf(gp[k], __uint_as_float(s[k]), gh[k]);
+  for (int k = 0; k < CH; ++k) h[k] = onward<GROW>(gp[k], __uint_as_float(s[k]), gh[k]);
   if (last && tile + 1 < c.tiles) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) publish(state + 64 * CH + 64 * k, __builtin_fmaf(P[k], h[k], H[k]));
+    for (int k = 0; k < CH; ++k) publish(state + 64 * CH + 64 * k, onward<GROW>(P[k], h[k], H[k]));
   }
 }
 
