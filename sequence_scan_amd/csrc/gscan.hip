@@ -332,12 +332,13 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs 
           di[k] = gm * u * (ei * pos);
         }
         const float by = g[j][k] * __builtin_fmaf(A[j][k], h[k], u * decay_slope<LERP>(A[j][k], M[j][k]));
-        const float bp = by * rpos;
+        const float rneg = er * rpos;
         if constexpr (RATE) {
+          const float bp = by * rpos;
           sum[k] -= decltype(whole)::value || j < at.n ? bp : 0.0f;
-          dr[k] = -bp * rate[k] * (er * rpos);
+          dr[k] = -bp * rate[k] * rneg;
         } else {
-          dr[k] = bp * er;
+          dr[k] = by * rneg;      // (by rpos would be about rpos^2 where it is small, and lost below 1e-38)
         }
         h[k] = __builtin_fmaf(A[j][k], h[k], M[j][k] * u);
       }

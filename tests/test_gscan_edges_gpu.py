@@ -89,3 +89,22 @@ def test_gradients_of_zero_through_growing_decays(L, rate, dtype):
     r[:, :40] = -6.0
     dout[:, 40:] = 0
     run(x, r, None, np.full(D, rate), True, dout, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("lerp", [True, False])
+def test_closed_and_open_gates_without_a_rate(gate, lerp, dtype):
+    """sigmoid(r) and 1 - sigmoid(r) down to fp32's smallest normal numbers: the gradient of r falls as they do.
+
+    Closed gates keep no state, so dr is about g h e^r: relative to that it is held to the bars of everything else
+    (a few roundings for each unit of |r|)."""
+    say(f"far gates {gate} {lerp} {dtype}")
+    B, L, D = 2, 150, 66
+    g = np.random.default_rng(1)
+    r = -g.uniform(40, 80, (B, L, D))
+    r[:, :, ::3] *= -1
+    r[:, ::5] = g.standard_normal(r[:, ::5].shape)
+    i = g.standard_normal((B, L, D)) if gate else None
+    run(g.standard_normal((B, L, D)), r, i, None, lerp, g.standard_normal((B, L, D)), dtype,
+        g.standard_normal((B, D)), g.standard_normal((B, D)))
