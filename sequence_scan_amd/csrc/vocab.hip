@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "device.h"
+#include "lds_load.h"
 #include "model.h"
 #include "vocab_plan.h"
 
@@ -14,7 +15,6 @@ namespace {
 using namespace vocab;
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
 // One side of a product, a bf16 matrix in either order:
@@ -26,23 +26,6 @@ struct Side {
   int32_t n;        // rows or columns of C that it gives (across: a multiple of 8)
   int32_t k;        // contracted elements that it has (along: a multiple of 8); past them it counts as 0
 };
-
-// A wavefront's load of 64 x 16 bytes straight to LDS through a buffer descriptor:
-// lane l's go to `to` + 16 l, and a lane whose offset lies past the buffer's end
-// leaves zeros.
-__device__ __forceinline__ void load_lds16(i32x4_t buffer, uint32_t off, uint32_t to) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, 0 offen lds"
-      :
-      : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(buffer)
-      : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)static_cast<const char*>(p);
-}
 
 // The descriptor of `rows` rows of `length` elements: reads past the last row's end give 0.
 __device__ __forceinline__ i32x4_t buffer_of(const uint16_t* p, int64_t ld, int64_t rows, int64_t length) {
@@ -135,13 +118,13 @@ struct Loader {
       // next row's, does not matter; past the last row there are zeros)
       const i32x4_t buffer = buffer_of(p + (int64_t)at * ld, ld, k - at < kK ? k - at : kK, length);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_lds16(buffer, off[j], to + j * 1024);
+      for (int j = 0; j < 4; ++j) load_lds(buffer, off[j], to + j * 1024);
     } else {
       const i32x4_t buffer = buffer_of(p, ld, length, k);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t past = at + (c ^ ((j & 1) << 2)) * 8 < k ? 0 : 0x80000000u;     // (descriptors end below 2^31)
-        load_lds16(buffer, (off[j] + at * 2) | past, to + j * 1024);
+        load_lds(buffer, (off[j] + at * 2) | past, to + j * 1024);
       }
     }
   }
@@ -242,19 +225,19 @@ __device__ __forceinline__ void multiply(const Side& A, const Side& B, int64_t m
   };
 #pragma unroll
   for (int t = 0; t < kS; ++t) load(t);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(8 * (kS - 1)) : "memory");      // (eight loads a stage)
+  loaded<8 * (kS - 1)>();      // (eight loads a stage)
   block_sync();
   read(0, 0);
   for (int t = 0; t < stages; ++t) {
     read(t, 1);
     products(0);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(8 * (kS - 2)) : "memory");
+    loaded_and_read<8 * (kS - 2)>();
     block_sync();
     load(t + kS);      // (past the last stage zeros, so that the counts hold)
     read(t + 1, 0);
     products(1);
   }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  loaded_and_read<0>();
 }
 
 // Two neighbouring operands' columns of a row of C, rounded to bf16, as eight in a row:
