@@ -35,7 +35,7 @@ extern "C" {
  *                  at most 2^24 elements apart)
  *   rate         : [width] fp32 or NULL; meant to be >= 0 (below, a > 1, and without
  *                  SSM_GSCAN_LERP m is NaN; with it, where the product of the decays of up to
-                  16 tiles leaves fp32's range, a state of 0 stays 0 and others are infinite)
+ *                  16 tiles leaves fp32's range, a state of 0 stays 0 and others are infinite)
  *   initial_state, last_state: [batch, width] fp32, each NULL for zero or not stored;
  *                  last_state may be initial_state (in place)
  *   out          : [batch, seqlen, width] in out_dtype
@@ -106,8 +106,8 @@ ssm_status ssm_gscan_update(const float* state, float* state_out, const void* x,
  * multiple of 8 elements apart, at most 2^22; rows at most 2^22, vocab from 1 to 2^30, x and
  * weight of at most 2^37 elements, and at most 2^22 tiles of 256 rows by 256 columns.
  * Logits and sums are fp32.  Workspace: 8 bytes for every row and 256 columns, or 128
- * where tiles are few, and 4 for every row; up to 16 rows: 8 bytes for every row and
- * wavefront of the device.
+ * where tiles are few, and 4 for every row; up to 16 rows of at most 4096: 8 bytes for every
+ * row and wavefront of the device.
  */
 #define SSM_VOCAB_MAX_WIDTH 65536
 ssm_status ssm_xent_fwd(const void* x, int64_t x_row, const void* weight, int64_t w_row, const int64_t* target,

@@ -65,7 +65,8 @@ struct Place {
 // sums, so what enters it is all that is missing when its loads are through: the wavefronts'
 // last (P, H) meet in LDS, the tile's in the chain.  Bound by HBM: x, r and i are read once,
 // out written once.  8 x 2048 x 5120 bf16 with all three (671 MB) 143 us, 4.7 TB/s; 1 x 65537 x
-// 2560 of two tensors (1007 MB) 196 us, 5.1 TB/s, what a large copy reaches (5.1).
+// 2560 of two tensors (1007 MB) 195 us, 5.2 TB/s, what a large copy reaches (5.1).  An odd width reads
+// the lines at the borders of strips twice: 3 x 1021 x 1537 fp32 (76 MB) 26 us and bf16 (39 MB) 21.
 template <typename T, bool RATE, bool LERP, bool GATE, int CH, Form FORM>
 __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs a, Chain c) {
   __shared__ float2 parts[kFwdWaves][CH][64];
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(64 * kFwdWaves, 4) gscan_fwd_kernel(GscanArgs 
 // stored every kGsSegment steps, by the same composition over at most 4 wavefronts.  x, r and
 // i stay in LDS as they were loaded between the two passes, a, m and g in registers; the
 // sigmoids are taken twice: registers that held those too would spill.  Bound by HBM: 4 x 2048 x 5120 bf16 reads four
-// tensors and the states and writes three, 608 MB in 145 us, 4.2 TB/s.
+// tensors and the states and writes three, 608 MB in 145 us, 4.2 TB/s; 3 x 1021 x 1537 fp32 (133 MB)
+// 38 us and bf16 (67 MB) 31, one value a lane.
 template <typename T, bool RATE, bool LERP, bool GATE, int CH, Form FORM>
 __global__ void __launch_bounds__(64 * kBwdWaves, 4) gscan_bwd_kernel(GscanArgs a, Chain c) {
   __shared__ uint32_t kept[kBwdWaves][3][kBwdSteps][64];      // x, r and i as they lie in memory, for the second pass
@@ -385,8 +387,9 @@ __global__ void __launch_bounds__(256) gscan_begin_kernel(Chain c, const float* 
   if (n == 0) *c.next = 0;
 }
 
-// One token: an element a lane.  256 x 8192 bf16 (34 MB with the states, which the caches
-// hold from call to call) 8.5 us, 1 x 2560 2.8, a launch's least.
+// One token: an element a lane.  256 x 8192 bf16 (34 MB with the states) 8.2 us a call from call to
+// call on the same tensors, which the caches hold, 8.9 over three sets of them in turn; 1 x 2560 2.8,
+// a launch's least.
 template <typename T, bool RATE, bool LERP, bool GATE>
 __global__ void __launch_bounds__(256) gscan_step_kernel(GscanArgs a) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;

@@ -11,9 +11,11 @@
 namespace ssm {
 namespace {
 
-// exp(-v), from which sigmoid(v) = 1 / (1 + e) and sigmoid(-v) = e / (1 + e), each to a few
-// ulp.  Where the second is needed, e is held at 8e37 past fp32's range, whose reciprocal is
-// still a normal number: the sigmoids are then 1.25e-38 and 1.  A NaN stays one.
+// exp(-v), from which sigmoid(v) = 1 / (1 + e) and sigmoid(-v) = e / (1 + e): each to a few
+// ulp, and about half an ulp more for a unit of |v|, by which the argument's rounding moves e
+// (by up to 8 half ulps at |v| = 10, 31 at 40, 62 at 80).  Where the second is needed, e is held at 8e37
+// past fp32's range, whose reciprocal is still a normal number: the sigmoids are then 1.25e-38
+// and 1.  A NaN stays one.
 template <bool BOTH>
 __device__ __forceinline__ float gate_exp(float v) {
   const float e = __builtin_amdgcn_exp2f(-v * kLog2e);

@@ -162,7 +162,7 @@ struct Reader {
 // acc = the tile at (m0, n0) of A B over the contracted elements k0 to k1 (k0 a multiple of 8).
 //
 // What bounds it is the matrix cores' power: in long runs of these products the clock falls
-// to about 2.06 GHz.  A training step of 8192 x 2560 x 50280 (8.4 TFLOP) 7000 us; without any
+// to about 2.06 GHz.  A training step of 8192 x 2560 x 50280 (8.4 TFLOP) 7000 to 7120 us on several boxes; without any
 // load from memory 5730 in place of 7156, from L2 alone 6 % less, with half the operands'
 // reads 2 %, with products alone 5020.  So everything that moves fewer bits through the
 // cores is worth more than anything that waits less: 16 x 16 x 32 products 7380 us, 32 x 32 x 16
@@ -293,7 +293,7 @@ static_assert(1 << kPlaceBits == kMostTops, "a place fits");
 // target's logit where it lies in them.  The logits live in the registers of a tile only:
 // what leaves is 8 bytes for a row of 256 columns.  8192 x 2560 x 50280: 1690 us, 1245 TFLOP/s
 // (a library's product of 8192 x 8192 x 8192 1328, of this form and size 1155 with its logits);
-// 2039 x 1536 x 50280 290 us, 1086 TFLOP/s, with the clock not yet down.
+// 2039 x 1536 x 50280 298 us with the join, 1056 TFLOP/s.
 template <typename Shape, StatsKind KIND>
 __global__ void __launch_bounds__(Shape::kThreads, Shape::kPerSimd) vocab_stats_kernel(VocabArgs a, float2* __restrict__ stats,
                                                                                        float* __restrict__ picked, Sorted sorted, int tiles_m,
