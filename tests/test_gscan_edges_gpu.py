@@ -108,3 +108,24 @@ def test_closed_and_open_gates_without_a_rate(gate, lerp, dtype):
     i = g.standard_normal((B, L, D)) if gate else None
     run(g.standard_normal((B, L, D)), r, i, None, lerp, g.standard_normal((B, L, D)), dtype,
         g.standard_normal((B, D)), g.standard_normal((B, D)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L", [13, 30, 60])
+def test_zeros_through_growing_decays_of_short_sequences(L, dtype):
+    """As above where one wavefront, or several of a workgroup, hold a sequence, of many rows."""
+    say(f"zeros, short {L} {dtype}")
+    B, D, rate = 21, 66, np.full(66, -30.0)
+    g = np.random.default_rng(4)
+    x, r, dout = g.standard_normal((B, L, D)), np.zeros((B, L, D)), g.standard_normal((B, L, D))
+    front, back = x.copy(), dout.copy()
+    front[:, :L - 3], back[:, 3:] = 0, 0
+    late, early = r.copy(), r.copy()
+    late[:, L - 3:], early[:, :3] = -6.0, -6.0
+    (xt, xd), (rt, rd) = pair(front, dtype), pair(late, dtype)
+    rate_t, ra = pair(rate, F32)
+    want = ref.Gscan(xd, rd, None, ra, True)
+    out = ssm.ssm_gscan_fwd(xt, rt, None, rate_t, True)
+    near(out, want.h, want.h_off, HALF[dtype], "out")
+    assert not out[:, :L - 3].any()
+    run(np.zeros_like(x), early, None, rate, True, back, dtype)
